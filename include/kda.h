@@ -335,6 +335,140 @@ kda_status kda_decode_step_gated(const kda_shape* shape, const void* q, const vo
                                  float* state_inout, void* out, kda_stream_t stream);
 
 /*
+ * Latent attention: the other token mixer of the models whose KDA layers this library runs
+ * ("Kimi K3 Architecture Teardown", section "Hybrid Attention for 1M Tokens: KDA and Gated
+ * MLA": three KDA layers, then one latent-attention layer).  It keeps ONE row a token for
+ * all heads in a paged cache: a latent vector c of 512 channels, from which a per-head
+ * up-projection makes keys and values, and, in models that rotate positions (the pages'
+ * layers do not), a key part r of 64 channels shared by the heads.  The projections are the
+ * caller's GEMMs, as for KDA.
+ *
+ *   kda_latent_append    new tokens' rows [c | R(p) r] into the cache, the queries' r part rotated too
+ *   kda_latent_gather    cached rows back to packed rows (for the up-projection of a cached prefix)
+ *   kda_latent_decode    absorbed form: queries in latent space attend over the cache
+ *   kda_latent_prefill   expanded form: per-head keys and values of packed prompts
+ *
+ * Conventions, beside those above:
+ * - cache [num_pages, page_size, latent_dim + rope_dim] in dtype: a row is c, then r.
+ * - block_table: DEVICE int32 [N, max_pages]; token p of sequence n lies on page
+ *   block_table[n, p / page_size], row p % page_size.  Pages may be shared by sequences
+ *   (common prefixes) and lie in any order.  Entries behind a sequence's last page are not read
+ *   by kda_latent_decode and kda_latent_gather, whatever they hold.  An entry outside
+ *   [0, num_pages) causes no access: its tokens read as zero rows and are not written.
+ * - seq_lens: DEVICE int32 [N], the tokens of each sequence INCLUDING those of the call; values
+ *   are clamped to [0, max_pages * page_size].
+ * - The cache rows behind a sequence's end, and rows of q, k, v behind the last sequence, may hold
+ *   anything (NaN too): they reach no result.  Values that a sequence itself holds are taken as
+ *   finite: an infinite or NaN value reaches every row of its tile.
+ * - Supported: dtype KDA_BF16, latent_dim 512, rope_dim 0 or 64, page_size a power of two in
+ *   16 .. 1024, H <= 1024, and at most 2^31 - 1 rows in the cache and in one block_table row.
+ */
+typedef struct {
+    int32_t num_seqs;       /* N >= 0                                         */
+    int64_t total_tokens;   /* T: the call's tokens, packed, >= 0             */
+    int32_t H;              /* query heads, >= 1                              */
+    int32_t latent_dim;     /* 512                                            */
+    int32_t rope_dim;       /* 0 or 64                                        */
+    int32_t page_size;      /* tokens a page                                  */
+    int32_t num_pages;      /* pages of the cache, >= 0                       */
+    int32_t max_pages;      /* entries of a block_table row, >= 0             */
+    kda_dtype dtype;        /* KDA_BF16                                       */
+} kda_latent_shape;
+
+/*
+ * kda_latent_append -- write the rows of T new tokens into the cache and rotate by position.
+ *
+ * Token j of the cnt tokens that sequence n has in the call (cu_seqlens as in kda_prefill; NULL:
+ * T/N each) has position p = seq_lens[n] - cnt + j and goes to row p of the sequence:
+ *
+ *   cache[page, row] = [ latent[t] | R(p) k_rope[t] ],   q_rope_out[t, h] = R(p) q_rope[t, h]
+ *
+ * R(p) rotates pair i of the 64 channels by the angle p * inv_freq[i] (taken in 64 bits, so that
+ * far positions keep their angles): (a, b) -> (a cos - b sin, a sin + b cos), rounded once.
+ * latent:   [T, 512] rows, latent_stride elements apart; k_rope: [T, 64] rows, k_rope_stride
+ *           elements apart (both may be columns of one projection); NULL with rope_dim 0.
+ * inv_freq: DEVICE fp32 [32], or NULL: no rotation, rows are copied.
+ * interleaved: 0 pairs channels (i, i + 32), 1 pairs channels (2i, 2i + 1).
+ * q_rope:   the queries' rotated part, [T, H] rows of 64, q_stride elements apart (64 for a tensor
+ *           of its own, dk for the end of each row of kda_latent_prefill's q), or NULL: none.
+ * q_rope_out: as q_rope with rows q_out_stride apart; the same pointer and stride rotate in
+ *           place, any other overlap is an error of the caller's that is not detected.
+ * A token whose position is negative or beyond the table, or whose page is outside the cache, is
+ * not written (its queries are rotated all the same); tokens that no sequence has leave cache and
+ * q_rope_out alone.  Two tokens of a call that land on one row leave either's bytes there.
+ * Errors: KDA_ERR_INVALID_ARG for NULL pointers, negative sizes, T % N != 0 without cu_seqlens,
+ * N = 0 with T > 0, a stride below the row's width, q_rope without q_rope_out or with rope_dim 0;
+ * KDA_ERR_UNSUPPORTED for the shape limits above, pointers not 16-byte aligned (int32 and
+ * inv_freq: 4) or strides that are not multiples of 8; KDA_ERR_CUDA if a launch fails.
+ */
+kda_status kda_latent_append(const kda_latent_shape* shape, const void* latent, int64_t latent_stride,
+                             const void* k_rope, int64_t k_rope_stride, const float* inv_freq,
+                             int32_t interleaved, const void* q_rope, int64_t q_stride, void* q_rope_out,
+                             int64_t q_out_stride, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                             const int32_t* block_table, void* cache, kda_stream_t stream);
+
+/*
+ * kda_latent_gather -- cached rows back to packed rows: output row cu_seqlens[n] + j is row
+ * starts[n] + j of sequence n (starts: DEVICE int32 [N], NULL: 0), its first 512 channels to
+ * latent [T, 512] and its last 64 to k_rope [T, 64] (NULL with rope_dim 0).  A row outside the
+ * table or on a page outside the cache is written as zeros; output rows that no sequence has are
+ * left alone.  H is not used (any value >= 1).  Errors: as kda_latent_append's.
+ */
+kda_status kda_latent_gather(const kda_latent_shape* shape, const void* cache, const int32_t* block_table,
+                             const int32_t* cu_seqlens, const int32_t* starts, void* latent, void* k_rope,
+                             kda_stream_t stream);
+
+/*
+ * kda_latent_decode -- the absorbed form: a step of T' tokens (1 <= T' <= 16) for each of N
+ * sequences, total_tokens = N * T', as in kda_decode_step.  The step's rows are in the cache
+ * already (kda_latent_append), so token t of sequence n sees rows 0 .. seq_lens[n] - T' + t:
+ *
+ *   s_j = scale * (q_latent . c_j + q_rope . r_j),   out = sum_j softmax(s)_j c_j,
+ *   lse = ln sum_j e^{s_j}
+ *
+ * q_latent [N*T', H, 512] (the query through the key up-projection), q_rope [N*T', H, 64] (NULL
+ * with rope_dim 0), out [N*T', H, 512] in dtype (the value up-projection is the caller's), lse
+ * [N*T', H] fp32 or NULL.  A token that sees nothing gets out = 0 and lse = -inf.
+ * workspace: DEVICE memory of kda_latent_decode_workspace_size bytes, 256-byte aligned, owned by
+ * the caller, overwritten by the call; its contents need not be kept or cleared.  Two calls in
+ * flight at once (two streams, or two graphs that may run at the same time) need two.
+ * Errors: those of kda_decode_step and kda_latent_append; KDA_ERR_INVALID_ARG also for a scale
+ * that is not finite and > 0 and a NULL or too small workspace, KDA_ERR_UNSUPPORTED for a
+ * misaligned one or T' > 16.
+ */
+kda_status kda_latent_decode(const kda_latent_shape* shape, const void* q_latent, const void* q_rope,
+                             const void* cache, const int32_t* block_table, const int32_t* seq_lens, float scale,
+                             void* out, float* lse, void* workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_latent_decode_workspace_size -- bytes of workspace kda_latent_decode needs (at most 40 MB
+ * and a little; it depends on H and T' only).  Writes *bytes; the errors of the shape.  No CUDA call.
+ */
+kda_status kda_latent_decode_workspace_size(const kda_latent_shape* shape, size_t* bytes);
+
+/*
+ * kda_latent_prefill -- the expanded form: causal attention over packed sequences with per-head
+ * keys and values, the keys' last dk - 128 channels shared by the heads.
+ *
+ * shape: num_seqs, total_tokens (T queries), H, dk = 128 or 192, dv = 128, dtype KDA_BF16.
+ * Sequence n has queries cu_seqlens[n] .. and keys cu_seqlens_k[n] .. (DEVICE int32 [N+1] each,
+ * as in kda_prefill; NULL: T/N, or total_kv/N, each).  Query i of nq sees keys 0 .. nk - nq + i:
+ * with nk > nq the first nk - nq keys are a cached prefix; with nk < nq the first nq - nk queries
+ * see nothing and get out = 0, lse = -inf.
+ * q [T, H, dk]; k, v [total_kv, H, 128] with the rows of consecutive (token, head) kv_stride
+ * elements apart (128 for tensors of their own, 256 for the halves of one up-projection);
+ * k_rope [total_kv, dk - 128] (NULL for dk = 128); out [T, H, 128] in dtype; lse [T, H] fp32 or NULL.
+ *   s_ij = scale * (q_i[:128] . k_j + q_i[128:] . r_j),   out_i = sum_j softmax(s_i)_j v_j
+ * Rows of out and lse behind the last sequence are left alone.
+ * Errors: those of kda_prefill; KDA_ERR_INVALID_ARG also for a negative total_kv, total_kv % N != 0
+ * without cu_seqlens_k, kv_stride < 128, a scale that is not finite and > 0;
+ * KDA_ERR_UNSUPPORTED for another dk, dv or dtype, H > 1024, or a kv_stride that is not a multiple of 8.
+ */
+kda_status kda_latent_prefill(const kda_shape* shape, int64_t total_kv, const void* q, const void* k, const void* v,
+                              int64_t kv_stride, const void* k_rope, float scale, const int32_t* cu_seqlens,
+                              const int32_t* cu_seqlens_k, void* out, float* lse, kda_stream_t stream);
+
+/*
  * kda_check_cu_seqlens -- validate a HOST copy of a cu_seqlens table:
  * cu[0] == 0, non-decreasing, cu[num_seqs] == total_tokens.  Returns KDA_OK
  * or KDA_ERR_INVALID_ARG.  No CUDA call.

@@ -26,6 +26,12 @@ class KdaShape(ctypes.Structure):
                 ("dtype", ctypes.c_int)]
 
 
+class KdaLatentShape(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int64), ("H", ctypes.c_int32),
+                ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("dtype", ctypes.c_int)]
+
+
 class KdaError(RuntimeError):
     def __init__(self, fn, status, name):
         super().__init__(f"{fn} returned {name} ({status})")
@@ -70,6 +76,17 @@ def lib():
         L.kda_prefill_split_workspace_size.restype = ctypes.c_int
         L.kda_prefill_frontend.argtypes = [sp, ctypes.c_int32, ctypes.c_float] + [vp] * 13
         L.kda_prefill_frontend.restype = ctypes.c_int
+        lp, i32, i64 = ctypes.POINTER(KdaLatentShape), ctypes.c_int32, ctypes.c_int64
+        L.kda_latent_append.argtypes = [lp, vp, i64, vp, i64, vp, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp]
+        L.kda_latent_append.restype = ctypes.c_int
+        L.kda_latent_gather.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp]
+        L.kda_latent_gather.restype = ctypes.c_int
+        L.kda_latent_decode.argtypes = [lp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp]
+        L.kda_latent_decode.restype = ctypes.c_int
+        L.kda_latent_decode_workspace_size.argtypes = [lp, ctypes.POINTER(ctypes.c_size_t)]
+        L.kda_latent_decode_workspace_size.restype = ctypes.c_int
+        L.kda_latent_prefill.argtypes = [sp, i64, vp, vp, vp, i64, vp, ctypes.c_float, vp, vp, vp, vp, vp]
+        L.kda_latent_prefill.restype = ctypes.c_int
         L.kda_status_string.argtypes = [ctypes.c_int]
         L.kda_status_string.restype = ctypes.c_char_p
         L.kda_version.argtypes = []
@@ -357,6 +374,224 @@ def kda_decode_step(q, k, v, log_alpha, beta, state, out=None, stream=None):
                                _ptr(beta), _ptr(state), _ptr(out), _stream(stream))
     _check("kda_decode_step", st)
     return out
+
+
+# ---------------------------------------------------------------- latent attention
+
+_LATENT, _ROPE, _HEAD = 512, 64, 128
+
+
+def _expect(name, t, shape, dtype, device, strides=False):
+    """A tensor argument of the latent-attention calls: its shape, type and device; contiguous unless
+    the call takes its strides."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, not on {t.device}")
+    if not strides and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _row_stride(name, t):
+    """Elements between consecutive rows of t [..., channels], all its leading axes one run of rows."""
+    rows = 1
+    step = None
+    for d in range(t.dim() - 2, -1, -1):
+        if t.shape[d] > 1:
+            if step is None:
+                step = t.stride(d)
+                if step < t.shape[-1] * rows or step % rows:
+                    raise ValueError(f"{name}: rows must not overlap")
+                step //= rows
+            elif t.stride(d) != step * rows:
+                raise ValueError(f"{name}: rows must be evenly spaced")
+        rows *= t.shape[d]
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: channels must be contiguous")
+    return max(t.shape[-1], 8) if step is None else step
+
+
+def _cuda(t):
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must be CUDA tensors")
+    return t.device
+
+
+def _table(name, table, tokens, device):
+    """A cu_seqlens argument: a CUDA int32 tensor as it is, a host table validated and copied."""
+    if not (isinstance(table, torch.Tensor) and table.is_cuda):
+        host = torch.as_tensor(table, dtype=torch.int32).cpu()
+        kda_check_cu_seqlens(host, tokens)
+        table = host.to(device)
+    if table.dim() != 1 or table.numel() < 1:
+        raise ValueError(f"{name} must hold N + 1 offsets")
+    _expect(name, table, table.shape, torch.int32, device)
+    return table
+
+
+def _latent_cache(cache, block_table, device):
+    """(rope_dim, page_size, num_pages, N, max_pages) of a latent cache and its table."""
+    if cache.dim() != 3 or cache.shape[2] not in (_LATENT, _LATENT + _ROPE):
+        raise ValueError(f"cache must be [pages, page_size, {_LATENT} or {_LATENT + _ROPE}], "
+                         f"not {tuple(cache.shape)}")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [N, max_pages]")
+    _expect("cache", cache, cache.shape, torch.bfloat16, device)
+    _expect("block_table", block_table, block_table.shape, torch.int32, device)
+    return cache.shape[2] - _LATENT, cache.shape[1], cache.shape[0], block_table.shape[0], block_table.shape[1]
+
+
+def _call(fn, device, stream, *args):
+    """Call fn(*args, stream) with the tensors' device current."""
+    if device.index == torch.cuda.current_device():
+        _check(fn, getattr(lib(), fn)(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn, getattr(lib(), fn)(*args, _stream(stream)))
+
+
+def kda_latent_append(latent, k_rope, cache, block_table, seq_lens, inv_freq=None, interleaved=False, q_rope=None,
+                      q_rope_out=None, cu_seqlens=None, stream=None):
+    """Write new tokens' rows into the paged latent cache, rotated by position (see ``include/kda.h``).
+
+    latent: [T, 512]; k_rope: [T, 64] (None for a cache without it), both possibly columns of one
+    projection; cache: [pages, page_size, 512 or 576] bf16, written in place; block_table: [N, max_pages]
+    int32; seq_lens: [N] int32, the lengths including these tokens.  ``inv_freq`` [32] fp32 gives the
+    angles a position (None: no rotation).  ``q_rope`` [T, H, 64], possibly the end of longer rows, is
+    rotated into ``q_rope_out`` (allocated when not given; q_rope itself rotates in place), which is
+    returned; None without queries."""
+    dev = _cuda(cache)
+    rope, page, pages, n, per = _latent_cache(cache, block_table, dev)
+    T = latent.shape[0]
+    p_latent = _expect("latent", latent, (T, _LATENT), torch.bfloat16, dev, True)
+    p_rope = _expect("k_rope", k_rope, (T, _ROPE), torch.bfloat16, dev, True) if rope else None
+    p_lens = _expect("seq_lens", seq_lens, (n,), torch.int32, dev)
+    p_freq = None if inv_freq is None else _expect("inv_freq", inv_freq, (_ROPE // 2,), torch.float32, dev)
+    if cu_seqlens is not None:
+        cu_seqlens = _table("cu_seqlens", cu_seqlens, T, dev)
+        _expect("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, dev)
+    H, p_q, p_out, q_step, out_step = 1, None, None, 0, 0
+    if q_rope is not None:
+        H = q_rope.shape[1]
+        p_q = _expect("q_rope", q_rope, (T, H, _ROPE), torch.bfloat16, dev, True)
+        q_step = _row_stride("q_rope", q_rope)
+        if q_rope_out is None:
+            q_rope_out = torch.empty((T, H, _ROPE), dtype=torch.bfloat16, device=dev)
+        p_out = _expect("q_rope_out", q_rope_out, (T, H, _ROPE), torch.bfloat16, dev, True)
+        out_step = _row_stride("q_rope_out", q_rope_out)
+    shape = KdaLatentShape(n, T, H, _LATENT, rope, page, pages, per, KDA_BF16)
+    _call("kda_latent_append", dev, stream, ctypes.byref(shape), p_latent, _row_stride("latent", latent), p_rope,
+          _row_stride("k_rope", k_rope) if rope else 0, p_freq, int(bool(interleaved)), p_q, q_step, p_out, out_step,
+          None if cu_seqlens is None else cu_seqlens.data_ptr(), p_lens, block_table.data_ptr(), cache.data_ptr())
+    return q_rope_out if q_rope is not None else None
+
+
+def kda_latent_gather(cache, block_table, cu_seqlens, total_tokens, starts=None, out=None, stream=None):
+    """Cached rows back to packed rows (see ``include/kda.h``): rows starts[n] .. of every sequence n, as
+    many as cu_seqlens gives it.  Returns (latent [T, 512], k_rope [T, 64] or None), or fills ``out``."""
+    dev = _cuda(cache)
+    rope, page, pages, n, per = _latent_cache(cache, block_table, dev)
+    T = int(total_tokens)
+    cu_seqlens = _table("cu_seqlens", cu_seqlens, T, dev)
+    _expect("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, dev)
+    p_starts = None if starts is None else _expect("starts", starts, (n,), torch.int32, dev)
+    if out is None:
+        out = (torch.empty((T, _LATENT), dtype=cache.dtype, device=dev),
+               torch.empty((T, rope), dtype=cache.dtype, device=dev) if rope else None)
+    latent, k_rope = out
+    p_latent = _expect("latent", latent, (T, _LATENT), torch.bfloat16, dev)
+    p_rope = _expect("k_rope", k_rope, (T, rope), torch.bfloat16, dev) if rope else None
+    shape = KdaLatentShape(n, T, 1, _LATENT, rope, page, pages, per, KDA_BF16)
+    _call("kda_latent_gather", dev, stream, ctypes.byref(shape), cache.data_ptr(), block_table.data_ptr(),
+          cu_seqlens.data_ptr(), p_starts, p_latent, p_rope)
+    return latent, k_rope
+
+
+def kda_latent_decode_workspace_size(num_seqs: int, total_tokens: int, H: int, rope_dim: int = 64) -> int:
+    """Bytes of workspace kda_latent_decode needs for total_tokens / num_seqs tokens a sequence and H heads."""
+    shape = KdaLatentShape(int(num_seqs), int(total_tokens), int(H), _LATENT, int(rope_dim), 64, 0, 0, KDA_BF16)
+    n = ctypes.c_size_t(0)
+    _check("kda_latent_decode_workspace_size",
+           lib().kda_latent_decode_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    return int(n.value)
+
+
+def kda_latent_decode(q_latent, q_rope, cache, block_table, seq_lens, scale, out=None, lse=None, workspace=None,
+                      stream=None):
+    """Absorbed latent attention over the paged cache, 1 to 16 tokens a sequence (see ``include/kda.h``).
+
+    q_latent: [N*T, H, 512]; q_rope: [N*T, H, 64] (None for a cache without it); seq_lens: [N] int32,
+    the step's tokens included (their rows are in the cache).  ``lse`` may be a [N*T, H] fp32 tensor to
+    fill, True to allocate one, or None; ``workspace`` a CUDA uint8 tensor of
+    kda_latent_decode_workspace_size bytes, allocated here when not given.  Returns (out [N*T, H, 512], lse)."""
+    dev = _cuda(cache)
+    rope, page, pages, n, per = _latent_cache(cache, block_table, dev)
+    rows, H = q_latent.shape[0], q_latent.shape[1]
+    p_q = _expect("q_latent", q_latent, (rows, H, _LATENT), torch.bfloat16, dev)
+    p_r = _expect("q_rope", q_rope, (rows, H, _ROPE), torch.bfloat16, dev) if rope else None
+    p_lens = _expect("seq_lens", seq_lens, (n,), torch.int32, dev)
+    if out is None:
+        out = torch.empty((rows, H, _LATENT), dtype=torch.bfloat16, device=dev)
+    if lse is True:
+        lse = torch.empty((rows, H), dtype=torch.float32, device=dev)
+    p_out = _expect("out", out, (rows, H, _LATENT), torch.bfloat16, dev)
+    p_lse = None if lse is None else _expect("lse", lse, (rows, H), torch.float32, dev)
+    shape = KdaLatentShape(n, rows, H, _LATENT, rope, page, pages, per, KDA_BF16)
+    if workspace is None:
+        need = ctypes.c_size_t(0)
+        _check("kda_latent_decode", lib().kda_latent_decode_workspace_size(ctypes.byref(shape), ctypes.byref(need)))
+        workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
+    _call("kda_latent_decode", dev, stream, ctypes.byref(shape), p_q, p_r, cache.data_ptr(), block_table.data_ptr(),
+          p_lens, float(scale), p_out, p_lse, _expect("workspace", workspace, workspace.shape, torch.uint8, dev),
+          workspace.numel())
+    return out, lse
+
+
+def kda_latent_prefill(q, k, v, k_rope, scale, cu_seqlens=None, cu_seqlens_k=None, num_seqs=None, out=None,
+                       lse=None, stream=None):
+    """Expanded latent attention, causal over packed sequences (see ``include/kda.h``).
+
+    q: [T, H, 128 or 192]; k, v: [S, H, 128], tensors of their own or the halves of one [S, H, 256]
+    projection; k_rope: [S, 64], shared by the heads (None for 128-wide q).  ``cu_seqlens`` and
+    ``cu_seqlens_k`` are CUDA int32 tensors or host tables (None: ``num_seqs`` equal sequences; keys as
+    queries where only cu_seqlens is given and S = T).  Returns (out [T, H, 128], lse)."""
+    dev = _cuda(q)
+    T, H, dk = q.shape
+    S = k.shape[0]
+    if dk not in (_HEAD, _HEAD + _ROPE):
+        raise ValueError(f"q must be [T, H, {_HEAD} or {_HEAD + _ROPE}], not {tuple(q.shape)}")
+    p_q = _expect("q", q, (T, H, dk), torch.bfloat16, dev)
+    p_k = _expect("k", k, (S, H, _HEAD), torch.bfloat16, dev, True)
+    p_v = _expect("v", v, (S, H, _HEAD), torch.bfloat16, dev, True)
+    p_r = _expect("k_rope", k_rope, (S, dk - _HEAD), torch.bfloat16, dev) if dk > _HEAD else None
+    step = _row_stride("k", k)
+    if S * H > 1 and step != _row_stride("v", v):
+        raise ValueError("k and v must have the same row stride")
+    n = 1 if num_seqs is None else int(num_seqs)
+    if cu_seqlens is not None:
+        cu_seqlens = _table("cu_seqlens", cu_seqlens, T, dev)
+        n = cu_seqlens.numel() - 1
+    if cu_seqlens_k is not None:
+        cu_seqlens_k = _table("cu_seqlens_k", cu_seqlens_k, S, dev)
+        if cu_seqlens is None:
+            n = cu_seqlens_k.numel() - 1
+        _expect("cu_seqlens_k", cu_seqlens_k, (n + 1,), torch.int32, dev)
+    elif cu_seqlens is not None and S == T:
+        cu_seqlens_k = cu_seqlens
+    if out is None:
+        out = torch.empty((T, H, _HEAD), dtype=torch.bfloat16, device=dev)
+    if lse is True:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    p_out = _expect("out", out, (T, H, _HEAD), torch.bfloat16, dev)
+    p_lse = None if lse is None else _expect("lse", lse, (T, H), torch.float32, dev)
+    shape = KdaShape(n, T, H, dk, _HEAD, KDA_BF16)
+    _call("kda_latent_prefill", dev, stream, ctypes.byref(shape), S, p_q, p_k, p_v, step, p_r, float(scale),
+          None if cu_seqlens is None else cu_seqlens.data_ptr(),
+          None if cu_seqlens_k is None else cu_seqlens_k.data_ptr(), p_out, p_lse)
+    return out, lse
 
 
 def kda_device_status(stream=None) -> int:

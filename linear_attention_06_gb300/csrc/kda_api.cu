@@ -93,6 +93,50 @@ kda_status check_gate(const kda_shape* s, const void* gate, const float* norm_w,
     return KDA_OK;
 }
 
+// Latent-attention shapes: sizes, then the limits that kda.h states.
+kda_status check_latent_shape(const kda_latent_shape* s) {
+    if (!s) return KDA_ERR_INVALID_ARG;
+    if (s->num_seqs < 0 || s->total_tokens < 0 || s->H <= 0 || s->latent_dim <= 0 || s->rope_dim < 0 ||
+        s->page_size <= 0 || s->num_pages < 0 || s->max_pages < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (s->dtype != KDA_BF16 || s->latent_dim != 512 || (s->rope_dim != 0 && s->rope_dim != 64) || s->H > 1024)
+        return KDA_ERR_UNSUPPORTED;
+    if (s->page_size < 16 || s->page_size > 1024 || (s->page_size & (s->page_size - 1)) != 0)
+        return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)s->num_pages * s->page_size > (int64_t)INT32_MAX ||
+        (int64_t)s->max_pages * s->page_size > (int64_t)INT32_MAX)
+        return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// A packed batch: T tokens of n sequences, split evenly without a table.
+kda_status check_split(int32_t n, int64_t tokens, const int32_t* cu) {
+    if (tokens > 0 && n == 0) return KDA_ERR_INVALID_ARG;
+    if (tokens > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (!cu && n > 0 && tokens % n != 0) return KDA_ERR_INVALID_ARG;
+    if (cu && !aligned(cu, 4)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// A decode step: the same number of tokens, 1 to kMaxDecodeTokens, for each of n sequences.
+kda_status check_step(int32_t n, int64_t tokens) {
+    if (n == 0) return tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
+    if (tokens <= 0 || tokens % n != 0) return KDA_ERR_INVALID_ARG;
+    if (tokens / n > kda::kMaxDecodeTokens || tokens > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// The cache and its table; either may be null where it has no entries.
+kda_status check_latent_cache(const kda_latent_shape* s, const void* cache, const int32_t* table) {
+    if ((s->num_pages > 0 && !cache) || (s->max_pages > 0 && !table)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(cache, 16) || !aligned(table, 4)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+kda::LatentCache latent_cache(const kda_latent_shape* s, void* cache, const int32_t* table) {
+    return {cache, table, s->page_size, s->num_pages, s->max_pages, s->rope_dim};
+}
+
 kda_status finish(cudaError_t e, cudaStream_t st) {
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     if (env_flag("KDA_DEBUG_SYNC")) return kda_device_status(st);
@@ -373,6 +417,127 @@ kda_status kda_prefill_frontend(const kda_shape* shape, int32_t conv_width, floa
                         shape->H, shape->dk, shape->dv, conv_width, eps, kda::DType::BF16};
     f.status = status;
     return finish(kda::launch_chunk_tc_frontend(a, f, s), s);
+}
+
+kda_status kda_latent_append(const kda_latent_shape* shape, const void* latent, int64_t latent_stride,
+                             const void* k_rope, int64_t k_rope_stride, const float* inv_freq,
+                             int32_t interleaved, const void* q_rope, int64_t q_stride, void* q_rope_out,
+                             int64_t q_out_stride, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                             const int32_t* block_table, void* cache, kda_stream_t stream) {
+    kda_status st = check_latent_shape(shape);
+    if (st != KDA_OK) return st;
+    st = check_split(shape->num_seqs, shape->total_tokens, cu_seqlens);
+    if (st != KDA_OK) return st;
+    if (shape->total_tokens == 0) return KDA_OK;
+    const bool rope = shape->rope_dim != 0;
+    if (!latent || (rope && !k_rope) || !seq_lens) return KDA_ERR_INVALID_ARG;
+    if (latent_stride < shape->latent_dim || (rope && k_rope_stride < shape->rope_dim)) return KDA_ERR_INVALID_ARG;
+    if (q_rope && (!rope || !q_rope_out || q_stride < shape->rope_dim || q_out_stride < shape->rope_dim))
+        return KDA_ERR_INVALID_ARG;
+    if ((interleaved != 0 && interleaved != 1)) return KDA_ERR_INVALID_ARG;
+    st = check_latent_cache(shape, cache, block_table);
+    if (st != KDA_OK) return st;
+    if (!aligned(latent, 16) || latent_stride % 8 != 0 || !aligned(seq_lens, 4)) return KDA_ERR_UNSUPPORTED;
+    if (rope && (!aligned(k_rope, 16) || k_rope_stride % 8 != 0 || !aligned(inv_freq, 4))) return KDA_ERR_UNSUPPORTED;
+    if (q_rope && (!aligned(q_rope, 16) || !aligned(q_rope_out, 16) || q_stride % 8 != 0 || q_out_stride % 8 != 0))
+        return KDA_ERR_UNSUPPORTED;
+    unsigned int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    kda::LatentAppendArgs a{latent_cache(shape, cache, block_table), latent, rope ? k_rope : nullptr,
+                            rope ? inv_freq : nullptr, q_rope, q_rope_out, cu_seqlens, seq_lens, latent_stride,
+                            k_rope_stride, q_stride, q_out_stride, shape->total_tokens, shape->num_seqs, shape->H,
+                            interleaved != 0, status};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return finish(kda::launch_latent_append(a, s), s);
+}
+
+kda_status kda_latent_gather(const kda_latent_shape* shape, const void* cache, const int32_t* block_table,
+                             const int32_t* cu_seqlens, const int32_t* starts, void* latent, void* k_rope,
+                             kda_stream_t stream) {
+    kda_status st = check_latent_shape(shape);
+    if (st != KDA_OK) return st;
+    st = check_split(shape->num_seqs, shape->total_tokens, cu_seqlens);
+    if (st != KDA_OK) return st;
+    if (shape->total_tokens == 0) return KDA_OK;
+    const bool rope = shape->rope_dim != 0;
+    if (!latent || (rope && !k_rope)) return KDA_ERR_INVALID_ARG;
+    st = check_latent_cache(shape, cache, block_table);
+    if (st != KDA_OK) return st;
+    if (!aligned(latent, 16) || (rope && !aligned(k_rope, 16)) || !aligned(starts, 4)) return KDA_ERR_UNSUPPORTED;
+    unsigned int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    kda::LatentGatherArgs a{latent_cache(shape, const_cast<void*>(cache), block_table), cu_seqlens, starts, latent,
+                            rope ? k_rope : nullptr, shape->total_tokens, shape->num_seqs, status};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return finish(kda::launch_latent_gather(a, s), s);
+}
+
+kda_status kda_latent_decode_workspace_size(const kda_latent_shape* shape, size_t* bytes) {
+    if (!bytes) return KDA_ERR_INVALID_ARG;
+    *bytes = 0;
+    kda_status st = check_latent_shape(shape);
+    if (st != KDA_OK) return st;
+    st = check_step(shape->num_seqs, shape->total_tokens);
+    if (st != KDA_OK || shape->num_seqs == 0) return st;
+    *bytes = kda::latent_decode_workspace_bytes((int)(shape->total_tokens / shape->num_seqs), shape->H);
+    return KDA_OK;
+}
+
+kda_status kda_latent_decode(const kda_latent_shape* shape, const void* q_latent, const void* q_rope,
+                             const void* cache, const int32_t* block_table, const int32_t* seq_lens, float scale,
+                             void* out, float* lse, void* workspace, size_t workspace_bytes, kda_stream_t stream) {
+    kda_status st = check_latent_shape(shape);
+    if (st != KDA_OK) return st;
+    st = check_step(shape->num_seqs, shape->total_tokens);
+    if (st != KDA_OK) return st;
+    if (!(scale > 0.f) || !(scale < INFINITY)) return KDA_ERR_INVALID_ARG;
+    if (shape->num_seqs == 0) return KDA_OK;
+    const bool rope = shape->rope_dim != 0;
+    if (!q_latent || (rope && !q_rope) || !seq_lens || !out || !workspace) return KDA_ERR_INVALID_ARG;
+    st = check_latent_cache(shape, cache, block_table);
+    if (st != KDA_OK) return st;
+    if (!aligned(q_latent, 16) || (rope && !aligned(q_rope, 16)) || !aligned(seq_lens, 4) || !aligned(out, 16) ||
+        !aligned(lse, 4) || !aligned(workspace, 256))
+        return KDA_ERR_UNSUPPORTED;
+    const int tps = (int)(shape->total_tokens / shape->num_seqs);
+    if (workspace_bytes < kda::latent_decode_workspace_bytes(tps, shape->H)) return KDA_ERR_INVALID_ARG;
+    unsigned int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    kda::LatentDecodeArgs a{latent_cache(shape, const_cast<void*>(cache), block_table), q_latent,
+                            rope ? q_rope : nullptr, seq_lens, out, lse, workspace, scale, shape->num_seqs, tps,
+                            shape->H, status};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return finish(kda::launch_latent_decode(a, s), s);
+}
+
+kda_status kda_latent_prefill(const kda_shape* shape, int64_t total_kv, const void* q, const void* k, const void* v,
+                              int64_t kv_stride, const void* k_rope, float scale, const int32_t* cu_seqlens,
+                              const int32_t* cu_seqlens_k, void* out, float* lse, kda_stream_t stream) {
+    if (!shape) return KDA_ERR_INVALID_ARG;
+    if (shape->num_seqs < 0 || shape->total_tokens < 0 || total_kv < 0 || shape->H <= 0 || shape->dk <= 0 ||
+        shape->dv <= 0)
+        return KDA_ERR_INVALID_ARG;
+    if (shape->dtype != KDA_BF16 || shape->dv != 128 || (shape->dk != 128 && shape->dk != 192) || shape->H > 1024)
+        return KDA_ERR_UNSUPPORTED;
+    kda_status st = check_split(shape->num_seqs, shape->total_tokens, cu_seqlens);
+    if (st != KDA_OK) return st;
+    st = check_split(shape->num_seqs, total_kv, cu_seqlens_k);
+    if (st != KDA_OK) return st;
+    if (!(scale > 0.f) || !(scale < INFINITY) || kv_stride < 128) return KDA_ERR_INVALID_ARG;
+    if (kv_stride % 8 != 0) return KDA_ERR_UNSUPPORTED;
+    if (shape->total_tokens == 0) return KDA_OK;
+    const bool rope = shape->dk > 128, keys = total_kv > 0;
+    if (!q || !out || (keys && (!k || !v || (rope && !k_rope)))) return KDA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+        (keys && (!aligned(k, 16) || !aligned(v, 16) || (rope && !aligned(k_rope, 16)))))
+        return KDA_ERR_UNSUPPORTED;
+    unsigned int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    kda::LatentPrefillArgs a{q, k, v, rope ? k_rope : nullptr, cu_seqlens, cu_seqlens_k, out, lse,
+                             shape->total_tokens, total_kv, kv_stride, scale, shape->num_seqs, shape->H, shape->dk,
+                             status};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return finish(kda::launch_latent_prefill(a, s), s);
 }
 
 kda_status kda_selftest_timeout(uint64_t limit_ns, kda_stream_t stream) {

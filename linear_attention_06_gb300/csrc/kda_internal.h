@@ -112,6 +112,68 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 bool decode_chunk_supported(const DecodeArgs& a);
 cudaError_t launch_decode_chunk(const DecodeArgs& a, cudaStream_t s);
 
+// Latent attention (see kda.h).  The paged cache and its table:
+struct LatentCache {
+    void* cache;                  // [num_pages, page_size, 512 + rope_dim] bf16
+    const int32_t* block_table;   // [N, max_pages]
+    int32_t page_size, num_pages, max_pages, rope_dim;
+};
+struct LatentAppendArgs {
+    LatentCache c;
+    const void* latent;           // [T, 512], rows latent_stride apart
+    const void* k_rope;           // [T, 64], rows k_rope_stride apart (null with rope_dim 0)
+    const float* inv_freq;        // [32] or null (no rotation)
+    const void* q_rope;           // [T, H] rows of 64, q_stride apart (null: none)
+    void* q_out;
+    const int32_t* cu_seqlens;    // may be null (equal split)
+    const int32_t* seq_lens;      // [N]
+    int64_t latent_stride, k_rope_stride, q_stride, q_out_stride, total_tokens;
+    int32_t num_seqs, H;
+    bool interleaved;
+    unsigned int* status;
+};
+cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t s);
+struct LatentGatherArgs {
+    LatentCache c;
+    const int32_t* cu_seqlens;
+    const int32_t* starts;        // [N] or null (zeros)
+    void* latent;                 // [T, 512]
+    void* k_rope;                 // [T, 64] (null with rope_dim 0)
+    int64_t total_tokens;
+    int32_t num_seqs;
+    unsigned int* status;
+};
+cudaError_t launch_latent_gather(const LatentGatherArgs& a, cudaStream_t s);
+struct LatentDecodeArgs {
+    LatentCache c;
+    const void* q_latent;         // [N*T, H, 512]
+    const void* q_rope;           // [N*T, H, 64] (null with rope_dim 0)
+    const int32_t* seq_lens;      // [N]
+    void* out;                    // [N*T, H, 512]
+    float* lse;                   // [N*T, H] or null
+    void* workspace;
+    float scale;
+    int32_t num_seqs, tokens_per_seq, H;
+    unsigned int* status;
+};
+size_t latent_decode_workspace_bytes(int tokens_per_seq, int H);
+cudaError_t launch_latent_decode(const LatentDecodeArgs& a, cudaStream_t s);
+struct LatentPrefillArgs {
+    const void* q;                // [T, H, dk]
+    const void* k;                // [S, H] rows of 128, kv_stride apart
+    const void* v;
+    const void* k_rope;           // [S, dk - 128] (null for dk = 128)
+    const int32_t* cu_q;          // may be null (equal split)
+    const int32_t* cu_k;
+    void* out;                    // [T, H, 128]
+    float* lse;                   // [T, H] or null
+    int64_t total_q, total_kv, kv_stride;
+    float scale;
+    int32_t num_seqs, H, dk;
+    unsigned int* status;
+};
+cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, cudaStream_t s);
+
 // Longest run of tokens per sequence that kda_decode_step accepts.
 constexpr int kMaxDecodeTokens = 16;
 
