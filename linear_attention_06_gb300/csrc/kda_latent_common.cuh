@@ -15,6 +15,13 @@ constexpr int kLatent = 512;   // channels of the latent (the cache row's first 
 constexpr int kRope = 64;      // channels of the rotated part, where there is one
 constexpr int kHead = 128;     // per-head channels of the expanded form
 
+// 2^x by the special function unit (2 units in the last place; results below 2^-126 become zero).
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Tokens [b, e) of sequence n; a table's offsets are clamped into [0, total] and a reversed range
 // is empty, so that no table leads outside the batch.
 __device__ __forceinline__ void bounds(const int32_t* cu, int n, int num_seqs, int64_t total, int64_t& b, int64_t& e) {

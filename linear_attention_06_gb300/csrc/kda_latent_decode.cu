@@ -1,74 +1,751 @@
 // kda_latent_decode.cu -- absorbed latent attention over the paged cache (kda_latent_decode).
 //
-// First form: one block per (sequence, token, head), its warps taking every eighth cached row with a
-// softmax of their own, joined at the end.  Right for every shape; it reads the cache once a head.
+// For one sequence, the R = T' H query rows x_r = [q_latent | q_rope] of its step and its cached rows
+// y_j = [c_j | r_j]:
+//
+//     s_rj = scale x_r . y_j,   p_rj = e^{s_rj - m_r},   o_r = sum_j p_rj c_j / sum_j p_rj.
+//
+// All rows read the same y_j, so a cached row is read once for up to 64 query rows: it is key (576 channels)
+// and value (its first 512) in one.  With 32 rows that is 60 flop a byte, far below the card's 280, and the
+// cache's bytes bound the call; with 128 rows (242 flop a byte) memory and tensor cores meet.
+//
+// Products, per tile of 64 cached rows (NR = query rows of a block, 16, 32 or 64), on tcgen05:
+//   S [64 x 64 tokens]    = X Y^T       M = 64 (rows beyond NR are not looked at), K = 512 + rope
+//   O^T [512 x NR]       += C^T P^T     four products of M = 128 channels, N = NR, K = 64 tokens
+// The second is transposed so that the 512 wide output lies on the 128 lanes of tensor memory in four blocks of
+// NR columns (a row-major O would need M = 128 rows for R = 32 and all of tensor memory), and so that the tile is
+// read in place, as it lies in the cache, by both products.
+//
+// Work: the tiles of all sequences form one line, cut into equal runs, one for each block of a grid of one
+// block an SM (divided by the row groups, which take the same run at the same time and so share the tile in
+// L2).  The lengths are on the device, so every block finds its own run.  A run that covers a sequence whole
+// writes its output; other pieces leave (O, m, l) in the workspace, and a second kernel joins them in their
+// order, whatever order the blocks ran in.
+//
+// Block: a producer warp (TMA boxes of page rows), an issuing warp, a query loader, and four warps that turn S
+// into P.  The running maximum m is only raised when a score exceeds it by more than 2^8: P then stays below 2^8
+// in bf16, whose precision does not depend on the exponent, sums are fp32, and the rescaling of O in tensor
+// memory is rare.  P is rounded to bf16 for the tensor cores; its sum is taken before that rounding.
+#include <atomic>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <math.h>
 #include <stdint.h>
 
 #include "kda_internal.h"
 #include "kda_latent_common.cuh"
+#include "sm103_primitives.cuh"
 
 namespace kda {
 namespace {
 
 using namespace latent;
+using namespace sm103;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kTile = 64;                     // cached rows a tile
+constexpr int kThreads = 256;                 // warps 0-3: producer, issuer, queries, (TMEM); warps 4-7: softmax
+constexpr int kSoft = 128;
+constexpr int kBar = 1;                       // named barrier of the softmax warps
+constexpr int kSMs = 152;
+constexpr float kRaise = 8.f;                 // log2 of how far a score may exceed the running maximum
+constexpr uint64_t kWaitNs = 4000000000ull;   // bound of every wait
 
-__global__ void __launch_bounds__(kThreads) decode_simple_kernel(const LatentDecodeArgs a) {
-    __shared__ float acc_s[kWarps][kLatent];
-    __shared__ float m_s[kWarps], l_s[kWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * a.H + blockIdx.y;
-    const int n = blockIdx.x / a.tokens_per_seq, t = blockIdx.x % a.tokens_per_seq;
-    const int seen = clamped_len(a.c, a.seq_lens, n) - a.tokens_per_seq + 1 + t;
-    const int width = kLatent + a.c.rope_dim, steps = width / 32;
-    float q[18], acc[16];
-    for (int k = 0; k < 16; ++k) {
-        acc[k] = 0.f;
-        q[k] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.q_latent)[row * kLatent + k * 32 + lane]);
+// Shared memory of a block with NR query rows: queries [slice][NR][64], P [2][NR][64], the rope slices of the
+// tiles in flight, then their latent slices in pairs (128 channels, one M = 128 operand).
+template <int NR, bool ROPE>
+struct Cfg {
+    static constexpr uint32_t kSlice = NR * 128, kSlices = ROPE ? 9 : 8;
+    static constexpr uint32_t kQ = 0, kP = kSlice * kSlices;
+    static constexpr uint32_t kRopeSlots = ROPE ? (NR == 64 ? 1 : 2) : 0;
+    static constexpr uint32_t kRopeAt = kP + 2 * kSlice, kPairAt = kRopeAt + kRopeSlots * 8192;
+    static constexpr uint32_t kPairs = (225 * 1024 - kPairAt) / 16384;
+    static constexpr uint32_t kSmall = kPairAt + kPairs * 16384;
+    static constexpr uint32_t kBytes = kSmall + 1024 + 1024;      // + alignment slack
+    static constexpr uint32_t kCols = NR == 64 ? 512 : 256;       // TMEM: O^T 4 NR, S 2 x 64
+    static_assert(kBytes <= 232448, "shared memory");
+    static_assert(64 * 128 <= kSmall - (kSlices - 1) * kSlice, "the M = 64 operand stays inside the block's memory");
+};
+
+struct Small {
+    uint64_t full[12], empty[12];             // latent pairs
+    uint64_t rope_full[2], rope_empty[2];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t o_free, drain;
+    uint32_t tmem;
+    int seq0, off0, runs;
+    int64_t total, begin, end;
+    float fac[64];                            // rescaling factors, then 1 / l
+};
+static_assert(sizeof(Small) <= 1024, "small area");
+
+// Position in a ring of SLOTS slots; `phase` flips each time round.
+template <uint32_t SLOTS>
+struct Ring {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == SLOTS) { slot = 0; phase ^= 1u; }
     }
-    for (int k = 16; k < steps; ++k)
-        q[k] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.q_rope)[row * kRope + (k - 16) * 32 + lane]);
-    float m = -INFINITY, l = 0.f;
-    for (int p = warp; p < seen; p += kWarps) {
-        const int64_t r = cache_row(a.c, n, p);
-        const __nv_bfloat16* c = static_cast<const __nv_bfloat16*>(a.c.cache) + r * width;
-        float x[18], s = 0.f;
-        for (int k = 0; k < steps; ++k) {
-            x[k] = r < 0 ? 0.f : __bfloat162float(c[k * 32 + lane]);
-            s += x[k] * q[k];
-        }
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= a.scale;
-        const float mn = fmaxf(m, s), f = expf(m - mn), w = expf(s - mn);
-        l = l * f + w;
-        for (int k = 0; k < 16; ++k) acc[k] = acc[k] * f + w * x[k];
-        m = mn;
+};
+
+struct Piece {                                // a run's share of one sequence
+    int n, len, off, tiles, all;              // sequence, its length, first tile, tiles here, tiles in all
+};
+
+__device__ __forceinline__ int tiles_of(int len) { return len > kTile ? (len + kTile - 1) / kTile : 1; }
+
+// Walks the sequences of a run; every role walks by itself.
+struct Walk {
+    int n, off;
+    int64_t left;
+    __device__ Walk(const Small* sw) : n(sw->seq0), off(sw->off0), left(sw->end - sw->begin) {}
+    __device__ __forceinline__ bool next(const LatentDecodeArgs& a, Piece& p) {
+        if (left <= 0) return false;
+        p.n = n;
+        p.len = clamped_len(a.c, a.seq_lens, n);
+        p.all = tiles_of(p.len);
+        p.off = off;
+        p.tiles = (int64_t)(p.all - off) < left ? p.all - off : (int)left;
+        left -= p.tiles;
+        off = 0;
+        ++n;
+        return true;
     }
-    for (int k = 0; k < 16; ++k) acc_s[warp][k * 32 + lane] = acc[k];
-    if (lane == 0) { m_s[warp] = m; l_s[warp] = l; }
+};
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_parked(bar, parity, kWaitNs); }
+
+// The first tile of run p of `runs` over `total` tiles, and the run that holds tile x.
+__host__ __device__ __forceinline__ int64_t run_begin(int64_t total, int runs, int p) { return total * p / runs; }
+__device__ __forceinline__ int run_of(int64_t total, int runs, int64_t x) { return (int)(((x + 1) * runs - 1) / total); }
+
+// Workspace: a header a block (the sequence whose first piece it holds), then per (block, 0 or 1) and row the
+// maximum (in log2) and the sum, then O.
+struct Head {
+    int n, parts, first_slot, pad;            // n = -1: none
+};
+template <int NR>
+struct Work {
+    static __host__ __device__ size_t ml_at(int grid) { return ((size_t)grid * sizeof(Head) + 255) / 256 * 256; }
+    static __host__ __device__ size_t o_at(int grid) {
+        return ml_at(grid) + ((size_t)grid * 2 * NR * sizeof(float2) + 255) / 256 * 256;
+    }
+    static __host__ __device__ size_t bytes(int grid) { return o_at(grid) + (size_t)grid * 2 * NR * kLatent * sizeof(float); }
+};
+
+struct Maps {
+    CUtensorMap q, qr, c;
+};
+
+// All threads: the run of this block and the sequence it starts in.
+__device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Small* sw, int64_t* scratch) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int64_t sum = 0;
+    for (int n = tid; n < a.num_seqs; n += kThreads) sum += tiles_of(clamped_len(a.c, a.seq_lens, n));
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) scratch[warp] = sum;
     __syncthreads();
-    float mx = -INFINITY, sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, m_s[w]);
-    for (int w = 0; w < kWarps; ++w) sum += m_s[w] == -INFINITY ? 0.f : l_s[w] * expf(m_s[w] - mx);
-    for (int i = threadIdx.x; i < kLatent; i += kThreads) {
-        float o = 0.f;
-        for (int w = 0; w < kWarps; ++w) o += m_s[w] == -INFINITY ? 0.f : acc_s[w][i] * expf(m_s[w] - mx);
-        static_cast<__nv_bfloat16*>(a.out)[row * kLatent + i] = __float2bfloat16_rn(seen > 0 ? o / sum : 0.f);
+    int64_t total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) total += scratch[w];
+    // with fewer tiles than blocks the first blocks take a tile each: a sequence's runs are consecutive
+    if (total < runs) runs = (int)total;
+    const int64_t begin = p < runs ? run_begin(total, runs, p) : 0, end = p < runs ? run_begin(total, runs, p + 1) : 0;
+    if (tid == 0) {
+        sw->runs = runs;
+        sw->total = total;
+        sw->begin = begin;
+        sw->end = end;
+        sw->seq0 = sw->off0 = 0;
     }
-    if (a.lse && threadIdx.x == 0) a.lse[row] = seen > 0 ? mx + logf(sum) : -INFINITY;
+    if (begin == end) { __syncthreads(); return; }
+    int64_t before = 0;                       // tiles of the sequences before this round's
+    for (int n0 = 0; n0 < a.num_seqs; n0 += kThreads) {
+        const int n = n0 + tid;
+        const int64_t mine = n < a.num_seqs ? tiles_of(clamped_len(a.c, a.seq_lens, n)) : 0;
+        int64_t x = mine;                     // inclusive sum over the round
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) scratch[warp] = x;
+        __syncthreads();
+        int64_t round = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) x += scratch[w];
+            round += scratch[w];
+        }
+        const int64_t first = before + x - mine;
+        if (mine > 0 && first <= begin && begin < first + mine) {
+            sw->seq0 = n;
+            sw->off0 = (int)(begin - first);
+        }
+        before += round;
+        if (before > begin) break;            // uniform: `before` is the same for every thread
+    }
+    __syncthreads();
+}
+
+template <int NR, bool ROPE>
+__global__ void __launch_bounds__(kThreads, 1)
+latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a, const int groups, const int map_rows) {
+    using G = Cfg<NR, ROPE>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    Small* sw = reinterpret_cast<Small*>(sm + G::kSmall);
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int runs = gridDim.x / groups, run = blockIdx.x / groups, group = blockIdx.x % groups;
+    const int R = a.tokens_per_seq * a.H;
+    const int rows = R - group * NR < NR ? R - group * NR : NR;      // live query rows
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 0) {
+        for (uint32_t i = 0; i < G::kPairs; ++i) { mbar_init(&sw->full[i], 1); mbar_init(&sw->empty[i], 1); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sw->rope_full[i], 1);
+            mbar_init(&sw->rope_empty[i], 1);
+            mbar_init(&sw->s_full[i], 1);
+            mbar_init(&sw->p_full[i], 4);
+            mbar_init(&sw->pv_done[i], 1);
+        }
+        mbar_init(&sw->q_full, 1);
+        mbar_init(&sw->q_empty, 1);
+        mbar_init(&sw->o_free, 4);
+        mbar_init(&sw->drain, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&maps.q);
+        if (ROPE) tma_prefetch_desc(&maps.qr);
+        tma_prefetch_desc(&maps.c);
+    }
+    if (warp == 3) {
+        tmem_alloc(&sw->tmem, G::kCols);
+        tmem_relinquish();
+    }
+    find_run(a, runs, run, sw, reinterpret_cast<int64_t*>(sw->fac));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = sw->tmem;
+    const uint32_t ts = tb + 4 * NR;          // S buffers
+    bool ok = true;
+    uint32_t loads = 0;                       // producer: latent pairs issued
+
+    if (warp == 0) {                          // ------------------------------------------------ producer
+        const int box = a.c.page_size < kTile ? a.c.page_size : kTile;
+        const int shift = 31 - __clz(a.c.page_size);
+        const int half = lane & 1, piece = lane >> 1;               // a lane issues one box of a pair
+        Walk walk(sw);
+        Piece p;
+        Ring<G::kPairs> ring;
+        Ring<ROPE ? G::kRopeSlots : 1> rope;
+        bool used = false, rope_used = false; // the ring has gone round once
+        while (ok && walk.next(a, p)) {
+            const int64_t table = (int64_t)p.n * a.c.max_pages;
+            // the page of this lane's box in tile x (a box outside the cache reads zeros)
+            auto row_of = [&](int x) -> int {
+                const int pos = x * kTile + piece * box;
+                if (piece * box >= kTile || pos >= p.len) return -1;
+                if (!KDA_INDEX_OK(table + (pos >> shift), (int64_t)a.num_seqs * a.c.max_pages, a.status)) return map_rows;
+                const int page = a.c.block_table[table + (pos >> shift)];
+                return page < 0 || page >= a.c.num_pages ? map_rows : (page << shift) + (pos & (a.c.page_size - 1));
+            };
+            int row = row_of(p.off);
+            for (int j = 0; ok && j < p.tiles; ++j) {
+                const int next_row = j + 1 < p.tiles ? row_of(p.off + j + 1) : -1;
+                const int live = p.len - (p.off + j) * kTile;
+                const int valid = live < 0 ? 0 : (live < kTile ? live : kTile);
+                const uint32_t boxes = (valid + box - 1) / box;
+                for (int k = 0; k < 4; ++k) {
+                    if (used && !(ok = wait(&sw->empty[ring.slot], ring.phase ^ 1u))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&sw->full[ring.slot], boxes * box * 256);
+                    __syncwarp();
+                    if (row >= 0)
+                        tma_load_2d(sm + G::kPairAt + ring.slot * 16384 + half * 8192 + piece * box * 128, &maps.c,
+                                    (2 * k + half) * 64, row, &sw->full[ring.slot]);
+                    ring.next();
+                    ++loads;
+                    if (ring.slot == 0) used = true;
+                }
+                if (!ok) break;
+                if constexpr (ROPE) {
+                    if (rope_used && !(ok = wait(&sw->rope_empty[rope.slot], rope.phase ^ 1u))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&sw->rope_full[rope.slot], boxes * box * 128);
+                    __syncwarp();
+                    if (row >= 0 && half == 0)
+                        tma_load_2d(sm + G::kRopeAt + rope.slot * 8192 + piece * box * 128, &maps.c, kLatent, row,
+                                    &sw->rope_full[rope.slot]);
+                    rope.next();
+                    if (rope.slot == 0) rope_used = true;
+                }
+                row = next_row;
+            }
+        }
+        if (!ok && lane == 0) {               // copies in flight land before the block ends
+            for (uint32_t i = 0; i < G::kPairs; ++i)
+                if (loads > i) mbar_wait_bounded(&sw->full[i], ((loads - 1 - i) / G::kPairs) & 1, kWaitNs);
+        }
+    } else if (warp == 1) {                   // ------------------------------------------------ issuer
+        constexpr uint32_t id_s = idesc_bf16_f32(64, 64, false, false);
+        constexpr uint32_t id_o = idesc_bf16_f32(128, NR, true, false);
+        const uint32_t sq = smem_u32(sm + G::kQ), sp = smem_u32(sm + G::kP), sc = smem_u32(sm + G::kPairAt),
+                       sr = smem_u32(sm + G::kRopeAt);
+        Walk walk(sw);
+        Piece p;
+        Ring<G::kPairs> in, out;              // next pair for S, next pair for O
+        Ring<ROPE ? G::kRopeSlots : 1> rope;
+        Ring<2> sb, pb;                       // S / P buffers
+        uint32_t seg = 0;
+        while (ok && walk.next(a, p)) {
+            if (!(ok = wait(&sw->q_full, seg & 1))) break;
+            int qk = 0, pv = 0;
+            while (pv < p.tiles) {
+                bool go = qk == pv;
+                if (!go && qk < p.tiles && qk == pv + 1) {           // ahead only when the tile has landed
+                    Ring<G::kPairs> last = in;
+                    last.next(); last.next(); last.next();
+                    bool landed = mbar_test(&sw->full[last.slot], last.phase);
+                    if (ROPE) landed = landed && mbar_test(&sw->rope_full[rope.slot], rope.phase);
+                    go = __all_sync(0xffffffffu, landed);
+                }
+                if (go) {
+                    const uint32_t d = ts + sb.slot * 64;
+                    for (int k = 0; k < 4; ++k) {
+                        if (!(ok = wait(&sw->full[in.slot], in.phase))) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                mma_ss(d, smem_desc(sq + (2 * k + (i >> 2)) * G::kSlice + (i & 3) * 32, 16, 1024, kSwizzle128B),
+                                       smem_desc(sc + in.slot * 16384 + (i >> 2) * 8192 + (i & 3) * 32, 16, 1024, kSwizzle128B),
+                                       id_s, k > 0 || i > 0);
+                        }
+                        in.next();
+                    }
+                    if (!ok) break;
+                    if constexpr (ROPE) {
+                        if (!(ok = wait(&sw->rope_full[rope.slot], rope.phase))) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mma_ss(d, smem_desc(sq + 8 * G::kSlice + i * 32, 16, 1024, kSwizzle128B),
+                                       smem_desc(sr + rope.slot * 8192 + i * 32, 16, 1024, kSwizzle128B), id_s, 1);
+                            mma_commit(&sw->rope_empty[rope.slot]);
+                        }
+                        rope.next();
+                    }
+                    if (elect_one()) {
+                        mma_commit(&sw->s_full[sb.slot]);
+                        if (qk + 1 == p.tiles) mma_commit(&sw->q_empty);
+                    }
+                    sb.next();
+                    ++qk;
+                } else {
+                    if (!(ok = wait(&sw->p_full[pb.slot], pb.phase))) break;
+                    if (pv == 0 && seg > 0 && !(ok = wait(&sw->o_free, (seg - 1) & 1))) break;
+                    tc_fence_after();
+                    for (int b = 0; b < 4; ++b) {
+                        if (elect_one()) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mma_ss(tb + b * NR, smem_desc(sc + out.slot * 16384 + i * 2048, 8192, 1024, kSwizzle128B),
+                                       smem_desc(sp + pb.slot * G::kSlice + i * 32, 16, 1024, kSwizzle128B), id_o,
+                                       pv > 0 || i > 0);
+                            mma_commit(&sw->empty[out.slot]);
+                        }
+                        out.next();
+                    }
+                    if (elect_one()) mma_commit(&sw->pv_done[pb.slot]);
+                    pb.next();
+                    ++pv;
+                }
+            }
+            ++seg;
+        }
+        if (!ok) {                            // products in flight land before TMEM is freed
+            if (elect_one()) mma_commit(&sw->drain);
+            wait(&sw->drain, 0);
+        }
+    } else if (warp == 2) {                   // ------------------------------------------------ queries
+        Walk walk(sw);
+        Piece p;
+        uint32_t seg = 0;
+        while (walk.next(a, p)) {
+            if (seg > 0 && !(ok = wait(&sw->q_empty, (seg - 1) & 1))) break;
+            if (lane == 0) mbar_arrive_expect_tx(&sw->q_full, G::kSlice * G::kSlices);
+            __syncwarp();
+            const int row = p.n * R + group * NR;
+            if (lane < 8)
+                tma_load_2d(sm + G::kQ + lane * G::kSlice, &maps.q, lane * 64, row, &sw->q_full);
+            else if (ROPE && lane == 8)
+                tma_load_2d(sm + G::kQ + 8 * G::kSlice, &maps.qr, 0, row, &sw->q_full);
+            ++seg;
+        }
+        if (!ok && seg > 0 && lane == 0) mbar_wait_bounded(&sw->q_full, (seg - 1) & 1, kWaitNs);
+    } else if (warp >= 4) {                   // ------------------------------------------------ softmax
+        const int w = warp - 4, t = tid - kSoft;
+        const bool active = 16 * w < NR;
+        const int r0 = 16 * w + lane / 4;     // this thread's rows: r0 and r0 + 8
+        const float c2 = a.scale * 1.44269504088896340736f;
+        const uint32_t lanes = tmem_addr(tb, 32 * w, 0);
+        const uint32_t s_lanes = tmem_addr(ts, 32 * w, 0);
+        Walk walk(sw);
+        Piece p;
+        Ring<G::kPairs> in;                   // the tile's first latent pair
+        Ring<2> sb, prev;                     // this tile's buffers; the previous tile's
+        bool first_piece = true, used0 = false, used1 = false;
+        Head head{-1, 0, 0, 0};
+        int64_t at = sw->begin;               // the piece's first tile in the line
+        while (ok && walk.next(a, p)) {
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            int seen[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = r0 + 8 * e;
+                seen[e] = r < rows ? p.len - a.tokens_per_seq + 1 + (group * NR + r) / a.H : 0;
+            }
+            for (int j = 0; j < p.tiles; ++j) {
+                const int base = (p.off + j) * kTile;
+                if (!(ok = wait(&sw->s_full[sb.slot], sb.phase))) break;
+                tc_fence_after();
+                uint32_t s[32];
+                float f[2] = {1.f, 1.f};
+                bool raise = false;
+                if (active) {
+                    tmem_ld_16x64(s_lanes + sb.slot * 64, s);
+                    tmem_wait_ld();
+                    if (__any_sync(0xffffffffu, seen[0] - base < kTile || seen[1] - base < kTile)) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int col = base + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
+                            if (col >= seen[(i >> 1) & 1]) s[i] = 0xff800000u;       // -inf
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = __uint_as_float(s[2 * e]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            x = fmaxf(x, __uint_as_float(s[4 * i + 2 * e]));
+                            x = fmaxf(x, __uint_as_float(s[4 * i + 2 * e + 1]));
+                        }
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                        if (x > m[e] && (x - m[e]) * c2 > kRaise) {                  // also the first finite maximum
+                            f[e] = exp2_fast((m[e] - x) * c2);
+                            m[e] = x;
+                            raise = true;
+                        }
+                        l[e] *= f[e];
+                    }
+                }
+                if (base + kTile > p.len) {   // the tile's rows behind the sequence's end become zeros
+                    const int valid = p.len - base < 0 ? 0 : p.len - base;
+                    Ring<G::kPairs> pair = in;
+                    for (int k = 0; k < 4; ++k, pair.next())
+                        for (int i = t; i < (kTile - valid) * 16; i += kSoft)
+                            *reinterpret_cast<uint4*>(sm + G::kPairAt + pair.slot * 16384 + ((i >> 3) & 1) * 8192 +
+                                                      (valid + (i >> 4)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                bool any;
+                {
+                    uint32_t r;
+                    asm volatile(
+                        "{\n\t.reg .pred p, q;\n\t"
+                        "setp.ne.u32 q, %1, 0;\n\t"
+                        "bar.red.or.pred p, %2, %3, q;\n\t"
+                        "selp.u32 %0, 1, 0, p;\n\t}"
+                        : "=r"(r)
+                        : "r"((uint32_t)(raise && j > 0)), "n"(kBar), "n"(kSoft)
+                        : "memory");
+                    any = r != 0;
+                }
+                if (any) {                    // rescale O^T, column r by f_r
+                    if (active && (lane & 3) == 0) {
+                        sw->fac[r0] = f[0];
+                        sw->fac[r0 + 8] = f[1];
+                    }
+                    asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kSoft) : "memory");
+                    if (!(ok = wait(&sw->pv_done[prev.slot], prev.phase))) break;
+                    tc_fence_after();
+                    for (int b = 0; b < 4; ++b)
+                        for (int k = 0; k < NR / 16; ++k) {
+                            uint32_t o[16];
+                            tmem_ld16(lanes + b * NR + k * 16, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * sw->fac[k * 16 + i]);
+                            tmem_st16(lanes + b * NR + k * 16, o);
+                        }
+                    tmem_wait_st();
+                }
+                // this P buffer was read by the products of two tiles ago
+                if ((sb.slot ? used1 : used0) && !(ok = wait(&sw->pv_done[sb.slot], sb.phase ^ 1u))) break;
+                if (active) {
+                    uint8_t* pt = sm + G::kP + sb.slot * G::kSlice;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float z = m[e] == -INFINITY ? 0.f : -m[e] * c2;
+                        float sum = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float x = exp2_fast(fmaf(__uint_as_float(s[4 * i + 2 * e]), c2, z));
+                            const float y = exp2_fast(fmaf(__uint_as_float(s[4 * i + 2 * e + 1]), c2, z));
+                            sum += x + y;
+                            *reinterpret_cast<uint32_t*>(pt + sw128_offset(r0 + 8 * e, 16 * i + 4 * (lane & 3))) =
+                                pack_bf16x2(x, y);
+                        }
+                        l[e] += sum;
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sw->p_full[sb.slot]);
+                if (sb.slot) used1 = true; else used0 = true;
+                prev = sb;
+                sb.next();
+                in.next(); in.next(); in.next(); in.next();
+            }
+            if (!ok) break;
+            // ---- the piece is done: its rows' sums, then O^T out of tensor memory
+            const bool whole = p.off == 0 && p.tiles == p.all;
+            const int slot = blockIdx.x * 2 + (first_piece ? 0 : 1);
+            if (p.off == 0 && !whole) {
+                head.n = p.n;
+                head.first_slot = first_piece ? 0 : 1;
+                head.parts = run_of(sw->total, sw->runs, at + p.all - 1) - run + 1;
+            }
+            uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+            float2* ml = reinterpret_cast<float2*>(ws + Work<NR>::ml_at(gridDim.x));
+            float* po = reinterpret_cast<float*>(ws + Work<NR>::o_at(gridDim.x));
+            if (active) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+                    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+                    const int r = r0 + 8 * e;
+                    if ((lane & 3) == 0) {
+                        sw->fac[r] = whole ? (l[e] > 0.f ? 1.f / l[e] : (l[e] == 0.f ? 0.f : l[e])) : 1.f;
+                        if (whole) {
+                            const int64_t row = (int64_t)p.n * R + group * NR + r;
+                            if (a.lse && r < rows && KDA_INDEX_OK(row, (int64_t)a.num_seqs * R, a.status))
+                                a.lse[row] = l[e] == 0.f ? -INFINITY : m[e] * a.scale + logf(l[e]);
+                        } else if (KDA_INDEX_OK((int64_t)slot * NR + r, (int64_t)gridDim.x * 2 * NR, a.status)) {
+                            ml[(int64_t)slot * NR + r] = make_float2(m[e] == -INFINITY ? m[e] : m[e] * c2, l[e]);
+                        }
+                    }
+                }
+            }
+            asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kSoft) : "memory");
+            if (!(ok = wait(&sw->pv_done[prev.slot], prev.phase))) break;
+            tc_fence_after();
+            for (int b = 0; b < 4; ++b)
+                for (int k = 0; k < NR / 16; ++k) {
+                    uint32_t o[16];
+                    tmem_ld16(lanes + b * NR + k * 16, o);
+                    tmem_wait_ld();
+                    const int channel = b * 128 + 32 * w + lane;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int r = k * 16 + i;
+                        if (r >= rows) break;
+                        if (whole) {
+                            const int64_t row = (int64_t)p.n * R + group * NR + r;
+                            if (KDA_INDEX_OK(row, (int64_t)a.num_seqs * R, a.status))
+                                static_cast<__nv_bfloat16*>(a.out)[row * kLatent + channel] =
+                                    __float2bfloat16_rn(__uint_as_float(o[i]) * sw->fac[r]);
+                        } else if (KDA_INDEX_OK((int64_t)slot * NR + r, (int64_t)gridDim.x * 2 * NR, a.status)) {
+                            po[((int64_t)slot * NR + r) * kLatent + channel] = __uint_as_float(o[i]);
+                        }
+                    }
+                }
+            tc_fence_before();
+            // everyone has read fac before the next piece writes it
+            asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kSoft) : "memory");
+            if (lane == 0) mbar_arrive(&sw->o_free);
+            at += p.tiles;
+            first_piece = false;
+        }
+        if (t == 0) reinterpret_cast<Head*>(a.workspace)[blockIdx.x] = head;
+    }
+    if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 3) tmem_dealloc(tb, G::kCols);
+}
+
+// Joins the pieces of the sequences that several runs share: out = sum_i w_i O_i / sum_i w_i l_i with
+// w_i = 2^{m_i - max m}, the pieces in order.  512 threads: 128 take four channels each, four times over, each
+// set every fourth piece.
+constexpr int kJoinThreads = 512, kMostParts = 1024;
+template <int NR>
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentDecodeArgs a, const int grid, const int groups) {
+    __shared__ int list_s[256], count_s;
+    __shared__ float w_s[kMostParts], total_s, max_s;
+    __shared__ float4 acc_s[3][128];
+    const int tid = threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
+    const Head* heads = reinterpret_cast<const Head*>(ws);
+    const float2* ml = reinterpret_cast<const float2*>(ws + Work<NR>::ml_at(grid));
+    const float4* po = reinterpret_cast<const float4*>(ws + Work<NR>::o_at(grid));
+    if (tid < 32) {
+        int count = 0;
+        for (int b = 0; b < grid; b += 32) {
+            const bool has = b + tid < grid && heads[b + tid].n >= 0;
+            const uint32_t mask = __ballot_sync(0xffffffffu, has);
+            if (has) list_s[count + __popc(mask & ((1u << tid) - 1))] = b + tid;
+            count += __popc(mask);
+        }
+        if (tid == 0) count_s = count;
+    }
+    __syncthreads();
+    const int R = a.tokens_per_seq * a.H, items = count_s * NR;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int block = list_s[item / NR], r = item % NR, group = block % groups;
+        if (group * NR + r >= R) continue;    // uniform
+        const Head h = heads[block];
+        const int parts = h.parts < kMostParts ? h.parts : kMostParts;
+        auto slot_of = [&](int i) { return ((int64_t)(block + i * groups) * 2 + (i == 0 ? h.first_slot : 0)) * NR + r; };
+        if (tid < 32) {
+            float mx = -INFINITY;
+            for (int i = tid; i < parts; i += 32) mx = fmaxf(mx, ml[slot_of(i)].x);
+            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            float sum = 0.f;
+            for (int i = tid; i < parts; i += 32) {
+                const float2 x = ml[slot_of(i)];
+                const float w = x.x == -INFINITY ? 0.f : exp2_fast(x.x - mx);
+                w_s[i] = w;
+                sum += w * x.y;
+            }
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (tid == 0) { total_s = sum; max_s = mx; }
+        }
+        __syncthreads();
+        const int set = tid >> 7, c = tid & 127;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int i = set; i < parts; i += 4) {
+            const float w = w_s[i];
+            const float4 x = po[slot_of(i) * (kLatent / 4) + c];
+            if (w != 0.f) { acc.x += w * x.x; acc.y += w * x.y; acc.z += w * x.z; acc.w += w * x.w; }
+        }
+        if (set) acc_s[set - 1][c] = acc;
+        __syncthreads();
+        if (!set) {
+            for (int i = 0; i < 3; ++i) {
+                const float4 x = acc_s[i][c];
+                acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+            }
+            const float total = total_s, f = total == 0.f ? 0.f : 1.f / total;
+            const int64_t row = (int64_t)h.n * R + group * NR + r;
+            if (KDA_INDEX_OK(row, (int64_t)a.num_seqs * R, a.status)) {
+                uint2 y;
+                y.x = pack_bf16x2(acc.x * f, acc.y * f);
+                y.y = pack_bf16x2(acc.z * f, acc.w * f);
+                reinterpret_cast<uint2*>(a.out)[row * (kLatent / 4) + c] = y;
+                if (a.lse && c == 0) a.lse[row] = total == 0.f ? -INFINITY : (max_s + log2f(total)) * 0.69314718055994530942f;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        return nullptr;
+    }();
+    return fn;
+}
+
+// [rows, width] bf16, boxes of 64 channels x box_rows, 128-byte swizzle.
+bool map_rows_2d(CUtensorMap* m, const void* base, int64_t rows, int width, int box_rows) {
+    const auto fn = encode();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Query rows a block takes: the smallest of 16, 32, 64 that holds them all, else 64 in several groups.
+int rows_a_block(int R) { return R <= 16 ? 16 : (R <= 32 ? 32 : 64); }
+int groups_of(int R) { return (R + rows_a_block(R) - 1) / rows_a_block(R); }
+int runs_of(int groups) { return groups < kSMs ? kSMs / groups : 1; }
+
+template <int NR, bool ROPE>
+cudaError_t launch(const LatentDecodeArgs& a, cudaStream_t s) {
+    using G = Cfg<NR, ROPE>;
+    const int R = a.tokens_per_seq * a.H, groups = groups_of(R), grid = runs_of(groups) * groups;
+    const int64_t q_rows = (int64_t)a.num_seqs * R;
+    const int box = a.c.page_size < kTile ? a.c.page_size : kTile;
+    // a cache without pages: any readable row; every box then starts behind the map's last row
+    const int64_t c_rows = a.c.num_pages > 0 ? (int64_t)a.c.num_pages * a.c.page_size : 1;
+    const void* c_base = a.c.num_pages > 0 ? a.c.cache : a.workspace;
+    Maps maps;
+    if (!map_rows_2d(&maps.q, a.q_latent, q_rows, kLatent, NR) ||
+        !map_rows_2d(&maps.qr, ROPE ? a.q_rope : a.q_latent, q_rows, ROPE ? kRope : kLatent, NR) ||
+        !map_rows_2d(&maps.c, c_base, c_rows, kLatent + (ROPE ? kRope : 0), box))
+        return cudaErrorInvalidValue;
+    static std::atomic<bool> ready[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(latent_decode_kernel<NR, ROPE>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kBytes);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true, std::memory_order_release);
+    }
+    latent_decode_kernel<NR, ROPE><<<grid, kThreads, G::kBytes, s>>>(maps, a, groups, (int)c_rows);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * kSMs);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, latent_join_kernel<NR>, a, grid, groups);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int NR>
+cudaError_t launch_rope(const LatentDecodeArgs& a, cudaStream_t s) {
+    return a.c.rope_dim ? launch<NR, true>(a, s) : launch<NR, false>(a, s);
 }
 
 }  // namespace
 
-size_t latent_decode_workspace_bytes(int, int) { return 256; }
+size_t latent_decode_workspace_bytes(int tokens_per_seq, int H) {
+    const int R = tokens_per_seq * H, groups = groups_of(R), grid = runs_of(groups) * groups;
+    if (runs_of(groups) == 1) return Work<64>::ml_at(grid);         // one run: every piece is a whole sequence
+    switch (rows_a_block(R)) {
+        case 16: return Work<16>::bytes(grid);
+        case 32: return Work<32>::bytes(grid);
+        default: return Work<64>::bytes(grid);
+    }
+}
 
 cudaError_t launch_latent_decode(const LatentDecodeArgs& a, cudaStream_t s) {
-    decode_simple_kernel<<<dim3((unsigned)(a.num_seqs * a.tokens_per_seq), (unsigned)a.H), kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    switch (rows_a_block(a.tokens_per_seq * a.H)) {
+        case 16: return launch_rope<16>(a, s);
+        case 32: return launch_rope<32>(a, s);
+        default: return launch_rope<64>(a, s);
+    }
 }
 
 }  // namespace kda
