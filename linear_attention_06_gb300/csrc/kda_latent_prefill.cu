@@ -1,71 +1,436 @@
 // kda_latent_prefill.cu -- expanded latent attention over packed sequences (kda_latent_prefill).
 //
-// First form: one block per (query, head), its warps taking every fourth key with a softmax of their
-// own, joined at the end.  Right for every shape; it reads the keys once a query.
+// For one head and query i of a sequence with nq queries and nk keys, over the keys j <= nk - nq + i:
+//
+//     s_ij = scale (q_i[:128] . k_j + q_i[128:] . r_j),   o_i = sum_j e^{s_ij - m_i} v_j / sum_j e^{s_ij - m_i}.
+//
+// One pass over the keys with the running maximum and sum.  2 (192 + 128) flop a visible pair against 2 (128 + 128)
+// bytes a key and head, read once for 256 queries: the tensor cores bound it.
+//
+// Block: 256 queries of one head as two tiles of 128, A and B, that take turns: while the tensor core works on
+// one, four warps turn the other's scores into weights.  Per tile of 128 keys and query tile X:
+//   S_X [128 x 128]  = Q_X K^T     both from shared memory (128-byte swizzle), K = 192 or 128
+//   O_X [128 x 128] += P_X V       P_X bf16 in tensor memory, over the columns that held S_X
+// S_A, S_B, O_A, O_B are all of tensor memory's 512 columns.  A thread owns a query's whole row of scores, so
+// maximum and sum need no exchange.  The maximum is raised only when a score exceeds it by more than 2^8 (weights
+// stay below 2^8 in bf16, whose precision does not depend on the exponent; sums are fp32), so O is rarely
+// rescaled; when it is, its last product is done already: S_X was issued behind it.
+//
+// Keys stream through a ring of 16 KB slices of 64 channels, each handed back when B's product has read it, values
+// through two stages of 32 KB.
+#include <atomic>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <math.h>
 #include <stdint.h>
 
 #include "kda_internal.h"
 #include "kda_latent_common.cuh"
+#include "sm103_primitives.cuh"
 
 namespace kda {
 namespace {
 
 using namespace latent;
+using namespace sm103;
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kM = 128, kBlockQ = 2 * kM, kN = 128;   // queries a tile and a block, keys a tile
+constexpr int kThreads = 320;                         // warps 0-3: A, 4-7: B, 8: producer, 9: issuer
+constexpr int kHeadsTogether = 8;                     // heads whose keys are in L2 at a time
+constexpr float kRaise = 8.f;                         // log2 of how far a score may exceed the running maximum
+constexpr uint64_t kWaitNs = 4000000000ull;           // bound of every wait
 
-__global__ void __launch_bounds__(kThreads) prefill_simple_kernel(const LatentPrefillArgs a) {
-    __shared__ float acc_s[kWarps][kHead];
-    __shared__ float m_s[kWarps], l_s[kWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t = blockIdx.x;
-    const int h = blockIdx.y;
-    int64_t qb, qe, kb, ke;
-    const int n = find_seq(a.cu_q, a.num_seqs, a.total_q, t, qb, qe);
-    if (n < 0) return;
-    bounds(a.cu_k, n, a.num_seqs, a.total_kv, kb, ke);
-    const int64_t seen = (ke - kb) - (qe - qb) + (t - qb) + 1;
-    const int64_t row = t * a.H + h;
-    const int steps = a.dk / 32;
-    float q[6], acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < steps; ++k)
-        q[k] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[row * a.dk + k * 32 + lane]);
-    float m = -INFINITY, l = 0.f;
-    for (int64_t p = warp; p < seen; p += kWarps) {
-        const __nv_bfloat16* k_row = static_cast<const __nv_bfloat16*>(a.k) + ((kb + p) * a.H + h) * a.kv_stride;
-        const __nv_bfloat16* v_row = static_cast<const __nv_bfloat16*>(a.v) + ((kb + p) * a.H + h) * a.kv_stride;
-        float s = 0.f;
-        for (int k = 0; k < 4; ++k) s += q[k] * __bfloat162float(k_row[k * 32 + lane]);
-        for (int k = 4; k < steps; ++k)
-            s += q[k] * __bfloat162float(
-                            static_cast<const __nv_bfloat16*>(a.k_rope)[(kb + p) * kRope + (k - 4) * 32 + lane]);
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= a.scale;
-        const float mn = fmaxf(m, s), f = expf(m - mn), w = expf(s - mn);
-        l = l * f + w;
-        for (int k = 0; k < 4; ++k) acc[k] = acc[k] * f + w * __bfloat162float(v_row[k * 32 + lane]);
-        m = mn;
+template <int DK>
+struct Cfg {
+    static constexpr uint32_t kSlices = DK / 64;                  // of queries and keys
+    static constexpr uint32_t kQ = 0, kV = 2 * kSlices * 16384;   // queries [A, B][slice][128][64], values [2][2][128][64]
+    static constexpr uint32_t kK = kV + 65536;
+    static constexpr uint32_t kKSlots = DK == 192 ? 4 : 6;
+    static constexpr uint32_t kSmall = kK + kKSlots * 16384;
+    static constexpr uint32_t kBytes = kSmall + 1024 + 1024;      // + alignment slack
+    static_assert(kBytes <= 232448, "shared memory");
+};
+
+struct Small {
+    uint64_t q_full[2], k_full[6], k_empty[6], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], drain;
+    uint32_t tmem;
+};
+static_assert(sizeof(Small) <= 1024, "small area");
+
+struct Maps {
+    CUtensorMap q, k, v, r;
+};
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_parked(bar, parity, kWaitNs); }
+
+// Two fp32 in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
+
+// The block's sequence, 256-query tile and head.  Tile slots: sequence n's start at floor(b_n / 256) + n, so that
+// ceil(T / 256) + N slots hold any lengths and a block finds its own by bisection.  Heads go in groups whose keys
+// stay in L2, and slots from the last (the longest rows of a sequence) down, so that the lightest end the launch.
+struct Place {
+    int n, h;
+    int64_t qb, q0, kb;                       // sequence's first query, this tile's first query in it, first key
+    int nq, nk;
+};
+__device__ __forceinline__ bool find_place(const LatentPrefillArgs& a, int64_t slots, Place& x) {
+    const int64_t b = blockIdx.x, per = slots * kHeadsTogether;
+    const int first = (int)(b / per) * kHeadsTogether;
+    const int together = a.H - first < kHeadsTogether ? a.H - first : kHeadsTogether;
+    const int64_t rem = b % per, slot = slots - 1 - rem / together;
+    x.h = first + (int)(rem % together);
+    int lo = 0, hi = a.num_seqs;              // the last n whose first slot is <= slot
+    auto first_slot = [&](int n) {
+        int64_t s, e;
+        bounds(a.cu_q, n, a.num_seqs, a.total_q, s, e);
+        return s / kBlockQ + n;
+    };
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first_slot(mid) <= slot) lo = mid; else hi = mid;
     }
-    for (int k = 0; k < 4; ++k) acc_s[warp][k * 32 + lane] = acc[k];
-    if (lane == 0) { m_s[warp] = m; l_s[warp] = l; }
+    int64_t qe, ke;
+    x.n = lo;
+    bounds(a.cu_q, lo, a.num_seqs, a.total_q, x.qb, qe);
+    bounds(a.cu_k, lo, a.num_seqs, a.total_kv, x.kb, ke);
+    x.nq = (int)(qe - x.qb);
+    x.nk = (int)(ke - x.kb);
+    x.q0 = (slot - (x.qb / kBlockQ + lo)) * kBlockQ;
+    return x.q0 >= 0 && x.q0 < x.nq;
+}
+
+// Key tiles that query tile X of a place looks at.
+__device__ __forceinline__ int tiles_of(const Place& x, int X) {
+    const int64_t first = x.q0 + X * kM;
+    if (first >= x.nq) return 0;
+    const int64_t last = first + kM < x.nq ? first + kM : x.nq;    // behind its last query
+    const int64_t seen = (int64_t)x.nk - x.nq + last;
+    return seen > 0 ? (int)((seen + kN - 1) / kN) : 0;
+}
+
+template <int DK>
+__global__ void __launch_bounds__(kThreads, 1)
+latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs a, const int64_t slots) {
+    using G = Cfg<DK>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    Small* sw = reinterpret_cast<Small*>(sm + G::kSmall);
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    Place x;
+    if (!find_place(a, slots, x)) return;     // a slot without queries
+    const int tiles[2] = {tiles_of(x, 0), tiles_of(x, 1)};
+    const int most = tiles[0] > tiles[1] ? tiles[0] : tiles[1];
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sw->q_full[i], 1);
+            mbar_init(&sw->v_full[i], 1);
+            mbar_init(&sw->v_empty[i], 1);
+            mbar_init(&sw->s_full[i], 1);
+            mbar_init(&sw->p_full[i], 4);
+            mbar_init(&sw->o_done[i], 1);
+        }
+        for (int i = 0; i < (int)G::kKSlots; ++i) { mbar_init(&sw->k_full[i], 1); mbar_init(&sw->k_empty[i], 1); }
+        mbar_init(&sw->drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(&sw->tmem, 512);
+        tmem_relinquish();
+    }
+    if (warp == 8 && lane < 4) tma_prefetch_desc(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : &maps.r);
+    tc_fence_before();
     __syncthreads();
-    float mx = -INFINITY, sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, m_s[w]);
-    for (int w = 0; w < kWarps; ++w) sum += m_s[w] == -INFINITY ? 0.f : l_s[w] * expf(m_s[w] - mx);
-    float o = 0.f;
-    for (int w = 0; w < kWarps; ++w) o += m_s[w] == -INFINITY ? 0.f : acc_s[w][threadIdx.x] * expf(m_s[w] - mx);
-    static_cast<__nv_bfloat16*>(a.out)[row * kHead + threadIdx.x] = __float2bfloat16_rn(seen > 0 ? o / sum : 0.f);
-    if (a.lse && threadIdx.x == 0) a.lse[row] = seen > 0 ? mx + logf(sum) : -INFINITY;
+    tc_fence_after();
+    const uint32_t tb = sw->tmem;             // columns: S_A, S_B, O_A, O_B
+    bool ok = true;
+
+    if (warp == 8) {                          // ------------------------------------------------ producer
+        uint32_t k_loads = 0, v_loads = 0, q_loads = 0;
+        if (elect_one()) {
+            auto load_k = [&](int j) {
+                for (uint32_t s = 0; ok && s < G::kSlices; ++s, ++k_loads) {
+                    const uint32_t slot = k_loads % G::kKSlots, round = k_loads / G::kKSlots;
+                    if (round > 0 && !(ok = wait(&sw->k_empty[slot], (round - 1) & 1))) return;
+                    mbar_arrive_expect_tx(&sw->k_full[slot], 16384);
+                    uint8_t* dst = sm + G::kK + slot * 16384;
+                    const int t = (int)x.kb + j * kN;
+                    if (s < 2)
+                        tma_load_3d(dst, &maps.k, s * 64, x.h, t, &sw->k_full[slot]);
+                    else
+                        tma_load_2d(dst, &maps.r, 0, t, &sw->k_full[slot]);
+                }
+            };
+            auto load_q = [&](int X) {
+                if (!tiles[X]) return;
+                mbar_arrive_expect_tx(&sw->q_full[X], G::kSlices * 16384);
+                for (uint32_t s = 0; s < G::kSlices; ++s)
+                    tma_load_3d(sm + G::kQ + (X * G::kSlices + s) * 16384, &maps.q, s * 64, x.h,
+                                (int)(x.qb + x.q0) + X * kM, &sw->q_full[X]);
+                q_loads |= 1u << X;
+            };
+            load_q(0);
+            if (most > 0) load_k(0);
+            load_q(1);
+            for (int j = 0; ok && j < most; ++j) {
+                if (j + 1 < most) load_k(j + 1);
+                if (!ok || (j > 1 && !(ok = wait(&sw->v_empty[j & 1], ((j >> 1) - 1) & 1)))) break;
+                mbar_arrive_expect_tx(&sw->v_full[j & 1], 32768);
+                for (int s = 0; s < 2; ++s)
+                    tma_load_3d(sm + G::kV + (j & 1) * 32768 + s * 16384, &maps.v, s * 64, x.h, (int)x.kb + j * kN,
+                                &sw->v_full[j & 1]);
+                ++v_loads;
+            }
+            if (!ok) {                        // copies in flight land before the block ends
+                for (uint32_t i = 0; i < G::kKSlots; ++i)
+                    if (k_loads > i) mbar_wait_bounded(&sw->k_full[i], ((k_loads - 1 - i) / G::kKSlots) & 1, kWaitNs);
+                for (uint32_t i = 0; i < 2; ++i) {
+                    if (v_loads > i) mbar_wait_bounded(&sw->v_full[i], ((v_loads - 1 - i) / 2) & 1, kWaitNs);
+                    if (q_loads >> i & 1) mbar_wait_bounded(&sw->q_full[i], 0, kWaitNs);
+                }
+                atomicOr(a.status, kStatusTimeout);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {                   // ------------------------------------------------ issuer
+        constexpr uint32_t id_s = idesc_bf16_f32(kM, kN, false, false), id_o = idesc_bf16_f32(kM, kHead, false, true);
+        const uint32_t sq = smem_u32(sm + G::kQ), sk = smem_u32(sm + G::kK), sv = smem_u32(sm + G::kV);
+        // S_X of key tile j
+        auto scores = [&](int X, int j) {
+            const bool first = X == 0 || j >= tiles[0], last = X == 1 || j >= tiles[1];
+            if (j == 0 && !(ok = wait(&sw->q_full[X], 0))) return;
+            for (uint32_t s = 0; s < G::kSlices; ++s) {
+                const uint32_t at = j * G::kSlices + s, slot = at % G::kKSlots;
+                if (first && !(ok = wait(&sw->k_full[slot], (at / G::kKSlots) & 1))) return;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mma_ss(tb + X * 128, smem_desc(sq + (X * G::kSlices + s) * 16384 + i * 32, 16, 1024, kSwizzle128B),
+                               smem_desc(sk + slot * 16384 + i * 32, 16, 1024, kSwizzle128B), id_s, s > 0 || i > 0);
+                    if (last) mma_commit(&sw->k_empty[slot]);
+                }
+            }
+            if (elect_one()) mma_commit(&sw->s_full[X]);
+        };
+        // O_X += P_X V of key tile j
+        auto values = [&](int X, int j) {
+            const bool last = X == 1 || j >= tiles[1];
+            if (!(ok = wait(&sw->v_full[j & 1], (j >> 1) & 1))) return;
+            if (!(ok = wait(&sw->p_full[X], j & 1))) return;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < kN / 16; ++i)
+                    mma_ts(tb + 256 + X * 128, tb + X * 128 + i * 8,
+                           smem_desc(sv + (j & 1) * 32768 + i * 2048, 16384, 1024, kSwizzle128B), id_o, j > 0 || i > 0);
+                if (last) mma_commit(&sw->v_empty[j & 1]);
+                if (j + 1 == tiles[X]) mma_commit(&sw->o_done[X]);
+            }
+        };
+        if (tiles[0]) scores(0, 0);
+        if (ok && tiles[1]) scores(1, 0);
+        for (int j = 0; ok && j < most; ++j)
+            for (int X = 0; ok && X < 2; ++X) {
+                if (j < tiles[X]) values(X, j);
+                if (ok && j + 1 < tiles[X]) scores(X, j + 1);
+            }
+        if (!ok) {                            // products in flight land before TMEM is freed
+            if (elect_one()) mma_commit(&sw->drain);
+            wait(&sw->drain, 0);
+            if (lane == 0) atomicOr(a.status, kStatusTimeout);
+        }
+    } else {                                  // ------------------------------------------------ softmax of tile X
+        const int X = warp >> 2, w = warp & 3, t = tid & 127;
+        const int64_t i = x.q0 + X * kM + t;  // the thread's query in its sequence
+        const int64_t seen = (int64_t)x.nk - x.nq + i + 1;
+        const float c2 = a.scale * 1.44269504088896340736f;
+        const uint32_t ts = tmem_addr(tb, 32 * w, X * 128), to = tmem_addr(tb, 32 * w, 256 + X * 128);
+        float m = -INFINITY, l = 0.f;
+        const int count = tiles[X];
+        for (int j = 0; j < count; ++j) {
+            if (!(ok = wait(&sw->s_full[X], j & 1))) break;
+            tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, s[b]);
+            tmem_wait_ld();
+            const int64_t lim = seen - (int64_t)j * kN;              // columns that the query sees
+            if (__any_sync(0xffffffffu, lim < kN)) {
+                const int edge = lim < 0 ? 0 : (lim < kN ? (int)lim : kN);
+#pragma unroll
+                for (int k = 0; k < kN; ++k)
+                    if (k >= edge) s[k >> 5][k & 31] = 0xff800000u;  // -inf
+            }
+            float mx = __uint_as_float(s[0][0]);
+#pragma unroll
+            for (int k = 1; k < kN; ++k) mx = fmaxf(mx, __uint_as_float(s[k >> 5][k & 31]));
+            float f = 1.f;
+            if (mx > m && (mx - m) * c2 > kRaise) {                  // also the first finite maximum
+                f = exp2_fast((m - mx) * c2);
+                m = mx;
+            }
+            l *= f;
+            if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {        // rescale the warp's rows of O
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t o[32];
+                    tmem_ld32(to + 32 * b, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tmem_st32(to + 32 * b, o);
+                }
+            }
+            const float z = m == -INFINITY ? 0.f : -m * c2;
+            const float2 c22 = make_float2(c2, c2), z2 = make_float2(z, z);
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t p[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float2 y = fma2(make_float2(__uint_as_float(s[b][2 * k]), __uint_as_float(s[b][2 * k + 1])), c22, z2);
+                    y.x = exp2_fast(y.x);
+                    y.y = exp2_fast(y.y);
+                    sum = add2(sum, y);
+                    p[k] = pack_bf16x2(y.x, y.y);
+                }
+                tmem_st16(ts + 16 * b, p);
+            }
+            l += sum.x + sum.y;
+            if ((int64_t)(j + 1) * kN > x.nk) {                      // value rows behind the sequence's end become zeros
+                if (!(ok = wait(&sw->v_full[j & 1], (j >> 1) & 1))) break;
+                if (j * kN + t >= x.nk)
+                    for (int k = 0; k < 16; ++k)
+                        *reinterpret_cast<uint4*>(sm + G::kV + (j & 1) * 32768 + (k >> 3) * 16384 + t * 128 + (k & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sw->p_full[X]);
+        }
+        if (ok && count && !(ok = wait(&sw->o_done[X], 0))) {}
+        if (ok) {                             // a thread stores its query's row
+            tc_fence_after();
+            const int64_t row = (x.qb + i) * a.H + x.h;
+            const bool live = i < x.nq && KDA_INDEX_OK(row, a.total_q * a.H, a.status);
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * kHead);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t o[32];
+                if (count) {
+                    tmem_ld32(to + 32 * b, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = 0u;
+                }
+                if (live) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint4 y;
+                        y.x = pack_bf16x2(__uint_as_float(o[8 * k]) * inv, __uint_as_float(o[8 * k + 1]) * inv);
+                        y.y = pack_bf16x2(__uint_as_float(o[8 * k + 2]) * inv, __uint_as_float(o[8 * k + 3]) * inv);
+                        y.z = pack_bf16x2(__uint_as_float(o[8 * k + 4]) * inv, __uint_as_float(o[8 * k + 5]) * inv);
+                        y.w = pack_bf16x2(__uint_as_float(o[8 * k + 6]) * inv, __uint_as_float(o[8 * k + 7]) * inv);
+                        out[4 * b + k] = y;
+                    }
+                }
+            }
+            if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
+        } else if (lane == 0) {
+            atomicOr(a.status, kStatusTimeout);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tb, 512);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        return nullptr;
+    }();
+    return fn;
+}
+
+// [tokens, heads] rows of `width` channels, `step` elements apart; boxes of 64 channels x 1 head x 128 tokens.
+bool map_heads(CUtensorMap* m, const void* base, int64_t tokens, int heads, int width, int64_t step) {
+    const auto fn = encode();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)step * 2, (cuuint64_t)step * heads * 2};
+    cuuint32_t box[3] = {64, 1, 128}, es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool map_shared(CUtensorMap* m, const void* base, int64_t tokens) {
+    const auto fn = encode();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)kRope, (cuuint64_t)tokens}, strides[1] = {(cuuint64_t)kRope * 2};
+    cuuint32_t box[2] = {64, 128}, es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DK>
+cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
+    using G = Cfg<DK>;
+    Maps maps;
+    // without keys nothing is loaded; the maps are then those of the queries
+    const bool keys = a.total_kv > 0;
+    if (!map_heads(&maps.q, a.q, a.total_q, a.H, DK, DK) ||
+        !(keys ? map_heads(&maps.k, a.k, a.total_kv, a.H, kHead, a.kv_stride) : map_heads(&maps.k, a.q, a.total_q, a.H, DK, DK)) ||
+        !(keys ? map_heads(&maps.v, a.v, a.total_kv, a.H, kHead, a.kv_stride) : map_heads(&maps.v, a.q, a.total_q, a.H, DK, DK)) ||
+        !(keys && DK > kHead ? map_shared(&maps.r, a.k_rope, a.total_kv) : map_heads(&maps.r, a.q, a.total_q, a.H, DK, DK)))
+        return cudaErrorInvalidValue;
+    static std::atomic<bool> ready[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(latent_prefill_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)G::kBytes);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true, std::memory_order_release);
+    }
+    const int64_t slots = (a.total_q + kBlockQ - 1) / kBlockQ + a.num_seqs, blocks = slots * a.H;
+    if (blocks > (int64_t)INT32_MAX) return cudaErrorInvalidConfiguration;
+    latent_prefill_kernel<DK><<<(unsigned)blocks, kThreads, G::kBytes, s>>>(maps, a, slots);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, cudaStream_t s) {
-    prefill_simple_kernel<<<dim3((unsigned)a.total_q, (unsigned)a.H), kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return a.dk == 192 ? launch<192>(a, s) : launch<128>(a, s);
 }
 
 }  // namespace kda
