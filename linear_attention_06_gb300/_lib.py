@@ -381,76 +381,86 @@ def kda_decode_step(q, k, v, log_alpha, beta, state, out=None, stream=None):
 _LATENT, _ROPE, _HEAD = 512, 64, 128
 
 
-def _expect(name, t, shape, dtype, device, strides=False):
-    """A tensor argument of the latent-attention calls: its shape, type and device; contiguous unless
-    the call takes its strides."""
+def _expect(name, t, shape, dtype, index, strides=False):
+    """The address of a tensor argument of the latent-attention calls, its shape, type and device (CUDA
+    device `index`) checked; contiguous unless the call takes its strides."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and (strides or t.is_contiguous()):
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, not on {t.device}")
-    if not strides and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, not on {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _row_stride(name, t):
     """Elements between consecutive rows of t [..., channels], all its leading axes one run of rows."""
-    rows = 1
-    step = None
-    for d in range(t.dim() - 2, -1, -1):
-        if t.shape[d] > 1:
-            if step is None:
-                step = t.stride(d)
-                if step < t.shape[-1] * rows or step % rows:
-                    raise ValueError(f"{name}: rows must not overlap")
-                step //= rows
-            elif t.stride(d) != step * rows:
-                raise ValueError(f"{name}: rows must be evenly spaced")
-        rows *= t.shape[d]
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    width = t.shape[-1]
+    if t.is_contiguous():
+        return max(width, 8)
+    strides = t.stride()
+    if width > 1 and strides[-1] != 1:
         raise ValueError(f"{name}: channels must be contiguous")
-    return max(t.shape[-1], 8) if step is None else step
+    rows, step = 1, None
+    for d in range(len(strides) - 2, -1, -1):
+        size = t.shape[d]
+        if size > 1:
+            if step is None:
+                step = strides[d]
+                if step < width * rows or step % rows:
+                    raise ValueError(f"{name}: rows must not overlap")
+            elif strides[d] != step * rows:
+                raise ValueError(f"{name}: rows must be evenly spaced")
+            rows *= size
+    return max(width, 8) if step is None else step
 
 
 def _cuda(t):
     if not t.is_cuda:
         raise ValueError("tensor arguments must be CUDA tensors")
-    return t.device
+    return t.get_device()
 
 
-def _table(name, table, tokens, device):
-    """A cu_seqlens argument: a CUDA int32 tensor as it is, a host table validated and copied."""
+def _table(name, table, tokens, n, index):
+    """The address (and the tensor, to keep it alive) of a cu_seqlens argument: a CUDA int32 tensor as it is, a
+    host table validated and copied.  n: the sequences it must have, or None."""
     if not (isinstance(table, torch.Tensor) and table.is_cuda):
         host = torch.as_tensor(table, dtype=torch.int32).cpu()
         kda_check_cu_seqlens(host, tokens)
-        table = host.to(device)
-    if table.dim() != 1 or table.numel() < 1:
-        raise ValueError(f"{name} must hold N + 1 offsets")
-    _expect(name, table, table.shape, torch.int32, device)
-    return table
+        table = host.to(torch.device("cuda", index))
+    if n is None:
+        if table.dim() != 1 or table.numel() < 1:
+            raise ValueError(f"{name} must hold N + 1 offsets")
+        n = table.shape[0] - 1
+    return _expect(name, table, (n + 1,), torch.int32, index), table
 
 
-def _latent_cache(cache, block_table, device):
-    """(rope_dim, page_size, num_pages, N, max_pages) of a latent cache and its table."""
-    if cache.dim() != 3 or cache.shape[2] not in (_LATENT, _LATENT + _ROPE):
+def _latent_cache(cache, block_table, H, tokens, index):
+    """Addresses of a latent cache and its table, and the shape descriptor of a call on them."""
+    pages, page, width = cache.shape if cache.dim() == 3 else (0, 0, 0)
+    if width != _LATENT and width != _LATENT + _ROPE:
         raise ValueError(f"cache must be [pages, page_size, {_LATENT} or {_LATENT + _ROPE}], "
                          f"not {tuple(cache.shape)}")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [N, max_pages]")
-    _expect("cache", cache, cache.shape, torch.bfloat16, device)
-    _expect("block_table", block_table, block_table.shape, torch.int32, device)
-    return cache.shape[2] - _LATENT, cache.shape[1], cache.shape[0], block_table.shape[0], block_table.shape[1]
+    n, per = block_table.shape
+    return (_expect("cache", cache, (pages, page, width), torch.bfloat16, index),
+            _expect("block_table", block_table, (n, per), torch.int32, index),
+            KdaLatentShape(n, tokens, H, _LATENT, width - _LATENT, page, pages, per, KDA_BF16))
 
 
-def _call(fn, device, stream, *args):
-    """Call fn(*args, stream) with the tensors' device current."""
-    if device.index == torch.cuda.current_device():
-        _check(fn, getattr(lib(), fn)(*args, _stream(stream)))
+def _call(fn, index, stream, *args):
+    """Call the library's fn(*args, stream) with the tensors' device current."""
+    f = getattr(_lib or lib(), fn)
+    if torch.cuda.current_device() == index:
+        st = f(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(device):
-            _check(fn, getattr(lib(), fn)(*args, _stream(stream)))
+        with torch.cuda.device(index):
+            st = f(*args, _stream(stream))
+    if st != KDA_OK:
+        raise KdaError(fn, st, status_string(st))
 
 
 def kda_latent_append(latent, k_rope, cache, block_table, seq_lens, inv_freq=None, interleaved=False, q_rope=None,
@@ -464,28 +474,31 @@ def kda_latent_append(latent, k_rope, cache, block_table, seq_lens, inv_freq=Non
     rotated into ``q_rope_out`` (allocated when not given; q_rope itself rotates in place), which is
     returned; None without queries."""
     dev = _cuda(cache)
-    rope, page, pages, n, per = _latent_cache(cache, block_table, dev)
-    T = latent.shape[0]
+    T, H = latent.shape[0], 1 if q_rope is None else q_rope.shape[1]
+    p_cache, p_table, shape = _latent_cache(cache, block_table, H, T, dev)
+    n, rope = shape.num_seqs, shape.rope_dim
+    p_rope = p_freq = p_cu = p_q = p_out = None
+    rope_step = q_step = out_step = 0
     p_latent = _expect("latent", latent, (T, _LATENT), torch.bfloat16, dev, True)
-    p_rope = _expect("k_rope", k_rope, (T, _ROPE), torch.bfloat16, dev, True) if rope else None
+    if rope:
+        p_rope = _expect("k_rope", k_rope, (T, _ROPE), torch.bfloat16, dev, True)
+        rope_step = _row_stride("k_rope", k_rope)
     p_lens = _expect("seq_lens", seq_lens, (n,), torch.int32, dev)
-    p_freq = None if inv_freq is None else _expect("inv_freq", inv_freq, (_ROPE // 2,), torch.float32, dev)
+    if inv_freq is not None:
+        p_freq = _expect("inv_freq", inv_freq, (_ROPE // 2,), torch.float32, dev)
     if cu_seqlens is not None:
-        cu_seqlens = _table("cu_seqlens", cu_seqlens, T, dev)
-        _expect("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, dev)
-    H, p_q, p_out, q_step, out_step = 1, None, None, 0, 0
+        p_cu, cu_seqlens = _table("cu_seqlens", cu_seqlens, T, n, dev)
     if q_rope is not None:
-        H = q_rope.shape[1]
         p_q = _expect("q_rope", q_rope, (T, H, _ROPE), torch.bfloat16, dev, True)
         q_step = _row_stride("q_rope", q_rope)
         if q_rope_out is None:
-            q_rope_out = torch.empty((T, H, _ROPE), dtype=torch.bfloat16, device=dev)
-        p_out = _expect("q_rope_out", q_rope_out, (T, H, _ROPE), torch.bfloat16, dev, True)
-        out_step = _row_stride("q_rope_out", q_rope_out)
-    shape = KdaLatentShape(n, T, H, _LATENT, rope, page, pages, per, KDA_BF16)
-    _call("kda_latent_append", dev, stream, ctypes.byref(shape), p_latent, _row_stride("latent", latent), p_rope,
-          _row_stride("k_rope", k_rope) if rope else 0, p_freq, int(bool(interleaved)), p_q, q_step, p_out, out_step,
-          None if cu_seqlens is None else cu_seqlens.data_ptr(), p_lens, block_table.data_ptr(), cache.data_ptr())
+            q_rope_out = torch.empty((T, H, _ROPE), dtype=torch.bfloat16, device=cache.device)
+            p_out, out_step = q_rope_out.data_ptr(), _ROPE
+        else:
+            p_out = _expect("q_rope_out", q_rope_out, (T, H, _ROPE), torch.bfloat16, dev, True)
+            out_step = _row_stride("q_rope_out", q_rope_out)
+    _call("kda_latent_append", dev, stream, shape, p_latent, _row_stride("latent", latent), p_rope, rope_step, p_freq,
+          1 if interleaved else 0, p_q, q_step, p_out, out_step, p_cu, p_lens, p_table, p_cache)
     return q_rope_out if q_rope is not None else None
 
 
@@ -493,20 +506,20 @@ def kda_latent_gather(cache, block_table, cu_seqlens, total_tokens, starts=None,
     """Cached rows back to packed rows (see ``include/kda.h``): rows starts[n] .. of every sequence n, as
     many as cu_seqlens gives it.  Returns (latent [T, 512], k_rope [T, 64] or None), or fills ``out``."""
     dev = _cuda(cache)
-    rope, page, pages, n, per = _latent_cache(cache, block_table, dev)
     T = int(total_tokens)
-    cu_seqlens = _table("cu_seqlens", cu_seqlens, T, dev)
-    _expect("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, dev)
+    p_cache, p_table, shape = _latent_cache(cache, block_table, 1, T, dev)
+    n, rope = shape.num_seqs, shape.rope_dim
+    p_cu, cu_seqlens = _table("cu_seqlens", cu_seqlens, T, n, dev)
     p_starts = None if starts is None else _expect("starts", starts, (n,), torch.int32, dev)
     if out is None:
-        out = (torch.empty((T, _LATENT), dtype=cache.dtype, device=dev),
-               torch.empty((T, rope), dtype=cache.dtype, device=dev) if rope else None)
-    latent, k_rope = out
-    p_latent = _expect("latent", latent, (T, _LATENT), torch.bfloat16, dev)
-    p_rope = _expect("k_rope", k_rope, (T, rope), torch.bfloat16, dev) if rope else None
-    shape = KdaLatentShape(n, T, 1, _LATENT, rope, page, pages, per, KDA_BF16)
-    _call("kda_latent_gather", dev, stream, ctypes.byref(shape), cache.data_ptr(), block_table.data_ptr(),
-          cu_seqlens.data_ptr(), p_starts, p_latent, p_rope)
+        latent = torch.empty((T, _LATENT), dtype=torch.bfloat16, device=cache.device)
+        k_rope = torch.empty((T, rope), dtype=torch.bfloat16, device=cache.device) if rope else None
+        p_latent, p_rope = latent.data_ptr(), k_rope.data_ptr() if rope else None
+    else:
+        latent, k_rope = out
+        p_latent = _expect("latent", latent, (T, _LATENT), torch.bfloat16, dev)
+        p_rope = _expect("k_rope", k_rope, (T, rope), torch.bfloat16, dev) if rope else None
+    _call("kda_latent_gather", dev, stream, shape, p_cache, p_table, p_cu, p_starts, p_latent, p_rope)
     return latent, k_rope
 
 
@@ -528,25 +541,25 @@ def kda_latent_decode(q_latent, q_rope, cache, block_table, seq_lens, scale, out
     fill, True to allocate one, or None; ``workspace`` a CUDA uint8 tensor of
     kda_latent_decode_workspace_size bytes, allocated here when not given.  Returns (out [N*T, H, 512], lse)."""
     dev = _cuda(cache)
-    rope, page, pages, n, per = _latent_cache(cache, block_table, dev)
     rows, H = q_latent.shape[0], q_latent.shape[1]
+    p_cache, p_table, shape = _latent_cache(cache, block_table, H, rows, dev)
     p_q = _expect("q_latent", q_latent, (rows, H, _LATENT), torch.bfloat16, dev)
-    p_r = _expect("q_rope", q_rope, (rows, H, _ROPE), torch.bfloat16, dev) if rope else None
-    p_lens = _expect("seq_lens", seq_lens, (n,), torch.int32, dev)
+    p_r = _expect("q_rope", q_rope, (rows, H, _ROPE), torch.bfloat16, dev) if shape.rope_dim else None
+    p_lens = _expect("seq_lens", seq_lens, (shape.num_seqs,), torch.int32, dev)
     if out is None:
-        out = torch.empty((rows, H, _LATENT), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((rows, H, _LATENT), dtype=torch.bfloat16, device=cache.device)
+        p_out = out.data_ptr()
+    else:
+        p_out = _expect("out", out, (rows, H, _LATENT), torch.bfloat16, dev)
     if lse is True:
-        lse = torch.empty((rows, H), dtype=torch.float32, device=dev)
-    p_out = _expect("out", out, (rows, H, _LATENT), torch.bfloat16, dev)
+        lse = torch.empty((rows, H), dtype=torch.float32, device=cache.device)
     p_lse = None if lse is None else _expect("lse", lse, (rows, H), torch.float32, dev)
-    shape = KdaLatentShape(n, rows, H, _LATENT, rope, page, pages, per, KDA_BF16)
     if workspace is None:
         need = ctypes.c_size_t(0)
-        _check("kda_latent_decode", lib().kda_latent_decode_workspace_size(ctypes.byref(shape), ctypes.byref(need)))
-        workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=dev)
-    _call("kda_latent_decode", dev, stream, ctypes.byref(shape), p_q, p_r, cache.data_ptr(), block_table.data_ptr(),
-          p_lens, float(scale), p_out, p_lse, _expect("workspace", workspace, workspace.shape, torch.uint8, dev),
-          workspace.numel())
+        _check("kda_latent_decode", lib().kda_latent_decode_workspace_size(shape, ctypes.byref(need)))
+        workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=cache.device)
+    _call("kda_latent_decode", dev, stream, shape, p_q, p_r, p_cache, p_table, p_lens, float(scale), p_out, p_lse,
+          _expect("workspace", workspace, workspace.shape, torch.uint8, dev), workspace.numel())
     return out, lse
 
 
@@ -570,27 +583,25 @@ def kda_latent_prefill(q, k, v, k_rope, scale, cu_seqlens=None, cu_seqlens_k=Non
     step = _row_stride("k", k)
     if S * H > 1 and step != _row_stride("v", v):
         raise ValueError("k and v must have the same row stride")
-    n = 1 if num_seqs is None else int(num_seqs)
+    n, p_cu, p_cu_k = 1 if num_seqs is None else int(num_seqs), None, None
     if cu_seqlens is not None:
-        cu_seqlens = _table("cu_seqlens", cu_seqlens, T, dev)
-        n = cu_seqlens.numel() - 1
+        p_cu, cu_seqlens = _table("cu_seqlens", cu_seqlens, T, None, dev)
+        n = cu_seqlens.shape[0] - 1
     if cu_seqlens_k is not None:
-        cu_seqlens_k = _table("cu_seqlens_k", cu_seqlens_k, S, dev)
-        if cu_seqlens is None:
-            n = cu_seqlens_k.numel() - 1
-        _expect("cu_seqlens_k", cu_seqlens_k, (n + 1,), torch.int32, dev)
+        p_cu_k, cu_seqlens_k = _table("cu_seqlens_k", cu_seqlens_k, S, None if cu_seqlens is None else n, dev)
+        n = cu_seqlens_k.shape[0] - 1
     elif cu_seqlens is not None and S == T:
-        cu_seqlens_k = cu_seqlens
+        p_cu_k = p_cu
     if out is None:
-        out = torch.empty((T, H, _HEAD), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, H, _HEAD), dtype=torch.bfloat16, device=q.device)
+        p_out = out.data_ptr()
+    else:
+        p_out = _expect("out", out, (T, H, _HEAD), torch.bfloat16, dev)
     if lse is True:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    p_out = _expect("out", out, (T, H, _HEAD), torch.bfloat16, dev)
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
     p_lse = None if lse is None else _expect("lse", lse, (T, H), torch.float32, dev)
-    shape = KdaShape(n, T, H, dk, _HEAD, KDA_BF16)
-    _call("kda_latent_prefill", dev, stream, ctypes.byref(shape), S, p_q, p_k, p_v, step, p_r, float(scale),
-          None if cu_seqlens is None else cu_seqlens.data_ptr(),
-          None if cu_seqlens_k is None else cu_seqlens_k.data_ptr(), p_out, p_lse)
+    _call("kda_latent_prefill", dev, stream, KdaShape(n, T, H, dk, _HEAD, KDA_BF16), S, p_q, p_k, p_v, step, p_r,
+          float(scale), p_cu, p_cu_k, p_out, p_lse)
     return out, lse
 
 

@@ -49,6 +49,7 @@ constexpr int kThreads = 256;                 // warps 0-3: producer, issuer, qu
 constexpr int kSoft = 128;
 constexpr int kBar = 1;                       // named barrier of the softmax warps
 constexpr int kSMs = 152;
+constexpr int kAhead = 3;                     // tiles between a tile's prefetch into L2 and its loads
 constexpr float kRaise = 8.f;                 // log2 of how far a score may exceed the running maximum
 constexpr uint64_t kWaitNs = 4000000000ull;   // bound of every wait
 
@@ -77,7 +78,8 @@ struct Small {
     uint32_t tmem;
     int seq0, off0, runs;
     int64_t total, begin, end;
-    float fac[64];                            // rescaling factors, then 1 / l
+    alignas(16) float fac[64];                // rescaling factors
+    alignas(16) float inv[64];                // 1 / l at a piece's end
 };
 static_assert(sizeof(Small) <= 1024, "small area");
 
@@ -116,6 +118,10 @@ struct Walk {
 };
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_parked(bar, parity, kWaitNs); }
+// The same for a converged warp whose next steps the compiler should know to be uniform.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_parked(bar, parity, kWaitNs));
+}
 
 // The first tile of run p of `runs` over `total` tiles, and the run that holds tile x.
 __host__ __device__ __forceinline__ int64_t run_begin(int64_t total, int runs, int p) { return total * p / runs; }
@@ -139,16 +145,36 @@ struct Maps {
     CUtensorMap q, qr, c;
 };
 
-// All threads: the run of this block and the sequence it starts in.
-__device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Small* sw, int64_t* scratch) {
+// All threads: the run of this block and the sequence it starts in.  Rounds of a sequence a thread; with up to
+// kThreads sequences the lengths are read once.
+__device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Small* sw, int* scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int64_t sum = 0;
-    for (int n = tid; n < a.num_seqs; n += kThreads) sum += tiles_of(clamped_len(a.c, a.seq_lens, n));
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) scratch[warp] = sum;
-    __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) total += scratch[w];
+    auto tiles_at = [&](int n) { return n < a.num_seqs ? tiles_of(clamped_len(a.c, a.seq_lens, n)) : 0; };
+    // the round's tiles before this thread's sequence, and in all (a round has at most 2^31 / 64 * 256 / ... tiles of
+    // a cache that fits the card: well inside 32 bits)
+    auto scan = [&](int mine, int& round) {
+        int x = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) scratch[warp] = x;
+        __syncthreads();
+        round = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) x += scratch[w];
+            round += scratch[w];
+        }
+        __syncthreads();
+        return x - mine;
+    };
+    int mine = tiles_at(tid), round, at = scan(mine, round);
+    int64_t total = round;
+    for (int n0 = kThreads; n0 < a.num_seqs; n0 += kThreads) {
+        int more;
+        scan(tiles_at(n0 + tid), more);
+        total += more;
+    }
     // with fewer tiles than blocks the first blocks take a tile each: a sequence's runs are consecutive
     if (total < runs) runs = (int)total;
     const int64_t begin = p < runs ? run_begin(total, runs, p) : 0, end = p < runs ? run_begin(total, runs, p + 1) : 0;
@@ -157,35 +183,20 @@ __device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Small* sw, 
         sw->total = total;
         sw->begin = begin;
         sw->end = end;
-        sw->seq0 = sw->off0 = 0;
     }
-    if (begin == end) { __syncthreads(); return; }
-    int64_t before = 0;                       // tiles of the sequences before this round's
-    for (int n0 = 0; n0 < a.num_seqs; n0 += kThreads) {
-        const int n = n0 + tid;
-        const int64_t mine = n < a.num_seqs ? tiles_of(clamped_len(a.c, a.seq_lens, n)) : 0;
-        int64_t x = mine;                     // inclusive sum over the round
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        __syncthreads();
-        if (lane == 31) scratch[warp] = x;
-        __syncthreads();
-        int64_t round = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) x += scratch[w];
-            round += scratch[w];
-        }
-        const int64_t first = before + x - mine;
+    int64_t before = 0;                       // tiles of the rounds before
+    for (int n0 = 0;;) {
+        const int64_t first = before + at;
         if (mine > 0 && first <= begin && begin < first + mine) {
-            sw->seq0 = n;
+            sw->seq0 = n0 + tid;
             sw->off0 = (int)(begin - first);
         }
         before += round;
-        if (before > begin) break;            // uniform: `before` is the same for every thread
+        n0 += kThreads;
+        if (before > begin || n0 >= a.num_seqs) break;               // uniform
+        mine = tiles_at(n0 + tid);
+        at = scan(mine, round);
     }
-    __syncthreads();
 }
 
 template <int NR, bool ROPE>
@@ -223,7 +234,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
         tmem_alloc(&sw->tmem, G::kCols);
         tmem_relinquish();
     }
-    find_run(a, runs, run, sw, reinterpret_cast<int64_t*>(sw->fac));
+    find_run(a, runs, run, sw, reinterpret_cast<int*>(sw->fac));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -235,6 +246,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
     if (warp == 0) {                          // ------------------------------------------------ producer
         const int box = a.c.page_size < kTile ? a.c.page_size : kTile;
         const int shift = 31 - __clz(a.c.page_size);
+        constexpr int width = kLatent + (ROPE ? kRope : 0);
         const int half = lane & 1, piece = lane >> 1;               // a lane issues one box of a pair
         Walk walk(sw);
         Piece p;
@@ -251,9 +263,22 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                 const int page = a.c.block_table[table + (pos >> shift)];
                 return page < 0 || page >= a.c.num_pages ? map_rows : (page << shift) + (pos & (a.c.page_size - 1));
             };
-            int row = row_of(p.off);
+            // a page's rows lie in a row: one prefetch into L2 for each box, kAhead tiles before its loads
+            auto prefetch = [&](int r, int x) {
+                const int left = p.len - x * kTile - piece * box;
+                if (half == 0 && r >= 0 && r < map_rows)
+                    bulk_prefetch_l2(static_cast<const uint8_t*>(a.c.cache) + (int64_t)r * width * 2,
+                                     (uint32_t)(left < box ? left : box) * width * 2);
+            };
+            int rows_ahead[kAhead + 1];       // rows of tiles j .. j + kAhead
+#pragma unroll
+            for (int d = 0; d < kAhead; ++d) {
+                rows_ahead[d] = d < p.tiles ? row_of(p.off + d) : -1;
+                if (d > 0 && d < p.tiles) prefetch(rows_ahead[d], p.off + d);
+            }
             for (int j = 0; ok && j < p.tiles; ++j) {
-                const int next_row = j + 1 < p.tiles ? row_of(p.off + j + 1) : -1;
+                rows_ahead[kAhead] = j + kAhead < p.tiles ? row_of(p.off + j + kAhead) : -1;
+                const int row = rows_ahead[0];
                 const int live = p.len - (p.off + j) * kTile;
                 const int valid = live < 0 ? 0 : (live < kTile ? live : kTile);
                 const uint32_t boxes = (valid + box - 1) / box;
@@ -279,7 +304,9 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                     rope.next();
                     if (rope.slot == 0) rope_used = true;
                 }
-                row = next_row;
+                prefetch(rows_ahead[kAhead], p.off + j + kAhead);
+#pragma unroll
+                for (int d = 0; d < kAhead; ++d) rows_ahead[d] = rows_ahead[d + 1];
             }
         }
         if (!ok && lane == 0) {               // copies in flight land before the block ends
@@ -289,8 +316,13 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
     } else if (warp == 1) {                   // ------------------------------------------------ issuer
         constexpr uint32_t id_s = idesc_bf16_f32(64, 64, false, false);
         constexpr uint32_t id_o = idesc_bf16_f32(128, NR, true, false);
-        const uint32_t sq = smem_u32(sm + G::kQ), sp = smem_u32(sm + G::kP), sc = smem_u32(sm + G::kPairAt),
-                       sr = smem_u32(sm + G::kRopeAt);
+        // base descriptors: queries and cached rows as keys, rope slices, P, cached rows as values
+        const uint64_t dq = smem_desc(smem_u32(sm + G::kQ), 16, 1024, kSwizzle128B);
+        const uint64_t dk = smem_desc(smem_u32(sm + G::kPairAt), 16, 1024, kSwizzle128B);
+        const uint64_t dr = smem_desc(smem_u32(sm + G::kRopeAt), 16, 1024, kSwizzle128B);
+        const uint64_t dp = smem_desc(smem_u32(sm + G::kP), 16, 1024, kSwizzle128B);
+        const uint64_t dv = smem_desc(smem_u32(sm + G::kPairAt), 8192, 1024, kSwizzle128B);
+        const uint32_t el = elect_one();
         Walk walk(sw);
         Piece p;
         Ring<G::kPairs> in, out;              // next pair for S, next pair for O
@@ -298,7 +330,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
         Ring<2> sb, pb;                       // S / P buffers
         uint32_t seg = 0;
         while (ok && walk.next(a, p)) {
-            if (!(ok = wait(&sw->q_full, seg & 1))) break;
+            if (!(ok = wait_warp(&sw->q_full, seg & 1))) break;
             int qk = 0, pv = 0;
             while (pv < p.tiles) {
                 bool go = qk == pv;
@@ -311,53 +343,47 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                 }
                 if (go) {
                     const uint32_t d = ts + sb.slot * 64;
-                    for (int k = 0; k < 4; ++k) {
-                        if (!(ok = wait(&sw->full[in.slot], in.phase))) break;
-                        tc_fence_after();
-                        if (elect_one()) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                mma_ss(d, smem_desc(sq + (2 * k + (i >> 2)) * G::kSlice + (i & 3) * 32, 16, 1024, kSwizzle128B),
-                                       smem_desc(sc + in.slot * 16384 + (i >> 2) * 8192 + (i & 3) * 32, 16, 1024, kSwizzle128B),
-                                       id_s, k > 0 || i > 0);
-                        }
+                    for (int k = 0; k < 4; ++k) {
+                        if (!(ok = wait_warp(&sw->full[in.slot], in.phase))) break;
+                        tc_fence_after();
+                        const uint64_t y = desc_at(dk, in.slot * 16384);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            mma_ss_elected(d, desc_at(dq, (2 * k + (i >> 2)) * G::kSlice + (i & 3) * 32),
+                                           desc_at(y, (i >> 2) * 8192 + (i & 3) * 32), id_s, k > 0 || i > 0, el);
                         in.next();
                     }
                     if (!ok) break;
                     if constexpr (ROPE) {
-                        if (!(ok = wait(&sw->rope_full[rope.slot], rope.phase))) break;
+                        if (!(ok = wait_warp(&sw->rope_full[rope.slot], rope.phase))) break;
                         tc_fence_after();
-                        if (elect_one()) {
+                        const uint64_t y = desc_at(dr, rope.slot * 8192);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                mma_ss(d, smem_desc(sq + 8 * G::kSlice + i * 32, 16, 1024, kSwizzle128B),
-                                       smem_desc(sr + rope.slot * 8192 + i * 32, 16, 1024, kSwizzle128B), id_s, 1);
-                            mma_commit(&sw->rope_empty[rope.slot]);
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            mma_ss_elected(d, desc_at(dq, 8 * G::kSlice + i * 32), desc_at(y, i * 32), id_s, 1, el);
+                        mma_commit_elected(&sw->rope_empty[rope.slot], el);
                         rope.next();
                     }
-                    if (elect_one()) {
-                        mma_commit(&sw->s_full[sb.slot]);
-                        if (qk + 1 == p.tiles) mma_commit(&sw->q_empty);
-                    }
+                    mma_commit_elected(&sw->s_full[sb.slot], el);
+                    if (qk + 1 == p.tiles) mma_commit_elected(&sw->q_empty, el);
                     sb.next();
                     ++qk;
                 } else {
-                    if (!(ok = wait(&sw->p_full[pb.slot], pb.phase))) break;
-                    if (pv == 0 && seg > 0 && !(ok = wait(&sw->o_free, (seg - 1) & 1))) break;
+                    if (!(ok = wait_warp(&sw->p_full[pb.slot], pb.phase))) break;
+                    if (pv == 0 && seg > 0 && !(ok = wait_warp(&sw->o_free, (seg - 1) & 1))) break;
                     tc_fence_after();
-                    for (int b = 0; b < 4; ++b) {
-                        if (elect_one()) {
+                    const uint64_t x = desc_at(dp, pb.slot * G::kSlice);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                mma_ss(tb + b * NR, smem_desc(sc + out.slot * 16384 + i * 2048, 8192, 1024, kSwizzle128B),
-                                       smem_desc(sp + pb.slot * G::kSlice + i * 32, 16, 1024, kSwizzle128B), id_o,
-                                       pv > 0 || i > 0);
-                            mma_commit(&sw->empty[out.slot]);
-                        }
+                    for (int b = 0; b < 4; ++b) {
+                        const uint64_t y = desc_at(dv, out.slot * 16384);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_ss_elected(tb + b * NR, desc_at(y, i * 2048), desc_at(x, i * 32), id_o, pv > 0 || i > 0, el);
+                        mma_commit_elected(&sw->empty[out.slot], el);
                         out.next();
                     }
-                    if (elect_one()) mma_commit(&sw->pv_done[pb.slot]);
+                    mma_commit_elected(&sw->pv_done[pb.slot], el);
                     pb.next();
                     ++pv;
                 }
@@ -365,7 +391,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
             ++seg;
         }
         if (!ok) {                            // products in flight land before TMEM is freed
-            if (elect_one()) mma_commit(&sw->drain);
+            mma_commit_elected(&sw->drain, el);
             wait(&sw->drain, 0);
         }
     } else if (warp == 2) {                   // ------------------------------------------------ queries
@@ -470,16 +496,22 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                     asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kSoft) : "memory");
                     if (!(ok = wait(&sw->pv_done[prev.slot], prev.phase))) break;
                     tc_fence_after();
-                    for (int b = 0; b < 4; ++b)
-                        for (int k = 0; k < NR / 16; ++k) {
+#pragma unroll 1
+                    for (int k = 0; k < NR / 16; ++k) {
+                        float g[16];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<float4*>(g + 4 * i) = *reinterpret_cast<const float4*>(sw->fac + 16 * k + 4 * i);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
                             uint32_t o[16];
                             tmem_ld16(lanes + b * NR + k * 16, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * sw->fac[k * 16 + i]);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * g[i]);
                             tmem_st16(lanes + b * NR + k * 16, o);
                         }
+                    }
                     tmem_wait_st();
                 }
                 // this P buffer was read by the products of two tiles ago
@@ -529,7 +561,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                     l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
                     const int r = r0 + 8 * e;
                     if ((lane & 3) == 0) {
-                        sw->fac[r] = whole ? (l[e] > 0.f ? 1.f / l[e] : (l[e] == 0.f ? 0.f : l[e])) : 1.f;
+                        sw->inv[r] = l[e] == 0.f ? 0.f : 1.f / l[e];
                         if (whole) {
                             const int64_t row = (int64_t)p.n * R + group * NR + r;
                             if (a.lse && r < rows && KDA_INDEX_OK(row, (int64_t)a.num_seqs * R, a.status))
@@ -543,28 +575,45 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
             asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kSoft) : "memory");
             if (!(ok = wait(&sw->pv_done[prev.slot], prev.phase))) break;
             tc_fence_after();
-            for (int b = 0; b < 4; ++b)
-                for (int k = 0; k < NR / 16; ++k) {
-                    uint32_t o[16];
-                    tmem_ld16(lanes + b * NR + k * 16, o);
-                    tmem_wait_ld();
-                    const int channel = b * 128 + 32 * w + lane;
+            // column r of block b: row r, channels 128 b ..; a lane stores its channel of 16 rows at a time, so a
+            // warp's store is 64 bytes of a row in bf16, 128 in fp32
+            const int64_t row = whole ? (int64_t)p.n * R + group * NR : (int64_t)slot * NR;
+            const bool inside = whole ? KDA_INDEX_OK(row + rows - 1, (int64_t)a.num_seqs * R, a.status)
+                                      : KDA_INDEX_OK(row + NR - 1, (int64_t)gridDim.x * 2 * NR, a.status);
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * kLatent + 32 * w + lane;
+            float* part = po + row * kLatent + 32 * w + lane;
+#pragma unroll 1
+            for (int k = 0; k < NR / 16; ++k) {
+                uint32_t o[4][16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int r = k * 16 + i;
-                        if (r >= rows) break;
-                        if (whole) {
-                            const int64_t row = (int64_t)p.n * R + group * NR + r;
-                            if (KDA_INDEX_OK(row, (int64_t)a.num_seqs * R, a.status))
-                                static_cast<__nv_bfloat16*>(a.out)[row * kLatent + channel] =
-                                    __float2bfloat16_rn(__uint_as_float(o[i]) * sw->fac[r]);
-                        } else if (KDA_INDEX_OK((int64_t)slot * NR + r, (int64_t)gridDim.x * 2 * NR, a.status)) {
-                            po[((int64_t)slot * NR + r) * kLatent + channel] = __uint_as_float(o[i]);
+                for (int b = 0; b < 4; ++b) tmem_ld16(lanes + b * NR + k * 16, o[b]);
+                tmem_wait_ld();
+                const int live = inside ? rows - 16 * k : 0;
+                if (whole) {
+                    float f[16];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<float4*>(f + 4 * i) = *reinterpret_cast<const float4*>(sw->inv + 16 * k + 4 * i);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (i < live) {
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                out[i * kLatent + b * 128] = __float2bfloat16_rn(__uint_as_float(o[b][i]) * f[i]);
                         }
-                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (i < live) {
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) part[i * kLatent + b * 128] = __uint_as_float(o[b][i]);
+                        }
                 }
+                out += 16 * kLatent;
+                part += 16 * kLatent;
+            }
             tc_fence_before();
-            // everyone has read fac before the next piece writes it
+            // everyone has read inv before the next piece writes it
             asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kSoft) : "memory");
             if (lane == 0) mbar_arrive(&sw->o_free);
             at += p.tiles;
@@ -580,77 +629,136 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
 }
 
 // Joins the pieces of the sequences that several runs share: out = sum_i w_i O_i / sum_i w_i l_i with
-// w_i = 2^{m_i - max m}, the pieces in order.  512 threads: 128 take four channels each, four times over, each
-// set every fourth piece.
-constexpr int kJoinThreads = 512, kMostParts = 1024;
+// w_i = 2^{m_i - max m}, the pieces in order.  A task is a quarter row (a float4 a lane).  Where a sequence has up to
+// 32 pieces a warp takes a task, with eight pieces' loads in flight; where it has more, a block does, its warps each
+// taking every eighth piece.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kFewParts = 32, kMostParts = 256, kMostGrid = kJoinThreads,
+              kJoinBlocks = 5 * kSMs;
 template <int NR>
 __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentDecodeArgs a, const int grid, const int groups) {
-    __shared__ int list_s[256], count_s;
+    __shared__ Head heads_s[kMostGrid];
+    __shared__ int list_s[2][kMostGrid], count_s[2][kJoinWarps];
     __shared__ float w_s[kMostParts], total_s, max_s;
-    __shared__ float4 acc_s[3][128];
-    const int tid = threadIdx.x;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ float4 acc_s[kJoinWarps][32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
-    const Head* heads = reinterpret_cast<const Head*>(ws);
     const float2* ml = reinterpret_cast<const float2*>(ws + Work<NR>::ml_at(grid));
     const float4* po = reinterpret_cast<const float4*>(ws + Work<NR>::o_at(grid));
-    if (tid < 32) {
-        int count = 0;
-        for (int b = 0; b < grid; b += 32) {
-            const bool has = b + tid < grid && heads[b + tid].n >= 0;
-            const uint32_t mask = __ballot_sync(0xffffffffu, has);
-            if (has) list_s[count + __popc(mask & ((1u << tid) - 1))] = b + tid;
-            count += __popc(mask);
-        }
-        if (tid == 0) count_s = count;
-    }
+    const int R = a.tokens_per_seq * a.H;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the sequences to join, of few pieces and of many, each in the order of their blocks: every block of this
+    // kernel makes the same lists
+    const Head mine = tid < grid ? reinterpret_cast<const Head*>(ws)[tid] : Head{-1, 0, 0, 0};
+    const bool few = mine.n >= 0 && mine.parts <= kFewParts, many = mine.n >= 0 && mine.parts > kFewParts;
+    const uint32_t fm = __ballot_sync(0xffffffffu, few), mm = __ballot_sync(0xffffffffu, many);
+    heads_s[tid] = mine;
+    if (lane == 0) { count_s[0][warp] = __popc(fm); count_s[1][warp] = __popc(mm); }
     __syncthreads();
-    const int R = a.tokens_per_seq * a.H, items = count_s * NR;
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const int block = list_s[item / NR], r = item % NR, group = block % groups;
-        if (group * NR + r >= R) continue;    // uniform
-        const Head h = heads[block];
-        const int parts = h.parts < kMostParts ? h.parts : kMostParts;
-        auto slot_of = [&](int i) { return ((int64_t)(block + i * groups) * 2 + (i == 0 ? h.first_slot : 0)) * NR + r; };
-        if (tid < 32) {
-            float mx = -INFINITY;
-            for (int i = tid; i < parts; i += 32) mx = fmaxf(mx, ml[slot_of(i)].x);
-            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            float sum = 0.f;
-            for (int i = tid; i < parts; i += 32) {
-                const float2 x = ml[slot_of(i)];
-                const float w = x.x == -INFINITY ? 0.f : exp2_fast(x.x - mx);
-                w_s[i] = w;
-                sum += w * x.y;
-            }
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (tid == 0) { total_s = sum; max_s = mx; }
+    int at[2] = {0, 0}, count[2] = {0, 0};
+    for (int w = 0; w < kJoinWarps; ++w)
+        for (int k = 0; k < 2; ++k) {
+            if (w < warp) at[k] += count_s[k][w];
+            count[k] += count_s[k][w];
         }
-        __syncthreads();
-        const int set = tid >> 7, c = tid & 127;
+    const uint32_t below = (1u << lane) - 1;
+    if (few) list_s[0][at[0] + __popc(fm & below)] = tid;
+    if (many) list_s[1][at[1] + __popc(mm & below)] = tid;
+    __syncthreads();
+    // task t of a list: the sequence's first block, its row and quarter
+    struct Task {
+        Head h;
+        int block, r, quarter;
+        int64_t row;
+        bool live;
+    };
+    auto task = [&](int kind, int t) {
+        Task x;
+        x.block = list_s[kind][t / (4 * NR)];
+        x.r = (t >> 2) % NR;
+        x.quarter = t & 3;
+        x.h = heads_s[x.block];
+        const int q = (x.block % groups) * NR + x.r;
+        x.row = (int64_t)x.h.n * R + q;
+        x.live = q < R;
+        return x;
+    };
+    auto slot = [&](const Task& x, int i) { return ((int64_t)(x.block + i * groups) * 2 + (i == 0 ? x.h.first_slot : 0)) * NR + x.r; };
+    auto part = [&](const Task& x, int i) { return po[slot(x, i) * (kLatent / 4) + x.quarter * 32 + lane]; };
+    auto store = [&](const Task& x, float4 o, float mx, float total) {
+        if (!KDA_INDEX_OK(x.row, (int64_t)a.num_seqs * R, a.status)) return;
+        const float f = total == 0.f ? 0.f : 1.f / total;
+        uint2 y;
+        y.x = pack_bf16x2(o.x * f, o.y * f);
+        y.y = pack_bf16x2(o.z * f, o.w * f);
+        reinterpret_cast<uint2*>(a.out)[x.row * (kLatent / 4) + x.quarter * 32 + lane] = y;
+        if (a.lse && x.quarter == 0 && lane == 0)
+            a.lse[x.row] = total == 0.f ? -INFINITY : (mx + log2f(total)) * 0.69314718055994530942f;
+    };
+    auto add = [](float4& acc, float w, float4 x) {
+        if (w != 0.f) { acc.x += w * x.x; acc.y += w * x.y; acc.z += w * x.z; acc.w += w * x.w; }
+    };
+    for (int t = blockIdx.x * kJoinWarps + warp; t < count[0] * NR * 4; t += gridDim.x * kJoinWarps) {
+        const Task x = task(0, t);
+        if (!x.live) continue;
+        const float2 y = lane < x.h.parts ? ml[slot(x, lane)] : make_float2(-INFINITY, 0.f);
+        float4 o[8];                          // the first loads go out before the weights are known
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < x.h.parts) o[k] = part(x, k);
+        float mx = y.x;
+        for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const float w = y.x == -INFINITY ? 0.f : exp2_fast(y.x - mx);
+        float total = w * y.y;
+        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int i = set; i < parts; i += 4) {
-            const float w = w_s[i];
-            const float4 x = po[slot_of(i) * (kLatent / 4) + c];
-            if (w != 0.f) { acc.x += w * x.x; acc.y += w * x.y; acc.z += w * x.z; acc.w += w * x.w; }
+        for (int i = 0; i < x.h.parts; i += 8) {
+            if (i > 0) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (i + k < x.h.parts) o[k] = part(x, i + k);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, w, (i + k) & 31);
+                if (i + k < x.h.parts) add(acc, wk, o[k]);
+            }
         }
-        if (set) acc_s[set - 1][c] = acc;
+        store(x, acc, mx, total);
+    }
+    for (int t = blockIdx.x; t < count[1] * NR * 4; t += gridDim.x) {
+        const Task x = task(1, t);
+        if (!x.live) continue;                // uniform
+        const int parts = x.h.parts < kMostParts ? x.h.parts : kMostParts;
+        if (warp == 0) {
+            float mx = -INFINITY;
+            for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, ml[slot(x, i)].x);
+            for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            float sum = 0.f;
+            for (int i = lane; i < parts; i += 32) {
+                const float2 y = ml[slot(x, i)];
+                const float w = y.x == -INFINITY ? 0.f : exp2_fast(y.x - mx);
+                w_s[i] = w;
+                sum += w * y.y;
+            }
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (lane == 0) { total_s = sum; max_s = mx; }
+        }
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = warp; i < parts; i += 8 * kJoinWarps) {
+            float4 o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i + k * kJoinWarps < parts) o[k] = part(x, i + k * kJoinWarps);
+            if (i == warp) __syncthreads();   // the weights; every warp has a piece, as there are more than 32
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i + k * kJoinWarps < parts) add(acc, w_s[i + k * kJoinWarps], o[k]);
+        }
+        acc_s[warp][lane] = acc;
         __syncthreads();
-        if (!set) {
-            for (int i = 0; i < 3; ++i) {
-                const float4 x = acc_s[i][c];
-                acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
-            }
-            const float total = total_s, f = total == 0.f ? 0.f : 1.f / total;
-            const int64_t row = (int64_t)h.n * R + group * NR + r;
-            if (KDA_INDEX_OK(row, (int64_t)a.num_seqs * R, a.status)) {
-                uint2 y;
-                y.x = pack_bf16x2(acc.x * f, acc.y * f);
-                y.y = pack_bf16x2(acc.z * f, acc.w * f);
-                reinterpret_cast<uint2*>(a.out)[row * (kLatent / 4) + c] = y;
-                if (a.lse && c == 0) a.lse[row] = total == 0.f ? -INFINITY : (max_s + log2f(total)) * 0.69314718055994530942f;
-            }
+        if (warp == 0) {
+            for (int k = 1; k < kJoinWarps; ++k) add(acc, 1.f, acc_s[k][lane]);
+            store(x, acc, max_s, total_s);
         }
         __syncthreads();
     }
@@ -714,7 +822,7 @@ cudaError_t launch(const LatentDecodeArgs& a, cudaStream_t s) {
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * kSMs);
+    cfg.gridDim = dim3(kJoinBlocks);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cfg.attrs = &attr;

@@ -64,6 +64,10 @@ struct Maps {
 };
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_parked(bar, parity, kWaitNs); }
+// The same for a converged warp whose next steps the compiler should know to be uniform.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_parked(bar, parity, kWaitNs));
+}
 
 // Two fp32 in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -210,39 +214,42 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
         __syncwarp();
     } else if (warp == 9) {                   // ------------------------------------------------ issuer
         constexpr uint32_t id_s = idesc_bf16_f32(kM, kN, false, false), id_o = idesc_bf16_f32(kM, kHead, false, true);
-        const uint32_t sq = smem_u32(sm + G::kQ), sk = smem_u32(sm + G::kK), sv = smem_u32(sm + G::kV);
+        const uint64_t dq = smem_desc(smem_u32(sm + G::kQ), 16, 1024, kSwizzle128B);
+        const uint64_t dk = smem_desc(smem_u32(sm + G::kK), 16, 1024, kSwizzle128B);
+        const uint64_t dv = smem_desc(smem_u32(sm + G::kV), 16384, 1024, kSwizzle128B);
+        const uint32_t el = elect_one();
+        uint32_t k_slot[2] = {0, 0}, k_phase[2] = {0, 0};            // the ring of key slices, as each tile walks it
         // S_X of key tile j
         auto scores = [&](int X, int j) {
             const bool first = X == 0 || j >= tiles[0], last = X == 1 || j >= tiles[1];
-            if (j == 0 && !(ok = wait(&sw->q_full[X], 0))) return;
-            for (uint32_t s = 0; s < G::kSlices; ++s) {
-                const uint32_t at = j * G::kSlices + s, slot = at % G::kKSlots;
-                if (first && !(ok = wait(&sw->k_full[slot], (at / G::kKSlots) & 1))) return;
-                tc_fence_after();
-                if (elect_one()) {
+            if (j == 0 && !(ok = wait_warp(&sw->q_full[X], 0))) return;
+            const uint64_t x = desc_at(dq, X * G::kSlices * 16384);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma_ss(tb + X * 128, smem_desc(sq + (X * G::kSlices + s) * 16384 + i * 32, 16, 1024, kSwizzle128B),
-                               smem_desc(sk + slot * 16384 + i * 32, 16, 1024, kSwizzle128B), id_s, s > 0 || i > 0);
-                    if (last) mma_commit(&sw->k_empty[slot]);
-                }
+            for (uint32_t s = 0; s < G::kSlices; ++s) {
+                const uint32_t slot = k_slot[X];
+                if (first && !(ok = wait_warp(&sw->k_full[slot], k_phase[X]))) return;
+                tc_fence_after();
+                const uint64_t y = desc_at(dk, slot * 16384);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mma_ss_elected(tb + X * 128, desc_at(x, s * 16384 + i * 32), desc_at(y, i * 32), id_s, s > 0 || i > 0, el);
+                if (last) mma_commit_elected(&sw->k_empty[slot], el);
+                if (++k_slot[X] == G::kKSlots) { k_slot[X] = 0; k_phase[X] ^= 1u; }
             }
-            if (elect_one()) mma_commit(&sw->s_full[X]);
+            mma_commit_elected(&sw->s_full[X], el);
         };
         // O_X += P_X V of key tile j
         auto values = [&](int X, int j) {
             const bool last = X == 1 || j >= tiles[1];
-            if (!(ok = wait(&sw->v_full[j & 1], (j >> 1) & 1))) return;
-            if (!(ok = wait(&sw->p_full[X], j & 1))) return;
+            if (!(ok = wait_warp(&sw->v_full[j & 1], (j >> 1) & 1))) return;
+            if (!(ok = wait_warp(&sw->p_full[X], j & 1))) return;
             tc_fence_after();
-            if (elect_one()) {
+            const uint64_t y = desc_at(dv, (j & 1) * 32768);
 #pragma unroll
-                for (int i = 0; i < kN / 16; ++i)
-                    mma_ts(tb + 256 + X * 128, tb + X * 128 + i * 8,
-                           smem_desc(sv + (j & 1) * 32768 + i * 2048, 16384, 1024, kSwizzle128B), id_o, j > 0 || i > 0);
-                if (last) mma_commit(&sw->v_empty[j & 1]);
-                if (j + 1 == tiles[X]) mma_commit(&sw->o_done[X]);
-            }
+            for (int i = 0; i < kN / 16; ++i)
+                mma_ts_elected(tb + 256 + X * 128, tb + X * 128 + i * 8, desc_at(y, i * 2048), id_o, j > 0 || i > 0, el);
+            if (last) mma_commit_elected(&sw->v_empty[j & 1], el);
+            if (j + 1 == tiles[X]) mma_commit_elected(&sw->o_done[X], el);
         };
         if (tiles[0]) scores(0, 0);
         if (ok && tiles[1]) scores(1, 0);
@@ -252,8 +259,8 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
                 if (ok && j + 1 < tiles[X]) scores(X, j + 1);
             }
         if (!ok) {                            // products in flight land before TMEM is freed
-            if (elect_one()) mma_commit(&sw->drain);
-            wait(&sw->drain, 0);
+            mma_commit_elected(&sw->drain, el);
+            wait_warp(&sw->drain, 0);
             if (lane == 0) atomicOr(a.status, kStatusTimeout);
         }
     } else {                                  // ------------------------------------------------ softmax of tile X

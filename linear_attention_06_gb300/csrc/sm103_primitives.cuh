@@ -230,14 +230,47 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, b
            | ((uint32_t)(M >> 4) << 24);   // M / 16
 }
 
-// One lane of a converged warp (the same one every time).  Products are issued under this rather than under
-// a thread-index test: the compiler then knows that their operands are warp-uniform and keeps the descriptors
-// in uniform registers.  Measured, M = 64, N = 64 products in a row: 37 cycles each, against 75 behind a
-// thread-index test.
-__device__ __forceinline__ bool elect_one() {
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ uint32_t elect_one() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
+    return r;
+}
+// A descriptor moved by a constant number of bytes (inside the 256 KB that its address field spans).
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) {
+    return (d & 0xFFFFFFFF00000000ull) | (uint32_t)((uint32_t)d + (bytes >> 4));
+}
+// The products and commits below are executed by a whole converged warp and predicated on `elected`
+// (elect_one's answer).  Without a branch, and with descriptors that are one sum away from a base, their
+// operands stay in uniform registers: M = 64, N = 64 products issue every 35 cycles, which is their rate,
+// against 52 under a branch with descriptors built in place and 75 behind a thread-index test.
+__device__ __forceinline__ void mma_ss_elected(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate, uint32_t elected) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_elected(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate, uint32_t elected) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_elected(uint64_t* bar, uint32_t elected) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(elected)
+        : "memory");
 }
 
 // D[tmem] (+)= A[smem desc] * B[smem desc]
