@@ -54,7 +54,7 @@ struct Cfg {
 };
 
 struct Small {
-    uint64_t q_full[2], k_full[6], k_empty[6], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], drain;
+    uint64_t q_full[2], k_full[6], k_empty[6], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], o_done[2], drain;
     uint32_t tmem;
 };
 static_assert(sizeof(Small) <= 1024, "small area");
@@ -69,6 +69,11 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_parked(bar, parity, kWaitNs));
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 // Two fp32 in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -147,6 +152,7 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
             mbar_init(&sw->v_full[i], 1);
             mbar_init(&sw->v_empty[i], 1);
             mbar_init(&sw->s_full[i], 1);
+            mbar_init(&sw->p_half[i], 4);
             mbar_init(&sw->p_full[i], 4);
             mbar_init(&sw->o_done[i], 1);
         }
@@ -192,14 +198,15 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
             load_q(0);
             if (most > 0) load_k(0);
             load_q(1);
+            // values before the next keys: their stage is free long before those keys' slices
             for (int j = 0; ok && j < most; ++j) {
-                if (j + 1 < most) load_k(j + 1);
-                if (!ok || (j > 1 && !(ok = wait(&sw->v_empty[j & 1], ((j >> 1) - 1) & 1)))) break;
+                if ((j > 1 && !(ok = wait(&sw->v_empty[j & 1], ((j >> 1) - 1) & 1)))) break;
                 mbar_arrive_expect_tx(&sw->v_full[j & 1], 32768);
                 for (int s = 0; s < 2; ++s)
                     tma_load_3d(sm + G::kV + (j & 1) * 32768 + s * 16384, &maps.v, s * 64, x.h, (int)x.kb + j * kN,
                                 &sw->v_full[j & 1]);
                 ++v_loads;
+                if (j + 1 < most) load_k(j + 1);
             }
             if (!ok) {                        // copies in flight land before the block ends
                 for (uint32_t i = 0; i < G::kKSlots; ++i)
@@ -242,12 +249,15 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
         auto values = [&](int X, int j) {
             const bool last = X == 1 || j >= tiles[1];
             if (!(ok = wait_warp(&sw->v_full[j & 1], (j >> 1) & 1))) return;
-            if (!(ok = wait_warp(&sw->p_full[X], j & 1))) return;
-            tc_fence_after();
             const uint64_t y = desc_at(dv, (j & 1) * 32768);
 #pragma unroll
-            for (int i = 0; i < kN / 16; ++i)
-                mma_ts_elected(tb + 256 + X * 128, tb + X * 128 + i * 8, desc_at(y, i * 2048), id_o, j > 0 || i > 0, el);
+            for (int half = 0; half < 2; ++half) {
+                if (!(ok = wait_warp(half ? &sw->p_full[X] : &sw->p_half[X], j & 1))) return;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 4 * half; i < 4 * half + 4; ++i)
+                    mma_ts_elected(tb + 256 + X * 128, tb + X * 128 + i * 8, desc_at(y, i * 2048), id_o, j > 0 || i > 0, el);
+            }
             if (last) mma_commit_elected(&sw->v_empty[j & 1], el);
             if (j + 1 == tiles[X]) mma_commit_elected(&sw->o_done[X], el);
         };
@@ -285,9 +295,16 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
                 for (int k = 0; k < kN; ++k)
                     if (k >= edge) s[k >> 5][k & 31] = 0xff800000u;  // -inf
             }
-            float mx = __uint_as_float(s[0][0]);
+            float part[4];                    // four chains of three-way maxima
 #pragma unroll
-            for (int k = 1; k < kN; ++k) mx = fmaxf(mx, __uint_as_float(s[k >> 5][k & 31]));
+            for (int b = 0; b < 4; ++b) {
+                part[b] = max3(__uint_as_float(s[b][0]), __uint_as_float(s[b][1]), __uint_as_float(s[b][2]));
+#pragma unroll
+                for (int k = 3; k < 31; k += 2)
+                    part[b] = max3(part[b], __uint_as_float(s[b][k]), __uint_as_float(s[b][k + 1]));
+                part[b] = fmaxf(part[b], __uint_as_float(s[b][31]));
+            }
+            const float mx = fmaxf(max3(part[0], part[1], part[2]), part[3]);
             float f = 1.f;
             if (mx > m && (mx - m) * c2 > kRaise) {                  // also the first finite maximum
                 f = exp2_fast((m - mx) * c2);
@@ -305,6 +322,14 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
                     tmem_st32(to + 32 * b, o);
                 }
             }
+            if ((int64_t)(j + 1) * kN > x.nk) {                      // value rows behind the sequence's end become zeros
+                if (!(ok = wait(&sw->v_full[j & 1], (j >> 1) & 1))) break;
+                if (j * kN + t >= x.nk)
+                    for (int k = 0; k < 16; ++k)
+                        *reinterpret_cast<uint4*>(sm + G::kV + (j & 1) * 32768 + (k >> 3) * 16384 + t * 128 + (k & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
             const float z = m == -INFINITY ? 0.f : -m * c2;
             const float2 c22 = make_float2(c2, c2), z2 = make_float2(z, z);
             float2 sum = make_float2(0.f, 0.f);
@@ -320,20 +345,14 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
                     p[k] = pack_bf16x2(y.x, y.y);
                 }
                 tmem_st16(ts + 16 * b, p);
+                if (b & 1) {                  // half of the weights: the value product can begin
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b == 1 ? &sw->p_half[X] : &sw->p_full[X]);
+                }
             }
             l += sum.x + sum.y;
-            if ((int64_t)(j + 1) * kN > x.nk) {                      // value rows behind the sequence's end become zeros
-                if (!(ok = wait(&sw->v_full[j & 1], (j >> 1) & 1))) break;
-                if (j * kN + t >= x.nk)
-                    for (int k = 0; k < 16; ++k)
-                        *reinterpret_cast<uint4*>(sm + G::kV + (j & 1) * 32768 + (k >> 3) * 16384 + t * 128 + (k & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sw->p_full[X]);
         }
         if (ok && count && !(ok = wait(&sw->o_done[X], 0))) {}
         if (ok) {                             // a thread stores its query's row
