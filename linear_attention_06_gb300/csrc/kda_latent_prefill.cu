@@ -25,6 +25,7 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "kda_internal.h"
 #include "kda_latent_common.cuh"
@@ -225,31 +226,38 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
         const uint64_t dk = smem_desc(smem_u32(sm + G::kK), 16, 1024, kSwizzle128B);
         const uint64_t dv = smem_desc(smem_u32(sm + G::kV), 16384, 1024, kSwizzle128B);
         const uint32_t el = elect_one();
-        uint32_t k_slot[2] = {0, 0}, k_phase[2] = {0, 0};            // the ring of key slices, as each tile walks it
+        const int ta = tiles[0], tc = tiles[1];
+        // the ring of key slices, as each query tile walks it
+        struct Ring {
+            uint32_t slot, phase;
+        };
+        Ring ra{0, 0}, rb{0, 0};
         // S_X of key tile j
-        auto scores = [&](int X, int j) {
-            const bool first = X == 0 || j >= tiles[0], last = X == 1 || j >= tiles[1];
+        auto scores = [&](auto which, Ring& ring, int j) {
+            constexpr int X = decltype(which)::value;
+            const bool first = X == 0 || j >= ta, last = X == 1 || j >= tc;
             if (j == 0 && !(ok = wait_warp(&sw->q_full[X], 0))) return;
-            const uint64_t x = desc_at(dq, X * G::kSlices * 16384);
 #pragma unroll
             for (uint32_t s = 0; s < G::kSlices; ++s) {
-                const uint32_t slot = k_slot[X];
-                if (first && !(ok = wait_warp(&sw->k_full[slot], k_phase[X]))) return;
+                const uint32_t slot = ring.slot;
+                if (first && !(ok = wait_warp(&sw->k_full[slot], ring.phase))) return;
                 tc_fence_after();
                 const uint64_t y = desc_at(dk, slot * 16384);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    mma_ss_elected(tb + X * 128, desc_at(x, s * 16384 + i * 32), desc_at(y, i * 32), id_s, s > 0 || i > 0, el);
+                    mma_ss_elected(tb + X * 128, desc_at(dq, (X * G::kSlices + s) * 16384 + i * 32), desc_at(y, i * 32), id_s,
+                                   s > 0 || i > 0, el);
                 if (last) mma_commit_elected(&sw->k_empty[slot], el);
-                if (++k_slot[X] == G::kKSlots) { k_slot[X] = 0; k_phase[X] ^= 1u; }
+                if (++ring.slot == G::kKSlots) { ring.slot = 0; ring.phase ^= 1u; }
             }
             mma_commit_elected(&sw->s_full[X], el);
         };
         // O_X += P_X V of key tile j
-        auto values = [&](int X, int j) {
-            const bool last = X == 1 || j >= tiles[1];
-            if (!(ok = wait_warp(&sw->v_full[j & 1], (j >> 1) & 1))) return;
+        auto values = [&](auto which, int j) {
+            constexpr int X = decltype(which)::value;
+            const bool first = X == 0 || j >= ta, last = X == 1 || j >= tc;
             const uint64_t y = desc_at(dv, (j & 1) * 32768);
+            if (first && !(ok = wait_warp(&sw->v_full[j & 1], (j >> 1) & 1))) return;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 if (!(ok = wait_warp(half ? &sw->p_full[X] : &sw->p_half[X], j & 1))) return;
@@ -259,15 +267,22 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
                     mma_ts_elected(tb + 256 + X * 128, tb + X * 128 + i * 8, desc_at(y, i * 2048), id_o, j > 0 || i > 0, el);
             }
             if (last) mma_commit_elected(&sw->v_empty[j & 1], el);
-            if (j + 1 == tiles[X]) mma_commit_elected(&sw->o_done[X], el);
+            if (j + 1 == (X ? tc : ta)) mma_commit_elected(&sw->o_done[X], el);
         };
-        if (tiles[0]) scores(0, 0);
-        if (ok && tiles[1]) scores(1, 0);
-        for (int j = 0; ok && j < most; ++j)
-            for (int X = 0; ok && X < 2; ++X) {
-                if (j < tiles[X]) values(X, j);
-                if (ok && j + 1 < tiles[X]) scores(X, j + 1);
+        constexpr std::integral_constant<int, 0> A{};
+        constexpr std::integral_constant<int, 1> B{};
+        if (ta) scores(A, ra, 0);
+        if (ok && tc) scores(B, rb, 0);
+        for (int j = 0; ok && j < most; ++j) {
+            if (j < ta) {
+                values(A, j);
+                if (ok && j + 1 < ta) scores(A, ra, j + 1);
             }
+            if (ok && j < tc) {
+                values(B, j);
+                if (ok && j + 1 < tc) scores(B, rb, j + 1);
+            }
+        }
         if (!ok) {                            // products in flight land before TMEM is freed
             mma_commit_elected(&sw->drain, el);
             wait_warp(&sw->drain, 0);
