@@ -76,7 +76,7 @@ struct Small {
     uint64_t s_full[2], p_full[2], pv_done[2];
     uint64_t o_free, drain;
     uint32_t tmem;
-    int seq0, off0, runs;
+    int seq0, off0, lead0, len0, runs;
     int64_t total, begin, end;
     alignas(16) float fac[64];                // rescaling factors
     alignas(16) float inv[64];                // 1 / l at a piece's end
@@ -97,23 +97,29 @@ struct Piece {                                // a run's share of one sequence
 };
 
 __device__ __forceinline__ int tiles_of(int len) { return len > kTile ? (len + kTile - 1) / kTile : 1; }
+// A sequence's places in the line: its tiles, behind kStart places that stand for what starting a piece costs a
+// block (queries in, O out), so that runs with many pieces get fewer tiles.
+constexpr int kStart = 1;
 
 // Walks the sequences of a run; every role walks by itself.
 struct Walk {
-    int n, off;
+    int n, off, lead, len;                    // next sequence, its first tile here, start places before it
     int64_t left;
-    __device__ Walk(const Small* sw) : n(sw->seq0), off(sw->off0), left(sw->end - sw->begin) {}
+    __device__ Walk(const Small* sw) : n(sw->seq0), off(sw->off0), lead(sw->lead0), len(sw->len0), left(sw->end - sw->begin) {}
     __device__ __forceinline__ bool next(const LatentDecodeArgs& a, Piece& p) {
         if (left <= 0) return false;
         p.n = n;
-        p.len = clamped_len(a.c, a.seq_lens, n);
+        p.len = len >= 0 ? len : clamped_len(a.c, a.seq_lens, n);
+        len = -1;
         p.all = tiles_of(p.len);
         p.off = off;
-        p.tiles = (int64_t)(p.all - off) < left ? p.all - off : (int)left;
-        left -= p.tiles;
+        const int64_t behind = left - lead;   // places of the run behind the sequence's start places
+        p.tiles = behind < p.all - off ? (behind > 0 ? (int)behind : 0) : p.all - off;
+        left = behind - p.tiles;
+        lead = kStart;
         off = 0;
         ++n;
-        return true;
+        return p.tiles > 0;                   // a run may end inside the start places
     }
 };
 
@@ -123,8 +129,11 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_parked(bar, parity, kWaitNs));
 }
 
-// The first tile of run p of `runs` over `total` tiles, and the run that holds tile x.
-__host__ __device__ __forceinline__ int64_t run_begin(int64_t total, int runs, int p) { return total * p / runs; }
+// The first tile of run p of `runs` over `total` tiles (a 32-bit division where it fits, a fifth of the time), and
+// the run that holds tile x.
+__device__ __forceinline__ int64_t run_begin(int64_t total, int runs, int p) {
+    return total < (1 << 23) ? (int64_t)((uint32_t)total * (uint32_t)p / (uint32_t)runs) : total * p / runs;
+}
 __device__ __forceinline__ int run_of(int64_t total, int runs, int64_t x) { return (int)(((x + 1) * runs - 1) / total); }
 
 // Workspace: a header a block (the sequence whose first piece it holds), then per (block, 0 or 1) and row the
@@ -149,7 +158,12 @@ struct Maps {
 // kThreads sequences the lengths are read once.
 __device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Small* sw, int* scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    auto tiles_at = [&](int n) { return n < a.num_seqs ? tiles_of(clamped_len(a.c, a.seq_lens, n)) : 0; };
+    int len = 0;
+    auto tiles_at = [&](int n) {
+        if (n >= a.num_seqs) return 0;
+        len = clamped_len(a.c, a.seq_lens, n);
+        return kStart + tiles_of(len);
+    };
     // the round's tiles before this thread's sequence, and in all (a round has at most 2^31 / 64 * 256 / ... tiles of
     // a cache that fits the card: well inside 32 bits)
     auto scan = [&](int mine, int& round) {
@@ -169,6 +183,7 @@ __device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Small* sw, 
         return x - mine;
     };
     int mine = tiles_at(tid), round, at = scan(mine, round);
+    int mine_len = len;
     int64_t total = round;
     for (int n0 = kThreads; n0 < a.num_seqs; n0 += kThreads) {
         int more;
@@ -189,12 +204,16 @@ __device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Small* sw, 
         const int64_t first = before + at;
         if (mine > 0 && first <= begin && begin < first + mine) {
             sw->seq0 = n0 + tid;
-            sw->off0 = (int)(begin - first);
+            const int into = (int)(begin - first);
+            sw->off0 = into > kStart ? into - kStart : 0;
+            sw->lead0 = into < kStart ? kStart - into : 0;
+            sw->len0 = mine_len;
         }
         before += round;
         n0 += kThreads;
         if (before > begin || n0 >= a.num_seqs) break;               // uniform
         mine = tiles_at(n0 + tid);
+        mine_len = len;
         at = scan(mine, round);
     }
 }
@@ -263,7 +282,8 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                 const int page = a.c.block_table[table + (pos >> shift)];
                 return page < 0 || page >= a.c.num_pages ? map_rows : (page << shift) + (pos & (a.c.page_size - 1));
             };
-            // a page's rows lie in a row: one prefetch into L2 for each box, kAhead tiles before its loads
+            // a page's rows lie in a row: one prefetch into L2 for each box, kAhead tiles before its loads.  The
+            // first tiles of a piece are only loaded: their ring slots are free
             auto prefetch = [&](int r, int x) {
                 const int left = p.len - x * kTile - piece * box;
                 if (half == 0 && r >= 0 && r < map_rows)
@@ -272,10 +292,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
             };
             int rows_ahead[kAhead + 1];       // rows of tiles j .. j + kAhead
 #pragma unroll
-            for (int d = 0; d < kAhead; ++d) {
-                rows_ahead[d] = d < p.tiles ? row_of(p.off + d) : -1;
-                if (d > 0 && d < p.tiles) prefetch(rows_ahead[d], p.off + d);
-            }
+            for (int d = 0; d < kAhead; ++d) rows_ahead[d] = d < p.tiles ? row_of(p.off + d) : -1;
             for (int j = 0; ok && j < p.tiles; ++j) {
                 rows_ahead[kAhead] = j + kAhead < p.tiles ? row_of(p.off + j + kAhead) : -1;
                 const int row = rows_ahead[0];
@@ -423,7 +440,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
         Ring<2> sb, prev;                     // this tile's buffers; the previous tile's
         bool first_piece = true, used0 = false, used1 = false;
         Head head{-1, 0, 0, 0};
-        int64_t at = sw->begin;               // the piece's first tile in the line
+        int64_t at = sw->begin + sw->lead0;   // the piece's first tile in the line
         while (ok && walk.next(a, p)) {
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
             int seen[2];
@@ -616,7 +633,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
             // everyone has read inv before the next piece writes it
             asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kSoft) : "memory");
             if (lane == 0) mbar_arrive(&sw->o_free);
-            at += p.tiles;
+            at += p.tiles + kStart;
             first_piece = false;
         }
         if (t == 0) reinterpret_cast<Head*>(a.workspace)[blockIdx.x] = head;
@@ -633,7 +650,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
 // 32 pieces a warp takes a task, with eight pieces' loads in flight; where it has more, a block does, its warps each
 // taking every eighth piece.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kFewParts = 32, kMostParts = 256, kMostGrid = kJoinThreads,
-              kJoinBlocks = 5 * kSMs;
+              kJoinBlocks = 5 * kSMs, kBatch = 8;
 template <int NR>
 __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentDecodeArgs a, const int grid, const int groups) {
     __shared__ Head heads_s[kMostGrid];
@@ -730,28 +747,33 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentD
         if (!x.live) continue;                // uniform
         const int parts = x.h.parts < kMostParts ? x.h.parts : kMostParts;
         if (warp == 0) {
+            float2 y[kMostParts / 32];
             float mx = -INFINITY;
-            for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, ml[slot(x, i)].x);
+#pragma unroll
+            for (int k = 0; k < kMostParts / 32; ++k)
+                y[k] = lane + 32 * k < parts ? ml[slot(x, lane + 32 * k)] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int k = 0; k < kMostParts / 32; ++k) mx = fmaxf(mx, y[k].x);
             for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
             float sum = 0.f;
-            for (int i = lane; i < parts; i += 32) {
-                const float2 y = ml[slot(x, i)];
-                const float w = y.x == -INFINITY ? 0.f : exp2_fast(y.x - mx);
-                w_s[i] = w;
-                sum += w * y.y;
+#pragma unroll
+            for (int k = 0; k < kMostParts / 32; ++k) {
+                const float w = y[k].x == -INFINITY ? 0.f : exp2_fast(y[k].x - mx);
+                w_s[lane + 32 * k] = w;
+                sum += w * y[k].y;
             }
             for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             if (lane == 0) { total_s = sum; max_s = mx; }
         }
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = warp; i < parts; i += 8 * kJoinWarps) {
-            float4 o[8];
+        for (int i = warp; i < parts; i += kBatch * kJoinWarps) {
+            float4 o[kBatch];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < kBatch; ++k)
                 if (i + k * kJoinWarps < parts) o[k] = part(x, i + k * kJoinWarps);
             if (i == warp) __syncthreads();   // the weights; every warp has a piece, as there are more than 32
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < kBatch; ++k)
                 if (i + k * kJoinWarps < parts) add(acc, w_s[i + k * kJoinWarps], o[k]);
         }
         acc_s[warp][lane] = acc;
