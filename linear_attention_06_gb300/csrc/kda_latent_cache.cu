@@ -6,8 +6,10 @@
 // few tokens, the launch and two dependent loads: the sequence's bounds, then the page).
 //
 // The angle of pair i is p * f_i.  In fp32 the product of a position near 10^6 and f_0 = 1 is off by
-// 0.03 rad, so the turns p * f_i / 2 pi are formed and reduced to [-1/2, 1/2] in fp64 (32 values a
-// token, shared by all heads); sine and cosine of the fp32 remainder are then good to about 2^-22.
+// 0.03 rad.  So f_i / 2 pi is taken in fp64, once a block, as a fraction of a turn in 64-bit fixed point, and
+// p times it modulo 2^64 is the reduced angle: exact but for the fraction's own 53 bits (2^-25 turns at p = 2^31).
+// Sine and cosine of the fp32 remainder are then good to about 2^-22.  (An fp64 product and reduction for every
+// token and pair took 3.5 us of 8000 tokens on this card, whose fp64 rate is a few operations a cycle and SM.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -28,12 +30,18 @@ struct Turn {
 
 // Eight pairs of one 64-channel row: the two 16-byte chunks that unit u (0..3) of the row owns, i.e.
 // channels 8u.. and 8u + 32.. (pairs i, i + 32), or 16u..16u + 15 (interleaved pairs).
+struct Unit {
+    uint4 x0, x1;
+};
 template <bool INTERLEAVED>
-__device__ __forceinline__ void rotate_unit(const __nv_bfloat16* src, __nv_bfloat16* dst, int u, const Turn* turn) {
-    const int first = INTERLEAVED ? 2 * u : u, second = INTERLEAVED ? 2 * u + 1 : u + 4;
-    const uint4 x0 = reinterpret_cast<const uint4*>(src)[first], x1 = reinterpret_cast<const uint4*>(src)[second];
-    const __nv_bfloat162* a = reinterpret_cast<const __nv_bfloat162*>(&x0);
-    const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&x1);
+__device__ __forceinline__ Unit load_unit(const __nv_bfloat16* src, int u) {
+    const uint4* p = reinterpret_cast<const uint4*>(src);
+    return {p[INTERLEAVED ? 2 * u : u], p[INTERLEAVED ? 2 * u + 1 : u + 4]};
+}
+template <bool INTERLEAVED>
+__device__ __forceinline__ void rotate_unit(const Unit& x, __nv_bfloat16* dst, int u, const Turn* turn) {
+    const __nv_bfloat162* a = reinterpret_cast<const __nv_bfloat162*>(&x.x0);
+    const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&x.x1);
     uint4 y0, y1;
     __nv_bfloat162* ya = reinterpret_cast<__nv_bfloat162*>(&y0);
     __nv_bfloat162* yb = reinterpret_cast<__nv_bfloat162*>(&y1);
@@ -50,69 +58,110 @@ __device__ __forceinline__ void rotate_unit(const __nv_bfloat16* src, __nv_bfloa
             yb[k] = __floats2bfloat162_rn(fa.x * t.s + fb.x * t.c, fa.y * v.s + fb.y * v.c);
         }
     }
-    reinterpret_cast<uint4*>(dst)[first] = y0;
-    reinterpret_cast<uint4*>(dst)[second] = y1;
+    reinterpret_cast<uint4*>(dst)[INTERLEAVED ? 2 * u : u] = y0;
+    reinterpret_cast<uint4*>(dst)[INTERLEAVED ? 2 * u + 1 : u + 4] = y1;
 }
 
-// TOK tokens a block.
+// find_seq by a whole warp: 32 offsets a step instead of one, since each step waits for memory.
+__device__ __forceinline__ int find_seq_warp(const int32_t* cu, int num_seqs, int64_t total, int64_t t, int64_t& b,
+                                             int64_t& e) {
+    if (!cu) return find_seq(cu, num_seqs, total, t, b, e);
+    const int lane = threadIdx.x & 31;
+    int lo = 0, count = num_seqs;               // the last n in [lo, lo + count) with cu[n] <= t
+    while (count > 1) {
+        const int step = (count + 31) / 32, at = lane * step;
+        const uint32_t mask = __ballot_sync(0xffffffffu, at < count && (lane == 0 || (int64_t)cu[lo + at] <= t));
+        const int skip = (31 - __clz(mask)) * step;
+        lo += skip;
+        count = count - skip < step ? count - skip : step;
+    }
+    bounds(cu, lo, num_seqs, total, b, e);
+    return t >= b && t < e ? lo : -1;
+}
+
+// TOK tokens a block.  The rows to copy and to rotate are requested before anything else: they arrive while the
+// block finds its tokens' sequences, pages and angles.  A thread's first kQ units of queries take part in that;
+// queries of more heads follow in a loop.
 template <int TOK, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) append_kernel(const LatentAppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(const LatentAppendArgs a) {
+    constexpr int kChunks = kLatent / 8, kLat = (TOK * kChunks + kThreads - 1) / kThreads, kQ = 4;
     __shared__ int64_t row_s[TOK], pos_s[TOK];
     __shared__ int live_s[TOK];
     __shared__ Turn turn_s[TOK][kRope / 2];
-    const int tid = threadIdx.x;
+    __shared__ uint64_t step_s[kRope / 2];      // a position's share of a turn, in 2^-64
+    const int tid = threadIdx.x, lane = tid & 31;
     const int64_t t0 = (int64_t)blockIdx.x * TOK;
     const int count = (int)(a.total_tokens - t0 < TOK ? a.total_tokens - t0 : TOK);
     const int width = kLatent + a.c.rope_dim;
-    const int64_t cache_rows = (int64_t)a.c.num_pages * a.c.page_size;
-    if (tid < count) {
+    const __nv_bfloat16* latent = static_cast<const __nv_bfloat16*>(a.latent);
+    const __nv_bfloat16* k_rope = static_cast<const __nv_bfloat16*>(a.k_rope);
+    const __nv_bfloat16* q_rope = static_cast<const __nv_bfloat16*>(a.q_rope);
+    const int units = q_rope ? 4 * a.H : 0;
+    uint4 lat[kLat];
+    Unit key{}, q[kQ];
+#pragma unroll
+    for (int k = 0; k < kLat; ++k) {
+        const int i = tid + k * kThreads;
+        if (i < count * kChunks)
+            lat[k] = reinterpret_cast<const uint4*>(latent + (t0 + i / kChunks) * a.latent_stride)[i % kChunks];
+    }
+    if (k_rope && tid < count * 4) key = load_unit<INTERLEAVED>(k_rope + (t0 + (tid >> 2)) * a.k_rope_stride, tid & 3);
+#pragma unroll
+    for (int k = 0; k < kQ; ++k) {
+        const int i = tid + k * kThreads;
+        if (i < count * units) q[k] = load_unit<INTERLEAVED>(q_rope + (t0 * a.H + (i >> 2)) * a.q_stride, i & 3);
+    }
+    if (a.inv_freq && tid >= kThreads - kRope / 2) {
+        const int k = tid - (kThreads - kRope / 2);
+        const double turn = (double)a.inv_freq[k] * 0.15915494309189533577;                   // / 2 pi
+        step_s[k] = (uint64_t)((turn - floor(turn)) * 18446744073709551616.0);                // * 2^64
+    }
+    for (int j = tid >> 5; j < count; j += kThreads / 32) {
         int64_t b, e;
-        const int n = find_seq(a.cu_seqlens, a.num_seqs, a.total_tokens, t0 + tid, b, e);
-        const int64_t p = n < 0 ? 0 : (int64_t)clamped_len(a.c, a.seq_lens, n) - (e - (t0 + tid));
-        live_s[tid] = n >= 0;
-        pos_s[tid] = p;
-        row_s[tid] = n < 0 ? -1 : cache_row(a.c, n, p);
+        const int n = find_seq_warp(a.cu_seqlens, a.num_seqs, a.total_tokens, t0 + j, b, e);
+        if (lane == 0) {
+            const int64_t p = n < 0 ? 0 : (int64_t)clamped_len(a.c, a.seq_lens, n) - (e - (t0 + j));
+            live_s[j] = n >= 0;
+            pos_s[j] = p;
+            int64_t row = n < 0 ? -1 : cache_row(a.c, n, p);
+            if (row >= 0 && !KDA_INDEX_OK(row, (int64_t)a.c.num_pages * a.c.page_size, a.status)) row = -1;
+            row_s[j] = row;
+        }
     }
     __syncthreads();
-    if (a.inv_freq) {
+    if (a.c.rope_dim) {
         for (int i = tid; i < count * (kRope / 2); i += kThreads) {
             const int j = i / (kRope / 2), k = i % (kRope / 2);
-            const double turns = (double)pos_s[j] * ((double)a.inv_freq[k] * 0.15915494309189533577);  // 1 / 2 pi
-            const float x = (float)(turns - rint(turns));
-            Turn t;
-            sincospif(2.f * x, &t.s, &t.c);
+            Turn t{1.f, 0.f};
+            if (a.inv_freq) {
+                const uint64_t angle = (uint64_t)pos_s[j] * step_s[k];
+                sincospif((float)(int32_t)(angle >> 32) * 0x1p-31f, &t.s, &t.c);              // half turns in [-1, 1]
+            }
             turn_s[j][k] = t;
         }
-    } else {
-        for (int i = tid; i < count * (kRope / 2); i += kThreads)
-            turn_s[i / (kRope / 2)][i % (kRope / 2)] = Turn{1.f, 0.f};
+        __syncthreads();
     }
     __nv_bfloat16* cache = static_cast<__nv_bfloat16*>(a.c.cache);
-    constexpr int kChunks = kLatent / 8;
-    for (int i = tid; i < count * kChunks; i += kThreads) {
-        const int j = i / kChunks, k = i % kChunks;
-        if (row_s[j] < 0 || !KDA_INDEX_OK(row_s[j], cache_rows, a.status)) continue;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.latent) + (t0 + j) * a.latent_stride;
-        reinterpret_cast<uint4*>(cache + row_s[j] * width)[k] = reinterpret_cast<const uint4*>(src)[k];
+#pragma unroll
+    for (int k = 0; k < kLat; ++k) {
+        const int i = tid + k * kThreads, j = i / kChunks;
+        if (i < count * kChunks && row_s[j] >= 0) reinterpret_cast<uint4*>(cache + row_s[j] * width)[i % kChunks] = lat[k];
     }
-    if (!a.c.rope_dim) return;
-    __syncthreads();
-    for (int i = tid; i < count * 4; i += kThreads) {
-        const int j = i >> 2, u = i & 3;
-        if (row_s[j] < 0 || !KDA_INDEX_OK(row_s[j], cache_rows, a.status)) continue;
-        rotate_unit<INTERLEAVED>(static_cast<const __nv_bfloat16*>(a.k_rope) + (t0 + j) * a.k_rope_stride,
-                                 cache + row_s[j] * width + kLatent, u, turn_s[j]);
+    if (k_rope && tid < count * 4 && row_s[tid >> 2] >= 0)
+        rotate_unit<INTERLEAVED>(key, cache + row_s[tid >> 2] * width + kLatent, tid & 3, turn_s[tid >> 2]);
+    auto turn_q = [&](int i, const Unit& x) {
+        const int j = i / units;
+        if (live_s[j])
+            rotate_unit<INTERLEAVED>(x, static_cast<__nv_bfloat16*>(a.q_out) + (t0 * a.H + (i >> 2)) * a.q_out_stride, i & 3,
+                                     turn_s[j]);
+    };
+#pragma unroll
+    for (int k = 0; k < kQ; ++k) {
+        const int i = tid + k * kThreads;
+        if (i < count * units) turn_q(i, q[k]);
     }
-    if (!a.q_rope) return;
-    const int units = 4 * a.H;
-#pragma unroll 4
-    for (int i = tid; i < count * units; i += kThreads) {
-        const int j = i / units, r = i - j * units, h = r >> 2, u = r & 3;
-        if (!live_s[j]) continue;
-        const int64_t row = (t0 + j) * a.H + h;
-        rotate_unit<INTERLEAVED>(static_cast<const __nv_bfloat16*>(a.q_rope) + row * a.q_stride,
-                                 static_cast<__nv_bfloat16*>(a.q_out) + row * a.q_out_stride, u, turn_s[j]);
-    }
+    for (int i = tid + kQ * kThreads; i < count * units; i += kThreads)
+        turn_q(i, load_unit<INTERLEAVED>(q_rope + (t0 * a.H + (i >> 2)) * a.q_stride, i & 3));
 }
 
 // ROWS rows a block, a 16-byte chunk a thread and step, all of a thread's loads before its stores.
