@@ -646,17 +646,18 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
 }
 
 // Joins the pieces of the sequences that several runs share: out = sum_i w_i O_i / sum_i w_i l_i with
-// w_i = 2^{m_i - max m}, the pieces in order.  A task is a quarter row (a float4 a lane).  Where a sequence has up to
-// 32 pieces a warp takes a task, with eight pieces' loads in flight; where it has more, a block does, its warps each
-// taking every eighth piece.
+// w_i = 2^{m_i - max m}, the pieces in order.  Where a sequence has up to 32 pieces, a warp takes a quarter row (a
+// float4 a lane) with eight pieces' loads in flight; where it has more, a block takes an eighth (a float2 a lane), its
+// warps every eighth piece, in one round of loads for a sequence over the whole card: the rounds' latency is all that
+// such a join takes (9000 cycles in three rounds, 41.5 us of a call; 6400 in one).
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kFewParts = 32, kMostParts = 256, kMostGrid = kJoinThreads,
-              kJoinBlocks = 5 * kSMs, kBatch = 8;
+              kJoinBlocks = 5 * kSMs, kBatch = 20;
 template <int NR>
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentDecodeArgs a, const int grid, const int groups) {
+__global__ void __launch_bounds__(kJoinThreads, 2) latent_join_kernel(const LatentDecodeArgs a, const int grid, const int groups) {
     __shared__ Head heads_s[kMostGrid];
     __shared__ int list_s[2][kMostGrid], count_s[2][kJoinWarps];
     __shared__ float w_s[kMostParts], total_s, max_s;
-    __shared__ float4 acc_s[kJoinWarps][32];
+    __shared__ float2 acc_s[kJoinWarps][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
     const float2* ml = reinterpret_cast<const float2*>(ws + Work<NR>::ml_at(grid));
@@ -681,18 +682,19 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentD
     if (few) list_s[0][at[0] + __popc(fm & below)] = tid;
     if (many) list_s[1][at[1] + __popc(mm & below)] = tid;
     __syncthreads();
-    // task t of a list: the sequence's first block, its row and quarter
+    // task t of a list: the sequence's first block, its row and the part of it
     struct Task {
         Head h;
-        int block, r, quarter;
+        int block, r, side;
         int64_t row;
         bool live;
     };
     auto task = [&](int kind, int t) {
+        const int sides = kind ? 8 : 4;
         Task x;
-        x.block = list_s[kind][t / (4 * NR)];
-        x.r = (t >> 2) % NR;
-        x.quarter = t & 3;
+        x.block = list_s[kind][t / (sides * NR)];
+        x.r = (t / sides) % NR;
+        x.side = t % sides;
         x.h = heads_s[x.block];
         const int q = (x.block % groups) * NR + x.r;
         x.row = (int64_t)x.h.n * R + q;
@@ -700,19 +702,16 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentD
         return x;
     };
     auto slot = [&](const Task& x, int i) { return ((int64_t)(x.block + i * groups) * 2 + (i == 0 ? x.h.first_slot : 0)) * NR + x.r; };
-    auto part = [&](const Task& x, int i) { return po[slot(x, i) * (kLatent / 4) + x.quarter * 32 + lane]; };
-    auto store = [&](const Task& x, float4 o, float mx, float total) {
-        if (!KDA_INDEX_OK(x.row, (int64_t)a.num_seqs * R, a.status)) return;
-        const float f = total == 0.f ? 0.f : 1.f / total;
-        uint2 y;
-        y.x = pack_bf16x2(o.x * f, o.y * f);
-        y.y = pack_bf16x2(o.z * f, o.w * f);
-        reinterpret_cast<uint2*>(a.out)[x.row * (kLatent / 4) + x.quarter * 32 + lane] = y;
-        if (a.lse && x.quarter == 0 && lane == 0)
+    auto part = [&](const Task& x, int i) { return po[slot(x, i) * (kLatent / 4) + x.side * 32 + lane]; };
+    auto part2 = [&](const Task& x, int i) {
+        return reinterpret_cast<const float2*>(po)[slot(x, i) * (kLatent / 2) + x.side * 32 + lane];
+    };
+    auto store_lse = [&](const Task& x, float mx, float total) {
+        if (a.lse && x.side == 0 && lane == 0)
             a.lse[x.row] = total == 0.f ? -INFINITY : (mx + log2f(total)) * 0.69314718055994530942f;
     };
     auto add = [](float4& acc, float w, float4 x) {
-        if (w != 0.f) { acc.x += w * x.x; acc.y += w * x.y; acc.z += w * x.z; acc.w += w * x.w; }
+        acc.x += w * x.x; acc.y += w * x.y; acc.z += w * x.z; acc.w += w * x.w;
     };
     for (int t = blockIdx.x * kJoinWarps + warp; t < count[0] * NR * 4; t += gridDim.x * kJoinWarps) {
         const Task x = task(0, t);
@@ -740,22 +739,33 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentD
                 if (i + k < x.h.parts) add(acc, wk, o[k]);
             }
         }
-        store(x, acc, mx, total);
+        if (KDA_INDEX_OK(x.row, (int64_t)a.num_seqs * R, a.status)) {
+            const float f = total == 0.f ? 0.f : 1.f / total;
+            uint2 v;
+            v.x = pack_bf16x2(acc.x * f, acc.y * f);
+            v.y = pack_bf16x2(acc.z * f, acc.w * f);
+            reinterpret_cast<uint2*>(a.out)[x.row * (kLatent / 4) + x.side * 32 + lane] = v;
+            store_lse(x, mx, total);
+        }
     }
-    for (int t = blockIdx.x; t < count[1] * NR * 4; t += gridDim.x) {
+    for (int t = blockIdx.x; t < count[1] * NR * 8; t += gridDim.x) {
         const Task x = task(1, t);
         if (!x.live) continue;                // uniform
         const int parts = x.h.parts < kMostParts ? x.h.parts : kMostParts;
+        float2 o[kBatch], y[kMostParts / 32], acc = make_float2(0.f, 0.f);
         if (warp == 0) {
-            float2 y[kMostParts / 32];
-            float mx = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kMostParts / 32; ++k)
                 y[k] = lane + 32 * k < parts ? ml[slot(x, lane + 32 * k)] : make_float2(-INFINITY, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (warp + k * kJoinWarps < parts) o[k] = part2(x, warp + k * kJoinWarps);
+        if (warp == 0) {
+            float mx = -INFINITY, sum = 0.f;
 #pragma unroll
             for (int k = 0; k < kMostParts / 32; ++k) mx = fmaxf(mx, y[k].x);
             for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            float sum = 0.f;
 #pragma unroll
             for (int k = 0; k < kMostParts / 32; ++k) {
                 const float w = y[k].x == -INFINITY ? 0.f : exp2_fast(y[k].x - mx);
@@ -765,22 +775,31 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentD
             for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             if (lane == 0) { total_s = sum; max_s = mx; }
         }
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        __syncthreads();
         for (int i = warp; i < parts; i += kBatch * kJoinWarps) {
-            float4 o[kBatch];
+            if (i > warp) {
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+                    if (i + k * kJoinWarps < parts) o[k] = part2(x, i + k * kJoinWarps);
+            }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k)
-                if (i + k * kJoinWarps < parts) o[k] = part(x, i + k * kJoinWarps);
-            if (i == warp) __syncthreads();   // the weights; every warp has a piece, as there are more than 32
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (i + k * kJoinWarps < parts) add(acc, w_s[i + k * kJoinWarps], o[k]);
+                if (i + k * kJoinWarps < parts) {
+                    const float w = w_s[i + k * kJoinWarps];
+                    acc.x += w * o[k].x;
+                    acc.y += w * o[k].y;
+                }
         }
         acc_s[warp][lane] = acc;
         __syncthreads();
-        if (warp == 0) {
-            for (int k = 1; k < kJoinWarps; ++k) add(acc, 1.f, acc_s[k][lane]);
-            store(x, acc, max_s, total_s);
+        if (warp == 0 && KDA_INDEX_OK(x.row, (int64_t)a.num_seqs * R, a.status)) {
+            for (int k = 1; k < kJoinWarps; ++k) {
+                acc.x += acc_s[k][lane].x;
+                acc.y += acc_s[k][lane].y;
+            }
+            const float f = total_s == 0.f ? 0.f : 1.f / total_s;
+            reinterpret_cast<uint32_t*>(a.out)[x.row * (kLatent / 2) + x.side * 32 + lane] = pack_bf16x2(acc.x * f, acc.y * f);
+            store_lse(x, max_s, total_s);
         }
         __syncthreads();
     }
