@@ -99,6 +99,8 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const LatentAppendA
     const int units = q_rope ? 4 * a.H : 0;
     uint4 lat[kLat];
     Unit key{}, q[kQ];
+    allow_next();
+    wait_before();
 #pragma unroll
     for (int k = 0; k < kLat; ++k) {
         const int i = tid + k * kThreads;
@@ -170,6 +172,8 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const LatentGatherArgs
     __shared__ int64_t row_s[ROWS];             // -1: zeros, -2: no sequence's
     const int tid = threadIdx.x;
     const int64_t t0 = (int64_t)blockIdx.x * ROWS;
+    allow_next();
+    wait_before();
     if (tid < ROWS) {
         int64_t r = -2;
         if (t0 + tid < a.total_tokens) {
@@ -202,40 +206,34 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const LatentGatherArgs
     }
 }
 
+// Calls of few tokens take few rows a block, so that every SM has some; they end sooner than the host makes the
+// next call, so an overlapped launch (about 1 us more of the host) only helps the others.
 template <int TOK>
-void append(const LatentAppendArgs& a, cudaStream_t s) {
+cudaError_t append(const LatentAppendArgs& a, bool overlapped, cudaStream_t s) {
     const unsigned blocks = (unsigned)((a.total_tokens + TOK - 1) / TOK);
-    if (a.interleaved)
-        append_kernel<TOK, true><<<blocks, kThreads, 0, s>>>(a);
-    else
-        append_kernel<TOK, false><<<blocks, kThreads, 0, s>>>(a);
+    const auto kernel = a.interleaved ? append_kernel<TOK, true> : append_kernel<TOK, false>;
+    if (overlapped) return launch_overlapped(kernel, blocks, kThreads, 0, s, a);
+    kernel<<<blocks, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 template <int ROWS>
-void gather(const LatentGatherArgs& a, cudaStream_t s) {
+cudaError_t gather(const LatentGatherArgs& a, bool overlapped, cudaStream_t s) {
     const unsigned blocks = (unsigned)((a.total_tokens + ROWS - 1) / ROWS);
-    if (a.c.rope_dim)
-        gather_kernel<ROWS, (kLatent + kRope) / 8><<<blocks, kThreads, 0, s>>>(a);
-    else
-        gather_kernel<ROWS, kLatent / 8><<<blocks, kThreads, 0, s>>>(a);
+    const auto kernel = a.c.rope_dim ? gather_kernel<ROWS, (kLatent + kRope) / 8> : gather_kernel<ROWS, kLatent / 8>;
+    if (overlapped) return launch_overlapped(kernel, blocks, kThreads, 0, s, a);
+    kernel<<<blocks, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t s) {
-    if (a.total_tokens < 2048)
-        append<1>(a, s);
-    else
-        append<8>(a, s);
-    return cudaGetLastError();
+    return a.total_tokens < 2048 ? append<1>(a, false, s) : append<8>(a, true, s);
 }
 
 cudaError_t launch_latent_gather(const LatentGatherArgs& a, cudaStream_t s) {
-    if (a.total_tokens < 8192)
-        gather<4>(a, s);
-    else
-        gather<32>(a, s);
-    return cudaGetLastError();
+    return a.total_tokens < 8192 ? gather<4>(a, false, s) : gather<32>(a, true, s);
 }
 
 }  // namespace kda

@@ -15,6 +15,28 @@ constexpr int kLatent = 512;   // channels of the latent (the cache row's first 
 constexpr int kRope = 64;      // channels of the rotated part, where there is one
 constexpr int kHead = 128;     // per-head channels of the expanded form
 
+// A kernel launched with launch_overlapped may start while the kernel before it in the stream still runs; nothing
+// of that kernel, and of all before it, may be read or overwritten until wait_before().  allow_next() lets the next
+// such kernel start; it waits in the same way, so a kernel that calls both keeps the order of all memory.
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t s,
+                              const Args&... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // 2^x by the special function unit (2 units in the last place; results below 2^-126 become zero).
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;

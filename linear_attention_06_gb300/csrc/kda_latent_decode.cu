@@ -232,7 +232,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
 
     // this kernel may start while the one before it in the stream ends, and the join while this one does: each
     // sets itself up and then waits for everything before it
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    allow_next();
     if (tid == 0) {
         for (uint32_t i = 0; i < G::kPairs; ++i) { mbar_init(&sw->full[i], 1); mbar_init(&sw->empty[i], 1); }
         for (int i = 0; i < 2; ++i) {
@@ -255,7 +255,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
         tmem_alloc(&sw->tmem, G::kCols);
         tmem_relinquish();
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_before();
     find_run(a, runs, run, sw, reinterpret_cast<int*>(sw->fac));
     tc_fence_before();
     __syncthreads();
@@ -666,8 +666,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) latent_join_kernel(const Late
     const float2* ml = reinterpret_cast<const float2*>(ws + Work<NR>::ml_at(grid));
     const float4* po = reinterpret_cast<const float4*>(ws + Work<NR>::o_at(grid));
     const int R = a.tokens_per_seq * a.H;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    allow_next();
+    wait_before();
     // the sequences to join, of few pieces and of many, each in the order of their blocks: every block of this
     // kernel makes the same lists
     const Head mine = tid < grid ? reinterpret_cast<const Head*>(ws)[tid] : Head{-1, 0, 0, 0};
@@ -860,23 +860,9 @@ cudaError_t launch(const LatentDecodeArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = G::kBytes;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, latent_decode_kernel<NR, ROPE>, maps, a, groups, (int)c_rows);
-    if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(kJoinBlocks);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, latent_join_kernel<NR>, a, grid, groups);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    const cudaError_t e = launch_overlapped(latent_decode_kernel<NR, ROPE>, grid, kThreads, G::kBytes, s, maps, a, groups,
+                                            (int)c_rows);
+    return e != cudaSuccess ? e : launch_overlapped(latent_join_kernel<NR>, kJoinBlocks, kJoinThreads, 0, s, a, grid, groups);
 }
 
 template <int NR>
