@@ -355,8 +355,10 @@ kda_status kda_decode_step_gated(const kda_shape* shape, const void* q, const vo
  *   (common prefixes) and lie in any order.  Entries behind a sequence's last page are not read
  *   by kda_latent_decode and kda_latent_gather, whatever they hold.  An entry outside
  *   [0, num_pages) causes no access: its tokens read as zero rows and are not written.
- * - seq_lens: DEVICE int32 [N], the tokens of each sequence INCLUDING those of the call; values
- *   are clamped to [0, max_pages * page_size].
+ * - seq_lens: DEVICE int32 [N], the tokens of each sequence INCLUDING those of the call.
+ *   kda_latent_decode clamps them to [0, max_pages * page_size].
+ * - Outputs must not overlap inputs but where a call says so.  A first call on a device, outside a
+ *   stream capture, loads the kernels; after it every call may be captured.
  * - The cache rows behind a sequence's end, and rows of q, k, v behind the last sequence, may hold
  *   anything (NaN too): they reach no result.  Values that a sequence itself holds are taken as
  *   finite: an infinite or NaN value reaches every row of its tile.
@@ -434,7 +436,7 @@ kda_status kda_latent_gather(const kda_latent_shape* shape, const void* cache, c
  * flight at once (two streams, or two graphs that may run at the same time) need two.
  * Errors: those of kda_decode_step and kda_latent_append; KDA_ERR_INVALID_ARG also for a scale
  * that is not finite and > 0 and a NULL or too small workspace, KDA_ERR_UNSUPPORTED for a
- * misaligned one or T' > 16.
+ * misaligned one, T' > 16 or N * T' * H > 2^31 - 1.
  */
 kda_status kda_latent_decode(const kda_latent_shape* shape, const void* q_latent, const void* q_rope,
                              const void* cache, const int32_t* block_table, const int32_t* seq_lens, float scale,

@@ -451,14 +451,22 @@ def _latent_cache(cache, block_table, H, tokens, index):
             KdaLatentShape(n, tokens, H, _LATENT, width - _LATENT, page, pages, per, KDA_BF16))
 
 
-def _call(fn, index, stream, *args):
-    """Call the library's fn(*args, stream) with the tensors' device current."""
+def _on(stream, t):
+    """Makes `stream` (a torch stream or a raw handle) current on t's device, so that what a call allocates and
+    copies belongs to the stream that it runs on."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    return torch.cuda.stream(stream)
+
+
+def _call(fn, index, *args):
+    """Call the library's fn(*args, stream) on the current stream of the tensors' device, that device current."""
     f = getattr(_lib or lib(), fn)
     if torch.cuda.current_device() == index:
-        st = f(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
+        st = f(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
-            st = f(*args, _stream(stream))
+            st = f(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != KDA_OK:
         raise KdaError(fn, st, status_string(st))
 
@@ -473,6 +481,10 @@ def kda_latent_append(latent, k_rope, cache, block_table, seq_lens, inv_freq=Non
     angles a position (None: no rotation).  ``q_rope`` [T, H, 64], possibly the end of longer rows, is
     rotated into ``q_rope_out`` (allocated when not given; q_rope itself rotates in place), which is
     returned; None without queries."""
+    if stream is not None:
+        with _on(stream, cache):
+            return kda_latent_append(latent, k_rope, cache, block_table, seq_lens, inv_freq, interleaved, q_rope,
+                                     q_rope_out, cu_seqlens)
     dev = _cuda(cache)
     T, H = latent.shape[0], 1 if q_rope is None else q_rope.shape[1]
     p_cache, p_table, shape = _latent_cache(cache, block_table, H, T, dev)
@@ -497,7 +509,7 @@ def kda_latent_append(latent, k_rope, cache, block_table, seq_lens, inv_freq=Non
         else:
             p_out = _expect("q_rope_out", q_rope_out, (T, H, _ROPE), torch.bfloat16, dev, True)
             out_step = _row_stride("q_rope_out", q_rope_out)
-    _call("kda_latent_append", dev, stream, shape, p_latent, _row_stride("latent", latent), p_rope, rope_step, p_freq,
+    _call("kda_latent_append", dev, shape, p_latent, _row_stride("latent", latent), p_rope, rope_step, p_freq,
           1 if interleaved else 0, p_q, q_step, p_out, out_step, p_cu, p_lens, p_table, p_cache)
     return q_rope_out if q_rope is not None else None
 
@@ -505,6 +517,9 @@ def kda_latent_append(latent, k_rope, cache, block_table, seq_lens, inv_freq=Non
 def kda_latent_gather(cache, block_table, cu_seqlens, total_tokens, starts=None, out=None, stream=None):
     """Cached rows back to packed rows (see ``include/kda.h``): rows starts[n] .. of every sequence n, as
     many as cu_seqlens gives it.  Returns (latent [T, 512], k_rope [T, 64] or None), or fills ``out``."""
+    if stream is not None:
+        with _on(stream, cache):
+            return kda_latent_gather(cache, block_table, cu_seqlens, total_tokens, starts, out)
     dev = _cuda(cache)
     T = int(total_tokens)
     p_cache, p_table, shape = _latent_cache(cache, block_table, 1, T, dev)
@@ -519,7 +534,7 @@ def kda_latent_gather(cache, block_table, cu_seqlens, total_tokens, starts=None,
         latent, k_rope = out
         p_latent = _expect("latent", latent, (T, _LATENT), torch.bfloat16, dev)
         p_rope = _expect("k_rope", k_rope, (T, rope), torch.bfloat16, dev) if rope else None
-    _call("kda_latent_gather", dev, stream, shape, p_cache, p_table, p_cu, p_starts, p_latent, p_rope)
+    _call("kda_latent_gather", dev, shape, p_cache, p_table, p_cu, p_starts, p_latent, p_rope)
     return latent, k_rope
 
 
@@ -540,6 +555,9 @@ def kda_latent_decode(q_latent, q_rope, cache, block_table, seq_lens, scale, out
     the step's tokens included (their rows are in the cache).  ``lse`` may be a [N*T, H] fp32 tensor to
     fill, True to allocate one, or None; ``workspace`` a CUDA uint8 tensor of
     kda_latent_decode_workspace_size bytes, allocated here when not given.  Returns (out [N*T, H, 512], lse)."""
+    if stream is not None:
+        with _on(stream, cache):
+            return kda_latent_decode(q_latent, q_rope, cache, block_table, seq_lens, scale, out, lse, workspace)
     dev = _cuda(cache)
     rows, H = q_latent.shape[0], q_latent.shape[1]
     p_cache, p_table, shape = _latent_cache(cache, block_table, H, rows, dev)
@@ -558,7 +576,7 @@ def kda_latent_decode(q_latent, q_rope, cache, block_table, seq_lens, scale, out
         need = ctypes.c_size_t(0)
         _check("kda_latent_decode", lib().kda_latent_decode_workspace_size(shape, ctypes.byref(need)))
         workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=cache.device)
-    _call("kda_latent_decode", dev, stream, shape, p_q, p_r, p_cache, p_table, p_lens, float(scale), p_out, p_lse,
+    _call("kda_latent_decode", dev, shape, p_q, p_r, p_cache, p_table, p_lens, float(scale), p_out, p_lse,
           _expect("workspace", workspace, workspace.shape, torch.uint8, dev), workspace.numel())
     return out, lse
 
@@ -571,6 +589,9 @@ def kda_latent_prefill(q, k, v, k_rope, scale, cu_seqlens=None, cu_seqlens_k=Non
     projection; k_rope: [S, 64], shared by the heads (None for 128-wide q).  ``cu_seqlens`` and
     ``cu_seqlens_k`` are CUDA int32 tensors or host tables (None: ``num_seqs`` equal sequences; keys as
     queries where only cu_seqlens is given and S = T).  Returns (out [T, H, 128], lse)."""
+    if stream is not None:
+        with _on(stream, q):
+            return kda_latent_prefill(q, k, v, k_rope, scale, cu_seqlens, cu_seqlens_k, num_seqs, out, lse)
     dev = _cuda(q)
     T, H, dk = q.shape
     S = k.shape[0]
@@ -600,7 +621,7 @@ def kda_latent_prefill(q, k, v, k_rope, scale, cu_seqlens=None, cu_seqlens_k=Non
     if lse is True:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
     p_lse = None if lse is None else _expect("lse", lse, (T, H), torch.float32, dev)
-    _call("kda_latent_prefill", dev, stream, KdaShape(n, T, H, dk, _HEAD, KDA_BF16), S, p_q, p_k, p_v, step, p_r,
+    _call("kda_latent_prefill", dev, KdaShape(n, T, H, dk, _HEAD, KDA_BF16), S, p_q, p_k, p_v, step, p_r,
           float(scale), p_cu, p_cu_k, p_out, p_lse)
     return out, lse
 

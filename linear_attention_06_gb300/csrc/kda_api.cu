@@ -499,6 +499,7 @@ kda_status kda_latent_decode(const kda_latent_shape* shape, const void* q_latent
     if (!aligned(q_latent, 16) || (rope && !aligned(q_rope, 16)) || !aligned(seq_lens, 4) || !aligned(out, 16) ||
         !aligned(lse, 4) || !aligned(workspace, 256))
         return KDA_ERR_UNSUPPORTED;
+    if (shape->total_tokens * shape->H > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;   // a query row's index
     const int tps = (int)(shape->total_tokens / shape->num_seqs);
     if (workspace_bytes < kda::latent_decode_workspace_bytes(tps, shape->H)) return KDA_ERR_INVALID_ARG;
     unsigned int* status = status_word();
@@ -525,6 +526,7 @@ kda_status kda_latent_prefill(const kda_shape* shape, int64_t total_kv, const vo
     if (st != KDA_OK) return st;
     if (!(scale > 0.f) || !(scale < INFINITY) || kv_stride < 128) return KDA_ERR_INVALID_ARG;
     if (kv_stride % 8 != 0) return KDA_ERR_UNSUPPORTED;
+    if ((shape->total_tokens / 256 + 1 + shape->num_seqs) * shape->H > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;   // grid
     if (shape->total_tokens == 0) return KDA_OK;
     const bool rope = shape->dk > 128, keys = total_kv > 0;
     if (!q || !out || (keys && (!k || !v || (rope && !k_rope)))) return KDA_ERR_INVALID_ARG;

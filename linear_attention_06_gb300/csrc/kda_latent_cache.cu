@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const LatentAppendA
         int64_t b, e;
         const int n = find_seq_warp(a.cu_seqlens, a.num_seqs, a.total_tokens, t0 + j, b, e);
         if (lane == 0) {
-            const int64_t p = n < 0 ? 0 : (int64_t)clamped_len(a.c, a.seq_lens, n) - (e - (t0 + j));
+            const int64_t p = n < 0 ? 0 : (int64_t)a.seq_lens[n] - (e - (t0 + j));
             live_s[j] = n >= 0;
             pos_s[j] = p;
             int64_t row = n < 0 ? -1 : cache_row(a.c, n, p);

@@ -96,7 +96,7 @@ struct Piece {                                // a run's share of one sequence
     int n, len, off, tiles, all;              // sequence, its length, first tile, tiles here, tiles in all
 };
 
-__device__ __forceinline__ int tiles_of(int len) { return len > kTile ? (len + kTile - 1) / kTile : 1; }
+__device__ __forceinline__ int tiles_of(int len) { return len > kTile ? (len - 1) / kTile + 1 : 1; }
 // A sequence's places in the line: its tiles, behind kStart places that stand for what starting a piece costs a
 // block (queries in, O out), so that runs with many pieces get fewer tiles.
 constexpr int kStart = 1;
@@ -123,11 +123,25 @@ struct Walk {
     }
 };
 
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_parked(bar, parity, kWaitNs); }
-// The same for a converged warp whose next steps the compiler should know to be uniform.
+// A converged warp waits, and agrees on whether all its lanes saw the phase end in time.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_parked(bar, parity, kWaitNs));
 }
+// OR and AND of a predicate over the softmax warps; also a barrier between them.
+__device__ __forceinline__ bool soft_or(bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, %2, %3, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)pred), "n"(kBar), "n"(kSoft)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ bool soft_and(bool pred) { return !soft_or(!pred); }
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kSoft) : "memory"); }
 
 // The first tile of run p of `runs` over `total` tiles (a 32-bit division where it fits, a fifth of the time), and
 // the run that holds tile x.
@@ -156,7 +170,7 @@ struct Maps {
 
 // All threads: the run of this block and the sequence it starts in.  Rounds of a sequence a thread; with up to
 // kThreads sequences the lengths are read once.
-__device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Small* sw, int* scratch) {
+__device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Small* sw, int64_t* scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int len = 0;
     auto tiles_at = [&](int n) {
@@ -164,12 +178,11 @@ __device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Small* sw, 
         len = clamped_len(a.c, a.seq_lens, n);
         return kStart + tiles_of(len);
     };
-    // the round's tiles before this thread's sequence, and in all (a round has at most 2^31 / 64 * 256 / ... tiles of
-    // a cache that fits the card: well inside 32 bits)
-    auto scan = [&](int mine, int& round) {
-        int x = mine;
+    // the round's places before this thread's sequence, and in all
+    auto scan = [&](int mine, int64_t& round) {
+        int64_t x = mine;
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
         if (lane == 31) scratch[warp] = x;
@@ -182,11 +195,12 @@ __device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Small* sw, 
         __syncthreads();
         return x - mine;
     };
-    int mine = tiles_at(tid), round, at = scan(mine, round);
+    int mine = tiles_at(tid);
+    int64_t round, at = scan(mine, round);
     int mine_len = len;
     int64_t total = round;
     for (int n0 = kThreads; n0 < a.num_seqs; n0 += kThreads) {
-        int more;
+        int64_t more;
         scan(tiles_at(n0 + tid), more);
         total += more;
     }
@@ -256,7 +270,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
         tmem_relinquish();
     }
     wait_before();
-    find_run(a, runs, run, sw, reinterpret_cast<int*>(sw->fac));
+    find_run(a, runs, run, sw, reinterpret_cast<int64_t*>(sw->fac));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -279,8 +293,8 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
             const int64_t table = (int64_t)p.n * a.c.max_pages;
             // the page of this lane's box in tile x (a box outside the cache reads zeros)
             auto row_of = [&](int x) -> int {
+                if (piece * box >= kTile || piece * box >= p.len - x * kTile) return -1;
                 const int pos = x * kTile + piece * box;
-                if (piece * box >= kTile || pos >= p.len) return -1;
                 if (!KDA_INDEX_OK(table + (pos >> shift), (int64_t)a.num_seqs * a.c.max_pages, a.status)) return map_rows;
                 const int page = a.c.block_table[table + (pos >> shift)];
                 return page < 0 || page >= a.c.num_pages ? map_rows : (page << shift) + (pos & (a.c.page_size - 1));
@@ -303,7 +317,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                 const int valid = live < 0 ? 0 : (live < kTile ? live : kTile);
                 const uint32_t boxes = (valid + box - 1) / box;
                 for (int k = 0; k < 4; ++k) {
-                    if (used && !(ok = wait(&sw->empty[ring.slot], ring.phase ^ 1u))) break;
+                    if (used && !(ok = wait_warp(&sw->empty[ring.slot], ring.phase ^ 1u))) break;
                     if (lane == 0) mbar_arrive_expect_tx(&sw->full[ring.slot], boxes * box * 256);
                     __syncwarp();
                     if (row >= 0)
@@ -315,7 +329,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                 }
                 if (!ok) break;
                 if constexpr (ROPE) {
-                    if (rope_used && !(ok = wait(&sw->rope_empty[rope.slot], rope.phase ^ 1u))) break;
+                    if (rope_used && !(ok = wait_warp(&sw->rope_empty[rope.slot], rope.phase ^ 1u))) break;
                     if (lane == 0) mbar_arrive_expect_tx(&sw->rope_full[rope.slot], boxes * box * 128);
                     __syncwarp();
                     if (row >= 0 && half == 0)
@@ -412,14 +426,14 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
         }
         if (!ok) {                            // products in flight land before TMEM is freed
             mma_commit_elected(&sw->drain, el);
-            wait(&sw->drain, 0);
+            wait_warp(&sw->drain, 0);
         }
     } else if (warp == 2) {                   // ------------------------------------------------ queries
         Walk walk(sw);
         Piece p;
         uint32_t seg = 0;
         while (walk.next(a, p)) {
-            if (seg > 0 && !(ok = wait(&sw->q_empty, (seg - 1) & 1))) break;
+            if (seg > 0 && !(ok = wait_warp(&sw->q_empty, (seg - 1) & 1))) break;
             if (lane == 0) mbar_arrive_expect_tx(&sw->q_full, G::kSlice * G::kSlices);
             __syncwarp();
             const int row = p.n * R + group * NR;
@@ -454,7 +468,8 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
             }
             for (int j = 0; j < p.tiles; ++j) {
                 const int base = (p.off + j) * kTile;
-                if (!(ok = wait(&sw->s_full[sb.slot], sb.phase))) break;
+                // a wait that runs out is not left alone: the four warps meet at barriers, and stop together
+                ok = ok && wait_warp(&sw->s_full[sb.slot], sb.phase);
                 tc_fence_after();
                 uint32_t s[32];
                 float f[2] = {1.f, 1.f};
@@ -462,12 +477,11 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                 if (active) {
                     tmem_ld_16x64(s_lanes + sb.slot * 64, s);
                     tmem_wait_ld();
-                    if (__any_sync(0xffffffffu, seen[0] - base < kTile || seen[1] - base < kTile)) {
+                    const int lim[2] = {seen[0] - base, seen[1] - base};             // columns that the rows see
+                    if (__any_sync(0xffffffffu, lim[0] < kTile || lim[1] < kTile)) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int col = base + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
-                            if (col >= seen[(i >> 1) & 1]) s[i] = 0xff800000u;       // -inf
-                        }
+                        for (int i = 0; i < 32; ++i)
+                            if (8 * (i >> 2) + 2 * (lane & 3) + (i & 1) >= lim[(i >> 1) & 1]) s[i] = 0xff800000u;   // -inf
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -487,7 +501,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                         l[e] *= f[e];
                     }
                 }
-                if (base + kTile > p.len) {   // the tile's rows behind the sequence's end become zeros
+                if (p.len - base < kTile) {   // the tile's rows behind the sequence's end become zeros
                     const int valid = p.len - base < 0 ? 0 : p.len - base;
                     Ring<G::kPairs> pair = in;
                     for (int k = 0; k < 4; ++k, pair.next())
@@ -495,26 +509,14 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                             *reinterpret_cast<uint4*>(sm + G::kPairAt + pair.slot * 16384 + ((i >> 3) & 1) * 8192 +
                                                       (valid + (i >> 4)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
-                bool any;
-                {
-                    uint32_t r;
-                    asm volatile(
-                        "{\n\t.reg .pred p, q;\n\t"
-                        "setp.ne.u32 q, %1, 0;\n\t"
-                        "bar.red.or.pred p, %2, %3, q;\n\t"
-                        "selp.u32 %0, 1, 0, p;\n\t}"
-                        : "=r"(r)
-                        : "r"((uint32_t)(raise && j > 0)), "n"(kBar), "n"(kSoft)
-                        : "memory");
-                    any = r != 0;
-                }
-                if (any) {                    // rescale O^T, column r by f_r
+                if (soft_or((raise && j > 0) || !ok)) {              // rescale O^T, column r by f_r
+                    if (!soft_and(ok)) { ok = false; break; }
                     if (active && (lane & 3) == 0) {
                         sw->fac[r0] = f[0];
                         sw->fac[r0 + 8] = f[1];
                     }
-                    asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kSoft) : "memory");
-                    if (!(ok = wait(&sw->pv_done[prev.slot], prev.phase))) break;
+                    soft_sync();
+                    ok = wait_warp(&sw->pv_done[prev.slot], prev.phase);
                     tc_fence_after();
 #pragma unroll 1
                     for (int k = 0; k < NR / 16; ++k) {
@@ -535,8 +537,8 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                     tmem_wait_st();
                 }
                 // this P buffer was read by the products of two tiles ago
-                if ((sb.slot ? used1 : used0) && !(ok = wait(&sw->pv_done[sb.slot], sb.phase ^ 1u))) break;
-                if (active) {
+                if (sb.slot ? used1 : used0) ok = ok && wait_warp(&sw->pv_done[sb.slot], sb.phase ^ 1u);
+                if (active && ok) {
                     uint8_t* pt = sm + G::kP + sb.slot * G::kSlice;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -556,13 +558,13 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sw->p_full[sb.slot]);
+                if (lane == 0 && ok) mbar_arrive(&sw->p_full[sb.slot]);
                 if (sb.slot) used1 = true; else used0 = true;
                 prev = sb;
                 sb.next();
                 in.next(); in.next(); in.next(); in.next();
             }
-            if (!ok) break;
+            if (!soft_and(ok)) { ok = false; break; }
             // ---- the piece is done: its rows' sums, then O^T out of tensor memory
             const bool whole = p.off == 0 && p.tiles == p.all;
             const int slot = blockIdx.x * 2 + (first_piece ? 0 : 1);
@@ -592,8 +594,8 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                     }
                 }
             }
-            asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kSoft) : "memory");
-            if (!(ok = wait(&sw->pv_done[prev.slot], prev.phase))) break;
+            ok = soft_and(wait_warp(&sw->pv_done[prev.slot], prev.phase));   // also: inv is written
+            if (!ok) break;
             tc_fence_after();
             // column r of block b: row r, channels 128 b ..; a lane stores its channel of 16 rows at a time, so a
             // warp's store is 64 bytes of a row in bf16, 128 in fp32
@@ -634,7 +636,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
             }
             tc_fence_before();
             // everyone has read inv before the next piece writes it
-            asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kSoft) : "memory");
+            soft_sync();
             if (lane == 0) mbar_arrive(&sw->o_free);
             at += p.tiles + kStart;
             first_piece = false;

@@ -65,7 +65,7 @@ struct Maps {
 };
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_parked(bar, parity, kWaitNs); }
-// The same for a converged warp whose next steps the compiler should know to be uniform.
+// The same for a converged warp, whose lanes agree on whether all of them saw the phase end in time.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_parked(bar, parity, kWaitNs));
 }
@@ -297,7 +297,7 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
         float m = -INFINITY, l = 0.f;
         const int count = tiles[X];
         for (int j = 0; j < count; ++j) {
-            if (!(ok = wait(&sw->s_full[X], j & 1))) break;
+            if (!(ok = wait_warp(&sw->s_full[X], j & 1))) break;
             tc_fence_after();
             uint32_t s[4][32];
 #pragma unroll
@@ -338,7 +338,7 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
                 }
             }
             if ((int64_t)(j + 1) * kN > x.nk) {                      // value rows behind the sequence's end become zeros
-                if (!(ok = wait(&sw->v_full[j & 1], (j >> 1) & 1))) break;
+                if (!(ok = wait_warp(&sw->v_full[j & 1], (j >> 1) & 1))) break;
                 if (j * kN + t >= x.nk)
                     for (int k = 0; k < 16; ++k)
                         *reinterpret_cast<uint4*>(sm + G::kV + (j & 1) * 32768 + (k >> 3) * 16384 + t * 128 + (k & 7) * 16) =
@@ -369,7 +369,7 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
             }
             l += sum.x + sum.y;
         }
-        if (ok && count && !(ok = wait(&sw->o_done[X], 0))) {}
+        if (ok && count) ok = wait_warp(&sw->o_done[X], 0);
         if (ok) {                             // a thread stores its query's row
             tc_fence_after();
             const int64_t row = (x.qb + i) * a.H + x.h;
@@ -463,7 +463,6 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
         ready[dev].store(true, std::memory_order_release);
     }
     const int64_t slots = (a.total_q + kBlockQ - 1) / kBlockQ + a.num_seqs, blocks = slots * a.H;
-    if (blocks > (int64_t)INT32_MAX) return cudaErrorInvalidConfiguration;
     latent_prefill_kernel<DK><<<(unsigned)blocks, kThreads, G::kBytes, s>>>(maps, a, slots);
     return cudaGetLastError();
 }

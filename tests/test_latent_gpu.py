@@ -151,9 +151,15 @@ def test_append_leaves_out_what_has_no_row():
     changed = (cache.view(torch.int16) != before.view(torch.int16)).any(-1).sum()
     assert int(changed) == 3
     assert bool(out.isfinite().all())
-    # lengths beyond the table are clamped to it, lengths below zero to zero
-    kda.kda_latent_append(lat, kr, cache, table, i32([10 ** 9, -5, 2]), q_rope=q, inv_freq=freqs())
+    # lengths beyond the table, and below zero, give positions without a row
+    before = cache.clone()
+    out = kda.kda_latent_append(lat, kr, cache, table, i32([10 ** 9, -5, 1]), q_rope=q, inv_freq=freqs())
     clean()
+    before[table[2, 0].long(), 0] = cache[table[2, 0].long(), 0]
+    assert torch.equal(cache.view(torch.int16), before.view(torch.int16))
+    pos = torch.tensor([10 ** 9 - 2, 10 ** 9 - 1, -7, -6, -1, 0], device=DEV)
+    y, b = ref.rotate(q, pos, freqs(), False)
+    ref.assert_within(out, y, b, "queries without a row")
 
 
 # ---------------------------------------------------------------- gather
@@ -315,6 +321,32 @@ def test_decode_cache_beyond_32_bit_offsets():
     assert torch.equal(got[:300].double(), ref.rows_of(cache, table, 0, 300)[:, :512])
 
 
+def test_decode_a_context_of_a_million_tokens():
+    """2^20 tokens over 64 distinct pages, and a short neighbour."""
+    g = gen(20)
+    cache = randn(g, 64, 1024, 576)
+    table = torch.randint(0, 64, (2, 1024), generator=g, device=DEV).to(torch.int32)
+    check = (randn(g, 2, 16, 512), randn(g, 2, 16, 64), cache, table, i32([2 ** 20, 77]), 0.07)
+    out, lse = kda.kda_latent_decode(*check, lse=True)
+    clean()
+    o, s, bo, bs = ref.decode(*check)
+    ref.assert_within(out, o, bo, "out")
+    ref.assert_within(lse, s, bs, "lse")
+
+
+def test_decode_without_pages():
+    """No pages, no table entries: nothing is seen."""
+    q, qr = torch.ones(3, 4, 512, dtype=BF, device=DEV), torch.ones(3, 4, 64, dtype=BF, device=DEV)
+    empty = torch.empty(0, 64, 576, dtype=BF, device=DEV)
+    out, lse = kda.kda_latent_decode(q, qr, empty, torch.empty(3, 0, dtype=torch.int32, device=DEV), i32([5, 0, 9]), 0.07, lse=True)
+    clean()
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    out, lse = kda.kda_latent_decode(q, qr, empty, torch.zeros(3, 2, dtype=torch.int32, device=DEV), i32([5, 0, 128]), 0.07, lse=True)
+    clean()                                                    # rows of pages that are not there are zeros
+    assert bool((out == 0).all())
+    torch.testing.assert_close(lse[:, 0].cpu(), torch.tensor([math.log(5), -math.inf, math.log(128)]), rtol=1e-6, atol=0)
+
+
 def test_decode_writes_no_row_but_its_own():
     g = gen(19)
     cache, table = paged([100, 40, 7], 16, 64, g)
@@ -445,6 +477,31 @@ def test_side_stream_and_captured_graph():
         o, s, bo, bs = ref.decode(q, qr, cache, table, lens, 0.07)
         ref.assert_within(out, o, bo, "replayed out")
         ref.assert_within(lse, s, bs, "replayed lse")
+    clean()
+
+
+def test_a_stream_argument_carries_the_whole_call():
+    """Outputs, workspaces and table copies of a call with stream= belong to that stream; a raw handle works too."""
+    g = gen(21)
+    cache, table = paged([700, 65], 64, 64, g)
+    q, qr, lens = randn(g, 2, 32, 512), randn(g, 2, 32, 64), i32([700, 65])
+    p = (randn(g, 300, 2, 192), randn(g, 300, 2, 128), randn(g, 300, 2, 128), randn(g, 300, 64), 0.07)
+    lat, kr, qn = randn(g, 2, 512), randn(g, 2, 64), randn(g, 2, 4, 64)
+    want = (kda.kda_latent_decode(q, qr, cache, table, lens, 0.07)[0], kda.kda_latent_prefill(*p, cu_seqlens=[0, 100, 300])[0],
+            kda.kda_latent_gather(cache, table, [0, 700, 765], 765)[0])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        got = []
+        for _ in range(20):                                    # memory is reused from call to call
+            got = [kda.kda_latent_decode(q, qr, cache, table, lens, 0.07, stream=stream)[0],
+                   kda.kda_latent_prefill(*p, cu_seqlens=[0, 100, 300], stream=stream)[0],
+                   kda.kda_latent_gather(cache, table, [0, 700, 765], 765, stream=stream)[0]]
+            torch.full((1 << 22,), 7.0, device=DEV)            # on the default stream
+        kda.kda_latent_append(lat, kr, cache.clone(), table, lens, q_rope=qn, stream=stream)
+        side.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
     clean()
 
 

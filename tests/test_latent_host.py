@@ -94,7 +94,7 @@ def test_decode_refusals(L):
                dict(sh=shape(n=4, T=6)), dict(sh=shape(T=0)), dict(sh=shape(n=0, T=2)), dict(size=0)):
         assert decode(L, **kw) == ARG, kw
     for kw in (dict(q=MIS), dict(qr=MIS), dict(cache=MIS), dict(out=MIS), dict(lse=FAKE + 2), dict(table=FAKE + 3),
-               dict(lens=FAKE + 2), dict(ws=FAKE + 128), dict(sh=shape(n=2, T=34))):
+               dict(lens=FAKE + 2), dict(ws=FAKE + 128), dict(sh=shape(n=2, T=34)), dict(sh=shape(n=2 ** 22, T=2 ** 22, H=512))):
         assert decode(L, **kw) == UNS, kw
     assert decode(L, shape(n=0, T=0), q=None, qr=None, cache=None, ws=None) == OK
 
@@ -116,7 +116,7 @@ def test_prefill_refusals(L):
         assert prefill(L, **kw) == ARG, kw
     for kw in (dict(dk=64), dict(dk=160), dict(dv=64), dict(dt=_lib.KDA_F32), dict(H=1025), dict(q=MIS), dict(k=MIS),
                dict(v=MIS), dict(kr=MIS), dict(out=MIS), dict(lse=FAKE + 2), dict(cu=FAKE + 1), dict(ck=FAKE + 2),
-               dict(step=132), dict(T=2 ** 31), dict(S=2 ** 31)):
+               dict(step=132), dict(T=2 ** 31), dict(S=2 ** 31), dict(T=2 ** 31 - 2, H=1024)):
         assert prefill(L, **kw) == UNS, kw
     assert prefill(L, T=0, q=None, out=None) == OK
     assert prefill(L, n=0, T=0, S=0, q=None, k=None, v=None, kr=None, out=None) == OK
