@@ -8,16 +8,23 @@
 // bytes a key and head, read once for 256 queries: the tensor cores bound it.
 //
 // Block: 256 queries of one head as two tiles of 128, A and B, that take turns: while the tensor core works on
-// one, four warps turn the other's scores into weights.  Per tile of 128 keys and query tile X:
+// one, eight warps turn the other's scores into weights.  Per tile of 128 keys and query tile X:
 //   S_X [128 x 128]  = Q_X K^T     both from shared memory (128-byte swizzle), K = 192 or 128
 //   O_X [128 x 128] += P_X V       P_X bf16 in tensor memory, over the columns that held S_X
-// S_A, S_B, O_A, O_B are all of tensor memory's 512 columns.  A thread owns a query's whole row of scores, so
-// maximum and sum need no exchange.  The maximum is raised only when a score exceeds it by more than 2^8 (weights
-// stay below 2^8 in bf16, whose precision does not depend on the exponent; sums are fp32), so O is rarely
-// rescaled; when it is, its last product is done already: S_X was issued behind it.
+// S_A, S_B, O_A, O_B are all of tensor memory's 512 columns, so a tile's chain (scores, weights, value product,
+// next scores) cannot overlap itself: two threads share a query's row, 64 keys each, which shortens it, and hand the
+// weights over in halves.  The maximum is raised only when a score exceeds it by more than 2^8 (weights stay below
+// 2^8 in bf16, whose precision does not depend on the exponent; sums are fp32), so O is rarely rescaled; when it is,
+// its last product is done already: S_X was issued behind it.
 //
 // Keys stream through a ring of 16 KB slices of 64 channels, each handed back when B's product has read it, values
 // through two stages of 32 KB.
+//
+// Measured (GB300): 4 x 8192 tokens x 32 heads, dk = 192: 1.76 ms, 1.57 PFLOP/s, 0.90 of the sustained cuBLAS rate,
+// under the power cap (1.7 GHz; the tensor pipe computes for about 0.75 of the cycles, a period of 3150 cycles for 2560
+// of products).  dk = 128, 2 x 1024 queries over 17408 keys: 416 us, 1.36 PFLOP/s: 3000 cycles for 2048 of products,
+// the chain of one tile (590 value product, 512 scores, 1480 weights, 400 hand-overs), and 256 blocks for 152 SMs.
+// A thread a query with 128 registers of scores: 1.78 ms and 420 us.
 #include <atomic>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -38,7 +45,8 @@ using namespace latent;
 using namespace sm103;
 
 constexpr int kM = 128, kBlockQ = 2 * kM, kN = 128;   // queries a tile and a block, keys a tile
-constexpr int kThreads = 320;                         // warps 0-3: A, 4-7: B, 8: producer, 9: issuer
+constexpr int kSoft = 256;                            // threads of a query tile: two for each query
+constexpr int kThreads = 2 * kSoft + 64;              // warps 0-7: A, 8-15: B, 16: producer, 17: issuer
 constexpr int kHeadsTogether = 8;                     // heads whose keys are in L2 at a time
 constexpr float kRaise = 8.f;                         // log2 of how far a score may exceed the running maximum
 constexpr uint64_t kWaitNs = 4000000000ull;           // bound of every wait
@@ -50,15 +58,16 @@ struct Cfg {
     static constexpr uint32_t kK = kV + 65536;
     static constexpr uint32_t kKSlots = DK == 192 ? 4 : 6;
     static constexpr uint32_t kSmall = kK + kKSlots * 16384;
-    static constexpr uint32_t kBytes = kSmall + 1024 + 1024;      // + alignment slack
+    static constexpr uint32_t kBytes = kSmall + 2048 + 1024;      // + alignment slack
     static_assert(kBytes <= 232448, "shared memory");
 };
 
 struct Small {
     uint64_t q_full[2], k_full[6], k_empty[6], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], o_done[2], drain;
     uint32_t tmem;
+    __nv_bfloat16 best[2][2][kM];             // [X][half of the keys][query]: maxima
 };
-static_assert(sizeof(Small) <= 1024, "small area");
+static_assert(sizeof(Small) <= 2048, "small area");
 
 struct Maps {
     CUtensorMap q, k, v, r;
@@ -70,6 +79,19 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_parked(bar, parity, kWaitNs));
 }
 
+// OR of a predicate over the warps of query tile X; also a barrier between them.
+__device__ __forceinline__ bool tile_or(int X, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, %2, %3, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)pred), "r"(1 + X), "n"(kSoft)
+        : "memory");
+    return r != 0;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -153,26 +175,26 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
             mbar_init(&sw->v_full[i], 1);
             mbar_init(&sw->v_empty[i], 1);
             mbar_init(&sw->s_full[i], 1);
-            mbar_init(&sw->p_half[i], 4);
-            mbar_init(&sw->p_full[i], 4);
+            mbar_init(&sw->p_half[i], 8);
+            mbar_init(&sw->p_full[i], 8);
             mbar_init(&sw->o_done[i], 1);
         }
         for (int i = 0; i < (int)G::kKSlots; ++i) { mbar_init(&sw->k_full[i], 1); mbar_init(&sw->k_empty[i], 1); }
         mbar_init(&sw->drain, 1);
         fence_mbar_init();
     }
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_alloc(&sw->tmem, 512);
         tmem_relinquish();
     }
-    if (warp == 8 && lane < 4) tma_prefetch_desc(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : &maps.r);
+    if (warp == 16 && lane < 4) tma_prefetch_desc(lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : &maps.r);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = sw->tmem;             // columns: S_A, S_B, O_A, O_B
     bool ok = true;
 
-    if (warp == 8) {                          // ------------------------------------------------ producer
+    if (warp == 16) {                         // ------------------------------------------------ producer
         uint32_t k_loads = 0, v_loads = 0, q_loads = 0;
         if (elect_one()) {
             auto load_k = [&](int j) {
@@ -220,7 +242,7 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
             }
         }
         __syncwarp();
-    } else if (warp == 9) {                   // ------------------------------------------------ issuer
+    } else if (warp == 17) {                  // ------------------------------------------------ issuer
         constexpr uint32_t id_s = idesc_bf16_f32(kM, kN, false, false), id_o = idesc_bf16_f32(kM, kHead, false, true);
         const uint64_t dq = smem_desc(smem_u32(sm + G::kQ), 16, 1024, kSwizzle128B);
         const uint64_t dk = smem_desc(smem_u32(sm + G::kK), 16, 1024, kSwizzle128B);
@@ -258,13 +280,16 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
             const bool first = X == 0 || j >= ta, last = X == 1 || j >= tc;
             const uint64_t y = desc_at(dv, (j & 1) * 32768);
             if (first && !(ok = wait_warp(&sw->v_full[j & 1], (j >> 1) & 1))) return;
+            // keys 0-31 and 64-95 first, then the others
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (!(ok = wait_warp(half ? &sw->p_full[X] : &sw->p_half[X], j & 1))) return;
+            for (int part = 0; part < 2; ++part) {
+                if (!(ok = wait_warp(part ? &sw->p_full[X] : &sw->p_half[X], j & 1))) return;
                 tc_fence_after();
 #pragma unroll
-                for (int i = 4 * half; i < 4 * half + 4; ++i)
+                for (int k = 0; k < 4; ++k) {
+                    const int i = 2 * part + (k & 1) + 4 * (k >> 1);
                     mma_ts_elected(tb + 256 + X * 128, tb + X * 128 + i * 8, desc_at(y, i * 2048), id_o, j > 0 || i > 0, el);
+                }
             }
             if (last) mma_commit_elected(&sw->v_empty[j & 1], el);
             if (j + 1 == (X ? tc : ta)) mma_commit_elected(&sw->o_done[X], el);
@@ -289,59 +314,67 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
             if (lane == 0) atomicOr(a.status, kStatusTimeout);
         }
     } else {                                  // ------------------------------------------------ softmax of tile X
-        const int X = warp >> 2, w = warp & 3, t = tid & 127;
+        // warps 0-3 of a tile take the first 64 keys of each query, warps 4-7 the others
+        const int X = warp >> 3, half = (warp >> 2) & 1, w = warp & 3, t = tid & 127;
         const int64_t i = x.q0 + X * kM + t;  // the thread's query in its sequence
         const int64_t seen = (int64_t)x.nk - x.nq + i + 1;
         const float c2 = a.scale * 1.44269504088896340736f;
-        const uint32_t ts = tmem_addr(tb, 32 * w, X * 128), to = tmem_addr(tb, 32 * w, 256 + X * 128);
+        const uint32_t ts = tmem_addr(tb, 32 * w, X * 128), to = tmem_addr(tb, 32 * w, 256 + X * 128 + 64 * half);
         float m = -INFINITY, l = 0.f;
         const int count = tiles[X];
         for (int j = 0; j < count; ++j) {
-            if (!(ok = wait_warp(&sw->s_full[X], j & 1))) break;
+            ok = ok && wait_warp(&sw->s_full[X], j & 1);
             tc_fence_after();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, s[b]);
+            uint32_t s[2][32];
+            tmem_ld32(ts + 64 * half, s[0]);
+            tmem_ld32(ts + 64 * half + 32, s[1]);
             tmem_wait_ld();
-            const int64_t lim = seen - (int64_t)j * kN;              // columns that the query sees
-            if (__any_sync(0xffffffffu, lim < kN)) {
-                const int edge = lim < 0 ? 0 : (lim < kN ? (int)lim : kN);
+            const int64_t lim = seen - (int64_t)j * kN - 64 * half;  // of these columns, those that the query sees
+            if (__any_sync(0xffffffffu, lim < 64)) {
+                const int edge = lim < 0 ? 0 : (lim < 64 ? (int)lim : 64);
 #pragma unroll
-                for (int k = 0; k < kN; ++k)
+                for (int k = 0; k < 64; ++k)
                     if (k >= edge) s[k >> 5][k & 31] = 0xff800000u;  // -inf
             }
-            float part[4];                    // four chains of three-way maxima
+            float part[2];                    // two chains of three-way maxima
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < 2; ++b) {
                 part[b] = max3(__uint_as_float(s[b][0]), __uint_as_float(s[b][1]), __uint_as_float(s[b][2]));
 #pragma unroll
                 for (int k = 3; k < 31; k += 2)
                     part[b] = max3(part[b], __uint_as_float(s[b][k]), __uint_as_float(s[b][k + 1]));
-                part[b] = fmaxf(part[b], __uint_as_float(s[b][31]));
             }
-            const float mx = fmaxf(max3(part[0], part[1], part[2]), part[3]);
+            const __nv_bfloat16 mine =
+                __float2bfloat16_rn(fmaxf(max3(part[0], part[1], __uint_as_float(s[0][31])), __uint_as_float(s[1][31])));
+            // The two threads of a query exchange their maxima, in bf16: m need not be the largest score, only near
+            // it and the same in both.  Behind the barrier every score is in registers, so the weights may go over
+            // them; the slots are written again behind s_full, which waits for this tile's weights.  A wait that
+            // ran out ends all of the tile's warps here
+            sw->best[X][half][t] = mine;
+            if (tile_or(X, !ok)) { ok = false; break; }
+            const float mx = fmaxf(__bfloat162float(mine), __bfloat162float(sw->best[X][half ^ 1][t]));
             float f = 1.f;
             if (mx > m && (mx - m) * c2 > kRaise) {                  // also the first finite maximum
                 f = exp2_fast((m - mx) * c2);
                 m = mx;
             }
             l *= f;
-            if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {        // rescale the warp's rows of O
+            if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {        // rescale the warp's half rows of O
 #pragma unroll 1
                 for (int b = 0; b < 4; ++b) {
-                    uint32_t o[32];
-                    tmem_ld32(to + 32 * b, o);
+                    uint32_t o[16];
+                    tmem_ld16(to + 16 * b, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                    tmem_st32(to + 32 * b, o);
+                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tmem_st16(to + 16 * b, o);
                 }
             }
             if ((int64_t)(j + 1) * kN > x.nk) {                      // value rows behind the sequence's end become zeros
-                if (!(ok = wait_warp(&sw->v_full[j & 1], (j >> 1) & 1))) break;
-                if (j * kN + t >= x.nk)
-                    for (int k = 0; k < 16; ++k)
-                        *reinterpret_cast<uint4*>(sm + G::kV + (j & 1) * 32768 + (k >> 3) * 16384 + t * 128 + (k & 7) * 16) =
+                ok = wait_warp(&sw->v_full[j & 1], (j >> 1) & 1);
+                if (ok && j * kN + t >= x.nk)
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4*>(sm + G::kV + (j & 1) * 32768 + half * 16384 + t * 128 + k * 16) =
                             make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
             }
@@ -349,7 +382,7 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
             const float2 c22 = make_float2(c2, c2), z2 = make_float2(z, z);
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < 2; ++b) {
                 uint32_t p[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
@@ -359,25 +392,29 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
                     sum = add2(sum, y);
                     p[k] = pack_bf16x2(y.x, y.y);
                 }
-                tmem_st16(ts + 16 * b, p);
-                if (b & 1) {                  // half of the weights: the value product can begin
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(b == 1 ? &sw->p_half[X] : &sw->p_full[X]);
-                }
+                tmem_st16(ts + 32 * half + 16 * b, p);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(b ? &sw->p_full[X] : &sw->p_half[X]);   // the product of half can begin
             }
             l += sum.x + sum.y;
         }
-        if (ok && count) ok = wait_warp(&sw->o_done[X], 0);
-        if (ok) {                             // a thread stores its query's row
+        if (count) {
+            ok = ok && wait_warp(&sw->o_done[X], 0);
+            float* sums = reinterpret_cast<float*>(sm + G::kQ + X * G::kSlices * 16384);   // the queries are done with
+            sums[half * kM + t] = l;
+            ok = !tile_or(X, !ok);
+            l = sums[t] + sums[kM + t];
+        }
+        if (ok) {                             // a thread stores half of its query's row
             tc_fence_after();
             const int64_t row = (x.qb + i) * a.H + x.h;
             const bool live = i < x.nq && KDA_INDEX_OK(row, a.total_q * a.H, a.status);
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * kHead);
+            uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * kHead + 64 * half);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < 2; ++b) {
                 uint32_t o[32];
                 if (count) {
                     tmem_ld32(to + 32 * b, o);
@@ -398,7 +435,7 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
                     }
                 }
             }
-            if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
+            if (live && a.lse && half == 0) a.lse[row] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
         } else if (lane == 0) {
             atomicOr(a.status, kStatusTimeout);
         }
@@ -406,7 +443,7 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_dealloc(tb, 512);
+    if (warp == 17) tmem_dealloc(tb, 512);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode() {
