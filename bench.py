@@ -665,7 +665,8 @@ def run_ours(args):
     ranks.close()
 
 
-PROFILE_CASES = ("prefill", "decode_chunk_T16", "decode_chunk_T4", "split_T32768", "frontend", "prefill_gated")
+PROFILE_CASES = ("prefill", "decode_chunk_T16", "decode_chunk_T4", "split_T32768", "frontend", "prefill_gated",
+                 "latent_decode", "latent_prefill")
 
 
 def run_profile_case(name):
@@ -709,6 +710,18 @@ def run_profile_case(name):
         cu = w.cu_seqlens.to(dev)
         call = lambda: kda.kda_prefill_gated(w.q, w.k, w.v, w.log_alpha, w.beta, lx.g_raw, lx.norm_weight,
                                              cu_seqlens=cu, out=out, final_state=fin)
+    elif name == "latent_decode":                       # 64 sequences of 2048..8192 cached tokens, 32 heads
+        lw = workloads.make_latent_inputs([2048 + 96 * i for i in range(64)], H, seed=17, device=dev)
+        ws = torch.empty(kda.kda_latent_decode_workspace_size(64, 64, H), dtype=torch.uint8, device=dev)
+        out = torch.empty_like(lw.q_latent)
+        call = lambda: kda.kda_latent_decode(lw.q_latent, lw.q_rope, lw.cache, lw.block_table, lw.seq_lens,
+                                             192 ** -0.5, out=out, workspace=ws)
+    elif name == "latent_prefill":                      # one prompt of T tokens, 32 heads
+        q = torch.randn(T, H, 192, device=dev).to(torch.bfloat16)
+        kv = torch.randn(T, H, 256, device=dev).to(torch.bfloat16)
+        kr = torch.randn(T, 64, device=dev).to(torch.bfloat16)
+        out = torch.empty(T, H, D, dtype=torch.bfloat16, device=dev)
+        call = lambda: kda.kda_latent_prefill(q, kv[..., :D], kv[..., D:], kr, 192 ** -0.5, out=out)
     else:
         raise SystemExit(f"unknown profile case {name}")
     for _ in range(3):

@@ -25,6 +25,9 @@ conv q, conv k, conv v, norm weight):
   a_raw ~ N(mu, 1) fp32 (decay logits; logsigmoid of it is log_alpha);
   b_raw ~ N(0, 1), gate logits g_raw ~ N(0, 1) in the input dtype;
   convolution taps ~ N(0, 1/W) fp32 (width W), norm weight ~ 1 + N(0, 0.1) fp32.
+
+Latent attention (``make_latent_inputs``): a paged cache with its pages in random order and a decode step's
+queries, all ~ N(0, 1) in bf16 (the latent is normalised before it is cached).
 """
 from __future__ import annotations
 
@@ -141,6 +144,35 @@ def make_layer_inputs(T, H, dk, dv, W=4, dtype=torch.bfloat16, seed=0, alpha_mu=
         cu = torch.as_tensor(cu_seqlens, dtype=torch.int32).cpu()
     return LayerInputs(name, q.to(dtype), k.to(dtype), v.to(dtype), a.contiguous(), b.to(dtype),
                        g.to(dtype), cq, ck, cv, nw, cu)
+
+
+@dataclass
+class LatentInputs:
+    name: str
+    cache: torch.Tensor        # [pages, page_size, 512 + rope] bf16
+    block_table: torch.Tensor  # [N, max_pages] int32, pages in random order
+    seq_lens: torch.Tensor     # [N] int32, the step's tokens included
+    q_latent: torch.Tensor     # [N * tokens, H, 512] bf16
+    q_rope: torch.Tensor | None  # [N * tokens, H, rope] bf16
+
+
+def make_latent_inputs(lengths, H, tokens=1, page_size=64, rope=64, seed=0, device="cpu", name="latent"):
+    """A paged latent cache holding `lengths` tokens a sequence, and a decode step's queries; all values
+    ~ N(0, 1) in bf16."""
+    gen = torch.Generator(device=device)
+    gen.manual_seed(int(seed))
+    pages = [-(-int(n) // page_size) for n in lengths]
+    order = torch.randperm(max(sum(pages), 1), generator=gen, device=device).to(torch.int32)
+    table = torch.full((len(pages), max(pages + [1])), -1, dtype=torch.int32, device=device)
+    at = 0
+    for n, k in enumerate(pages):
+        table[n, :k] = order[at:at + k]
+        at += k
+    cache = _normal((order.numel(), page_size, 512 + rope), gen, device).to(torch.bfloat16)
+    rows = len(pages) * tokens
+    q = _normal((rows, H, 512), gen, device).to(torch.bfloat16)
+    r = _normal((rows, H, rope), gen, device).to(torch.bfloat16) if rope else None
+    return LatentInputs(name, cache, table, torch.tensor([int(n) for n in lengths], dtype=torch.int32, device=device), q, r)
 
 
 def varlen_lengths(num_seqs, seed, lo=128, hi=32768):
