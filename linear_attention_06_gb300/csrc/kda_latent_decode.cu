@@ -26,6 +26,12 @@
 // into P.  The running maximum m is only raised when a score exceeds it by more than 2^8: P then stays below 2^8
 // in bf16, whose precision does not depend on the exponent, sums are fp32, and the rescaling of O in tensor
 // memory is rare.  P is rounded to bf16 for the tensor cores; its sum is taken before that rounding.
+//
+// Measured (GB300, 6688 GB/s measured copy rate), 32 heads, one token: 608 x 4096 cached tokens 445 us, 0.96 of that
+// rate; 64 x 8192 110 us (0.82); 1 x 131072 40 us (0.56).  What is missing there is fixed: 3 us until a block's first
+// load (lengths, then page entries), 3 us from its last row to its result, 3-5 us of join; and the SMs' unequal shares
+// of the bandwidth (their ends are spread over 5%).  128 heads, 64 x 8192: 220 us, 660 TFLOP/s: two groups of 64 rows,
+// each with room for two tiles only, so that a tile's load waits for the one before the last.
 #include <atomic>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -77,6 +83,7 @@ struct Small {
     uint64_t o_free, drain;
     uint32_t tmem;
     int seq0, off0, lead0, len0, runs;
+    int piece[5], more;                       // the softmax warps' piece
     int64_t total, begin, end;
     alignas(16) float fac[64];                // rescaling factors
     alignas(16) float inv[64];                // 1 / l at a piece's end
@@ -107,7 +114,7 @@ struct Walk {
     int64_t left;
     __device__ Walk(const Small* sw) : n(sw->seq0), off(sw->off0), lead(sw->lead0), len(sw->len0), left(sw->end - sw->begin) {}
     __device__ __forceinline__ bool next(const LatentDecodeArgs& a, Piece& p) {
-        if (left <= 0) return false;
+        if (left <= 0 || n >= a.num_seqs) return false;
         p.n = n;
         p.len = len >= 0 ? len : clamped_len(a.c, a.seq_lens, n);
         len = -1;
@@ -277,7 +284,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
     const uint32_t tb = sw->tmem;
     const uint32_t ts = tb + 4 * NR;          // S buffers
     bool ok = true;
-    uint32_t loads = 0;                       // producer: latent pairs issued
+    uint32_t loads = 0, rope_loads = 0;       // producer: latent pairs and rope slices issued
 
     if (warp == 0) {                          // ------------------------------------------------ producer
         const int box = a.c.page_size < kTile ? a.c.page_size : kTile;
@@ -336,6 +343,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                         tma_load_2d(sm + G::kRopeAt + rope.slot * 8192 + piece * box * 128, &maps.c, kLatent, row,
                                     &sw->rope_full[rope.slot]);
                     rope.next();
+                    ++rope_loads;
                     if (rope.slot == 0) rope_used = true;
                 }
                 prefetch(rows_ahead[kAhead], p.off + j + kAhead);
@@ -346,6 +354,8 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
         if (!ok && lane == 0) {               // copies in flight land before the block ends
             for (uint32_t i = 0; i < G::kPairs; ++i)
                 if (loads > i) mbar_wait_bounded(&sw->full[i], ((loads - 1 - i) / G::kPairs) & 1, kWaitNs);
+            for (uint32_t i = 0; i < G::kRopeSlots; ++i)
+                if (rope_loads > i) mbar_wait_bounded(&sw->rope_full[i], ((rope_loads - 1 - i) / G::kRopeSlots) & 1, kWaitNs);
         }
     } else if (warp == 1) {                   // ------------------------------------------------ issuer
         constexpr uint32_t id_s = idesc_bf16_f32(64, 64, false, false);
@@ -452,13 +462,22 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
         const uint32_t lanes = tmem_addr(tb, 32 * w, 0);
         const uint32_t s_lanes = tmem_addr(ts, 32 * w, 0);
         Walk walk(sw);
-        Piece p;
+        Piece p{};
         Ring<G::kPairs> in;                   // the tile's first latent pair
         Ring<2> sb, prev;                     // this tile's buffers; the previous tile's
         bool first_piece = true, used0 = false, used1 = false;
         Head head{-1, 0, 0, 0};
         int64_t at = sw->begin + sw->lead0;   // the piece's first tile in the line
-        while (ok && walk.next(a, p)) {
+        while (ok) {
+            // one thread reads the next sequence's length for all: these warps meet at barriers and must agree on the
+            // number of tiles, whatever a caller does to the lengths meanwhile
+            if (t == 0) {
+                sw->more = walk.next(a, p);
+                sw->piece[0] = p.n; sw->piece[1] = p.len; sw->piece[2] = p.off; sw->piece[3] = p.tiles; sw->piece[4] = p.all;
+            }
+            soft_sync();
+            if (!sw->more) break;
+            p = Piece{sw->piece[0], sw->piece[1], sw->piece[2], sw->piece[3], sw->piece[4]};
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
             int seen[2];
 #pragma unroll

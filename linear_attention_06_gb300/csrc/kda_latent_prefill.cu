@@ -62,9 +62,16 @@ struct Cfg {
     static_assert(kBytes <= 232448, "shared memory");
 };
 
+struct Place {                                // a block's sequence, 256 queries and head
+    int n, h;
+    int64_t qb, q0, kb;                       // sequence's first query, this tile's first query in it, first key
+    int nq, nk;
+};
+
 struct Small {
     uint64_t q_full[2], k_full[6], k_empty[6], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], o_done[2], drain;
     uint32_t tmem;
+    int count[2];                             // key tiles of A and B, as one thread read them
     __nv_bfloat16 best[2][2][kM];             // [X][half of the keys][query]: maxima
 };
 static_assert(sizeof(Small) <= 2048, "small area");
@@ -116,11 +123,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // The block's sequence, 256-query tile and head.  Tile slots: sequence n's start at floor(b_n / 256) + n, so that
 // ceil(T / 256) + N slots hold any lengths and a block finds its own by bisection.  Heads go in groups whose keys
 // stay in L2, and slots from the last (the longest rows of a sequence) down, so that the lightest end the launch.
-struct Place {
-    int n, h;
-    int64_t qb, q0, kb;                       // sequence's first query, this tile's first query in it, first key
-    int nq, nk;
-};
 __device__ __forceinline__ bool find_place(const LatentPrefillArgs& a, int64_t slots, Place& x) {
     const int64_t b = blockIdx.x, per = slots * kHeadsTogether;
     const int first = (int)(b / per) * kHeadsTogether;
@@ -182,6 +184,8 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
         for (int i = 0; i < (int)G::kKSlots; ++i) { mbar_init(&sw->k_full[i], 1); mbar_init(&sw->k_empty[i], 1); }
         mbar_init(&sw->drain, 1);
         fence_mbar_init();
+        sw->count[0] = tiles[0];
+        sw->count[1] = tiles[1];
     }
     if (warp == 17) {
         tmem_alloc(&sw->tmem, 512);
@@ -321,7 +325,9 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
         const float c2 = a.scale * 1.44269504088896340736f;
         const uint32_t ts = tmem_addr(tb, 32 * w, X * 128), to = tmem_addr(tb, 32 * w, 256 + X * 128 + 64 * half);
         float m = -INFINITY, l = 0.f;
-        const int count = tiles[X];
+        // one thread's count for all: these warps meet at barriers and must agree on it, whatever a caller does to
+        // the tables meanwhile
+        const int count = sw->count[X];
         for (int j = 0; j < count; ++j) {
             ok = ok && wait_warp(&sw->s_full[X], j & 1);
             tc_fence_after();
