@@ -58,7 +58,7 @@ struct Cfg {
     static constexpr uint32_t kK = kV + 65536;
     static constexpr uint32_t kKSlots = DK == 192 ? 4 : 6;
     static constexpr uint32_t kSmall = kK + kKSlots * 16384;
-    static constexpr uint32_t kBytes = kSmall + 2048 + 1024;      // + alignment slack
+    static constexpr uint32_t kBytes = kSmall + 2560;
     static_assert(kBytes <= 232448, "shared memory");
 };
 
@@ -72,9 +72,9 @@ struct Small {
     uint64_t q_full[2], k_full[6], k_empty[6], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2], o_done[2], drain;
     uint32_t tmem;
     int count[2];                             // key tiles of A and B, as one thread read them
-    __nv_bfloat16 best[2][2][kM];             // [X][half of the keys][query]: maxima
+    float best[2][2][kM];                     // [X][half of the keys][query]: maxima
 };
-static_assert(sizeof(Small) <= 2048, "small area");
+static_assert(sizeof(Small) <= 2560, "small area");
 
 struct Maps {
     CUtensorMap q, k, v, r;
@@ -162,8 +162,11 @@ template <int DK>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs a, const int64_t slots) {
     using G = Cfg<DK>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t sm[];   // swizzled tiles start at multiples of 1024 bytes
+    if (smem_u32(sm) & 1023u) {               // the declaration's alignment; without it there would be no room for slack
+        if (threadIdx.x == 0) atomicOr(a.status, kStatusTimeout);
+        return;
+    }
     Small* sw = reinterpret_cast<Small*>(sm + G::kSmall);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     Place x;
@@ -350,15 +353,13 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
                 for (int k = 3; k < 31; k += 2)
                     part[b] = max3(part[b], __uint_as_float(s[b][k]), __uint_as_float(s[b][k + 1]));
             }
-            const __nv_bfloat16 mine =
-                __float2bfloat16_rn(fmaxf(max3(part[0], part[1], __uint_as_float(s[0][31])), __uint_as_float(s[1][31])));
-            // The two threads of a query exchange their maxima, in bf16: m need not be the largest score, only near
-            // it and the same in both.  Behind the barrier every score is in registers, so the weights may go over
-            // them; the slots are written again behind s_full, which waits for this tile's weights.  A wait that
-            // ran out ends all of the tile's warps here
+            const float mine = fmaxf(max3(part[0], part[1], __uint_as_float(s[0][31])), __uint_as_float(s[1][31]));
+            // The two threads of a query exchange their maxima.  Behind the barrier every score is in registers, so
+            // the weights may go over them; the slots are written again behind s_full, which waits for this tile's
+            // weights.  A wait that ran out ends all of the tile's warps here
             sw->best[X][half][t] = mine;
             if (tile_or(X, !ok)) { ok = false; break; }
-            const float mx = fmaxf(__bfloat162float(mine), __bfloat162float(sw->best[X][half ^ 1][t]));
+            const float mx = fmaxf(mine, sw->best[X][half ^ 1][t]);
             float f = 1.f;
             if (mx > m && (mx - m) * c2 > kRaise) {                  // also the first finite maximum
                 f = exp2_fast((m - mx) * c2);
