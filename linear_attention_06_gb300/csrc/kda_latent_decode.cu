@@ -69,7 +69,7 @@ struct Cfg {
     static constexpr uint32_t kRopeAt = kP + 2 * kSlice, kPairAt = kRopeAt + kRopeSlots * 8192;
     static constexpr uint32_t kPairs = (225 * 1024 - kPairAt) / 16384;
     static constexpr uint32_t kSmall = kPairAt + kPairs * 16384;
-    static constexpr uint32_t kBytes = kSmall + 1024 + 1024;      // + alignment slack
+    static constexpr uint32_t kBytes = kSmall + 1024;
     static constexpr uint32_t kCols = NR == 64 ? 512 : 256;       // TMEM: O^T 4 NR, S 2 x 64
     static_assert(kBytes <= 232448, "shared memory");
     static_assert(64 * 128 <= kSmall - (kSlices - 1) * kSlice, "the M = 64 operand stays inside the block's memory");
@@ -243,8 +243,11 @@ template <int NR, bool ROPE>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a, const int groups, const int map_rows) {
     using G = Cfg<NR, ROPE>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t sm[];   // swizzled tiles start at multiples of 1024 bytes
+    if (smem_u32(sm) & 1023u) {               // the declaration's alignment
+        if (threadIdx.x == 0) atomicOr(a.status, kStatusTimeout);
+        return;
+    }
     Small* sw = reinterpret_cast<Small*>(sm + G::kSmall);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int runs = gridDim.x / groups, run = blockIdx.x / groups, group = blockIdx.x % groups;
