@@ -27,11 +27,11 @@
 // in bf16, whose precision does not depend on the exponent, sums are fp32, and the rescaling of O in tensor
 // memory is rare.  P is rounded to bf16 for the tensor cores; its sum is taken before that rounding.
 //
-// Measured (GB300, 6688 GB/s measured copy rate), 32 heads, one token: 608 x 4096 cached tokens 445 us, 0.96 of that
-// rate; 64 x 8192 110 us (0.82); 1 x 131072 40 us (0.56).  What is missing there is fixed: 3 us until a block's first
-// load (lengths, then page entries), 3 us from its last row to its result, 3-5 us of join; and the SMs' unequal shares
-// of the bandwidth (their ends are spread over 5%).  128 heads, 64 x 8192: 220 us, 660 TFLOP/s: two groups of 64 rows,
-// each with room for two tiles only, so that a tile's load waits for the one before the last.
+// Measured (GB300, 6688 GB/s measured copy rate), 32 heads, one token: 608 x 4096 cached tokens 411 us, 1.04 of that
+// rate; 64 x 8192 104.6 us (0.86); 1 x 131072 36.3 us (0.62).  What is missing there is fixed: 3 us until a block's
+// first load (lengths, then page entries), 3 us from its last row to its result, 3-5 us of join; and the SMs' unequal
+// shares of the bandwidth (their ends are spread over 5%).  128 heads, 64 x 8192: 216 us, 676 TFLOP/s: two groups of
+// 64 rows, each with room for two tiles only, so that a tile's load waits for the one before the last.
 #include <atomic>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -55,7 +55,6 @@ constexpr int kThreads = 256;                 // warps 0-3: producer, issuer, qu
 constexpr int kSoft = 128;
 constexpr int kBar = 1;                       // named barrier of the softmax warps
 constexpr int kSMs = 152;
-constexpr int kAhead = 3;                     // tiles between a tile's prefetch into L2 and its loads
 constexpr float kRaise = 8.f;                 // log2 of how far a score may exceed the running maximum
 constexpr uint64_t kWaitNs = 4000000000ull;   // bound of every wait
 
@@ -309,20 +308,20 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                 const int page = a.c.block_table[table + (pos >> shift)];
                 return page < 0 || page >= a.c.num_pages ? map_rows : (page << shift) + (pos & (a.c.page_size - 1));
             };
-            // a page's rows lie in a row: one prefetch into L2 for each box, kAhead tiles before its loads.  The
-            // first tiles of a piece are only loaded: their ring slots are free
+            // Where a tile lies on one page, the next tile is prefetched into L2 behind this one's loads, in one
+            // request: its own loads wait for ring slots and then find it near.  Further ahead is slower (64 x 8192
+            // cached tokens, 32 heads: 104.6 us one tile ahead, 106.7 two, 112.5 three, 136 five, 106.9 without):
+            // the rows wait in both halves of L2.  So are prefetches of several small pages a tile (pages of 16:
+            // 118.7 us with, 112.3 without).
             auto prefetch = [&](int r, int x) {
-                const int left = p.len - x * kTile - piece * box;
-                if (half == 0 && r >= 0 && r < map_rows)
+                const int left = p.len - x * kTile;
+                if (box == kTile && half == 0 && r >= 0 && r < map_rows)
                     bulk_prefetch_l2(static_cast<const uint8_t*>(a.c.cache) + (int64_t)r * width * 2,
-                                     (uint32_t)(left < box ? left : box) * width * 2);
+                                     (uint32_t)(left < kTile ? left : kTile) * width * 2);
             };
-            int rows_ahead[kAhead + 1];       // rows of tiles j .. j + kAhead
-#pragma unroll
-            for (int d = 0; d < kAhead; ++d) rows_ahead[d] = d < p.tiles ? row_of(p.off + d) : -1;
+            int row = row_of(p.off);
             for (int j = 0; ok && j < p.tiles; ++j) {
-                rows_ahead[kAhead] = j + kAhead < p.tiles ? row_of(p.off + j + kAhead) : -1;
-                const int row = rows_ahead[0];
+                const int next_row = j + 1 < p.tiles ? row_of(p.off + j + 1) : -1;
                 const int live = p.len - (p.off + j) * kTile;
                 const int valid = live < 0 ? 0 : (live < kTile ? live : kTile);
                 const uint32_t boxes = (valid + box - 1) / box;
@@ -349,9 +348,8 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                     ++rope_loads;
                     if (rope.slot == 0) rope_used = true;
                 }
-                prefetch(rows_ahead[kAhead], p.off + j + kAhead);
-#pragma unroll
-                for (int d = 0; d < kAhead; ++d) rows_ahead[d] = rows_ahead[d + 1];
+                prefetch(next_row, p.off + j + 1);
+                row = next_row;
             }
         }
         if (!ok && lane == 0) {               // copies in flight land before the block ends
