@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libkda (argument marshalling only).
+"""Thin binding of libkda (argument marshalling only): ctypes, and for the short latent-attention calls the
+compiled module built from csrc/latent_binding.cpp.
 
 Every step of the KDA path runs in the CUDA library; this module only turns
 torch tensors into the pointers, sizes and stream that ``include/kda.h``
@@ -9,6 +10,7 @@ missing, loading fails with an error that says how to build it.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -378,77 +380,25 @@ def kda_decode_step(q, k, v, log_alpha, beta, state, out=None, stream=None):
 
 # ---------------------------------------------------------------- latent attention
 
-_LATENT, _ROPE, _HEAD = 512, 64, 128
+_ENTRIES = ("kda_latent_append", "kda_latent_gather", "kda_latent_decode", "kda_latent_decode_workspace_size",
+            "kda_latent_prefill")
+_native = None
 
 
-def _expect(name, t, shape, dtype, index, strides=False):
-    """The address of a tensor argument of the latent-attention calls, its shape, type and device (CUDA
-    device `index`) checked; contiguous unless the call takes its strides."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == index and (strides or t.is_contiguous()):
-        return t.data_ptr()
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}, not on {t.device}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _row_stride(name, t):
-    """Elements between consecutive rows of t [..., channels], all its leading axes one run of rows."""
-    width = t.shape[-1]
-    if t.is_contiguous():
-        return max(width, 8)
-    strides = t.stride()
-    if width > 1 and strides[-1] != 1:
-        raise ValueError(f"{name}: channels must be contiguous")
-    rows, step = 1, None
-    for d in range(len(strides) - 2, -1, -1):
-        size = t.shape[d]
-        if size > 1:
-            if step is None:
-                step = strides[d]
-                if step < width * rows or step % rows:
-                    raise ValueError(f"{name}: rows must not overlap")
-            elif strides[d] != step * rows:
-                raise ValueError(f"{name}: rows must be evenly spaced")
-            rows *= size
-    return max(width, 8) if step is None else step
-
-
-def _cuda(t):
-    if not t.is_cuda:
-        raise ValueError("tensor arguments must be CUDA tensors")
-    return t.get_device()
-
-
-def _table(name, table, tokens, n, index):
-    """The address (and the tensor, to keep it alive) of a cu_seqlens argument: a CUDA int32 tensor as it is, a
-    host table validated and copied.  n: the sequences it must have, or None."""
-    if not (isinstance(table, torch.Tensor) and table.is_cuda):
-        host = torch.as_tensor(table, dtype=torch.int32).cpu()
-        kda_check_cu_seqlens(host, tokens)
-        table = host.to(torch.device("cuda", index))
-    if n is None:
-        if table.dim() != 1 or table.numel() < 1:
-            raise ValueError(f"{name} must hold N + 1 offsets")
-        n = table.shape[0] - 1
-    return _expect(name, table, (n + 1,), torch.int32, index), table
-
-
-def _latent_cache(cache, block_table, H, tokens, index):
-    """Addresses of a latent cache and its table, and the shape descriptor of a call on them."""
-    pages, page, width = cache.shape if cache.dim() == 3 else (0, 0, 0)
-    if width != _LATENT and width != _LATENT + _ROPE:
-        raise ValueError(f"cache must be [pages, page_size, {_LATENT} or {_LATENT + _ROPE}], "
-                         f"not {tuple(cache.shape)}")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [N, max_pages]")
-    n, per = block_table.shape
-    return (_expect("cache", cache, (pages, page, width), torch.bfloat16, index),
-            _expect("block_table", block_table, (n, per), torch.int32, index),
-            KdaLatentShape(n, tokens, H, _LATENT, width - _LATENT, page, pages, per, KDA_BF16))
+def _latent():
+    """The compiled half of these calls (csrc/latent_binding.cpp), on the entry points of the loaded library."""
+    global _native
+    if _native is None:
+        path = os.path.join(_PKG, "_latent.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} not found: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
+        spec = importlib.util.spec_from_file_location("_latent", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        L = lib()
+        module.bind({name: ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _ENTRIES}, _check)
+        _native = module
+    return _native
 
 
 def _on(stream, t):
@@ -459,16 +409,15 @@ def _on(stream, t):
     return torch.cuda.stream(stream)
 
 
-def _call(fn, index, *args):
-    """Call the library's fn(*args, stream) on the current stream of the tensors' device, that device current."""
-    f = getattr(_lib or lib(), fn)
-    if torch.cuda.current_device() == index:
-        st = f(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(index):
-            st = f(*args, torch._C._cuda_getCurrentRawStream(index))
-    if st != KDA_OK:
-        raise KdaError(fn, st, status_string(st))
+def _table(table, tokens, t):
+    """A cu_seqlens argument: a CUDA tensor as it is, a host table validated and copied to t's device."""
+    if table is None or (isinstance(table, torch.Tensor) and table.is_cuda):
+        return table
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must be CUDA tensors")
+    host = torch.as_tensor(table, dtype=torch.int32).cpu()
+    kda_check_cu_seqlens(host, tokens)
+    return host.to(t.device)
 
 
 def kda_latent_append(latent, k_rope, cache, block_table, seq_lens, inv_freq=None, interleaved=False, q_rope=None,
@@ -480,38 +429,14 @@ def kda_latent_append(latent, k_rope, cache, block_table, seq_lens, inv_freq=Non
     int32; seq_lens: [N] int32, the lengths including these tokens.  ``inv_freq`` [32] fp32 gives the
     angles a position (None: no rotation).  ``q_rope`` [T, H, 64], possibly the end of longer rows, is
     rotated into ``q_rope_out`` (allocated when not given; q_rope itself rotates in place), which is
-    returned; None without queries."""
+    returned; None without queries.  ``cu_seqlens``: a CUDA int32 tensor or a host table (None: equal
+    numbers of tokens)."""
     if stream is not None:
         with _on(stream, cache):
             return kda_latent_append(latent, k_rope, cache, block_table, seq_lens, inv_freq, interleaved, q_rope,
                                      q_rope_out, cu_seqlens)
-    dev = _cuda(cache)
-    T, H = latent.shape[0], 1 if q_rope is None else q_rope.shape[1]
-    p_cache, p_table, shape = _latent_cache(cache, block_table, H, T, dev)
-    n, rope = shape.num_seqs, shape.rope_dim
-    p_rope = p_freq = p_cu = p_q = p_out = None
-    rope_step = q_step = out_step = 0
-    p_latent = _expect("latent", latent, (T, _LATENT), torch.bfloat16, dev, True)
-    if rope:
-        p_rope = _expect("k_rope", k_rope, (T, _ROPE), torch.bfloat16, dev, True)
-        rope_step = _row_stride("k_rope", k_rope)
-    p_lens = _expect("seq_lens", seq_lens, (n,), torch.int32, dev)
-    if inv_freq is not None:
-        p_freq = _expect("inv_freq", inv_freq, (_ROPE // 2,), torch.float32, dev)
-    if cu_seqlens is not None:
-        p_cu, cu_seqlens = _table("cu_seqlens", cu_seqlens, T, n, dev)
-    if q_rope is not None:
-        p_q = _expect("q_rope", q_rope, (T, H, _ROPE), torch.bfloat16, dev, True)
-        q_step = _row_stride("q_rope", q_rope)
-        if q_rope_out is None:
-            q_rope_out = torch.empty((T, H, _ROPE), dtype=torch.bfloat16, device=cache.device)
-            p_out, out_step = q_rope_out.data_ptr(), _ROPE
-        else:
-            p_out = _expect("q_rope_out", q_rope_out, (T, H, _ROPE), torch.bfloat16, dev, True)
-            out_step = _row_stride("q_rope_out", q_rope_out)
-    _call("kda_latent_append", dev, shape, p_latent, _row_stride("latent", latent), p_rope, rope_step, p_freq,
-          1 if interleaved else 0, p_q, q_step, p_out, out_step, p_cu, p_lens, p_table, p_cache)
-    return q_rope_out if q_rope is not None else None
+    return (_native or _latent()).append(latent, k_rope, cache, block_table, seq_lens, inv_freq, interleaved, q_rope,
+                                         q_rope_out, _table(cu_seqlens, latent.shape[0], cache))
 
 
 def kda_latent_gather(cache, block_table, cu_seqlens, total_tokens, starts=None, out=None, stream=None):
@@ -520,27 +445,14 @@ def kda_latent_gather(cache, block_table, cu_seqlens, total_tokens, starts=None,
     if stream is not None:
         with _on(stream, cache):
             return kda_latent_gather(cache, block_table, cu_seqlens, total_tokens, starts, out)
-    dev = _cuda(cache)
-    T = int(total_tokens)
-    p_cache, p_table, shape = _latent_cache(cache, block_table, 1, T, dev)
-    n, rope = shape.num_seqs, shape.rope_dim
-    p_cu, cu_seqlens = _table("cu_seqlens", cu_seqlens, T, n, dev)
-    p_starts = None if starts is None else _expect("starts", starts, (n,), torch.int32, dev)
-    if out is None:
-        latent = torch.empty((T, _LATENT), dtype=torch.bfloat16, device=cache.device)
-        k_rope = torch.empty((T, rope), dtype=torch.bfloat16, device=cache.device) if rope else None
-        p_latent, p_rope = latent.data_ptr(), k_rope.data_ptr() if rope else None
-    else:
-        latent, k_rope = out
-        p_latent = _expect("latent", latent, (T, _LATENT), torch.bfloat16, dev)
-        p_rope = _expect("k_rope", k_rope, (T, rope), torch.bfloat16, dev) if rope else None
-    _call("kda_latent_gather", dev, shape, p_cache, p_table, p_cu, p_starts, p_latent, p_rope)
-    return latent, k_rope
+    latent, k_rope = (None, None) if out is None else out
+    return (_native or _latent()).gather(cache, block_table, _table(cu_seqlens, total_tokens, cache), total_tokens, starts,
+                                         latent, k_rope)
 
 
 def kda_latent_decode_workspace_size(num_seqs: int, total_tokens: int, H: int, rope_dim: int = 64) -> int:
     """Bytes of workspace kda_latent_decode needs for total_tokens / num_seqs tokens a sequence and H heads."""
-    shape = KdaLatentShape(int(num_seqs), int(total_tokens), int(H), _LATENT, int(rope_dim), 64, 0, 0, KDA_BF16)
+    shape = KdaLatentShape(int(num_seqs), int(total_tokens), int(H), 512, int(rope_dim), 64, 0, 0, KDA_BF16)
     n = ctypes.c_size_t(0)
     _check("kda_latent_decode_workspace_size",
            lib().kda_latent_decode_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
@@ -558,27 +470,9 @@ def kda_latent_decode(q_latent, q_rope, cache, block_table, seq_lens, scale, out
     if stream is not None:
         with _on(stream, cache):
             return kda_latent_decode(q_latent, q_rope, cache, block_table, seq_lens, scale, out, lse, workspace)
-    dev = _cuda(cache)
-    rows, H = q_latent.shape[0], q_latent.shape[1]
-    p_cache, p_table, shape = _latent_cache(cache, block_table, H, rows, dev)
-    p_q = _expect("q_latent", q_latent, (rows, H, _LATENT), torch.bfloat16, dev)
-    p_r = _expect("q_rope", q_rope, (rows, H, _ROPE), torch.bfloat16, dev) if shape.rope_dim else None
-    p_lens = _expect("seq_lens", seq_lens, (shape.num_seqs,), torch.int32, dev)
-    if out is None:
-        out = torch.empty((rows, H, _LATENT), dtype=torch.bfloat16, device=cache.device)
-        p_out = out.data_ptr()
-    else:
-        p_out = _expect("out", out, (rows, H, _LATENT), torch.bfloat16, dev)
-    if lse is True:
-        lse = torch.empty((rows, H), dtype=torch.float32, device=cache.device)
-    p_lse = None if lse is None else _expect("lse", lse, (rows, H), torch.float32, dev)
-    if workspace is None:
-        need = ctypes.c_size_t(0)
-        _check("kda_latent_decode", lib().kda_latent_decode_workspace_size(shape, ctypes.byref(need)))
-        workspace = torch.empty(max(need.value, 1), dtype=torch.uint8, device=cache.device)
-    _call("kda_latent_decode", dev, shape, p_q, p_r, p_cache, p_table, p_lens, float(scale), p_out, p_lse,
-          _expect("workspace", workspace, workspace.shape, torch.uint8, dev), workspace.numel())
-    return out, lse
+    new = lse is True
+    return (_native or _latent()).decode(q_latent, q_rope, cache, block_table, seq_lens, scale, out, None if new else lse,
+                                         new, workspace)
 
 
 def kda_latent_prefill(q, k, v, k_rope, scale, cu_seqlens=None, cu_seqlens_k=None, num_seqs=None, out=None,
@@ -592,38 +486,10 @@ def kda_latent_prefill(q, k, v, k_rope, scale, cu_seqlens=None, cu_seqlens_k=Non
     if stream is not None:
         with _on(stream, q):
             return kda_latent_prefill(q, k, v, k_rope, scale, cu_seqlens, cu_seqlens_k, num_seqs, out, lse)
-    dev = _cuda(q)
-    T, H, dk = q.shape
-    S = k.shape[0]
-    if dk not in (_HEAD, _HEAD + _ROPE):
-        raise ValueError(f"q must be [T, H, {_HEAD} or {_HEAD + _ROPE}], not {tuple(q.shape)}")
-    p_q = _expect("q", q, (T, H, dk), torch.bfloat16, dev)
-    p_k = _expect("k", k, (S, H, _HEAD), torch.bfloat16, dev, True)
-    p_v = _expect("v", v, (S, H, _HEAD), torch.bfloat16, dev, True)
-    p_r = _expect("k_rope", k_rope, (S, dk - _HEAD), torch.bfloat16, dev) if dk > _HEAD else None
-    step = _row_stride("k", k)
-    if S * H > 1 and step != _row_stride("v", v):
-        raise ValueError("k and v must have the same row stride")
-    n, p_cu, p_cu_k = 1 if num_seqs is None else int(num_seqs), None, None
-    if cu_seqlens is not None:
-        p_cu, cu_seqlens = _table("cu_seqlens", cu_seqlens, T, None, dev)
-        n = cu_seqlens.shape[0] - 1
-    if cu_seqlens_k is not None:
-        p_cu_k, cu_seqlens_k = _table("cu_seqlens_k", cu_seqlens_k, S, None if cu_seqlens is None else n, dev)
-        n = cu_seqlens_k.shape[0] - 1
-    elif cu_seqlens is not None and S == T:
-        p_cu_k = p_cu
-    if out is None:
-        out = torch.empty((T, H, _HEAD), dtype=torch.bfloat16, device=q.device)
-        p_out = out.data_ptr()
-    else:
-        p_out = _expect("out", out, (T, H, _HEAD), torch.bfloat16, dev)
-    if lse is True:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    p_lse = None if lse is None else _expect("lse", lse, (T, H), torch.float32, dev)
-    _call("kda_latent_prefill", dev, KdaShape(n, T, H, dk, _HEAD, KDA_BF16), S, p_q, p_k, p_v, step, p_r,
-          float(scale), p_cu, p_cu_k, p_out, p_lse)
-    return out, lse
+    new = lse is True
+    return (_native or _latent()).prefill(q, k, v, k_rope, scale, _table(cu_seqlens, q.shape[0], q),
+                                          _table(cu_seqlens_k, k.shape[0], q), 1 if num_seqs is None else num_seqs, out,
+                                          None if new else lse, new)
 
 
 def kda_device_status(stream=None) -> int:

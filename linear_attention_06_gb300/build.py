@@ -1,8 +1,10 @@
-"""In-tree build of libkda.so (CUDA, sm_103a only).
+"""In-tree build of libkda.so (CUDA, sm_103a only) and of the C++ half of its Python binding.
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel with nvcc for
 ``-gencode arch=compute_103a,code=sm_103a`` and linked into
-``linear_attention_06_gb300/libkda.so``.  Objects go to ``_build/``.  No cmake.
+``linear_attention_06_gb300/libkda.so``; ``csrc/latent_binding.cpp`` is compiled
+against the installed torch into ``linear_attention_06_gb300/_latent.so``.  Objects go
+to ``_build/``.  No cmake.
 """
 from __future__ import annotations
 
@@ -16,6 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
+BINDING = os.path.join(PKG, "_latent.so")
 HEADERS = [os.path.join(ROOT, "include", "kda.h")]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -33,6 +36,32 @@ def _stale(target, deps):
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _start_binding(force: bool):
+    """Start compiling the C++ binding of the latent-attention entry points against the installed torch, if it is
+    stale; returns (its path, the process or None)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    src = os.path.join(CSRC, "latent_binding.cpp")
+    stamp = os.path.join(BUILD, "latent_binding.txt")
+    built_for = f"torch {torch.__version__} python {sys.version}\n"
+    same = os.path.exists(stamp) and open(stamp).read() == built_for
+    if not force and same and not _stale(BINDING, [src] + HEADERS):
+        return src, None
+    with open(stamp, "w") as f:
+        f.write(built_for)
+    inc = cpp_extension.include_paths() + ["/usr/local/cuda/include", sysconfig.get_paths()["include"],
+                                           os.path.join(ROOT, "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [x for i in inc for x in ("-isystem", i)] + [src, "-o", BINDING]
+    cmd += [f"-L{p}" for p in cpp_extension.library_paths()]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    return src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None, tag=None) -> str:
@@ -55,15 +84,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, tag=None
             if verbose:
                 print(" ".join(cmd), file=sys.stderr)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    if not tag:
+        src, p = _start_binding(force)
+        if p is not None:
+            procs.append((src, p))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
         if p.returncode != 0:
             failed.append((src, out.decode(errors="replace")))
+            if src.endswith(".cpp") and os.path.exists(BINDING):
+                os.remove(BINDING)               # not an older one in its place
         elif verbose and out:
             print(out.decode(errors="replace"), file=sys.stderr)
     if failed:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(f"{s}\n{o}" for s, o in failed))
+        raise RuntimeError("compilation failed:\n" + "\n".join(f"{s}\n{o}" for s, o in failed))
     if force or _stale(lib, objs):
         cmd = [NVCC] + ARCH + ["-shared", "-o", lib] + objs
         subprocess.run(cmd, check=True)

@@ -18,7 +18,7 @@ def main() -> int:
     from linear_attention_06_gb300 import _lib
     from linear_attention_06_gb300 import build as _build
     _lib.LIB_PATH = _build.build(extra_flags=["-DKDA_CHECK_BOUNDS"], tag="bounds")
-    _lib._lib = None
+    _lib._lib = _lib._native = None
 
     import torch
 

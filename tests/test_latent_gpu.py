@@ -442,6 +442,45 @@ def test_prefill_repeats_bit_for_bit():
     assert torch.equal(a, b) and torch.equal(la, lb)
 
 
+# ---------------------------------------------------------------- what the binding refuses
+
+def test_binding_refusals():
+    g = gen(22)
+    cache, table = paged([70, 40], 16, 64, g)
+    lens = i32([70, 40])
+    lat, kr, q, qr = randn(g, 2, 512), randn(g, 2, 64), randn(g, 2, 4, 512), randn(g, 2, 4, 64)
+    ok = dict(q_latent=q, q_rope=qr, cache=cache, block_table=table, seq_lens=lens, scale=0.07)
+    kda.kda_latent_decode(**ok)
+    for bad, error in ((dict(q_latent=q.float()), TypeError), (dict(q_latent=q[0]), ValueError), (dict(q_rope=None), ValueError),
+                       (dict(q_rope=qr[:, :3]), ValueError), (dict(cache=cache[0]), ValueError), (dict(cache=cache[..., :500]), ValueError),
+                       (dict(cache=cache[:, ::2]), ValueError), (dict(block_table=table.long()), TypeError),
+                       (dict(block_table=table[0]), ValueError), (dict(seq_lens=lens[:1]), ValueError), (dict(seq_lens=lens.cpu()), ValueError),
+                       (dict(out=q[:1]), ValueError), (dict(lse=torch.empty(2, 4, dtype=BF, device=DEV)), TypeError),
+                       (dict(workspace=torch.empty(9, device=DEV)), TypeError), (dict(q_latent=q.transpose(0, 1).contiguous().transpose(0, 1)), ValueError)):
+        with pytest.raises(error):
+            kda.kda_latent_decode(**{**ok, **bad})
+    for bad, status in ((dict(scale=-1.0), 1), (dict(workspace=torch.empty(256, dtype=torch.uint8, device=DEV)), 1),
+                        (dict(cache=cache.view(-1, 4, 576)), 2)):
+        with pytest.raises(kda.KdaError) as e:
+            kda.kda_latent_decode(**{**ok, **bad})
+        assert e.value.status == status
+    for bad, error in ((dict(latent=lat.float()), TypeError), (dict(k_rope=None), ValueError), (dict(inv_freq=freqs()[:5]), ValueError),
+                       (dict(cu_seqlens=i32([0, 1])), ValueError), (dict(cu_seqlens=[0, 2, 1]), kda.KdaError),
+                       (dict(q_rope=qr[:, :3]), ValueError), (dict(latent=lat.t().contiguous().t()), ValueError)):
+        with pytest.raises(error):
+            kda.kda_latent_append(**{**dict(latent=lat, k_rope=kr, cache=cache, block_table=table, seq_lens=lens), **bad})
+    p = dict(q=randn(g, 10, 2, 192), k=randn(g, 10, 2, 128), v=randn(g, 10, 2, 128), k_rope=randn(g, 10, 64), scale=0.07)
+    kda.kda_latent_prefill(**p)
+    for bad, error in ((dict(q=p["q"][..., :100]), ValueError), (dict(k_rope=None), ValueError), (dict(v=randn(g, 10, 2, 256)[..., :128]), ValueError),
+                       (dict(k=p["k"][:9]), ValueError), (dict(cu_seqlens=i32([0, 10]), cu_seqlens_k=i32([0, 5, 10])), ValueError),
+                       (dict(num_seqs=3), kda.KdaError), (dict(q=p["q"].half()), TypeError), (dict(lse=torch.empty(3, device=DEV)), ValueError)):
+        with pytest.raises(error):
+            kda.kda_latent_prefill(**{**p, **bad})
+    with pytest.raises(ValueError):
+        kda.kda_latent_gather(cache, table, i32([0, 1]), 1)
+    clean()
+
+
 # ---------------------------------------------------------------- streams, graphs, the run of them
 
 def test_side_stream_and_captured_graph():

@@ -129,7 +129,7 @@ def test_valid_calls_without_a_gpu_report_a_cuda_error(L):
         assert f(L) == _lib.KDA_ERR_CUDA
 
 
-def test_binding_refuses_cpu_tensors_and_wrong_shapes():
+def test_binding_refuses_cpu_tensors(L):
     z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
     t = torch.zeros(1, 1, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
@@ -145,12 +145,12 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
 @pytest.mark.parametrize("t,step", [
     (torch.zeros(4, 3, 64), 64), (torch.zeros(4, 3, 192)[..., 128:], 192), (torch.zeros(1, 1, 64), 64),
     (torch.zeros(5, 576)[:, 512:], 576), (torch.zeros(4, 6, 64)[:, 2:3], 384), (torch.zeros(1, 3, 192)[..., :64], 192)])
-def test_row_strides_read_from_a_tensor(t, step):
-    assert _lib._row_stride("t", t) == step
+def test_row_strides_read_from_a_tensor(L, t, step):
+    assert _lib._latent().row_stride("t", t) == step
 
 
 @pytest.mark.parametrize("t", [torch.zeros(4, 6, 64)[:, ::2][:, :2], torch.zeros(3, 4, 64).transpose(0, 1),
                                torch.zeros(4, 3, 128)[..., ::2], torch.zeros(1, 64).expand(4, 64)])
-def test_rows_that_are_not_evenly_spaced_are_refused(t):
+def test_rows_that_are_not_evenly_spaced_are_refused(L, t):
     with pytest.raises(ValueError):
-        _lib._row_stride("t", t)
+        _lib._latent().row_stride("t", t)
