@@ -624,7 +624,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
                                       : KDA_INDEX_OK(row + NR - 1, (int64_t)gridDim.x * 2 * NR, a.status);
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * kLatent + 32 * w + lane;
             float* part = po + row * kLatent + 32 * w + lane;
-#pragma unroll 1
+#pragma unroll
             for (int k = 0; k < NR / 16; ++k) {
                 uint32_t o[4][16];
 #pragma unroll
