@@ -47,7 +47,7 @@ using namespace sm103;
 constexpr int kM = 128, kBlockQ = 2 * kM, kN = 128;   // queries a tile and a block, keys a tile
 constexpr int kSoft = 256;                            // threads of a query tile: two for each query
 constexpr int kThreads = 2 * kSoft + 64;              // warps 0-7: A, 8-15: B, 16: producer, 17: issuer
-constexpr int kHeadsTogether = 8;                     // heads whose keys are in L2 at a time
+constexpr int64_t kKeysInL2 = (int64_t)40 << 20;      // bytes of keys and values of the heads that run together
 constexpr float kRaise = 8.f;                         // log2 of how far a score may exceed the running maximum
 constexpr uint64_t kWaitNs = 4000000000ull;           // bound of every wait
 
@@ -123,10 +123,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // The block's sequence, 256-query tile and head.  Tile slots: sequence n's start at floor(b_n / 256) + n, so that
 // ceil(T / 256) + N slots hold any lengths and a block finds its own by bisection.  Heads go in groups whose keys
 // stay in L2, and slots from the last (the longest rows of a sequence) down, so that the lightest end the launch.
-__device__ __forceinline__ bool find_place(const LatentPrefillArgs& a, int64_t slots, Place& x) {
-    const int64_t b = blockIdx.x, per = slots * kHeadsTogether;
-    const int first = (int)(b / per) * kHeadsTogether;
-    const int together = a.H - first < kHeadsTogether ? a.H - first : kHeadsTogether;
+__device__ __forceinline__ bool find_place(const LatentPrefillArgs& a, int64_t slots, int group, Place& x) {
+    const int64_t b = blockIdx.x, per = slots * group;
+    const int first = (int)(b / per) * group;
+    const int together = a.H - first < group ? a.H - first : group;
     const int64_t rem = b % per, slot = slots - 1 - rem / together;
     x.h = first + (int)(rem % together);
     int lo = 0, hi = a.num_seqs;              // the last n whose first slot is <= slot
@@ -160,7 +160,7 @@ __device__ __forceinline__ int tiles_of(const Place& x, int X) {
 
 template <int DK>
 __global__ void __launch_bounds__(kThreads, 1)
-latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs a, const int64_t slots) {
+latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs a, const int64_t slots, const int group) {
     using G = Cfg<DK>;
     extern __shared__ __align__(1024) uint8_t sm[];   // swizzled tiles start at multiples of 1024 bytes
     if (smem_u32(sm) & 1023u) {               // the declaration's alignment; without it there would be no room for slack
@@ -170,7 +170,7 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
     Small* sw = reinterpret_cast<Small*>(sm + G::kSmall);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     Place x;
-    if (!find_place(a, slots, x)) return;     // a slot without queries
+    if (!find_place(a, slots, group, x)) return;     // a slot without queries
     const int tiles[2] = {tiles_of(x, 0), tiles_of(x, 1)};
     const int most = tiles[0] > tiles[1] ? tiles[0] : tiles[1];
 
@@ -507,7 +507,13 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
         ready[dev].store(true, std::memory_order_release);
     }
     const int64_t slots = (a.total_q + kBlockQ - 1) / kBlockQ + a.num_seqs, blocks = slots * a.H;
-    latent_prefill_kernel<DK><<<(unsigned)blocks, kThreads, G::kBytes, s>>>(maps, a, slots);
+    // Heads run together, longest rows first, as far as the keys and values of an average sequence fit into L2, in groups
+    // of one size.  All heads together end evenly, but long keys would be read from memory over and over: 1 x 2048 tokens,
+    // 32 heads 37 us in one group and 46 in four; 1 x 8192 377 us in four groups, 383 in two, 436 in unequal ones.
+    const int64_t head_bytes = (a.total_kv / a.num_seqs + 1) * 2 * kHead * 2;
+    const int64_t fit = kKeysInL2 / head_bytes < 8 ? 8 : kKeysInL2 / head_bytes, groups = (a.H + fit - 1) / fit;
+    const int group = (int)((a.H + groups - 1) / groups);            // groups of one size
+    latent_prefill_kernel<DK><<<(unsigned)blocks, kThreads, G::kBytes, s>>>(maps, a, slots, group);
     return cudaGetLastError();
 }
 
