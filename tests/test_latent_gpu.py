@@ -286,6 +286,17 @@ def test_decode_many_sequences_and_few_long_ones():
     check_decode([0] * 40 + [5000] + [1] * 40, 1, 16, 64, 64, seed=16)
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_decode_cuts_of_mixed_batches(seed):
+    """Batches of short and long sequences in random order: whole sequences, cut ones and empty ones side by side."""
+    g = torch.Generator().manual_seed(1000 + seed)
+    pick = lambda xs: xs[int(torch.randint(len(xs), (1,), generator=g))]  # noqa: E731
+    H, T, rope = pick([4, 32, 40, 64]), pick([1, 2, 8]), pick([0, 64])
+    choices = [0, 1, 63, 64, 65, 128, 300, 384, 385, 1000, 3000][:pick([6, 9, 11])]
+    lens = [pick(choices) for _ in range(pick([2, 9, 37, 150, 400]))]
+    check_decode(lens, T, H, pick([16, 64, 256]), rope, seed=2000 + seed)
+
+
 def test_decode_repeats_bit_for_bit_and_shares_pages():
     out, lse, args = check_decode([3000, 129, 64, 3000], 1, 32, 64, 64, seed=17)
     q, qr, cache, table, lens, scale = args
