@@ -406,6 +406,8 @@ def _on(stream, t):
     copies belongs to the stream that it runs on."""
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {t.device}")
     return torch.cuda.stream(stream)
 
 

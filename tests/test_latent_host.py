@@ -154,3 +154,17 @@ def test_row_strides_read_from_a_tensor(L, t, step):
 def test_rows_that_are_not_evenly_spaced_are_refused(L, t):
     with pytest.raises(ValueError):
         _lib._latent().row_stride("t", t)
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        cuda_stream, device = FAKE, torch.device("cuda", 1)
+    t = torch.zeros(2, 16, 576, dtype=torch.bfloat16)
+    i = torch.zeros(1, 2, dtype=torch.int32)
+    for call in (lambda: kda.kda_latent_append(t[0, :1, :512], t[0, :1, 512:], t, i, i[0, :1], stream=Stream()),
+                 lambda: kda.kda_latent_gather(t, i, [0, 1], 1, stream=Stream()),
+                 lambda: kda.kda_latent_decode(t[:1, :4, :512], t[:1, :4, 512:], t, i, i[0, :1], 1.0, stream=Stream()),
+                 lambda: kda.kda_latent_prefill(t[:, :, :192], t[:, :, :128], t[:, :, :128], t[0, :2, :64], 1.0,
+                                                stream=Stream())):
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            call()
