@@ -608,7 +608,9 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
             if (p.off == 0 && !whole) {
                 head.n = p.n;
                 head.first_slot = first_piece ? 0 : 1;
-                head.parts = run_of(sw->total, sw->runs, at + p.all - 1) - run + 1;
+                // never past the last run, whatever happens to the lengths while the call runs: the join reads by it
+                const int last = run_of(sw->total, sw->runs, at + p.all - 1);
+                head.parts = (last >= run && last < runs ? last : runs - 1) - run + 1;
             }
             uint8_t* ws = static_cast<uint8_t*>(a.workspace);
             float2* ml = reinterpret_cast<float2*>(ws + Work<NR>::ml_at(gridDim.x));
