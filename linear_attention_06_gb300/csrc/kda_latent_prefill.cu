@@ -509,9 +509,10 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
     const int64_t slots = (a.total_q + kBlockQ - 1) / kBlockQ + a.num_seqs, blocks = slots * a.H;
     // Heads run together, longest rows first, as far as the keys and values of an average sequence fit into L2, in groups
     // of one size.  All heads together end evenly, but long keys would be read from memory over and over: 1 x 2048 tokens,
-    // 32 heads 37 us in one group and 46 in four; 1 x 8192 377 us in four groups, 383 in two, 436 in unequal ones.
+    // 32 heads 37 us in one group and 46 in four; 1 x 8192 377 us in four groups, 383 in two, 436 in unequal ones;
+    // 1 x 32768 5.97 ms in groups of two heads, 6.05 in groups of eight.
     const int64_t head_bytes = (a.total_kv / a.num_seqs + 1) * 2 * kHead * 2;
-    const int64_t fit = kKeysInL2 / head_bytes < 8 ? 8 : kKeysInL2 / head_bytes, groups = (a.H + fit - 1) / fit;
+    const int64_t fit = kKeysInL2 > head_bytes ? kKeysInL2 / head_bytes : 1, groups = (a.H + fit - 1) / fit;
     const int group = (int)((a.H + groups - 1) / groups);            // groups of one size
     latent_prefill_kernel<DK><<<(unsigned)blocks, kThreads, G::kBytes, s>>>(maps, a, slots, group);
     return cudaGetLastError();
