@@ -121,7 +121,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // The block's sequence, 256-query tile and head.  Tile slots: sequence n's start at floor(b_n / 256) + n, so that
-// ceil(T / 256) + N slots hold any lengths and a block finds its own by bisection.  Heads go in groups whose keys
+// ceil(T / 256) + N - 1 slots hold any lengths and a block finds its own by bisection.  Heads go in groups whose keys
 // stay in L2, and slots from the last (the longest rows of a sequence) down, so that the lightest end the launch.
 __device__ __forceinline__ bool find_place(const LatentPrefillArgs& a, int64_t slots, int group, Place& x) {
     const int64_t b = blockIdx.x, per = slots * group;
@@ -506,7 +506,7 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
-    const int64_t slots = (a.total_q + kBlockQ - 1) / kBlockQ + a.num_seqs, blocks = slots * a.H;
+    const int64_t slots = (a.total_q + kBlockQ - 1) / kBlockQ + a.num_seqs - 1, blocks = slots * a.H;
     // Heads run together, longest rows first, as far as the keys and values of an average sequence fit into L2, in groups
     // of one size.  All heads together end evenly, but long keys would be read from memory over and over: 1 x 2048 tokens,
     // 32 heads 37 us in one group and 46 in four; 1 x 8192 377 us in four groups, 383 in two, 436 in unequal ones;
