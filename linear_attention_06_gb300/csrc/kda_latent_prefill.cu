@@ -17,6 +17,9 @@
 // 2^8 in bf16, whose precision does not depend on the exponent; sums are fp32), so O is rarely rescaled; when it is,
 // its last product is done already: S_X was issued behind it.
 //
+// Few queries over many keys leave SMs idle: then up to eight blocks, a cluster, take a share of the same queries' keys
+// each, leave O in fp32 in their shared memory, where queries, keys and values were, and join it by reading one another's.
+//
 // Keys stream through a ring of 16 KB slices of 64 channels, each handed back when B's product has read it, values
 // through two stages of 32 KB.
 //
@@ -99,6 +102,8 @@ __device__ __forceinline__ bool tile_or(int X, bool pred) {
         : "memory");
     return r != 0;
 }
+// A barrier of both query tiles' warps.
+__device__ __forceinline__ void soft_meet() { asm volatile("bar.sync 3, %0;" ::"n"(2 * kSoft) : "memory"); }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -120,11 +125,38 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+// Clusters: this block's number in its own; all threads meet, what they wrote before seen by all behind it (blocks that
+// ended count as there); reads of another block's shared memory.
+__device__ __forceinline__ int cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return (int)r;
+}
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t smem, int rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float cluster_load(uint32_t addr) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(addr) : "memory");
+    return x;
+}
+
 // The block's sequence, 256-query tile and head.  Tile slots: sequence n's start at floor(b_n / 256) + n, so that
 // ceil(T / 256) + N - 1 slots hold any lengths and a block finds its own by bisection.  Heads go in groups whose keys
 // stay in L2, and slots from the last (the longest rows of a sequence) down, so that the lightest end the launch.
-__device__ __forceinline__ bool find_place(const LatentPrefillArgs& a, int64_t slots, int group, Place& x) {
-    const int64_t b = blockIdx.x, per = slots * group;
+__device__ __forceinline__ bool find_place(const LatentPrefillArgs& a, int64_t slots, int group, int64_t b, Place& x) {
+    const int64_t per = slots * group;
     const int first = (int)(b / per) * group;
     const int together = a.H - first < group ? a.H - first : group;
     const int64_t rem = b % per, slot = slots - 1 - rem / together;
@@ -158,9 +190,53 @@ __device__ __forceinline__ int tiles_of(const Place& x, int X) {
     return seen > 0 ? (int)((seen + kN - 1) / kN) : 0;
 }
 
-template <int DK>
+// Joins a row of the P blocks of a cluster, each with O [32 chunks of 4 channels][128 rows] in fp32 at the start of its
+// shared memory (a tile's behind the other's), the row's maximum and sum in `best`.  Block `rank` joins 32 / P of the
+// chunks, a thread half of those; the parts in their order, eight loads in flight.
+template <int P>
+__device__ __forceinline__ void join_row(const LatentPrefillArgs& a, uint32_t o, uint32_t best, int rank, int half, float c2,
+                                         int64_t row, bool live) {
+    constexpr int kEach = 16 / P, kAhead = 8 / P;
+    float w[P], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int r = 0; r < P; ++r) {
+        w[r] = cluster_load(cluster_addr(best, r));
+        m = fmaxf(m, w[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < P; ++r) {
+        w[r] = w[r] == -INFINITY ? 0.f : exp2_fast((w[r] - m) * c2);
+        if (w[r] > 0.f) l += w[r] * cluster_load(cluster_addr(best + 4 * kM, r));
+    }
+    if (!live) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int first = rank * 2 * kEach + half * kEach;
+    uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * kHead) + first;
+#pragma unroll
+    for (int c = 0; c < kEach; c += kAhead) {
+        float4 x[kAhead][P];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int r = 0; r < P; ++r)       // a part without weight left nothing there
+                x[k][r] = w[r] > 0.f ? cluster_load4(cluster_addr(o + (first + c + k) * 16 * kM, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int r = 0; r < P; ++r) {
+                y.x += w[r] * x[k][r].x; y.y += w[r] * x[k][r].y; y.z += w[r] * x[k][r].z; y.w += w[r] * x[k][r].w;
+            }
+            out[c + k] = make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+        }
+    }
+    if (a.lse && rank == 0 && half == 0) a.lse[row] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
+}
+
+template <int DK, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
-latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs a, const int64_t slots, const int group) {
+latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs a, const int64_t slots, const int group,
+                      const int parts) {
     using G = Cfg<DK>;
     extern __shared__ __align__(1024) uint8_t sm[];   // swizzled tiles start at multiples of 1024 bytes
     if (smem_u32(sm) & 1023u) {               // the declaration's alignment; without it there would be no room for slack
@@ -169,10 +245,24 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
     }
     Small* sw = reinterpret_cast<Small*>(sm + G::kSmall);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int rank = SPLIT ? cluster_rank() : 0;
     Place x;
-    if (!find_place(a, slots, group, x)) return;     // a slot without queries
-    const int tiles[2] = {tiles_of(x, 0), tiles_of(x, 1)};
-    const int most = tiles[0] > tiles[1] ? tiles[0] : tiles[1];
+    if (!find_place(a, slots, group, SPLIT ? blockIdx.x / parts : blockIdx.x, x)) {     // a slot without queries
+        if (SPLIT) { cluster_meet(); cluster_meet(); }
+        return;
+    }
+    int tiles[2] = {tiles_of(x, 0), tiles_of(x, 1)}, most = tiles[0] > tiles[1] ? tiles[0] : tiles[1];
+    if (SPLIT) {                              // this block's share of the key tiles, which then are tiles 0, 1, ..
+        const int from = (int)((int64_t)most * rank / parts), share = (int)((int64_t)most * (rank + 1) / parts) - from;
+        most = share;
+#pragma unroll
+        for (int X = 0; X < 2; ++X) {
+            const int left = tiles[X] - from;
+            tiles[X] = left < 0 ? 0 : (left < share ? left : share);
+        }
+        x.kb += (int64_t)from * kN;
+        x.nk -= from * kN;
+    }
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -414,9 +504,40 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
             ok = !tile_or(X, !ok);
             l = sums[t] + sums[kM + t];
         }
-        if (ok) {                             // a thread stores half of its query's row
+        const int64_t row = (x.qb + i) * a.H + x.h;
+        if constexpr (SPLIT) {
+            // Both tiles' products are done: queries, keys and values make room for O.  After a wait that ran out the
+            // part has no weight.
+            const bool any = ok && count > 0;
+            if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
+            soft_meet();
             tc_fence_after();
-            const int64_t row = (x.qb + i) * a.H + x.h;
+            if (any) {
+                float4* o = reinterpret_cast<float4*>(sm) + (X * 32 + 16 * half) * kM + t;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t y[32];
+                    tmem_ld32(to + 32 * b, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        o[(8 * b + k) * kM] = make_float4(__uint_as_float(y[4 * k]), __uint_as_float(y[4 * k + 1]),
+                                                          __uint_as_float(y[4 * k + 2]), __uint_as_float(y[4 * k + 3]));
+                }
+            }
+            if (half == 0) {
+                sw->best[X][0][t] = any ? m : -INFINITY;
+                sw->best[X][1][t] = l;
+            }
+            cluster_meet();
+            const bool live = i < x.nq && KDA_INDEX_OK(row, a.total_q * a.H, a.status);
+            const uint32_t o = smem_u32(sm) + (X * 32 * kM + t) * 16, best = smem_u32(&sw->best[X][0][t]);
+            if (parts == 2) join_row<2>(a, o, best, rank, half, c2, row, live);
+            else if (parts == 4) join_row<4>(a, o, best, rank, half, c2, row, live);
+            else join_row<8>(a, o, best, rank, half, c2, row, live);
+            cluster_meet();                   // no block ends while another reads its memory
+        } else if (ok) {                      // a thread stores half of its query's row
+            tc_fence_after();
             const bool live = i < x.nq && KDA_INDEX_OK(row, a.total_q * a.H, a.status);
             const float inv = l == 0.f ? 0.f : 1.f / l;
             uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * kHead + 64 * half);
@@ -447,6 +568,7 @@ latent_prefill_kernel(const __grid_constant__ Maps maps, const LatentPrefillArgs
             atomicOr(a.status, kStatusTimeout);
         }
     }
+    if (SPLIT && warp >= 16) { cluster_meet(); cluster_meet(); }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -486,9 +608,68 @@ bool map_shared(CUtensorMap* m, const void* base, int64_t tokens) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int kDevices = 64;
+
+// The kernel's shared memory, set once a device.
+template <int DK, bool SPLIT>
+cudaError_t set_up(int dev) {
+    static std::atomic<bool> ready[kDevices];
+    if (ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(latent_prefill_kernel<DK, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)Cfg<DK>::kBytes);
+    if (e == cudaSuccess) ready[dev].store(true, std::memory_order_release);
+    return e;
+}
+
+// A launch of `blocks` clusters of `parts` blocks; `attr` is its attribute and has to live as long.
+template <int DK>
+cudaLaunchConfig_t config(int64_t blocks, int parts, cudaStream_t s, cudaLaunchAttribute* attr) {
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = (unsigned)parts;
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks * parts));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<DK>::kBytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = parts > 1 ? 1 : 0;
+    return cfg;
+}
+
+// Clusters of `parts` blocks that run at the same time: what the SMs of each cluster's neighbourhood hold, which differs
+// from card to card.  (Here 144 of 152 SMs in clusters of four, fewer than 128 in clusters of eight.)
+template <int DK>
+int clusters_at_once(int dev, int parts) {
+    static std::atomic<int> known[kDevices][9];           // one more than the number; 0: not asked yet
+    int n = known[dev][parts].load(std::memory_order_relaxed) - 1;
+    if (n >= 0) return n;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config<DK>(1, parts, nullptr, &attr);
+    if (cudaOccupancyMaxActiveClusters(&n, latent_prefill_kernel<DK, true>, &cfg) != cudaSuccess) return 0;
+    known[dev][parts].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+// How many blocks share the keys of a block of queries: as many as there are SMs for, up to eight and each with a tile
+// of an average sequence, if that saves each kJoinTiles tiles, which is what the join costs (3 us).  Measured, dk = 192:
+// 1 x 100 queries over 16384 keys, 32 heads, 53 us in fours and 168 alone; 1 x 128 over 8192, one head, 19 in eights,
+// 29 in fours, 86 alone; 1 x 64 over 600, 8 heads, 10.8 in fours and 11.6 alone; 1 x 512 without prefix, 8 heads, 14.6 in
+// twos and 12.8 alone; 1 x 200 over 4096, 18 heads, more clusters of eight than run at once 34.5, in fours 22.7.
+constexpr int kJoinTiles = 3;
+template <int DK>
+int parts_of(const LatentPrefillArgs& a, int dev) {
+    const int64_t each_q = (a.total_q + a.num_seqs - 1) / a.num_seqs, tiles = a.total_kv / a.num_seqs / kN;
+    const int64_t blocks = (each_q + kBlockQ - 1) / kBlockQ * a.num_seqs * a.H;
+    for (int parts = 8; parts > 1; parts /= 2)
+        if (tiles >= parts && tiles - (tiles + parts - 1) / parts >= kJoinTiles &&
+            blocks <= clusters_at_once<DK>(dev, parts))
+            return parts;
+    return 1;
+}
+
 template <int DK>
 cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
-    using G = Cfg<DK>;
     Maps maps;
     // without keys nothing is loaded; the maps are then those of the queries
     const bool keys = a.total_kv > 0;
@@ -497,15 +678,6 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
         !(keys ? map_heads(&maps.v, a.v, a.total_kv, a.H, kHead, a.kv_stride) : map_heads(&maps.v, a.q, a.total_q, a.H, DK, DK)) ||
         !(keys && DK > kHead ? map_shared(&maps.r, a.k_rope, a.total_kv) : map_heads(&maps.r, a.q, a.total_q, a.H, DK, DK)))
         return cudaErrorInvalidValue;
-    static std::atomic<bool> ready[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!ready[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(latent_prefill_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)G::kBytes);
-        if (e != cudaSuccess) return e;
-        ready[dev].store(true, std::memory_order_release);
-    }
     const int64_t slots = (a.total_q + kBlockQ - 1) / kBlockQ + a.num_seqs - 1, blocks = slots * a.H;
     // Heads run together, longest rows first, as far as the keys and values of an average sequence fit into L2, in groups
     // of one size.  All heads together end evenly, but long keys would be read from memory over and over: 1 x 2048 tokens,
@@ -514,8 +686,17 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
     const int64_t head_bytes = (a.total_kv / a.num_seqs + 1) * 2 * kHead * 2;
     const int64_t fit = kKeysInL2 > head_bytes ? kKeysInL2 / head_bytes : 1, groups = (a.H + fit - 1) / fit;
     const int group = (int)((a.H + groups - 1) / groups);            // groups of one size
-    latent_prefill_kernel<DK><<<(unsigned)blocks, kThreads, G::kBytes, s>>>(maps, a, slots, group);
-    return cudaGetLastError();
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    cudaError_t e = set_up<DK, false>(dev);
+    if (e == cudaSuccess) e = set_up<DK, true>(dev);
+    if (e != cudaSuccess) return e;
+    const int parts = parts_of<DK>(a, dev);
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config<DK>(blocks, parts, s, &attr);
+    e = cudaLaunchKernelEx(&cfg, parts > 1 ? latent_prefill_kernel<DK, true> : latent_prefill_kernel<DK, false>, maps, a, slots,
+                           group, parts);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace

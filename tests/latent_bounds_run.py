@@ -74,6 +74,12 @@ def main() -> int:
         kda.kda_latent_prefill(q, kv[..., :128], kv[..., 128:], kr, 0.07, i32([0, 50, 20, 900, -4, 10 ** 9]),
                                i32([3, 2000, 5, 10, 10, 1210]), lse=True)
         check(f"prefill, bad tables rope={rope}")
+        # few queries over many keys, which blocks share
+        kv = torch.randn(9000, 3, 256, device=dev).to(bf)
+        kr = torch.randn(9000, 64, device=dev).to(bf) if rope else None
+        for qs, ks in (([0, 90, 90, 700], [0, 3000, 3001, 9000]), ([0, 50, 20, 10 ** 9], [3, 20000, 5, 9000])):
+            kda.kda_latent_prefill(q, kv[..., :128], kv[..., 128:], kr, 0.07, i32(qs), i32(ks), lse=True)
+            check(f"prefill, shared keys rope={rope}")
     if failures:
         print("index checks failed:", ", ".join(failures))
         return 1

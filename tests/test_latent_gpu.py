@@ -421,6 +421,29 @@ def test_prefill_over_a_prefix(rope):
     check_prefill([513], [2049], 2, rope, seed=5)
 
 
+@pytest.mark.parametrize("rope", [0, 64])
+@pytest.mark.parametrize("nq,past,H", [
+    ([100], [1948], 32), ([1], [1300], 3), ([128], [2048], 16), ([129], [5000], 4), ([256], [4096], 1), ([700], [8000], 6),
+    ([40, 3], [3000, 2500], 9), ([300, 1, 0, 257], [1, 6000, 900, 2222], 4), ([5, 5, 5], [0, 9000, 130], 7)])
+def test_prefill_few_queries_over_many_keys(nq, past, H, rope):
+    """Queries too few for all SMs, whose keys several blocks share."""
+    check_prefill(nq, [a + b for a, b in zip(nq, past)], H, rope, seed=sum(past) + H)
+
+
+def test_prefill_shared_keys_repeat_bit_for_bit_and_rising_scores():
+    g = gen(77)
+    q, kv, kr = randn(g, 60, 8, 192), randn(g, 4060, 8, 256), randn(g, 4060, 64)
+    kv[..., :128] *= torch.linspace(0.01, 6, 4060, device=DEV)[:, None, None].to(BF)     # the maximum rises with the keys
+    call = lambda: kda.kda_latent_prefill(q, kv[..., :128], kv[..., 128:], kr, 0.3, lse=True, num_seqs=1)  # noqa: E731
+    out, lse = call()
+    again = call()
+    clean()
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    o, s, bo, bs = ref.prefill(q, kv[..., :128], kv[..., 128:], kr, 0.3, [0, 60], [0, 4060])
+    ref.assert_within(out, o, bo, "out")
+    ref.assert_within(lse, s, bs, "lse")
+
+
 def test_prefill_with_fewer_keys_than_queries():
     out, lse = check_prefill([10, 300, 5, 140], [4, 20, 0, 139], 2, 64, seed=6, tail=3)
     assert bool((out[:6] == 0).all()) and bool((lse[:6] == -math.inf).all())
@@ -528,6 +551,48 @@ def test_side_stream_and_captured_graph():
         ref.assert_within(out, o, bo, "replayed out")
         ref.assert_within(lse, s, bs, "replayed lse")
     clean()
+
+
+FIRST_CAPTURE = """
+import torch, linear_attention_06_gb300 as kda
+BF, d = torch.bfloat16, "cuda"
+z = lambda *s: torch.randn(*s, device=d).to(BF)
+i = lambda x: torch.tensor(x, dtype=torch.int32, device=d)
+def call(H, T, rope, nq, nk, n):
+    page = 64
+    cache, table = z(40 * n, page, 512 + rope), torch.arange(n * 40, dtype=torch.int32, device=d).view(n, 40)
+    lens, f = i([min(2500, nk)] * n), torch.rand(32, device=d)
+    lat, kr, q = z(n * T, 512), z(n * T, 64) if rope else None, z(n * T, H, 64) if rope else None
+    ql, k, v = z(n * T, H, 512), z(nk, H, 128), z(nk, H, 128)
+    qq, kr2 = z(nq, H, 128 + rope), z(nk, 64) if rope else None
+    cu = torch.arange(n + 1, dtype=torch.int32, device=d) * 100
+    def run():
+        kda.kda_latent_append(lat, kr, cache, table, lens, inv_freq=f if rope else None, q_rope=q)
+        return (kda.kda_latent_gather(cache, table, cu, 100 * n)[0],
+                kda.kda_latent_decode(ql, q, cache, table, lens, 0.1)[0],
+                kda.kda_latent_prefill(qq, k, v, kr2, 0.1, num_seqs=1)[0])
+    return run
+call(4, 1, 64, 20, 20, 1)()
+call(4, 1, 0, 20, 20, 1)()
+torch.cuda.synchronize()
+for args in ((4, 1, 64, 100, 4000, 1), (32, 2, 0, 100, 8000, 40), (64, 1, 64, 700, 700, 2), (20, 1, 0, 30, 30, 3)):
+    run = call(*args)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    graph.replay()
+    torch.cuda.synchronize()
+    first = [x.clone() for x in got]
+    for a, b in zip(first, run()):
+        assert torch.equal(a, b), args
+assert kda.kda_device_status() == 0
+"""
+
+
+def test_forms_first_met_in_a_capture():
+    """One call of each operator and row width loads its kernels: every other form may then first be met in a capture."""
+    done = subprocess.run([sys.executable, "-c", FIRST_CAPTURE], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_a_stream_argument_carries_the_whole_call():
