@@ -646,7 +646,10 @@ int clusters_at_once(int dev, int parts) {
     if (n >= 0) return n;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config<DK>(1, parts, nullptr, &attr);
-    if (cudaOccupancyMaxActiveClusters(&n, latent_prefill_kernel<DK, true>, &cfg) != cudaSuccess) return 0;
+    if (cudaOccupancyMaxActiveClusters(&n, latent_prefill_kernel<DK, true>, &cfg) != cudaSuccess) {
+        cudaGetLastError();                   // not the launch's
+        return 0;
+    }
     known[dev][parts].store(n + 1, std::memory_order_relaxed);
     return n;
 }
