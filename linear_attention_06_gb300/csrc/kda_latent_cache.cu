@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const LatentAppendA
         turn_q(i, load_unit<INTERLEAVED>(q_rope + (t0 * a.H + (i >> 2)) * a.q_stride, i & 3));
 }
 
-// ROWS rows a block, a 16-byte chunk a thread and step, all of a thread's loads before its stores.
+// ROWS rows a block, a 16-byte chunk a thread and step, all of a thread's loads before its stores.  The rows are read
+// once, past L1 and never as read-only data: an overlapped block starts while the append before it may still write them.
 template <int ROWS, int CHUNKS>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const LatentGatherArgs a) {
     __shared__ int64_t row_s[ROWS];             // -1: zeros, -2: no sequence's
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const LatentGatherArgs
         x[k] = make_uint4(0, 0, 0, 0);
         if (i < ROWS * CHUNKS && row_s[j] >= 0 &&
             KDA_INDEX_OK(row_s[j], (int64_t)a.c.num_pages * a.c.page_size, a.status))
-            x[k] = __ldg(cache + row_s[j] * CHUNKS + c);
+            x[k] = __ldcg(cache + row_s[j] * CHUNKS + c);
     }
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
