@@ -389,7 +389,7 @@ typedef struct {
  * far positions keep their angles): (a, b) -> (a cos - b sin, a sin + b cos), rounded once.
  * latent:   [T, 512] rows, latent_stride elements apart; k_rope: [T, 64] rows, k_rope_stride
  *           elements apart (both may be columns of one projection); NULL with rope_dim 0.
- * inv_freq: DEVICE fp32 [32], or NULL: no rotation, rows are copied.
+ * inv_freq: DEVICE fp32 [32], or NULL: no rotation, rows are copied bit for bit.
  * interleaved: 0 pairs channels (i, i + 32), 1 pairs channels (2i, 2i + 1).
  * q_rope:   the queries' rotated part, [T, H] rows of 64, q_stride elements apart (64 for a tensor
  *           of its own, dk for the end of each row of kda_latent_prefill's q), or NULL: none.

@@ -39,7 +39,15 @@ __device__ __forceinline__ Unit load_unit(const __nv_bfloat16* src, int u) {
     return {p[INTERLEAVED ? 2 * u : u], p[INTERLEAVED ? 2 * u + 1 : u + 4]};
 }
 template <bool INTERLEAVED>
+__device__ __forceinline__ void store_unit(uint4 y0, uint4 y1, __nv_bfloat16* dst, int u) {
+    reinterpret_cast<uint4*>(dst)[INTERLEAVED ? 2 * u : u] = y0;
+    reinterpret_cast<uint4*>(dst)[INTERLEAVED ? 2 * u + 1 : u + 4] = y1;
+}
+// Without angles a row is copied bit for bit: a product with (1, 0) would turn an infinite channel's partner into NaN
+// and could lose the sign of a zero.
+template <bool INTERLEAVED>
 __device__ __forceinline__ void rotate_unit(const Unit& x, __nv_bfloat16* dst, int u, const Turn* turn) {
+    if (!turn) return store_unit<INTERLEAVED>(x.x0, x.x1, dst, u);
     const __nv_bfloat162* a = reinterpret_cast<const __nv_bfloat162*>(&x.x0);
     const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&x.x1);
     uint4 y0, y1;
@@ -58,8 +66,7 @@ __device__ __forceinline__ void rotate_unit(const Unit& x, __nv_bfloat16* dst, i
             yb[k] = __floats2bfloat162_rn(fa.x * t.s + fb.x * t.c, fa.y * v.s + fb.y * v.c);
         }
     }
-    reinterpret_cast<uint4*>(dst)[INTERLEAVED ? 2 * u : u] = y0;
-    reinterpret_cast<uint4*>(dst)[INTERLEAVED ? 2 * u + 1 : u + 4] = y1;
+    store_unit<INTERLEAVED>(y0, y1, dst, u);
 }
 
 // find_seq by a whole warp: 32 offsets a step instead of one, since each step waits for memory.
@@ -131,18 +138,17 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const LatentAppendA
         }
     }
     __syncthreads();
-    if (a.c.rope_dim) {
+    if (a.inv_freq) {
         for (int i = tid; i < count * (kRope / 2); i += kThreads) {
             const int j = i / (kRope / 2), k = i % (kRope / 2);
-            Turn t{1.f, 0.f};
-            if (a.inv_freq) {
-                const uint64_t angle = (uint64_t)pos_s[j] * step_s[k];
-                sincospif((float)(int32_t)(angle >> 32) * 0x1p-31f, &t.s, &t.c);              // half turns in [-1, 1]
-            }
+            const uint64_t angle = (uint64_t)pos_s[j] * step_s[k];
+            Turn t;
+            sincospif((float)(int32_t)(angle >> 32) * 0x1p-31f, &t.s, &t.c);                  // half turns in [-1, 1]
             turn_s[j][k] = t;
         }
         __syncthreads();
     }
+    auto turns = [&](int j) -> const Turn* { return a.inv_freq ? turn_s[j] : nullptr; };
     __nv_bfloat16* cache = static_cast<__nv_bfloat16*>(a.c.cache);
 #pragma unroll
     for (int k = 0; k < kLat; ++k) {
@@ -150,12 +156,12 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const LatentAppendA
         if (i < count * kChunks && row_s[j] >= 0) reinterpret_cast<uint4*>(cache + row_s[j] * width)[i % kChunks] = lat[k];
     }
     if (k_rope && tid < count * 4 && row_s[tid >> 2] >= 0)
-        rotate_unit<INTERLEAVED>(key, cache + row_s[tid >> 2] * width + kLatent, tid & 3, turn_s[tid >> 2]);
+        rotate_unit<INTERLEAVED>(key, cache + row_s[tid >> 2] * width + kLatent, tid & 3, turns(tid >> 2));
     auto turn_q = [&](int i, const Unit& x) {
         const int j = i / units;
         if (live_s[j])
             rotate_unit<INTERLEAVED>(x, static_cast<__nv_bfloat16*>(a.q_out) + (t0 * a.H + (i >> 2)) * a.q_out_stride, i & 3,
-                                     turn_s[j]);
+                                     turns(j));
     };
 #pragma unroll
     for (int k = 0; k < kQ; ++k) {

@@ -51,3 +51,37 @@ def test_rows_gathered_before_and_after_they_are_replaced(rope):
     for x, y in zip(new, got):
         assert torch.equal(x[0], y[0])
         assert not rope or torch.equal(x[1], y[1])
+
+
+def bits(g, *shape):
+    """Every bit pattern alike: infinities, NaN, negative zeros and subnormals among them."""
+    return torch.randint(-2 ** 15, 2 ** 15, shape, generator=g, device=DEV).to(torch.int16).view(BF)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,H,rope", [(1, 1, 64), (37, 300, 64), (37, 4, 0), (2500, 40, 64), (2500, 3, 0)])
+def test_rows_without_rotation_are_copied_bit_for_bit(T, H, rope, interleaved):
+    """Without inv_freq: a few tokens a block and many, queries within a thread's first loads and behind them."""
+    g = gen(T + H)
+    page = 16
+    per = -(-T // page)
+    table = torch.randperm(per, generator=g, device=DEV).to(torch.int32).view(1, per)
+    cache = bits(g, per, page, 512 + rope)
+    both, q = bits(g, T, 576), bits(g, T, H, 192)
+    pos = torch.arange(T, device=DEV)
+    slot = table.long()[0, pos // page] * page + pos % page
+    want = cache.clone().view(torch.int16)
+    want.view(-1, 512 + rope)[slot] = both[:, :512 + rope].view(torch.int16)
+    before = q.clone()
+    args = (both[:, :512], both[:, 512:] if rope else None, cache, table, i32([T]))
+    got = kda.kda_latent_append(*args, interleaved=interleaved, q_rope=q[..., 128:] if rope else None)
+    clean()
+    assert torch.equal(cache.view(torch.int16), want)
+    if rope:
+        assert torch.equal(got.view(torch.int16), q[..., 128:].contiguous().view(torch.int16))
+        kda.kda_latent_append(*args, interleaved=interleaved, q_rope=q[..., 128:], q_rope_out=q[..., 128:])
+        clean()
+        assert torch.equal(q.view(torch.int16), before.view(torch.int16))
+        assert torch.equal(cache.view(torch.int16), want)
+    else:
+        assert got is None
