@@ -42,6 +42,7 @@
 
 #include "kda_internal.h"
 #include "kda_latent_common.cuh"
+#include "kda_latent_runs.h"
 #include "sm103_primitives.cuh"
 
 namespace kda {
@@ -50,7 +51,6 @@ namespace {
 using namespace latent;
 using namespace sm103;
 
-constexpr int kTile = 64;                     // cached rows a tile
 constexpr int kThreads = 256;                 // warps 0-3: producer, issuer, queries, (TMEM); warps 4-7: softmax
 constexpr int kSoft = 128;
 constexpr int kBar = 1;                       // named barrier of the softmax warps
@@ -98,39 +98,17 @@ struct Ring {
     }
 };
 
-struct Piece {                                // a run's share of one sequence
-    int n, len, off, tiles, all;              // sequence, its length, first tile, tiles here, tiles in all
-};
-
-__device__ __forceinline__ int tiles_of(int len) { return len > kTile ? (len - 1) / kTile + 1 : 1; }
-// A sequence's places in the line: its tiles, behind kStart places that stand for what starting a piece costs a
-// block (queries in, O out), so that runs with many pieces get fewer tiles.
-constexpr int kStart = 1;
 // Sequences of at most so many tiles are not cut, if runs have two places or more: the cut goes to the nearer end.  The
 // partial results of two pieces cost more than the unevenness: 182 sequences of up to 285 tokens, 64 heads, 26.4 us
 // against 34.7 when cut (28.9 with a limit of 4 tiles); 100 of up to 400, 32 heads, 16.8 against 19.7; with a limit of
 // 8 tiles unevenness wins (57 of up to 1084, 8 tokens x 12 heads: 45 us, 39 with 6, 37 when cut).
 constexpr int kShort = 6;
 
-// Walks the sequences of a run; every role walks by itself.
-struct Walk {
-    int n, off, lead, len;                    // next sequence, its first tile here, start places before it
-    int64_t left;
-    __device__ Walk(const Small* sw) : n(sw->seq0), off(sw->off0), lead(sw->lead0), len(sw->len0), left(sw->end - sw->begin) {}
+// Walks the sequences of this block's run; every role walks by itself.
+struct Walk : RunWalk {
+    __device__ Walk(const Small* sw) : RunWalk{sw->seq0, sw->off0, sw->lead0, sw->len0, sw->end - sw->begin} {}
     __device__ __forceinline__ bool next(const LatentDecodeArgs& a, Piece& p) {
-        if (left <= 0 || n >= a.num_seqs) return false;
-        p.n = n;
-        p.len = len >= 0 ? len : clamped_len(a.c, a.seq_lens, n);
-        len = -1;
-        p.all = tiles_of(p.len);
-        p.off = off;
-        const int64_t behind = left - lead;   // places of the run behind the sequence's start places
-        p.tiles = behind < p.all - off ? (behind > 0 ? (int)behind : 0) : p.all - off;
-        left = behind - p.tiles;
-        lead = kStart;
-        off = 0;
-        ++n;
-        return p.tiles > 0;                   // a run may end inside the start places
+        return RunWalk::next(a.num_seqs, [&](int seq) { return clamped_len(a.c, a.seq_lens, seq); }, p);
     }
 };
 
@@ -153,13 +131,6 @@ __device__ __forceinline__ bool soft_or(bool pred) {
 }
 __device__ __forceinline__ bool soft_and(bool pred) { return !soft_or(!pred); }
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kSoft) : "memory"); }
-
-// The first tile of run p of `runs` over `total` tiles (a 32-bit division where it fits, a fifth of the time), and
-// the run that holds tile x.
-__device__ __forceinline__ int64_t run_begin(int64_t total, int runs, int p) {
-    return total < (1 << 23) ? (int64_t)((uint32_t)total * (uint32_t)p / (uint32_t)runs) : total * p / runs;
-}
-__device__ __forceinline__ int run_of(int64_t total, int runs, int64_t x) { return (int)(((x + 1) * runs - 1) / total); }
 
 // Workspace: a header a block (the sequence whose first piece it holds), then per (block, 0 or 1) and row the
 // maximum (in log2) and the sum, then O.
@@ -603,7 +574,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
             }
             if (!soft_and(ok)) { ok = false; break; }
             // ---- the piece is done: its rows' sums, then O^T out of tensor memory
-            const bool whole = p.off == 0 && p.tiles == p.all;
+            const bool whole = is_whole(p, runs);
             const int slot = blockIdx.x * 2 + (first_piece ? 0 : 1);
             if (p.off == 0 && !whole) {
                 head.n = p.n;
@@ -915,7 +886,7 @@ cudaError_t launch_rope(const LatentDecodeArgs& a, cudaStream_t s) {
 
 size_t latent_decode_workspace_bytes(int tokens_per_seq, int H) {
     const int R = tokens_per_seq * H, groups = groups_of(R), grid = runs_of(groups) * groups;
-    if (runs_of(groups) == 1) return Work<64>::ml_at(grid);         // one run: every piece is a whole sequence
+    if (runs_of(groups) == 1) return Work<64>::ml_at(grid);         // one run: no piece goes to the workspace (is_whole)
     switch (rows_a_block(R)) {
         case 16: return Work<16>::bytes(grid);
         case 32: return Work<32>::bytes(grid);

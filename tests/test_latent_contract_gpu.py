@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import linear_attention_06_gb300 as kda
+from tests import latent_reference as ref
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -85,3 +86,23 @@ def test_rows_without_rotation_are_copied_bit_for_bit(T, H, rope, interleaved):
         assert torch.equal(cache.view(torch.int16), want)
     else:
         assert got is None
+
+
+@pytest.mark.parametrize("T,H,rope", [(7, 640, 64), (5, 1024, 0), (16, 1024, 64)])
+def test_decode_of_so_many_rows_that_few_runs_are_left(T, H, rope):
+    """Two runs and one run over the sequences, with a workspace of exactly the size asked for: bytes behind it stay."""
+    g = gen(T)
+    page, lens = 16, [T, 200, 0, 700, 65, T - 1]
+    per = -(-max(lens) // page)
+    cache = randn(g, len(lens) * per, page, 512 + rope)
+    table = torch.randperm(len(lens) * per, generator=g, device=DEV).to(torch.int32).view(len(lens), per)
+    rows = len(lens) * T
+    q, qr = randn(g, rows, H, 512), randn(g, rows, H, 64) if rope else None
+    size = kda.kda_latent_decode_workspace_size(len(lens), rows, H, rope)
+    ws = torch.full((size + 4096,), 7, dtype=torch.uint8, device=DEV)
+    out, lse = kda.kda_latent_decode(q, qr, cache, table, i32(lens), 0.07, lse=True, workspace=ws[:size])
+    clean()
+    assert bool((ws[size:] == 7).all())
+    o, s, bo, bs = ref.decode(q, qr, cache, table, i32(lens), 0.07)
+    ref.assert_within(out, o, bo, "out")
+    ref.assert_within(lse, s, bs, "lse")

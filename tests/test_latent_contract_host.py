@@ -2,9 +2,11 @@
 import glob
 import os
 import re
+import subprocess
 
 import pytest
 
+import linear_attention_06_gb300 as kda
 from linear_attention_06_gb300 import build as kbuild
 
 
@@ -15,3 +17,73 @@ def test_overlapped_kernels_read_nothing_as_read_only_data(path):
     with open(path) as f:
         code = re.sub(r"//.*", "", f.read())
     assert not re.search(r"__ldg\b|ld\.global(\.\w+)*\.nc|__restrict__", code)
+
+
+RUNS = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+#include "kda_latent_runs.h"
+using namespace kda::latent;
+
+// A line in `runs` runs over sequences of the given lengths; length(n) is what the walk reads.  Returns the pieces that
+// go to the workspace, -1 if a piece leaves its sequence, and counts the tiles of each sequence.
+template <typename Length>
+static int walk(const std::vector<int>& lens, int runs, const Length& length, std::vector<int>& tiles) {
+    const int count = (int)lens.size();
+    int64_t total = 0;
+    std::vector<int64_t> first;
+    for (int x : lens) { first.push_back(total); total += kStart + tiles_of(x); }
+    if (total < runs) runs = (int)total;
+    int partial = 0;
+    for (int r = 0; r < runs; ++r) {
+        const int64_t begin = run_begin(total, runs, r), end = run_begin(total, runs, r + 1);
+        int n = count - 1;
+        while (first[n] > begin) --n;
+        const int into = (int)(begin - first[n]);
+        RunWalk w{n, into < kStart ? 0 : into - kStart, into < kStart ? kStart - into : 0, lens[n], end - begin};
+        Piece p;
+        while (w.next(count, length, p)) {
+            if (p.n < 0 || p.n >= count || p.off < 0 || p.tiles <= 0 || p.off + p.tiles > p.all) return -1;
+            tiles[p.n] += p.tiles;
+            partial += !is_whole(p, runs);
+        }
+    }
+    return partial;
+}
+
+int main() {
+    srand(1);
+    for (int round = 0; round < 4000; ++round) {
+        std::vector<int> lens(1 + rand() % 12);
+        for (int& x : lens) x = rand() % 4 ? rand() % 700 : rand() % 9000;
+        std::vector<int> tiles(lens.size());
+        if (walk(lens, 1, [&](int n) { return lens[n]; }, tiles) != 0) return printf("one run leaves a part\n"), 1;
+        for (size_t n = 0; n < lens.size(); ++n)
+            if (tiles[n] != tiles_of(lens[n])) return printf("tiles missed\n"), 1;
+        // lengths that change after the line was measured: nothing may go to the workspace, which has no room for it
+        if (walk(lens, 1, [&](int n) { return rand() % 2 ? lens[n] + rand() % 5000 : rand() % (lens[n] + 1); }, tiles) != 0)
+            return printf("one run leaves a part when lengths change\n"), 1;
+        std::vector<int> again(lens.size());
+        if (walk(lens, 2 + rand() % 150, [&](int n) { return lens[n]; }, again) < 0) return printf("a piece leaves its sequence\n"), 1;
+        for (size_t n = 0; n < lens.size(); ++n)
+            if (again[n] != tiles_of(lens[n])) return printf("tiles missed or taken twice\n"), 1;
+    }
+    printf("ok\n");
+    return 0;
+}
+"""
+
+
+def test_a_line_in_one_run_never_uses_the_workspace(tmp_path):
+    """With so many rows a step that one run is all the grid holds, the workspace has no room for partial results: the
+    walk of the run asks for none, not even where lengths change while the call runs."""
+    kbuild.build()
+    per_row = 512 * 4
+    for T, H in ((5, 1024), (16, 1024)):
+        assert kda.kda_latent_decode_workspace_size(2, 2 * T, H) < 64 * per_row
+    src, exe = tmp_path / "runs.cpp", tmp_path / "runs"
+    src.write_text(RUNS)
+    subprocess.run([os.environ.get("CXX", "g++"), "-std=c++17", "-O1", "-I", kbuild.CSRC, str(src), "-o", str(exe)], check=True)
+    done = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert done.returncode == 0 and done.stdout == "ok\n", done.stdout
