@@ -19,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 BINDING = os.path.join(PKG, "_latent.so")
+STAMP = os.path.join(BUILD, "latent_binding.txt")    # what the binding was compiled against
 HEADERS = [os.path.join(ROOT, "include", "kda.h")]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -38,30 +39,45 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _remove(*paths):
+    for path in paths:
+        if os.path.exists(path):
+            os.remove(path)
+
+
+def _built_for():
+    import torch
+    return f"torch {torch.__version__} python {sys.version}\n"
+
+
 def _start_binding(force: bool):
     """Start compiling the C++ binding of the latent-attention entry points against the installed torch, if it is
-    stale; returns (its path, the process or None)."""
+    stale; returns (its source, the process or None).  An older binding and its stamp go first, and the new ones
+    come after success (_finish_binding): a compilation that is cut short leaves nothing that could be loaded."""
     import sysconfig
 
     import torch
     from torch.utils import cpp_extension
 
     src = os.path.join(CSRC, "latent_binding.cpp")
-    stamp = os.path.join(BUILD, "latent_binding.txt")
-    built_for = f"torch {torch.__version__} python {sys.version}\n"
-    same = os.path.exists(stamp) and open(stamp).read() == built_for
+    same = os.path.exists(STAMP) and open(STAMP).read() == _built_for()
     if not force and same and not _stale(BINDING, [src] + HEADERS):
         return src, None
-    with open(stamp, "w") as f:
-        f.write(built_for)
+    _remove(STAMP, BINDING)
     inc = cpp_extension.include_paths() + ["/usr/local/cuda/include", sysconfig.get_paths()["include"],
                                            os.path.join(ROOT, "include")]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
-    cmd += [x for i in inc for x in ("-isystem", i)] + [src, "-o", BINDING]
+    cmd += [x for i in inc for x in ("-isystem", i)] + [src, "-o", os.path.join(BUILD, "latent_binding.so")]
     cmd += [f"-L{p}" for p in cpp_extension.library_paths()]
     cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
     return src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish_binding():
+    os.replace(os.path.join(BUILD, "latent_binding.so"), BINDING)
+    with open(STAMP, "w") as f:
+        f.write(_built_for())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None, tag=None) -> str:
@@ -93,9 +109,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, tag=None
         out, _ = p.communicate()
         if p.returncode != 0:
             failed.append((src, out.decode(errors="replace")))
-            if src.endswith(".cpp") and os.path.exists(BINDING):
-                os.remove(BINDING)               # not an older one in its place
-        elif verbose and out:
+            continue
+        if src.endswith(".cpp"):
+            _finish_binding()
+        if verbose and out:
             print(out.decode(errors="replace"), file=sys.stderr)
     if failed:
         raise RuntimeError("compilation failed:\n" + "\n".join(f"{s}\n{o}" for s, o in failed))
