@@ -389,7 +389,8 @@ typedef struct {
  * far positions keep their angles): (a, b) -> (a cos - b sin, a sin + b cos), rounded once.
  * latent:   [T, 512] rows, latent_stride elements apart; k_rope: [T, 64] rows, k_rope_stride
  *           elements apart (both may be columns of one projection); NULL with rope_dim 0.
- * inv_freq: DEVICE fp32 [32], or NULL: no rotation, rows are copied bit for bit.
+ * inv_freq: DEVICE fp32 [32], or NULL: no rotation, rows are copied bit for bit.  With rope_dim 0
+ *           there is nothing to rotate, and a table is accepted and not read.
  * interleaved: 0 pairs channels (i, i + 32), 1 pairs channels (2i, 2i + 1).
  * q_rope:   the queries' rotated part, [T, H] rows of 64, q_stride elements apart (64 for a tensor
  *           of its own, dk for the end of each row of kda_latent_prefill's q), or NULL: none.
@@ -399,7 +400,8 @@ typedef struct {
  * not written (its queries are rotated all the same); tokens that no sequence has leave cache and
  * q_rope_out alone.  Two tokens of a call that land on one row leave either's bytes there.
  * Errors: KDA_ERR_INVALID_ARG for NULL pointers, negative sizes, T % N != 0 without cu_seqlens,
- * N = 0 with T > 0, a stride below the row's width, q_rope without q_rope_out or with rope_dim 0;
+ * N = 0 with T > 0, a stride below the row's width, q_rope without q_rope_out or the reverse, k_rope
+ * or q_rope with rope_dim 0 (data that a call has no place for is refused, never dropped);
  * KDA_ERR_UNSUPPORTED for the shape limits above, pointers not 16-byte aligned (int32 and
  * inv_freq: 4) or strides that are not multiples of 8; KDA_ERR_CUDA if a launch fails.
  */
@@ -435,7 +437,7 @@ kda_status kda_latent_gather(const kda_latent_shape* shape, const void* cache, c
  * the caller, overwritten by the call; its contents need not be kept or cleared.  Two calls in
  * flight at once (two streams, or two graphs that may run at the same time) need two.
  * Errors: those of kda_decode_step and kda_latent_append; KDA_ERR_INVALID_ARG also for a scale
- * that is not finite and > 0 and a NULL or too small workspace, KDA_ERR_UNSUPPORTED for a
+ * that is not finite and > 0, q_rope with rope_dim 0 and a NULL or too small workspace, KDA_ERR_UNSUPPORTED for a
  * misaligned one, T' > 16 or N * T' * H > 2^31 - 1.
  */
 kda_status kda_latent_decode(const kda_latent_shape* shape, const void* q_latent, const void* q_rope,
@@ -463,7 +465,7 @@ kda_status kda_latent_decode_workspace_size(const kda_latent_shape* shape, size_
  *   s_ij = scale * (q_i[:128] . k_j + q_i[128:] . r_j),   out_i = sum_j softmax(s_i)_j v_j
  * Rows of out and lse behind the last sequence are left alone.
  * Errors: those of kda_prefill; KDA_ERR_INVALID_ARG also for a negative total_kv, total_kv % N != 0
- * without cu_seqlens_k, kv_stride < 128, a scale that is not finite and > 0;
+ * without cu_seqlens_k, kv_stride < 128, k_rope with dk = 128, a scale that is not finite and > 0;
  * KDA_ERR_UNSUPPORTED for another dk, dv or dtype, H > 1024, or a kv_stride that is not a multiple of 8.
  */
 kda_status kda_latent_prefill(const kda_shape* shape, int64_t total_kv, const void* q, const void* k, const void* v,

@@ -432,7 +432,7 @@ def kda_latent_append(latent, k_rope, cache, block_table, seq_lens, inv_freq=Non
     angles a position (None: no rotation).  ``q_rope`` [T, H, 64], possibly the end of longer rows, is
     rotated into ``q_rope_out`` (allocated when not given; q_rope itself rotates in place), which is
     returned; None without queries.  ``cu_seqlens``: a CUDA int32 tensor or a host table (None: equal
-    numbers of tokens)."""
+    numbers of tokens).  What the cache's width has no place for (k_rope, q_rope) is refused."""
     if stream is not None:
         with _on(stream, cache):
             return kda_latent_append(latent, k_rope, cache, block_table, seq_lens, inv_freq, interleaved, q_rope,
@@ -465,7 +465,7 @@ def kda_latent_decode(q_latent, q_rope, cache, block_table, seq_lens, scale, out
                       stream=None):
     """Absorbed latent attention over the paged cache, 1 to 16 tokens a sequence (see ``include/kda.h``).
 
-    q_latent: [N*T, H, 512]; q_rope: [N*T, H, 64] (None for a cache without it); seq_lens: [N] int32,
+    q_latent: [N*T, H, 512]; q_rope: [N*T, H, 64] (None for a cache without it, refused there); seq_lens: [N] int32,
     the step's tokens included (their rows are in the cache).  ``lse`` may be a [N*T, H] fp32 tensor to
     fill, True to allocate one, or None; ``workspace`` a CUDA uint8 tensor of
     kda_latent_decode_workspace_size bytes, allocated here when not given.  Returns (out [N*T, H, 512], lse)."""
@@ -482,7 +482,7 @@ def kda_latent_prefill(q, k, v, k_rope, scale, cu_seqlens=None, cu_seqlens_k=Non
     """Expanded latent attention, causal over packed sequences (see ``include/kda.h``).
 
     q: [T, H, 128 or 192]; k, v: [S, H, 128], tensors of their own or the halves of one [S, H, 256]
-    projection; k_rope: [S, 64], shared by the heads (None for 128-wide q).  ``cu_seqlens`` and
+    projection; k_rope: [S, 64], shared by the heads (None for 128-wide q, refused there).  ``cu_seqlens`` and
     ``cu_seqlens_k`` are CUDA int32 tensors or host tables (None: ``num_seqs`` equal sequences; keys as
     queries where only cu_seqlens is given and S = T).  Returns (out [T, H, 128], lse)."""
     if stream is not None:
@@ -490,7 +490,7 @@ def kda_latent_prefill(q, k, v, k_rope, scale, cu_seqlens=None, cu_seqlens_k=Non
             return kda_latent_prefill(q, k, v, k_rope, scale, cu_seqlens, cu_seqlens_k, num_seqs, out, lse)
     new = lse is True
     return (_native or _latent()).prefill(q, k, v, k_rope, scale, _table(cu_seqlens, q.shape[0], q),
-                                          _table(cu_seqlens_k, k.shape[0], q), 1 if num_seqs is None else num_seqs, out,
+                                          _table(cu_seqlens_k, k.shape[0], q), num_seqs, out,
                                           None if new else lse, new)
 
 

@@ -430,11 +430,11 @@ kda_status kda_latent_append(const kda_latent_shape* shape, const void* latent, 
     if (st != KDA_OK) return st;
     if (shape->total_tokens == 0) return KDA_OK;
     const bool rope = shape->rope_dim != 0;
-    if (!latent || (rope && !k_rope) || !seq_lens) return KDA_ERR_INVALID_ARG;
+    if (!latent || rope != (k_rope != nullptr) || !seq_lens) return KDA_ERR_INVALID_ARG;
     if (latent_stride < shape->latent_dim || (rope && k_rope_stride < shape->rope_dim)) return KDA_ERR_INVALID_ARG;
     if (q_rope && (!rope || !q_rope_out || q_stride < shape->rope_dim || q_out_stride < shape->rope_dim))
         return KDA_ERR_INVALID_ARG;
-    if ((interleaved != 0 && interleaved != 1)) return KDA_ERR_INVALID_ARG;
+    if ((q_rope_out && !q_rope) || (interleaved != 0 && interleaved != 1)) return KDA_ERR_INVALID_ARG;
     st = check_latent_cache(shape, cache, block_table);
     if (st != KDA_OK) return st;
     if (!aligned(latent, 16) || latent_stride % 8 != 0 || !aligned(seq_lens, 4)) return KDA_ERR_UNSUPPORTED;
@@ -460,7 +460,7 @@ kda_status kda_latent_gather(const kda_latent_shape* shape, const void* cache, c
     if (st != KDA_OK) return st;
     if (shape->total_tokens == 0) return KDA_OK;
     const bool rope = shape->rope_dim != 0;
-    if (!latent || (rope && !k_rope)) return KDA_ERR_INVALID_ARG;
+    if (!latent || rope != (k_rope != nullptr)) return KDA_ERR_INVALID_ARG;
     st = check_latent_cache(shape, cache, block_table);
     if (st != KDA_OK) return st;
     if (!aligned(latent, 16) || (rope && !aligned(k_rope, 16)) || !aligned(starts, 4)) return KDA_ERR_UNSUPPORTED;
@@ -493,7 +493,7 @@ kda_status kda_latent_decode(const kda_latent_shape* shape, const void* q_latent
     if (!(scale > 0.f) || !(scale < INFINITY)) return KDA_ERR_INVALID_ARG;
     if (shape->num_seqs == 0) return KDA_OK;
     const bool rope = shape->rope_dim != 0;
-    if (!q_latent || (rope && !q_rope) || !seq_lens || !out || !workspace) return KDA_ERR_INVALID_ARG;
+    if (!q_latent || rope != (q_rope != nullptr) || !seq_lens || !out || !workspace) return KDA_ERR_INVALID_ARG;
     st = check_latent_cache(shape, cache, block_table);
     if (st != KDA_OK) return st;
     if (!aligned(q_latent, 16) || (rope && !aligned(q_rope, 16)) || !aligned(seq_lens, 4) || !aligned(out, 16) ||
@@ -529,7 +529,7 @@ kda_status kda_latent_prefill(const kda_shape* shape, int64_t total_kv, const vo
     if ((shape->total_tokens / 256 + 1 + shape->num_seqs) * shape->H > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;   // grid
     if (shape->total_tokens == 0) return KDA_OK;
     const bool rope = shape->dk > 128, keys = total_kv > 0;
-    if (!q || !out || (keys && (!k || !v || (rope && !k_rope)))) return KDA_ERR_INVALID_ARG;
+    if (!q || !out || (keys && (!k || !v || (rope && !k_rope))) || (!rope && k_rope)) return KDA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
         (keys && (!aligned(k, 16) || !aligned(v, 16) || (rope && !aligned(k_rope, 16)))))
         return KDA_ERR_UNSUPPORTED;

@@ -55,6 +55,12 @@ void* expect(const char* name, const Opt& t, at::IntArrayRef shape, at::ScalarTy
     return expect(name, *t, shape, type, device, strides);
 }
 
+// An argument that the call's shape has no place for: it is refused, not dropped.
+void expect_none(const char* name, const Opt& t, const char* why) {
+    if (t) throw py::value_error(text(name, " must be None: ", why));
+}
+constexpr char kNoRope[] = "the cache's rows have no rotated part";
+
 c10::DeviceIndex index_of(const at::Tensor& t) {
     if (!t.is_cuda()) throw py::value_error("tensor arguments must be CUDA tensors");
     return (c10::DeviceIndex)t.get_device();
@@ -122,6 +128,8 @@ std::optional<at::Tensor> append(const at::Tensor& latent, const Opt& k_rope, co
     const int64_t latent_step = row_stride("latent", latent);
     const void* p_rope = shape.rope_dim ? expect("k_rope", k_rope, {T, kRope}, at::kBFloat16, dev, true) : nullptr;
     const int64_t rope_step = shape.rope_dim ? row_stride("k_rope", *k_rope) : 0;
+    if (!shape.rope_dim) expect_none("k_rope", k_rope, kNoRope);
+    if (!q_rope) expect_none("q_rope_out", q_out, "there is no q_rope");
     const void* p_lens = expect("seq_lens", lens, {n}, at::kInt, dev);
     const void* p_freq = inv_freq ? expect("inv_freq", *inv_freq, {kRope / 2}, at::kFloat, dev) : nullptr;
     const void* p_cu = cu ? expect("cu_seqlens", *cu, {n + 1}, at::kInt, dev) : nullptr;
@@ -155,7 +163,9 @@ std::pair<at::Tensor, std::optional<at::Tensor>> gather(const at::Tensor& cache,
     const int64_t n = shape.num_seqs;
     const void* p_cu = expect("cu_seqlens", cu, {n + 1}, at::kInt, dev);
     const void* p_starts = starts ? expect("starts", *starts, {n}, at::kInt, dev) : nullptr;
+    if (!shape.rope_dim) expect_none("k_rope", k_rope, kNoRope);
     if (!latent) {
+        expect_none("k_rope", k_rope, "out names no latent to go with it");
         latent = make({T, kLatent}, at::kBFloat16, cache);
         if (shape.rope_dim) k_rope = make({T, kRope}, at::kBFloat16, cache);
     }
@@ -182,6 +192,7 @@ std::pair<at::Tensor, std::optional<at::Tensor>> decode(const at::Tensor& q, con
     const kda_latent_shape shape = latent_shape(cache, table, rows, H, dev);
     const void* p_q = expect("q_latent", q, {rows, H, kLatent}, at::kBFloat16, dev);
     const void* p_r = shape.rope_dim ? expect("q_rope", q_rope, {rows, H, kRope}, at::kBFloat16, dev) : nullptr;
+    if (!shape.rope_dim) expect_none("q_rope", q_rope, kNoRope);
     const void* p_lens = expect("seq_lens", lens, {shape.num_seqs}, at::kInt, dev);
     if (!out) out = make({rows, H, kLatent}, at::kBFloat16, cache);
     if (make_lse) lse = make({rows, H}, at::kFloat, cache);
@@ -206,7 +217,7 @@ std::pair<at::Tensor, std::optional<at::Tensor>> decode(const at::Tensor& q, con
 
 std::pair<at::Tensor, std::optional<at::Tensor>> prefill(const at::Tensor& q, const at::Tensor& k, const at::Tensor& v,
                                                          const Opt& k_rope, double scale, const Opt& cu, const Opt& cu_k,
-                                                         int64_t num_seqs, Opt out, Opt lse, bool make_lse) {
+                                                         std::optional<int64_t> num_seqs, Opt out, Opt lse, bool make_lse) {
     const auto dev = index_of(q);
     const c10::cuda::CUDAGuard guard(dev);
     if (q.dim() != 3 || (q.size(2) != kHead && q.size(2) != kHead + kRope))
@@ -217,9 +228,10 @@ std::pair<at::Tensor, std::optional<at::Tensor>> prefill(const at::Tensor& q, co
     const void* p_k = expect("k", k, {S, H, kHead}, at::kBFloat16, dev, true);
     const void* p_v = expect("v", v, {S, H, kHead}, at::kBFloat16, dev, true);
     const void* p_r = dk > kHead ? expect("k_rope", k_rope, {S, dk - kHead}, at::kBFloat16, dev) : nullptr;
+    if (dk == kHead) expect_none("k_rope", k_rope, "q has no rotated part");
     const int64_t step = row_stride("k", k);
     if (S * H > 1 && step != row_stride("v", v)) throw py::value_error("k and v must have the same row stride");
-    int64_t n = num_seqs;
+    int64_t n = num_seqs.value_or(1);
     if (cu) {
         if (cu->dim() != 1 || cu->numel() < 1) throw py::value_error("cu_seqlens must hold N + 1 offsets");
         n = cu->numel() - 1;
@@ -227,6 +239,7 @@ std::pair<at::Tensor, std::optional<at::Tensor>> prefill(const at::Tensor& q, co
         if (cu_k->dim() != 1 || cu_k->numel() < 1) throw py::value_error("cu_seqlens_k must hold N + 1 offsets");
         n = cu_k->numel() - 1;
     }
+    if (num_seqs && *num_seqs != n) throw py::value_error(text("num_seqs is ", *num_seqs, ", but the offsets are those of ", n));
     if (n < 0 || n > INT32_MAX || H > INT32_MAX) throw py::value_error("too many sequences or heads");
     const void* p_cu = cu ? expect("cu_seqlens", *cu, {n + 1}, at::kInt, dev) : nullptr;
     // the queries' table serves the keys where there are as many

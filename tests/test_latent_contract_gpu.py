@@ -106,3 +106,39 @@ def test_decode_of_so_many_rows_that_few_runs_are_left(T, H, rope):
     o, s, bo, bs = ref.decode(q, qr, cache, table, i32(lens), 0.07)
     ref.assert_within(out, o, bo, "out")
     ref.assert_within(lse, s, bs, "lse")
+
+
+def test_the_binding_drops_no_argument():
+    """A rotated part for rows that have none, an output without its input, a number of sequences that the offsets
+    contradict: refused with the argument's name, and nothing is written."""
+    g = gen(31)
+    cache, table, lens = randn(g, 4, 16, 512), i32([[0, 1], [2, 3]]), i32([20, 32])
+    full = randn(g, 4, 16, 576)
+    before = cache.clone(), full.clone()
+    lat, kr, q, qr = randn(g, 2, 512), randn(g, 2, 64), randn(g, 2, 4, 512), randn(g, 2, 4, 64)
+    p = (randn(g, 10, 2, 128), randn(g, 10, 2, 128), randn(g, 10, 2, 128))
+    wide, cu = randn(g, 10, 2, 192), i32([0, 4, 10])
+    new = lambda: torch.empty(2, 512, dtype=BF, device=DEV)    # noqa: E731
+    freq = torch.ones(32, device=DEV)
+    for name, call in (
+            ("k_rope", lambda: kda.kda_latent_append(lat, kr, cache, table, lens)),
+            ("q_rope", lambda: kda.kda_latent_append(lat, None, cache, table, lens, inv_freq=freq, q_rope=qr)),
+            ("q_rope_out", lambda: kda.kda_latent_append(lat, kr, full, table, lens, q_rope_out=qr)),
+            ("k_rope", lambda: kda.kda_latent_gather(cache, table, [0, 1, 2], 2, out=(new(), kr))),
+            ("k_rope", lambda: kda.kda_latent_gather(cache, table, [0, 1, 2], 2, out=(None, kr))),
+            ("k_rope", lambda: kda.kda_latent_gather(full, table, [0, 1, 2], 2, out=(None, kr))),
+            ("q_rope", lambda: kda.kda_latent_decode(q, qr, cache, table, lens, 0.07)),
+            ("k_rope", lambda: kda.kda_latent_prefill(*p, randn(g, 10, 64), 0.07)),
+            ("num_seqs", lambda: kda.kda_latent_prefill(*p, None, 0.07, cu_seqlens=cu, num_seqs=5)),
+            ("num_seqs", lambda: kda.kda_latent_prefill(wide, *p[1:], randn(g, 10, 64), 0.07, cu_seqlens_k=cu, num_seqs=1))):
+        with pytest.raises((ValueError, kda.KdaError), match=name if name != "q_rope" else "q_rope|INVALID_ARG"):
+            call()
+    clean()
+    assert torch.equal(cache, before[0]) and torch.equal(full, before[1])
+    # the same calls as they belong
+    kda.kda_latent_append(lat, None, cache, table, lens, inv_freq=freq)
+    kda.kda_latent_append(lat, kr, full, table, lens, q_rope=qr, q_rope_out=qr)
+    kda.kda_latent_gather(cache, table, [0, 1, 2], 2, out=(new(), None))
+    kda.kda_latent_decode(q, None, cache, table, lens, 0.07)
+    kda.kda_latent_prefill(*p, None, 0.07, cu_seqlens=cu, num_seqs=2)
+    clean()

@@ -1,12 +1,15 @@
 """Latent attention on the host: promises of the calls that need no GPU to be checked."""
+import ctypes
 import glob
 import os
 import re
 import subprocess
 
 import pytest
+import torch
 
 import linear_attention_06_gb300 as kda
+from linear_attention_06_gb300 import _lib
 from linear_attention_06_gb300 import build as kbuild
 
 
@@ -87,3 +90,38 @@ def test_a_line_in_one_run_never_uses_the_workspace(tmp_path):
     subprocess.run([os.environ.get("CXX", "g++"), "-std=c++17", "-O1", "-I", kbuild.CSRC, str(src), "-o", str(exe)], check=True)
     done = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
     assert done.returncode == 0 and done.stdout == "ok\n", done.stdout
+
+
+FAKE = 0x10000                          # never dereferenced
+
+
+def test_data_without_a_place_is_refused():
+    """Rotated parts beside a cache or queries that have none, and an output without its input: all refused before any
+    CUDA call; the same calls without them get as far as the device."""
+    kbuild.build()
+    L = kda.lib()
+    bare = ctypes.byref(kda.KdaLatentShape(2, 2, 4, 512, 0, 64, 8, 4, _lib.KDA_BF16))
+    full = ctypes.byref(kda.KdaLatentShape(2, 2, 4, 512, 64, 64, 8, 4, _lib.KDA_BF16))
+    narrow = ctypes.byref(kda.KdaShape(2, 4, 3, 128, 128, _lib.KDA_BF16))
+    ends = (None, FAKE, FAKE, FAKE, None)                      # cu_seqlens, seq_lens, block_table, cache, stream
+
+    def append(shape, k_rope, freq, q, q_out):
+        return L.kda_latent_append(shape, FAKE, 512, k_rope, 64, freq, 0, q, 64, q_out, 64, *ends)
+
+    def gather(k_rope):
+        return L.kda_latent_gather(bare, FAKE, FAKE, FAKE, None, FAKE, k_rope, None)
+
+    def decode(q_rope):
+        return L.kda_latent_decode(bare, FAKE, q_rope, FAKE, FAKE, FAKE, 1.0, FAKE, None, FAKE, 1 << 40, None)
+
+    def prefill(k_rope, total_kv=4):
+        return L.kda_latent_prefill(narrow, total_kv, FAKE, FAKE, FAKE, 128, k_rope, 1.0, None, None, FAKE, None, None)
+
+    for st in (append(bare, FAKE, None, None, None), append(bare, FAKE, FAKE, None, None), append(bare, None, None, FAKE, FAKE),
+               append(full, FAKE, FAKE, None, FAKE), gather(FAKE), decode(FAKE), prefill(FAKE), prefill(FAKE, 0)):
+        assert st == _lib.KDA_ERR_INVALID_ARG
+    if torch.cuda.is_available():
+        return                                                 # the calls below would run on the addresses
+    for st in (append(bare, None, None, None, None), append(bare, None, FAKE, None, None), append(full, FAKE, FAKE, None, None),
+               gather(None), decode(None), prefill(None), prefill(None, 0)):
+        assert st == _lib.KDA_ERR_CUDA
