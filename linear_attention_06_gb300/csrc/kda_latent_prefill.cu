@@ -39,6 +39,7 @@
 
 #include "kda_internal.h"
 #include "kda_latent_common.cuh"
+#include "kda_latent_split.h"
 #include "sm103_primitives.cuh"
 
 namespace kda {
@@ -654,21 +655,16 @@ int clusters_at_once(int dev, int parts) {
     return n;
 }
 
-// How many blocks share the keys of a block of queries: as many as there are SMs for, up to eight and each with a tile
-// of an average sequence, if that saves each kJoinTiles tiles, which is what the join costs (3 us).  Measured, dk = 192:
-// 1 x 100 queries over 16384 keys, 32 heads, 53 us in fours and 168 alone; 1 x 128 over 8192, one head, 19 in eights,
-// 29 in fours, 86 alone; 1 x 64 over 600, 8 heads, 10.8 in fours and 11.6 alone; 1 x 512 without prefix, 8 heads, 14.6 in
-// twos and 12.8 alone; 1 x 200 over 4096, 18 heads, more clusters of eight than run at once 34.5, in fours 22.7.
-constexpr int kJoinTiles = 3;
+// How many blocks share the keys of a block of queries: a rule on average lengths (kda_latent_split.h).  Measured, dk =
+// 192: 1 x 100 queries over 16384 keys, 32 heads, 52 us in fours and 167 alone; 1 x 128 over 8192, one head, 19 in eights,
+// 29 in fours, 86 alone; 1 x 64 over 600, 8 heads, 10.5 in fours and 11.4 alone; 1 x 512 without prefix, 8 heads, 12.2 in
+// fours, 14.2 in twos and 12.3 alone; 1 x 200 over 4096, 18 heads, more clusters of eight than run at once 34.0, in fours
+// 22.2; 4 x 512 without prefix, 4 heads, whose slots are more clusters of four than run at once, 15.6, alone 12.6.
 template <int DK>
-int parts_of(const LatentPrefillArgs& a, int dev) {
+int parts_of(const LatentPrefillArgs& a, int64_t slots, int dev) {
     const int64_t each_q = (a.total_q + a.num_seqs - 1) / a.num_seqs, tiles = a.total_kv / a.num_seqs / kN;
-    const int64_t blocks = (each_q + kBlockQ - 1) / kBlockQ * a.num_seqs * a.H;
-    for (int parts = 8; parts > 1; parts /= 2)
-        if (tiles >= parts && tiles - (tiles + parts - 1) / parts >= kJoinTiles &&
-            blocks <= clusters_at_once<DK>(dev, parts))
-            return parts;
-    return 1;
+    const int64_t busy = (each_q + kBlockQ - 1) / kBlockQ * a.num_seqs * a.H;
+    return split_of(tiles, busy, slots * a.H, [&](int parts) { return clusters_at_once<DK>(dev, parts); });
 }
 
 template <int DK>
@@ -694,7 +690,7 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
     cudaError_t e = set_up<DK, false>(dev);
     if (e == cudaSuccess) e = set_up<DK, true>(dev);
     if (e != cudaSuccess) return e;
-    const int parts = parts_of<DK>(a, dev);
+    const int parts = parts_of<DK>(a, slots, dev);
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config<DK>(blocks, parts, s, &attr);
     e = cudaLaunchKernelEx(&cfg, parts > 1 ? latent_prefill_kernel<DK, true> : latent_prefill_kernel<DK, false>, maps, a, slots,

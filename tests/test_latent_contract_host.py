@@ -125,3 +125,55 @@ def test_data_without_a_place_is_refused():
     for st in (append(bare, None, None, None, None), append(bare, None, FAKE, None, None), append(full, FAKE, FAKE, None, None),
                gather(None), decode(None), prefill(None), prefill(None, 0)):
         assert st == _lib.KDA_ERR_CUDA
+
+
+SPLIT = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "kda_latent_split.h"
+int main(int argc, char** argv) {
+    // tiles, clusters with queries, clusters, and how many of two, four and eight blocks run at once
+    const int room[3] = {atoi(argv[4]), atoi(argv[5]), atoi(argv[6])};
+    printf("%d", kda::latent::split_of(atoll(argv[1]), atoll(argv[2]), atoll(argv[3]),
+                                       [&](int parts) { return room[parts == 2 ? 0 : parts == 4 ? 1 : 2]; }));
+    return 0;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def split(tmp_path_factory):
+    d = tmp_path_factory.mktemp("split")
+    (d / "split.cpp").write_text(SPLIT)
+    subprocess.run([os.environ.get("CXX", "g++"), "-std=c++17", "-I", kbuild.CSRC, str(d / "split.cpp"), "-o", str(d / "split")],
+                   check=True)
+
+    def call(n, nq, nk, H, room=(76, 36, 15)):
+        busy, slots = -(-nq // 256) * n * H, (-(-n * nq // 256) + n - 1) * H
+        args = [nk // 128, busy, slots, *room]
+        return int(subprocess.run([str(d / "split"), *map(str, args)], capture_output=True, text=True, check=True).stdout)
+    return call
+
+
+@pytest.mark.parametrize("n,nq,nk,H,good", [
+    # more slots than clusters that start together: the times of 1, 2 and 4 blocks (us) stand behind each
+    (4, 512, 512, 4, (1,)),                                    # 12.6, 15.0, 15.6
+    (9, 256, 512, 4, (1,)),                                    # 12.7, 15.6, 25.0
+    (12, 100, 512, 3, (1,)),                                   # 11.3, 11.7, 16.2
+    (8, 256, 1024, 4, (1, 2)),                                 # 18.2, 18.1, 21.1
+    (4, 256, 1024, 16, (1,)),                                  # 18.6, 23.3, 34.5
+    (9, 256, 2048, 4, (2,)),                                   # 29.3, 23.8, 29.4
+    (4, 256, 4096, 8, (4,)),                                   # 50.7, 34.0, 29.1
+    (8, 256, 4096, 8, (2,)),                                   # 57.4, 45.0, 56.7
+    # one sequence, all its clusters at work together
+    (1, 100, 16384, 32, (4,)), (1, 128, 8192, 1, (8,)), (1, 64, 600, 8, (4,)), (1, 200, 4096, 18, (4,)),
+    (1, 512, 512, 8, (1, 4)), (1, 512, 512, 32, (1,)), (1, 1024, 1024, 1, (8,)), (1, 2048, 2048, 8, (2,)),
+    (3, 100, 100, 32, (1,)), (4, 8192, 8192, 32, (1,))])
+def test_blocks_share_keys_only_where_that_is_faster(split, n, nq, nk, H, good):
+    """The number of blocks that share a block's keys, against what was measured on a card that runs 76 clusters of
+    two, 36 of four and 15 of eight at once."""
+    assert split(n, nq, nk, H) in good
+
+
+def test_no_sharing_where_no_cluster_runs(split):
+    assert split(1, 100, 16384, 32, room=(0, 0, 0)) == 1
