@@ -28,26 +28,28 @@ struct Turn {
     float c, s;
 };
 
+// What happens to a row's rotated part: copied, pairs (i, i + 32) turned, pairs (2i, 2i + 1) turned.  A copy keeps every
+// bit: a product with (1, 0) would turn an infinite channel's partner into NaN and could lose the sign of a zero.
+enum Turning { kCopied, kHalves, kInterleaved };
+
 // Eight pairs of one 64-channel row: the two 16-byte chunks that unit u (0..3) of the row owns, i.e.
 // channels 8u.. and 8u + 32.. (pairs i, i + 32), or 16u..16u + 15 (interleaved pairs).
 struct Unit {
     uint4 x0, x1;
 };
-template <bool INTERLEAVED>
+template <Turning TURN>
 __device__ __forceinline__ Unit load_unit(const __nv_bfloat16* src, int u) {
     const uint4* p = reinterpret_cast<const uint4*>(src);
-    return {p[INTERLEAVED ? 2 * u : u], p[INTERLEAVED ? 2 * u + 1 : u + 4]};
+    return {p[TURN == kInterleaved ? 2 * u : u], p[TURN == kInterleaved ? 2 * u + 1 : u + 4]};
 }
-template <bool INTERLEAVED>
+template <Turning TURN>
 __device__ __forceinline__ void store_unit(uint4 y0, uint4 y1, __nv_bfloat16* dst, int u) {
-    reinterpret_cast<uint4*>(dst)[INTERLEAVED ? 2 * u : u] = y0;
-    reinterpret_cast<uint4*>(dst)[INTERLEAVED ? 2 * u + 1 : u + 4] = y1;
+    reinterpret_cast<uint4*>(dst)[TURN == kInterleaved ? 2 * u : u] = y0;
+    reinterpret_cast<uint4*>(dst)[TURN == kInterleaved ? 2 * u + 1 : u + 4] = y1;
 }
-// Without angles a row is copied bit for bit: a product with (1, 0) would turn an infinite channel's partner into NaN
-// and could lose the sign of a zero.
-template <bool INTERLEAVED>
+template <Turning TURN>
 __device__ __forceinline__ void rotate_unit(const Unit& x, __nv_bfloat16* dst, int u, const Turn* turn) {
-    if (!turn) return store_unit<INTERLEAVED>(x.x0, x.x1, dst, u);
+    if constexpr (TURN == kCopied) return store_unit<TURN>(x.x0, x.x1, dst, u);
     const __nv_bfloat162* a = reinterpret_cast<const __nv_bfloat162*>(&x.x0);
     const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&x.x1);
     uint4 y0, y1;
@@ -56,7 +58,7 @@ __device__ __forceinline__ void rotate_unit(const Unit& x, __nv_bfloat16* dst, i
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const float2 fa = __bfloat1622float2(a[k]), fb = __bfloat1622float2(b[k]);
-        if constexpr (INTERLEAVED) {            // fa, fb are pairs 8u + k and 8u + 4 + k
+        if constexpr (TURN == kInterleaved) {   // fa, fb are pairs 8u + k and 8u + 4 + k
             const Turn t = turn[8 * u + k], v = turn[8 * u + 4 + k];
             ya[k] = __floats2bfloat162_rn(fa.x * t.c - fa.y * t.s, fa.x * t.s + fa.y * t.c);
             yb[k] = __floats2bfloat162_rn(fb.x * v.c - fb.y * v.s, fb.x * v.s + fb.y * v.c);
@@ -66,7 +68,7 @@ __device__ __forceinline__ void rotate_unit(const Unit& x, __nv_bfloat16* dst, i
             yb[k] = __floats2bfloat162_rn(fa.x * t.s + fb.x * t.c, fa.y * v.s + fb.y * v.c);
         }
     }
-    store_unit<INTERLEAVED>(y0, y1, dst, u);
+    store_unit<TURN>(y0, y1, dst, u);
 }
 
 // find_seq by a whole warp: 32 offsets a step instead of one, since each step waits for memory.
@@ -89,7 +91,7 @@ __device__ __forceinline__ int find_seq_warp(const int32_t* cu, int num_seqs, in
 // TOK tokens a block.  The rows to copy and to rotate are requested before anything else: they arrive while the
 // block finds its tokens' sequences, pages and angles.  A thread's first kQ units of queries take part in that;
 // queries of more heads follow in a loop.
-template <int TOK, bool INTERLEAVED>
+template <int TOK, Turning TURN>
 __global__ void __launch_bounds__(kThreads, 3) append_kernel(const LatentAppendArgs a) {
     constexpr int kChunks = kLatent / 8, kLat = (TOK * kChunks + kThreads - 1) / kThreads, kQ = 4;
     __shared__ int64_t row_s[TOK], pos_s[TOK];
@@ -114,13 +116,13 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const LatentAppendA
         if (i < count * kChunks)
             lat[k] = reinterpret_cast<const uint4*>(latent + (t0 + i / kChunks) * a.latent_stride)[i % kChunks];
     }
-    if (k_rope && tid < count * 4) key = load_unit<INTERLEAVED>(k_rope + (t0 + (tid >> 2)) * a.k_rope_stride, tid & 3);
+    if (k_rope && tid < count * 4) key = load_unit<TURN>(k_rope + (t0 + (tid >> 2)) * a.k_rope_stride, tid & 3);
 #pragma unroll
     for (int k = 0; k < kQ; ++k) {
         const int i = tid + k * kThreads;
-        if (i < count * units) q[k] = load_unit<INTERLEAVED>(q_rope + (t0 * a.H + (i >> 2)) * a.q_stride, i & 3);
+        if (i < count * units) q[k] = load_unit<TURN>(q_rope + (t0 * a.H + (i >> 2)) * a.q_stride, i & 3);
     }
-    if (a.inv_freq && tid >= kThreads - kRope / 2) {
+    if (TURN != kCopied && tid >= kThreads - kRope / 2) {
         const int k = tid - (kThreads - kRope / 2);
         const double turn = (double)a.inv_freq[k] * 0.15915494309189533577;                   // / 2 pi
         step_s[k] = (uint64_t)((turn - floor(turn)) * 18446744073709551616.0);                // * 2^64
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const LatentAppendA
         }
     }
     __syncthreads();
-    if (a.inv_freq) {
+    if (TURN != kCopied) {
         for (int i = tid; i < count * (kRope / 2); i += kThreads) {
             const int j = i / (kRope / 2), k = i % (kRope / 2);
             const uint64_t angle = (uint64_t)pos_s[j] * step_s[k];
@@ -148,7 +150,6 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const LatentAppendA
         }
         __syncthreads();
     }
-    auto turns = [&](int j) -> const Turn* { return a.inv_freq ? turn_s[j] : nullptr; };
     __nv_bfloat16* cache = static_cast<__nv_bfloat16*>(a.c.cache);
 #pragma unroll
     for (int k = 0; k < kLat; ++k) {
@@ -156,12 +157,12 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const LatentAppendA
         if (i < count * kChunks && row_s[j] >= 0) reinterpret_cast<uint4*>(cache + row_s[j] * width)[i % kChunks] = lat[k];
     }
     if (k_rope && tid < count * 4 && row_s[tid >> 2] >= 0)
-        rotate_unit<INTERLEAVED>(key, cache + row_s[tid >> 2] * width + kLatent, tid & 3, turns(tid >> 2));
+        rotate_unit<TURN>(key, cache + row_s[tid >> 2] * width + kLatent, tid & 3, turn_s[tid >> 2]);
     auto turn_q = [&](int i, const Unit& x) {
         const int j = i / units;
         if (live_s[j])
-            rotate_unit<INTERLEAVED>(x, static_cast<__nv_bfloat16*>(a.q_out) + (t0 * a.H + (i >> 2)) * a.q_out_stride, i & 3,
-                                     turns(j));
+            rotate_unit<TURN>(x, static_cast<__nv_bfloat16*>(a.q_out) + (t0 * a.H + (i >> 2)) * a.q_out_stride, i & 3,
+                                     turn_s[j]);
     };
 #pragma unroll
     for (int k = 0; k < kQ; ++k) {
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const LatentAppendA
         if (i < count * units) turn_q(i, q[k]);
     }
     for (int i = tid + kQ * kThreads; i < count * units; i += kThreads)
-        turn_q(i, load_unit<INTERLEAVED>(q_rope + (t0 * a.H + (i >> 2)) * a.q_stride, i & 3));
+        turn_q(i, load_unit<TURN>(q_rope + (t0 * a.H + (i >> 2)) * a.q_stride, i & 3));
 }
 
 // ROWS rows a block, a 16-byte chunk a thread and step, all of a thread's loads before its stores.  The rows are read
@@ -218,7 +219,8 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const LatentGatherArgs
 template <int TOK>
 cudaError_t append(const LatentAppendArgs& a, bool overlapped, cudaStream_t s) {
     const unsigned blocks = (unsigned)((a.total_tokens + TOK - 1) / TOK);
-    const auto kernel = a.interleaved ? append_kernel<TOK, true> : append_kernel<TOK, false>;
+    const auto kernel = !a.inv_freq ? append_kernel<TOK, kCopied>
+                        : a.interleaved ? append_kernel<TOK, kInterleaved> : append_kernel<TOK, kHalves>;
     if (overlapped) return launch_overlapped(kernel, blocks, kThreads, 0, s, a);
     kernel<<<blocks, kThreads, 0, s>>>(a);
     return cudaGetLastError();
