@@ -142,3 +142,53 @@ def test_the_binding_drops_no_argument():
     kda.kda_latent_decode(q, None, cache, table, lens, 0.07)
     kda.kda_latent_prefill(*p, None, 0.07, cu_seqlens=cu, num_seqs=2)
     clean()
+
+
+def test_captured_calls_behind_two_branches():
+    """A capture that forks and joins: calls that may start early behind work of two streams, replayed with new rows."""
+    g = gen(41)
+    n, each, page = 3, 4000, 64
+    per = -(-each // page)
+    cache = [randn(g, n * per, page, 576) for _ in range(2)]
+    table = torch.arange(n * per, dtype=torch.int32, device=DEV).view(n, per)
+    lens, cu = i32([each] * n), i32([each * k for k in range(n + 1)])
+    T = n * each
+    new = [(randn(g, T, 512), randn(g, T, 64)) for _ in range(2)]
+    q, qr = randn(g, n, 32, 512), randn(g, n, 32, 64)
+    rows = [(torch.empty(T, 512, dtype=BF, device=DEV), torch.empty(T, 64, dtype=BF, device=DEV)) for _ in range(3)]
+    ws = [torch.empty(kda.kda_latent_decode_workspace_size(n, n, 32), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    out = [torch.empty_like(q) for _ in range(2)]
+    side = torch.cuda.Stream()
+
+    def run():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        for k, stream in enumerate((main, side)):
+            with torch.cuda.stream(stream):
+                kda.kda_latent_append(*new[k], cache[k], table, lens, cu_seqlens=cu)
+                kda.kda_latent_decode(q, qr, cache[k], table, lens, 0.07, out=out[k], workspace=ws[k])
+                kda.kda_latent_gather(cache[k], table, cu, T, out=rows[k])
+        main.wait_stream(side)
+        kda.kda_latent_append(*new[0], cache[1], table, lens, cu_seqlens=cu)      # behind both branches
+        kda.kda_latent_gather(cache[1], table, cu, T, out=rows[2])
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for seed in range(4):
+        h = gen(100 + seed)
+        for x in new:
+            for y in x:
+                y.copy_(randn(h, *y.shape))
+        graph.replay()
+        clean()
+        for got, want in zip(rows, (new[0], new[1], new[0])):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        for k in range(2):
+            c = torch.cat(new[k], 1).view(n, each, 576)
+            for i in range(n):
+                o, _, bo, _ = ref.attend(torch.cat([q[i], qr[i]], -1).double(), c[i].double(), c[i, :, :512].double(), 0.07,
+                                         torch.full((32,), each, device=DEV))
+                ref.assert_within(out[k][i], o, bo, "out")
