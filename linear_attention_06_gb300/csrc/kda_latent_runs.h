@@ -54,9 +54,12 @@ struct RunWalk {
 };
 
 // Whether a piece's result is its sequence's, and goes to the output.  Other pieces go to the workspace, which a line in
-// one run does not have: there every piece is the only one of its sequence, also where a length that grew since the line
-// was measured makes it look cut.
-KDA_RUNS_FN bool is_whole(const Piece& p, int runs) { return runs == 1 || (p.off == 0 && p.tiles == p.all); }
+// one run does not have: there every piece is the only one of its sequence (settle), also where a length that grew since
+// the line was measured makes it look cut.
+KDA_RUNS_FN void settle(Piece& p, int runs) {
+    if (runs == 1) p.all = p.off + p.tiles;
+}
+KDA_RUNS_FN bool is_whole(const Piece& p) { return p.off == 0 && p.tiles == p.all; }
 
 }  // namespace latent
 }  // namespace kda

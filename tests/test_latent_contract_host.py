@@ -49,7 +49,8 @@ static int walk(const std::vector<int>& lens, int runs, const Length& length, st
         while (w.next(count, length, p)) {
             if (p.n < 0 || p.n >= count || p.off < 0 || p.tiles <= 0 || p.off + p.tiles > p.all) return -1;
             tiles[p.n] += p.tiles;
-            partial += !is_whole(p, runs);
+            settle(p, runs);
+            partial += !is_whole(p);
         }
     }
     return partial;
