@@ -362,6 +362,9 @@ kda_status kda_decode_step_gated(const kda_shape* shape, const void* q, const vo
  * - The cache rows behind a sequence's end, and rows of q, k, v behind the last sequence, may hold
  *   anything (NaN too): they reach no result.  Values that a sequence itself holds are taken as
  *   finite: an infinite or NaN value reaches every row of its tile.
+ * - Scores, maxima, sums and partial results of kda_latent_decode and kda_latent_prefill are fp32;
+ *   the softmax weights are rounded to bf16, the tensor cores' operand type, for the product with
+ *   the values (their sum is not), and the output is rounded once more.
  * - Supported: dtype KDA_BF16, latent_dim 512, rope_dim 0 or 64, page_size a power of two in
  *   16 .. 1024, H <= 1024, and at most 2^31 - 1 rows in the cache and in one block_table row.
  */

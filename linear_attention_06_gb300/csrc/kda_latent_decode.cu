@@ -27,10 +27,10 @@
 // in bf16, whose precision does not depend on the exponent, sums are fp32, and the rescaling of O in tensor
 // memory is rare.  P is rounded to bf16 for the tensor cores; its sum is taken before that rounding.
 //
-// Measured (GB300, 6688 GB/s measured copy rate), 32 heads, one token: 608 x 4096 cached tokens 411 us, 1.04 of that
-// rate; 64 x 8192 105.1 us (0.86); 1 x 131072 36.4 us (0.62).  What is missing there is fixed: 3 us until a block's
+// Measured (GB300, 6688 GB/s measured copy rate), 32 heads, one token: 608 x 4096 cached tokens 417 us, 1.03 of that
+// rate; 64 x 8192 105.3 us (0.86); 1 x 131072 36.5 us (0.62).  What is missing there is fixed: 3 us until a block's
 // first load (lengths, then page entries), 3 us from its last row to its result, 3-5 us of join; and the SMs' unequal
-// shares of the bandwidth (their ends are spread over 5%).  128 heads, 64 x 8192: 212.3 us, 688 TFLOP/s: two groups of
+// shares of the bandwidth (their ends are spread over 5%).  128 heads, 64 x 8192: 211.8 us, 689 TFLOP/s: two groups of
 // 64 rows, each with room for two tiles only, so that a tile's load waits for the one before the last.
 #include <atomic>
 #include <cuda.h>

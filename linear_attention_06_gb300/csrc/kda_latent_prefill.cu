@@ -23,9 +23,9 @@
 // Keys stream through a ring of 16 KB slices of 64 channels, each handed back when B's product has read it, values
 // through two stages of 32 KB.
 //
-// Measured (GB300): 4 x 8192 tokens x 32 heads, dk = 192: 1.71 ms, 1.61 PFLOP/s, 0.92 of the sustained cuBLAS rate,
+// Measured (GB300): 4 x 8192 tokens x 32 heads, dk = 192: 1.70 ms, 1.62 PFLOP/s, 0.93 of the sustained cuBLAS rate,
 // under the power cap (1.7 GHz; 1.51 ms in a short run before it; the tensor pipe computes for 0.81 of a launch).
-// dk = 128, 2 x 1024 queries over 17408 keys: 397 us, 1.43 PFLOP/s: about 2800 cycles for 2048 of products, the chain
+// dk = 128, 2 x 1024 queries over 17408 keys: 390 us, 1.45 PFLOP/s: about 2800 cycles for 2048 of products, the chain
 // of one tile, and 256 blocks for 152 SMs.  A thread a query with 128 registers of scores was 1% slower in both (1.78
 // against 1.76 ms, 420 against 416 us, before the last steps).
 #include <atomic>
