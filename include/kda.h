@@ -454,6 +454,66 @@ kda_status kda_latent_decode(const kda_latent_shape* shape, const void* q_latent
 kda_status kda_latent_decode_workspace_size(const kda_latent_shape* shape, size_t* bytes);
 
 /*
+ * The latent cache in 8 bits: half the bytes a cached token, so half the time of a decode step, which they bound, and
+ * twice the tokens that a cache holds.
+ *
+ *   kda_latent_append_q8   new tokens' rows quantised into the cache, queries rotated as by kda_latent_append
+ *   kda_latent_gather_q8   cached rows back to packed bf16 rows (then: up-projection, kda_latent_prefill)
+ *   kda_latent_decode_q8   kda_latent_decode over the 8-bit cache
+ *
+ * cache [num_pages, page_size, latent_dim + rope_dim] in e4m3 (OCP 8-bit floating point, 4 exponent and 3 mantissa
+ * bits, largest number 448), scales [num_pages, page_size] bytes: a row's power of two, e8m0 (byte = e + 127).  Row
+ * values are e4m3 number * 2^e.  The append takes, for a row x (rotated part included, in fp32),
+ *
+ *   e = the smallest integer with max |x_i| <= 448 * 2^e, within -64 .. 120 (-64 for a row of zeros),
+ *   number_i = x_i * 2^-e rounded to the nearest e4m3, ties to even.
+ *
+ * One scale a row and not a page: rows come one at a time in decoding, and a row once written is not rounded again.
+ * A power of two: scaling by it is exact, so that a value is rounded once, is off by at most 2^-4 of itself
+ * (2^-10 * 2^e near zero), and is exact in bf16.  Bytes of scales outside 63 .. 247 count as the nearest of these.
+ * Everything else is as for the bf16 cache above (dtype KDA_BF16: the type of queries, rows in and out), with
+ * cache aligned to 16 bytes and scales (1 byte each) anywhere.  Cache rows and scales behind a sequence's end may hold
+ * anything.
+ */
+
+/*
+ * kda_latent_append_q8 -- kda_latent_append into an 8-bit cache: the same arguments, then scales [num_pages, page_size].
+ * Without inv_freq k_rope is quantised as it is.  An infinite or NaN channel reaches its own row only, which then holds
+ * 448 * 2^120 or NaN there.  Two tokens of a call that land on one row leave a row of neither.
+ * Errors: kda_latent_append's; KDA_ERR_INVALID_ARG also for scales NULL with num_pages > 0.
+ */
+kda_status kda_latent_append_q8(const kda_latent_shape* shape, const void* latent, int64_t latent_stride,
+                                const void* k_rope, int64_t k_rope_stride, const float* inv_freq,
+                                int32_t interleaved, const void* q_rope, int64_t q_stride, void* q_rope_out,
+                                int64_t q_out_stride, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                                const int32_t* block_table, void* cache, uint8_t* scales, kda_stream_t stream);
+
+/*
+ * kda_latent_gather_q8 -- kda_latent_gather from an 8-bit cache: packed rows of the values in bf16, exactly (but for
+ * values of 2^128, which become infinite).  Errors: as kda_latent_append_q8's.
+ */
+kda_status kda_latent_gather_q8(const kda_latent_shape* shape, const void* cache, const uint8_t* scales,
+                                const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* starts,
+                                void* latent, void* k_rope, kda_stream_t stream);
+
+/*
+ * kda_latent_decode_q8 -- kda_latent_decode over an 8-bit cache: the same formulas, on the rows' values.  Scores,
+ * maxima, sums and partial results are fp32.  The tensor cores multiply e4m3 numbers: a query row and a row of softmax
+ * weights go in as the sum of two e4m3 numbers under one power of two, which holds 8 significant bits (those of bf16)
+ * down to 2^-10 of a query row's largest channel and to 2^-13 of a row's largest weight, and absolute steps
+ * of 2^-18 and 2^-21 of these below.
+ * Errors: kda_latent_decode's, with kda_latent_decode_q8_workspace_size; KDA_ERR_INVALID_ARG also for scales NULL with
+ * num_pages > 0.
+ */
+kda_status kda_latent_decode_q8(const kda_latent_shape* shape, const void* q_latent, const void* q_rope,
+                                const void* cache, const uint8_t* scales, const int32_t* block_table,
+                                const int32_t* seq_lens, float scale, void* out, float* lse, void* workspace,
+                                size_t workspace_bytes, kda_stream_t stream);
+
+/* kda_latent_decode_q8_workspace_size -- as kda_latent_decode_workspace_size, for kda_latent_decode_q8. */
+kda_status kda_latent_decode_q8_workspace_size(const kda_latent_shape* shape, size_t* bytes);
+
+/*
  * kda_latent_prefill -- the expanded form: causal attention over packed sequences with per-head
  * keys and values, the keys' last dk - 128 channels shared by the heads.
  *

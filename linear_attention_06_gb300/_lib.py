@@ -87,6 +87,14 @@ def lib():
         L.kda_latent_decode.restype = ctypes.c_int
         L.kda_latent_decode_workspace_size.argtypes = [lp, ctypes.POINTER(ctypes.c_size_t)]
         L.kda_latent_decode_workspace_size.restype = ctypes.c_int
+        L.kda_latent_append_q8.argtypes = [lp, vp, i64, vp, i64, vp, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp]
+        L.kda_latent_append_q8.restype = ctypes.c_int
+        L.kda_latent_gather_q8.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.kda_latent_gather_q8.restype = ctypes.c_int
+        L.kda_latent_decode_q8.argtypes = [lp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp]
+        L.kda_latent_decode_q8.restype = ctypes.c_int
+        L.kda_latent_decode_q8_workspace_size.argtypes = [lp, ctypes.POINTER(ctypes.c_size_t)]
+        L.kda_latent_decode_q8_workspace_size.restype = ctypes.c_int
         L.kda_latent_prefill.argtypes = [sp, i64, vp, vp, vp, i64, vp, ctypes.c_float, vp, vp, vp, vp, vp]
         L.kda_latent_prefill.restype = ctypes.c_int
         L.kda_status_string.argtypes = [ctypes.c_int]
@@ -381,6 +389,7 @@ def kda_decode_step(q, k, v, log_alpha, beta, state, out=None, stream=None):
 # ---------------------------------------------------------------- latent attention
 
 _ENTRIES = ("kda_latent_append", "kda_latent_gather", "kda_latent_decode", "kda_latent_decode_workspace_size",
+            "kda_latent_append_q8", "kda_latent_gather_q8", "kda_latent_decode_q8", "kda_latent_decode_q8_workspace_size",
             "kda_latent_prefill")
 _native = None
 
@@ -454,10 +463,13 @@ def kda_latent_gather(cache, block_table, cu_seqlens, total_tokens, starts=None,
 
 def kda_latent_decode_workspace_size(num_seqs: int, total_tokens: int, H: int, rope_dim: int = 64) -> int:
     """Bytes of workspace kda_latent_decode needs for total_tokens / num_seqs tokens a sequence and H heads."""
+    return _workspace_size("kda_latent_decode_workspace_size", num_seqs, total_tokens, H, rope_dim)
+
+
+def _workspace_size(name, num_seqs, total_tokens, H, rope_dim):
     shape = KdaLatentShape(int(num_seqs), int(total_tokens), int(H), 512, int(rope_dim), 64, 0, 0, KDA_BF16)
     n = ctypes.c_size_t(0)
-    _check("kda_latent_decode_workspace_size",
-           lib().kda_latent_decode_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    _check(name, getattr(lib(), name)(ctypes.byref(shape), ctypes.byref(n)))
     return int(n.value)
 
 
@@ -475,6 +487,50 @@ def kda_latent_decode(q_latent, q_rope, cache, block_table, seq_lens, scale, out
     new = lse is True
     return (_native or _latent()).decode(q_latent, q_rope, cache, block_table, seq_lens, scale, out, None if new else lse,
                                          new, workspace)
+
+
+def kda_latent_append_q8(latent, k_rope, cache, scales, block_table, seq_lens, inv_freq=None, interleaved=False,
+                         q_rope=None, q_rope_out=None, cu_seqlens=None, stream=None):
+    """Quantise new tokens' rows into the 8-bit paged latent cache, rotated by position (see ``include/kda.h``).
+
+    As kda_latent_append, with cache: [pages, page_size, 512 or 576] torch.float8_e4m3fn and scales:
+    [pages, page_size] torch.float8_e8m0fnu (a row's power of two), both written in place."""
+    if stream is not None:
+        with _on(stream, cache):
+            return kda_latent_append_q8(latent, k_rope, cache, scales, block_table, seq_lens, inv_freq, interleaved,
+                                        q_rope, q_rope_out, cu_seqlens)
+    return (_native or _latent()).append_q8(latent, k_rope, cache, scales, block_table, seq_lens, inv_freq, interleaved,
+                                            q_rope, q_rope_out, _table(cu_seqlens, latent.shape[0], cache))
+
+
+def kda_latent_gather_q8(cache, scales, block_table, cu_seqlens, total_tokens, starts=None, out=None, stream=None):
+    """Rows of the 8-bit cache back to packed bf16 rows of their values (see ``include/kda.h``): as kda_latent_gather,
+    with cache and scales as in kda_latent_append_q8."""
+    if stream is not None:
+        with _on(stream, cache):
+            return kda_latent_gather_q8(cache, scales, block_table, cu_seqlens, total_tokens, starts, out)
+    latent, k_rope = (None, None) if out is None else out
+    return (_native or _latent()).gather_q8(cache, scales, block_table, _table(cu_seqlens, total_tokens, cache),
+                                            total_tokens, starts, latent, k_rope)
+
+
+def kda_latent_decode_q8_workspace_size(num_seqs: int, total_tokens: int, H: int, rope_dim: int = 64) -> int:
+    """Bytes of workspace kda_latent_decode_q8 needs for total_tokens / num_seqs tokens a sequence and H heads."""
+    return _workspace_size("kda_latent_decode_q8_workspace_size", num_seqs, total_tokens, H, rope_dim)
+
+
+def kda_latent_decode_q8(q_latent, q_rope, cache, scales, block_table, seq_lens, scale, out=None, lse=None,
+                         workspace=None, stream=None):
+    """Absorbed latent attention over the 8-bit paged cache, 1 to 16 tokens a sequence (see ``include/kda.h``).
+
+    As kda_latent_decode, with cache and scales as in kda_latent_append_q8 and a workspace of
+    kda_latent_decode_q8_workspace_size bytes.  Returns (out [N*T, H, 512], lse)."""
+    if stream is not None:
+        with _on(stream, cache):
+            return kda_latent_decode_q8(q_latent, q_rope, cache, scales, block_table, seq_lens, scale, out, lse, workspace)
+    new = lse is True
+    return (_native or _latent()).decode_q8(q_latent, q_rope, cache, scales, block_table, seq_lens, scale, out,
+                                            None if new else lse, new, workspace)
 
 
 def kda_latent_prefill(q, k, v, k_rope, scale, cu_seqlens=None, cu_seqlens_k=None, num_seqs=None, out=None,

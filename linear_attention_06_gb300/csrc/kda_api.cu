@@ -127,20 +127,118 @@ kda_status check_step(int32_t n, int64_t tokens) {
 }
 
 // The cache and its table; either may be null where it has no entries.
-kda_status check_latent_cache(const kda_latent_shape* s, const void* cache, const int32_t* table) {
-    if ((s->num_pages > 0 && !cache) || (s->max_pages > 0 && !table)) return KDA_ERR_INVALID_ARG;
+kda_status check_latent_cache(const kda_latent_shape* s, const void* cache, const int32_t* table, const uint8_t* scales, bool q8) {
+    if ((s->num_pages > 0 && (!cache || (q8 && !scales))) || (s->max_pages > 0 && !table)) return KDA_ERR_INVALID_ARG;
     if (!aligned(cache, 16) || !aligned(table, 4)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
-kda::LatentCache latent_cache(const kda_latent_shape* s, void* cache, const int32_t* table) {
-    return {cache, table, s->page_size, s->num_pages, s->max_pages, s->rope_dim};
+kda::LatentCache latent_cache(const kda_latent_shape* s, void* cache, const int32_t* table, uint8_t* scales) {
+    return {cache, table, s->page_size, s->num_pages, s->max_pages, s->rope_dim, scales};
 }
 
 kda_status finish(cudaError_t e, cudaStream_t st) {
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     if (env_flag("KDA_DEBUG_SYNC")) return kda_device_status(st);
     return KDA_OK;
+}
+
+// The latent calls over a bf16 cache (scales null, q8 false) and over an 8-bit one.
+size_t workspace_bytes_of(int tokens_per_seq, int H, bool q8) {
+    return q8 ? kda::latent_decode_q8_workspace_bytes(tokens_per_seq, H) : kda::latent_decode_workspace_bytes(tokens_per_seq, H);
+}
+
+kda_status append_rows(const kda_latent_shape* shape, const void* latent, int64_t latent_stride, const void* k_rope,
+                       int64_t k_rope_stride, const float* inv_freq, int32_t interleaved, const void* q_rope,
+                       int64_t q_stride, void* q_rope_out, int64_t q_out_stride, const int32_t* cu_seqlens,
+                       const int32_t* seq_lens, const int32_t* block_table, void* cache, uint8_t* scales, bool q8,
+                       kda_stream_t stream) {
+    kda_status st = check_latent_shape(shape);
+    if (st != KDA_OK) return st;
+    st = check_split(shape->num_seqs, shape->total_tokens, cu_seqlens);
+    if (st != KDA_OK) return st;
+    if (shape->total_tokens == 0) return KDA_OK;
+    const bool rope = shape->rope_dim != 0;
+    if (!latent || rope != (k_rope != nullptr) || !seq_lens) return KDA_ERR_INVALID_ARG;
+    if (latent_stride < shape->latent_dim || (rope && k_rope_stride < shape->rope_dim)) return KDA_ERR_INVALID_ARG;
+    if (q_rope && (!rope || !q_rope_out || q_stride < shape->rope_dim || q_out_stride < shape->rope_dim))
+        return KDA_ERR_INVALID_ARG;
+    if ((q_rope_out && !q_rope) || (interleaved != 0 && interleaved != 1)) return KDA_ERR_INVALID_ARG;
+    st = check_latent_cache(shape, cache, block_table, scales, q8);
+    if (st != KDA_OK) return st;
+    if (!aligned(latent, 16) || latent_stride % 8 != 0 || !aligned(seq_lens, 4)) return KDA_ERR_UNSUPPORTED;
+    if (rope && (!aligned(k_rope, 16) || k_rope_stride % 8 != 0 || !aligned(inv_freq, 4))) return KDA_ERR_UNSUPPORTED;
+    if (q_rope && (!aligned(q_rope, 16) || !aligned(q_rope_out, 16) || q_stride % 8 != 0 || q_out_stride % 8 != 0))
+        return KDA_ERR_UNSUPPORTED;
+    unsigned int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    kda::LatentAppendArgs a{latent_cache(shape, cache, block_table, scales), latent, rope ? k_rope : nullptr,
+                            rope ? inv_freq : nullptr, q_rope, q_rope_out, cu_seqlens, seq_lens, latent_stride,
+                            k_rope_stride, q_stride, q_out_stride, shape->total_tokens, shape->num_seqs, shape->H,
+                            interleaved != 0, status};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return finish(q8 ? kda::launch_latent_append_q8(a, s) : kda::launch_latent_append(a, s), s);
+}
+
+kda_status gather_rows(const kda_latent_shape* shape, const void* cache, const uint8_t* scales, bool q8,
+                       const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* starts, void* latent,
+                       void* k_rope, kda_stream_t stream) {
+    kda_status st = check_latent_shape(shape);
+    if (st != KDA_OK) return st;
+    st = check_split(shape->num_seqs, shape->total_tokens, cu_seqlens);
+    if (st != KDA_OK) return st;
+    if (shape->total_tokens == 0) return KDA_OK;
+    const bool rope = shape->rope_dim != 0;
+    if (!latent || rope != (k_rope != nullptr)) return KDA_ERR_INVALID_ARG;
+    st = check_latent_cache(shape, cache, block_table, scales, q8);
+    if (st != KDA_OK) return st;
+    if (!aligned(latent, 16) || (rope && !aligned(k_rope, 16)) || !aligned(starts, 4)) return KDA_ERR_UNSUPPORTED;
+    unsigned int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    kda::LatentGatherArgs a{latent_cache(shape, const_cast<void*>(cache), block_table, const_cast<uint8_t*>(scales)),
+                            cu_seqlens, starts, latent,
+                            rope ? k_rope : nullptr, shape->total_tokens, shape->num_seqs, status};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return finish(q8 ? kda::launch_latent_gather_q8(a, s) : kda::launch_latent_gather(a, s), s);
+}
+
+kda_status decode_workspace(const kda_latent_shape* shape, bool q8, size_t* bytes) {
+    if (!bytes) return KDA_ERR_INVALID_ARG;
+    *bytes = 0;
+    kda_status st = check_latent_shape(shape);
+    if (st != KDA_OK) return st;
+    st = check_step(shape->num_seqs, shape->total_tokens);
+    if (st != KDA_OK || shape->num_seqs == 0) return st;
+    *bytes = workspace_bytes_of((int)(shape->total_tokens / shape->num_seqs), shape->H, q8);
+    return KDA_OK;
+}
+
+kda_status decode_rows(const kda_latent_shape* shape, const void* q_latent, const void* q_rope, const void* cache,
+                       const uint8_t* scales, bool q8, const int32_t* block_table, const int32_t* seq_lens, float scale,
+                       void* out, float* lse, void* workspace, size_t workspace_bytes, kda_stream_t stream) {
+    kda_status st = check_latent_shape(shape);
+    if (st != KDA_OK) return st;
+    st = check_step(shape->num_seqs, shape->total_tokens);
+    if (st != KDA_OK) return st;
+    if (!(scale > 0.f) || !(scale < INFINITY)) return KDA_ERR_INVALID_ARG;
+    if (shape->num_seqs == 0) return KDA_OK;
+    const bool rope = shape->rope_dim != 0;
+    if (!q_latent || rope != (q_rope != nullptr) || !seq_lens || !out || !workspace) return KDA_ERR_INVALID_ARG;
+    st = check_latent_cache(shape, cache, block_table, scales, q8);
+    if (st != KDA_OK) return st;
+    if (!aligned(q_latent, 16) || (rope && !aligned(q_rope, 16)) || !aligned(seq_lens, 4) || !aligned(out, 16) ||
+        !aligned(lse, 4) || !aligned(workspace, 256))
+        return KDA_ERR_UNSUPPORTED;
+    if (shape->total_tokens * shape->H > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;   // a query row's index
+    const int tps = (int)(shape->total_tokens / shape->num_seqs);
+    if (workspace_bytes < workspace_bytes_of(tps, shape->H, q8)) return KDA_ERR_INVALID_ARG;
+    unsigned int* status = status_word();
+    if (!status) return KDA_ERR_CUDA;
+    kda::LatentDecodeArgs a{latent_cache(shape, const_cast<void*>(cache), block_table, const_cast<uint8_t*>(scales)), q_latent,
+                            rope ? q_rope : nullptr, seq_lens, out, lse, workspace, scale, shape->num_seqs, tps,
+                            shape->H, status};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return finish(q8 ? kda::launch_latent_decode_q8(a, s) : kda::launch_latent_decode(a, s), s);
 }
 
 }  // namespace
@@ -424,91 +522,52 @@ kda_status kda_latent_append(const kda_latent_shape* shape, const void* latent, 
                              int32_t interleaved, const void* q_rope, int64_t q_stride, void* q_rope_out,
                              int64_t q_out_stride, const int32_t* cu_seqlens, const int32_t* seq_lens,
                              const int32_t* block_table, void* cache, kda_stream_t stream) {
-    kda_status st = check_latent_shape(shape);
-    if (st != KDA_OK) return st;
-    st = check_split(shape->num_seqs, shape->total_tokens, cu_seqlens);
-    if (st != KDA_OK) return st;
-    if (shape->total_tokens == 0) return KDA_OK;
-    const bool rope = shape->rope_dim != 0;
-    if (!latent || rope != (k_rope != nullptr) || !seq_lens) return KDA_ERR_INVALID_ARG;
-    if (latent_stride < shape->latent_dim || (rope && k_rope_stride < shape->rope_dim)) return KDA_ERR_INVALID_ARG;
-    if (q_rope && (!rope || !q_rope_out || q_stride < shape->rope_dim || q_out_stride < shape->rope_dim))
-        return KDA_ERR_INVALID_ARG;
-    if ((q_rope_out && !q_rope) || (interleaved != 0 && interleaved != 1)) return KDA_ERR_INVALID_ARG;
-    st = check_latent_cache(shape, cache, block_table);
-    if (st != KDA_OK) return st;
-    if (!aligned(latent, 16) || latent_stride % 8 != 0 || !aligned(seq_lens, 4)) return KDA_ERR_UNSUPPORTED;
-    if (rope && (!aligned(k_rope, 16) || k_rope_stride % 8 != 0 || !aligned(inv_freq, 4))) return KDA_ERR_UNSUPPORTED;
-    if (q_rope && (!aligned(q_rope, 16) || !aligned(q_rope_out, 16) || q_stride % 8 != 0 || q_out_stride % 8 != 0))
-        return KDA_ERR_UNSUPPORTED;
-    unsigned int* status = status_word();
-    if (!status) return KDA_ERR_CUDA;
-    kda::LatentAppendArgs a{latent_cache(shape, cache, block_table), latent, rope ? k_rope : nullptr,
-                            rope ? inv_freq : nullptr, q_rope, q_rope_out, cu_seqlens, seq_lens, latent_stride,
-                            k_rope_stride, q_stride, q_out_stride, shape->total_tokens, shape->num_seqs, shape->H,
-                            interleaved != 0, status};
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return finish(kda::launch_latent_append(a, s), s);
+    return append_rows(shape, latent, latent_stride, k_rope, k_rope_stride, inv_freq, interleaved, q_rope, q_stride, q_rope_out,
+                       q_out_stride, cu_seqlens, seq_lens, block_table, cache, nullptr, false, stream);
+}
+
+kda_status kda_latent_append_q8(const kda_latent_shape* shape, const void* latent, int64_t latent_stride,
+                                const void* k_rope, int64_t k_rope_stride, const float* inv_freq,
+                                int32_t interleaved, const void* q_rope, int64_t q_stride, void* q_rope_out,
+                                int64_t q_out_stride, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                                const int32_t* block_table, void* cache, uint8_t* scales, kda_stream_t stream) {
+    return append_rows(shape, latent, latent_stride, k_rope, k_rope_stride, inv_freq, interleaved, q_rope, q_stride, q_rope_out,
+                       q_out_stride, cu_seqlens, seq_lens, block_table, cache, scales, true, stream);
 }
 
 kda_status kda_latent_gather(const kda_latent_shape* shape, const void* cache, const int32_t* block_table,
                              const int32_t* cu_seqlens, const int32_t* starts, void* latent, void* k_rope,
                              kda_stream_t stream) {
-    kda_status st = check_latent_shape(shape);
-    if (st != KDA_OK) return st;
-    st = check_split(shape->num_seqs, shape->total_tokens, cu_seqlens);
-    if (st != KDA_OK) return st;
-    if (shape->total_tokens == 0) return KDA_OK;
-    const bool rope = shape->rope_dim != 0;
-    if (!latent || rope != (k_rope != nullptr)) return KDA_ERR_INVALID_ARG;
-    st = check_latent_cache(shape, cache, block_table);
-    if (st != KDA_OK) return st;
-    if (!aligned(latent, 16) || (rope && !aligned(k_rope, 16)) || !aligned(starts, 4)) return KDA_ERR_UNSUPPORTED;
-    unsigned int* status = status_word();
-    if (!status) return KDA_ERR_CUDA;
-    kda::LatentGatherArgs a{latent_cache(shape, const_cast<void*>(cache), block_table), cu_seqlens, starts, latent,
-                            rope ? k_rope : nullptr, shape->total_tokens, shape->num_seqs, status};
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return finish(kda::launch_latent_gather(a, s), s);
+    return gather_rows(shape, cache, nullptr, false, block_table, cu_seqlens, starts, latent, k_rope, stream);
+}
+
+kda_status kda_latent_gather_q8(const kda_latent_shape* shape, const void* cache, const uint8_t* scales,
+                                const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* starts,
+                                void* latent, void* k_rope, kda_stream_t stream) {
+    return gather_rows(shape, cache, scales, true, block_table, cu_seqlens, starts, latent, k_rope, stream);
 }
 
 kda_status kda_latent_decode_workspace_size(const kda_latent_shape* shape, size_t* bytes) {
-    if (!bytes) return KDA_ERR_INVALID_ARG;
-    *bytes = 0;
-    kda_status st = check_latent_shape(shape);
-    if (st != KDA_OK) return st;
-    st = check_step(shape->num_seqs, shape->total_tokens);
-    if (st != KDA_OK || shape->num_seqs == 0) return st;
-    *bytes = kda::latent_decode_workspace_bytes((int)(shape->total_tokens / shape->num_seqs), shape->H);
-    return KDA_OK;
+    return decode_workspace(shape, false, bytes);
+}
+
+kda_status kda_latent_decode_q8_workspace_size(const kda_latent_shape* shape, size_t* bytes) {
+    return decode_workspace(shape, true, bytes);
 }
 
 kda_status kda_latent_decode(const kda_latent_shape* shape, const void* q_latent, const void* q_rope,
                              const void* cache, const int32_t* block_table, const int32_t* seq_lens, float scale,
                              void* out, float* lse, void* workspace, size_t workspace_bytes, kda_stream_t stream) {
-    kda_status st = check_latent_shape(shape);
-    if (st != KDA_OK) return st;
-    st = check_step(shape->num_seqs, shape->total_tokens);
-    if (st != KDA_OK) return st;
-    if (!(scale > 0.f) || !(scale < INFINITY)) return KDA_ERR_INVALID_ARG;
-    if (shape->num_seqs == 0) return KDA_OK;
-    const bool rope = shape->rope_dim != 0;
-    if (!q_latent || rope != (q_rope != nullptr) || !seq_lens || !out || !workspace) return KDA_ERR_INVALID_ARG;
-    st = check_latent_cache(shape, cache, block_table);
-    if (st != KDA_OK) return st;
-    if (!aligned(q_latent, 16) || (rope && !aligned(q_rope, 16)) || !aligned(seq_lens, 4) || !aligned(out, 16) ||
-        !aligned(lse, 4) || !aligned(workspace, 256))
-        return KDA_ERR_UNSUPPORTED;
-    if (shape->total_tokens * shape->H > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;   // a query row's index
-    const int tps = (int)(shape->total_tokens / shape->num_seqs);
-    if (workspace_bytes < kda::latent_decode_workspace_bytes(tps, shape->H)) return KDA_ERR_INVALID_ARG;
-    unsigned int* status = status_word();
-    if (!status) return KDA_ERR_CUDA;
-    kda::LatentDecodeArgs a{latent_cache(shape, const_cast<void*>(cache), block_table), q_latent,
-                            rope ? q_rope : nullptr, seq_lens, out, lse, workspace, scale, shape->num_seqs, tps,
-                            shape->H, status};
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return finish(kda::launch_latent_decode(a, s), s);
+    return decode_rows(shape, q_latent, q_rope, cache, nullptr, false, block_table, seq_lens, scale, out, lse, workspace,
+                       workspace_bytes, stream);
+}
+
+kda_status kda_latent_decode_q8(const kda_latent_shape* shape, const void* q_latent, const void* q_rope,
+                                const void* cache, const uint8_t* scales, const int32_t* block_table,
+                                const int32_t* seq_lens, float scale, void* out, float* lse, void* workspace,
+                                size_t workspace_bytes, kda_stream_t stream) {
+    return decode_rows(shape, q_latent, q_rope, cache, scales, true, block_table, seq_lens, scale, out, lse, workspace,
+                       workspace_bytes, stream);
 }
 
 kda_status kda_latent_prefill(const kda_shape* shape, int64_t total_kv, const void* q, const void* k, const void* v,

@@ -117,6 +117,7 @@ struct LatentCache {
     void* cache;                  // [num_pages, page_size, 512 + rope_dim] bf16
     const int32_t* block_table;   // [N, max_pages]
     int32_t page_size, num_pages, max_pages, rope_dim;
+    uint8_t* scales;              // [num_pages, page_size] e8m0: of an 8-bit cache, whose rows are e4m3 (else null)
 };
 struct LatentAppendArgs {
     LatentCache c;
@@ -133,6 +134,7 @@ struct LatentAppendArgs {
     unsigned int* status;
 };
 cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t s);
+cudaError_t launch_latent_append_q8(const LatentAppendArgs& a, cudaStream_t s);
 struct LatentGatherArgs {
     LatentCache c;
     const int32_t* cu_seqlens;
@@ -144,6 +146,7 @@ struct LatentGatherArgs {
     unsigned int* status;
 };
 cudaError_t launch_latent_gather(const LatentGatherArgs& a, cudaStream_t s);
+cudaError_t launch_latent_gather_q8(const LatentGatherArgs& a, cudaStream_t s);
 struct LatentDecodeArgs {
     LatentCache c;
     const void* q_latent;         // [N*T, H, 512]
@@ -158,6 +161,8 @@ struct LatentDecodeArgs {
 };
 size_t latent_decode_workspace_bytes(int tokens_per_seq, int H);
 cudaError_t launch_latent_decode(const LatentDecodeArgs& a, cudaStream_t s);
+size_t latent_decode_q8_workspace_bytes(int tokens_per_seq, int H);
+cudaError_t launch_latent_decode_q8(const LatentDecodeArgs& a, cudaStream_t s);
 struct LatentPrefillArgs {
     const void* q;                // [T, H, dk]
     const void* k;                // [S, H] rows of 128, kv_stride apart

@@ -1,0 +1,57 @@
+// kda_latent_q8.cuh -- a row of the 8-bit latent cache: e4m3 numbers y and one power of two 2^e, values y 2^e.
+//
+//     e = the smallest integer with max |x| <= 448 2^e, within kLeastPower .. kMostPower,   y = e4m3(x 2^-e).
+//
+// e4m3 is a floating format: a power of two costs it no precision, only range (the largest number of a row lies above
+// 224), the scaling is exact, so that y is rounded once, and a value has four significant bits and is exact in bf16.
+// The bounds keep 2^e and 2^-e normal fp32 numbers, and sums of 2^-e over 2^31 rows finite.  A row of zeros takes the
+// lowest e: it never sets the range of the softmax weights of the rows beside it.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace kda {
+namespace latent {
+
+constexpr int kLeastPower = -64, kMostPower = 120;
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127) << 23); }
+
+// e for the largest magnitude of a row, given by its bits (which order as magnitudes do, NaN above infinity).
+// 448 = 1.75 * 2^8.
+__device__ __forceinline__ int power_for(uint32_t bits) {
+    const int e = (int)(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7);
+    return bits == 0 || e < kLeastPower ? kLeastPower : (e > kMostPower ? kMostPower : e);
+}
+
+// The scale byte of a row (e8m0: e + 127), and e of a byte; bytes outside the format's range count as its nearest.
+__device__ __forceinline__ uint8_t power_byte(int e) { return (uint8_t)(e + 127); }
+__device__ __forceinline__ int power_of(uint8_t byte) {
+    const int e = (int)byte - 127;
+    return e < kLeastPower ? kLeastPower : (e > kMostPower ? kMostPower : e);
+}
+
+// Two numbers to e4m3, lo in the low byte: to nearest even, beyond 448 to 448.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
+    return to_e4m3x2(a, b) | (to_e4m3x2(c, d) << 16);
+}
+// Two e4m3 numbers (the low 16 bits), exactly.
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t x) {
+    uint32_t h;
+    float2 f;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)x));
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(h));
+    return f;
+}
+
+}  // namespace latent
+}  // namespace kda

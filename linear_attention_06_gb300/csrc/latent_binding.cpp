@@ -28,6 +28,10 @@ struct Entry {
     decltype(&kda_latent_gather) gather = nullptr;
     decltype(&kda_latent_decode) decode = nullptr;
     decltype(&kda_latent_decode_workspace_size) workspace_size = nullptr;
+    decltype(&kda_latent_append_q8) append_q8 = nullptr;
+    decltype(&kda_latent_gather_q8) gather_q8 = nullptr;
+    decltype(&kda_latent_decode_q8) decode_q8 = nullptr;
+    decltype(&kda_latent_decode_q8_workspace_size) workspace_size_q8 = nullptr;
     decltype(&kda_latent_prefill) prefill = nullptr;
 } entry;
 PyObject* check_status = nullptr;             // check_status(name, status) raises; lives as long as the process
@@ -99,13 +103,14 @@ at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& li
     return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
 }
 
-// The descriptor of a call on a cache and its table, with their addresses.
-kda_latent_shape latent_shape(const at::Tensor& cache, const at::Tensor& table, int64_t tokens, int64_t heads,
+// The descriptor of a call on a cache (8-bit where it has scales) and its table, checked.
+kda_latent_shape latent_shape(const at::Tensor& cache, const Opt& scales, const at::Tensor& table, int64_t tokens, int64_t heads,
                               c10::DeviceIndex device) {
     if (cache.dim() != 3 || (cache.size(2) != kLatent && cache.size(2) != kLatent + kRope))
         throw py::value_error(text("cache must be [pages, page_size, ", kLatent, " or ", kLatent + kRope, "], not ", cache.sizes()));
     if (table.dim() != 2) throw py::value_error("block_table must be [N, max_pages]");
-    expect("cache", cache, cache.sizes(), at::kBFloat16, device);
+    expect("cache", cache, cache.sizes(), scales ? at::kFloat8_e4m3fn : at::kBFloat16, device);
+    if (scales) expect("scales", *scales, {cache.size(0), cache.size(1)}, at::kFloat8_e8m0fnu, device);
     expect("block_table", table, table.sizes(), at::kInt, device);
     const auto most = (int64_t)INT32_MAX;
     if (cache.size(0) > most || cache.size(1) > most || table.size(0) > most || table.size(1) > most || heads > most)
@@ -114,15 +119,15 @@ kda_latent_shape latent_shape(const at::Tensor& cache, const at::Tensor& table, 
             (int32_t)cache.size(1), (int32_t)cache.size(0), (int32_t)table.size(1), KDA_BF16};
 }
 
-std::optional<at::Tensor> append(const at::Tensor& latent, const Opt& k_rope, const at::Tensor& cache, const at::Tensor& table,
-                                 const at::Tensor& lens, const Opt& inv_freq, bool interleaved, const Opt& q_rope, Opt q_out,
-                                 const Opt& cu) {
+std::optional<at::Tensor> append_rows(const at::Tensor& latent, const Opt& k_rope, const at::Tensor& cache, const Opt& scales,
+                                      const at::Tensor& table, const at::Tensor& lens, const Opt& inv_freq, bool interleaved,
+                                      const Opt& q_rope, Opt q_out, const Opt& cu) {
     const auto dev = index_of(cache);
     const c10::cuda::CUDAGuard guard(dev);
     if (latent.dim() != 2) throw py::value_error("latent must be [T, 512]");
     if (q_rope && q_rope->dim() != 3) throw py::value_error("q_rope must be [T, H, 64]");
     const int64_t T = latent.size(0), H = q_rope ? q_rope->size(1) : 1;
-    const kda_latent_shape shape = latent_shape(cache, table, T, H, dev);
+    const kda_latent_shape shape = latent_shape(cache, scales, table, T, H, dev);
     const int64_t n = shape.num_seqs;
     const void* p_latent = expect("latent", latent, {T, kLatent}, at::kBFloat16, dev, true);
     const int64_t latent_step = row_stride("latent", latent);
@@ -146,20 +151,34 @@ std::optional<at::Tensor> append(const at::Tensor& latent, const Opt& k_rope, co
     kda_status st;
     {
         py::gil_scoped_release free;
-        st = entry.append(&shape, p_latent, latent_step, p_rope, rope_step, static_cast<const float*>(p_freq), interleaved,
-                          p_q, q_step, p_out, out_step, static_cast<const int32_t*>(p_cu), static_cast<const int32_t*>(p_lens),
-                          static_cast<const int32_t*>(table.data_ptr()), cache.data_ptr(), stream_of(dev));
+        const auto call = [&](auto fn, auto... scale_bytes) {
+            return fn(&shape, p_latent, latent_step, p_rope, rope_step, static_cast<const float*>(p_freq), interleaved, p_q, q_step,
+                      p_out, out_step, static_cast<const int32_t*>(p_cu), static_cast<const int32_t*>(p_lens),
+                      static_cast<const int32_t*>(table.data_ptr()), cache.data_ptr(), scale_bytes..., stream_of(dev));
+        };
+        st = scales ? call(entry.append_q8, static_cast<uint8_t*>(scales->data_ptr())) : call(entry.append);
     }
-    check("kda_latent_append", st);
+    check(scales ? "kda_latent_append_q8" : "kda_latent_append", st);
     return q_rope ? q_out : std::nullopt;
 }
+std::optional<at::Tensor> append(const at::Tensor& latent, const Opt& k_rope, const at::Tensor& cache, const at::Tensor& table,
+                                 const at::Tensor& lens, const Opt& inv_freq, bool interleaved, const Opt& q_rope, const Opt& q_out,
+                                 const Opt& cu) {
+    return append_rows(latent, k_rope, cache, std::nullopt, table, lens, inv_freq, interleaved, q_rope, q_out, cu);
+}
+std::optional<at::Tensor> append_q8(const at::Tensor& latent, const Opt& k_rope, const at::Tensor& cache, const at::Tensor& scales,
+                                    const at::Tensor& table, const at::Tensor& lens, const Opt& inv_freq, bool interleaved,
+                                    const Opt& q_rope, const Opt& q_out, const Opt& cu) {
+    return append_rows(latent, k_rope, cache, scales, table, lens, inv_freq, interleaved, q_rope, q_out, cu);
+}
 
-std::pair<at::Tensor, std::optional<at::Tensor>> gather(const at::Tensor& cache, const at::Tensor& table, const at::Tensor& cu,
-                                                        int64_t T, const Opt& starts, Opt latent, Opt k_rope) {
+std::pair<at::Tensor, std::optional<at::Tensor>> gather_rows(const at::Tensor& cache, const Opt& scales, const at::Tensor& table,
+                                                             const at::Tensor& cu, int64_t T, const Opt& starts, Opt latent,
+                                                             Opt k_rope) {
     const auto dev = index_of(cache);
     const c10::cuda::CUDAGuard guard(dev);
     if (T < 0) throw py::value_error("total_tokens must not be negative");
-    const kda_latent_shape shape = latent_shape(cache, table, T, 1, dev);
+    const kda_latent_shape shape = latent_shape(cache, scales, table, T, 1, dev);
     const int64_t n = shape.num_seqs;
     const void* p_cu = expect("cu_seqlens", cu, {n + 1}, at::kInt, dev);
     const void* p_starts = starts ? expect("starts", *starts, {n}, at::kInt, dev) : nullptr;
@@ -174,22 +193,34 @@ std::pair<at::Tensor, std::optional<at::Tensor>> gather(const at::Tensor& cache,
     kda_status st;
     {
         py::gil_scoped_release free;
-        st = entry.gather(&shape, cache.data_ptr(), static_cast<const int32_t*>(table.data_ptr()),
-                          static_cast<const int32_t*>(p_cu), static_cast<const int32_t*>(p_starts), p_latent, p_rope,
-                          stream_of(dev));
+        const auto call = [&](auto fn, auto... scale_bytes) {
+            return fn(&shape, cache.data_ptr(), scale_bytes..., static_cast<const int32_t*>(table.data_ptr()),
+                      static_cast<const int32_t*>(p_cu), static_cast<const int32_t*>(p_starts), p_latent, p_rope, stream_of(dev));
+        };
+        st = scales ? call(entry.gather_q8, static_cast<const uint8_t*>(scales->data_ptr())) : call(entry.gather);
     }
-    check("kda_latent_gather", st);
+    check(scales ? "kda_latent_gather_q8" : "kda_latent_gather", st);
     return {*latent, shape.rope_dim ? k_rope : std::nullopt};
 }
+std::pair<at::Tensor, std::optional<at::Tensor>> gather(const at::Tensor& cache, const at::Tensor& table, const at::Tensor& cu,
+                                                        int64_t T, const Opt& starts, const Opt& latent, const Opt& k_rope) {
+    return gather_rows(cache, std::nullopt, table, cu, T, starts, latent, k_rope);
+}
+std::pair<at::Tensor, std::optional<at::Tensor>> gather_q8(const at::Tensor& cache, const at::Tensor& scales, const at::Tensor& table,
+                                                           const at::Tensor& cu, int64_t T, const Opt& starts, const Opt& latent,
+                                                           const Opt& k_rope) {
+    return gather_rows(cache, scales, table, cu, T, starts, latent, k_rope);
+}
 
-std::pair<at::Tensor, std::optional<at::Tensor>> decode(const at::Tensor& q, const Opt& q_rope, const at::Tensor& cache,
-                                                        const at::Tensor& table, const at::Tensor& lens, double scale, Opt out,
-                                                        Opt lse, bool make_lse, Opt workspace) {
+std::pair<at::Tensor, std::optional<at::Tensor>> decode_rows(const at::Tensor& q, const Opt& q_rope, const at::Tensor& cache,
+                                                             const Opt& scales, const at::Tensor& table, const at::Tensor& lens,
+                                                             double scale, Opt out, Opt lse, bool make_lse, Opt workspace) {
+    const char* name = scales ? "kda_latent_decode_q8" : "kda_latent_decode";
     const auto dev = index_of(cache);
     const c10::cuda::CUDAGuard guard(dev);
     if (q.dim() != 3) throw py::value_error("q_latent must be [N * T, H, 512]");
     const int64_t rows = q.size(0), H = q.size(1);
-    const kda_latent_shape shape = latent_shape(cache, table, rows, H, dev);
+    const kda_latent_shape shape = latent_shape(cache, scales, table, rows, H, dev);
     const void* p_q = expect("q_latent", q, {rows, H, kLatent}, at::kBFloat16, dev);
     const void* p_r = shape.rope_dim ? expect("q_rope", q_rope, {rows, H, kRope}, at::kBFloat16, dev) : nullptr;
     if (!shape.rope_dim) expect_none("q_rope", q_rope, kNoRope);
@@ -200,19 +231,33 @@ std::pair<at::Tensor, std::optional<at::Tensor>> decode(const at::Tensor& q, con
     void* p_lse = lse ? expect("lse", *lse, {rows, H}, at::kFloat, dev) : nullptr;
     if (!workspace) {
         size_t need = 0;
-        check("kda_latent_decode", entry.workspace_size(&shape, &need));
+        check(name, (scales ? entry.workspace_size_q8 : entry.workspace_size)(&shape, &need));
         workspace = make({std::max<int64_t>((int64_t)need, 1)}, at::kByte, cache);
     }
     void* p_ws = expect("workspace", *workspace, workspace->sizes(), at::kByte, dev);
     kda_status st;
     {
         py::gil_scoped_release free;
-        st = entry.decode(&shape, p_q, p_r, cache.data_ptr(), static_cast<const int32_t*>(table.data_ptr()),
-                          static_cast<const int32_t*>(p_lens), (float)scale, p_out, static_cast<float*>(p_lse), p_ws,
-                          (size_t)workspace->numel(), stream_of(dev));
+        const auto call = [&](auto fn, auto... scale_bytes) {
+            return fn(&shape, p_q, p_r, cache.data_ptr(), scale_bytes..., static_cast<const int32_t*>(table.data_ptr()),
+                      static_cast<const int32_t*>(p_lens), (float)scale, p_out, static_cast<float*>(p_lse), p_ws,
+                      (size_t)workspace->numel(), stream_of(dev));
+        };
+        st = scales ? call(entry.decode_q8, static_cast<const uint8_t*>(scales->data_ptr())) : call(entry.decode);
     }
-    check("kda_latent_decode", st);
+    check(name, st);
     return {*out, lse};
+}
+std::pair<at::Tensor, std::optional<at::Tensor>> decode(const at::Tensor& q, const Opt& q_rope, const at::Tensor& cache,
+                                                        const at::Tensor& table, const at::Tensor& lens, double scale,
+                                                        const Opt& out, const Opt& lse, bool make_lse, const Opt& workspace) {
+    return decode_rows(q, q_rope, cache, std::nullopt, table, lens, scale, out, lse, make_lse, workspace);
+}
+std::pair<at::Tensor, std::optional<at::Tensor>> decode_q8(const at::Tensor& q, const Opt& q_rope, const at::Tensor& cache,
+                                                           const at::Tensor& scales, const at::Tensor& table,
+                                                           const at::Tensor& lens, double scale, const Opt& out, const Opt& lse,
+                                                           bool make_lse, const Opt& workspace) {
+    return decode_rows(q, q_rope, cache, scales, table, lens, scale, out, lse, make_lse, workspace);
 }
 
 std::pair<at::Tensor, std::optional<at::Tensor>> prefill(const at::Tensor& q, const at::Tensor& k, const at::Tensor& v,
@@ -265,6 +310,10 @@ void bind(py::dict addresses, py::function raise) {
     entry.gather = reinterpret_cast<decltype(entry.gather)>(at("kda_latent_gather"));
     entry.decode = reinterpret_cast<decltype(entry.decode)>(at("kda_latent_decode"));
     entry.workspace_size = reinterpret_cast<decltype(entry.workspace_size)>(at("kda_latent_decode_workspace_size"));
+    entry.append_q8 = reinterpret_cast<decltype(entry.append_q8)>(at("kda_latent_append_q8"));
+    entry.gather_q8 = reinterpret_cast<decltype(entry.gather_q8)>(at("kda_latent_gather_q8"));
+    entry.decode_q8 = reinterpret_cast<decltype(entry.decode_q8)>(at("kda_latent_decode_q8"));
+    entry.workspace_size_q8 = reinterpret_cast<decltype(entry.workspace_size_q8)>(at("kda_latent_decode_q8_workspace_size"));
     entry.prefill = reinterpret_cast<decltype(entry.prefill)>(at("kda_latent_prefill"));
     check_status = raise.release().ptr();
 }
@@ -277,5 +326,8 @@ PYBIND11_MODULE(_latent, m) {
     m.def("append", &append);
     m.def("gather", &gather);
     m.def("decode", &decode);
+    m.def("append_q8", &append_q8);
+    m.def("gather_q8", &gather_q8);
+    m.def("decode_q8", &decode_q8);
     m.def("prefill", &prefill);
 }
