@@ -1,10 +1,34 @@
 // kda_latent_decode_q8.cu -- absorbed latent attention over the 8-bit paged cache (kda_latent_decode_q8).
 //
-// For a query row x = [q_latent | q_rope] and the cached rows y_j 2^{e_j} (the first 512 channels c_j are the values):
+// For one sequence, the R = T' H query rows x_r = [q_latent | q_rope] of its step and its cached rows y_j 2^{e_j}
+// (kda_latent_q8.cuh), whose first 512 channels c_j are the values too:
 //
-//     s_j = scale 2^{e_j} x . y_j,   p_j = e^{s_j - m},   o = sum_j p_j 2^{e_j} c_j / sum_j p_j.
+//     s_rj = scale 2^{e_j} x_r . y_j,   o_r = sum_j p_rj 2^{e_j} c_j / sum_j p_rj,   p_rj = e^{s_rj}.
 //
-// The plain form: a block a query row, a thread a cached row of a tile for the scores, four channels for the output.
+// The cache's bytes bound the call, half as many as in bf16, so the tile has to be multiplied as it lies in memory:
+// widening it to 16 bits in shared memory would move four times its bytes there.  tcgen05 multiplies 8-bit operands; the
+// other operand, where it is not 8-bit by nature, goes in as the sum of two 8-bit numbers:
+//
+// - A query row under a power of two, x = 2^k (x' + x''), both e4m3: eight significant bits, all of a bf16 channel, down
+//   to 2^-10 of the row's largest.  x' and x'' are two rows of one operand, so that the tile is read once for both.
+// - A weight w_rj = 2^{log2 p_rj + e_j - m_r} as e4m3 + e5m2: 2^-8 of it, as in bf16.  The e5m2 part, whose smallest number
+//   is 2^-16, keeps faint weights from being lost: m_r, the row's reference, is held where the largest weight of every
+//   tile lies in 2^-2 .. 2^8, and is lowered as well as raised (a first token that takes nearly all weight and a long
+//   faint tail behind it is what models really do), but never to more than 2^30 above the faintest reference that counts:
+//   O and the sums then stay far inside fp32.
+//
+// Products, per tile of 128 cached rows (NR = query rows of a block, 16, 32 or 64):
+//   S [128 tokens x 2 NR]  = Y X^T            M = 128, N = 2 NR (x' and x'' of each row), K = 512 + rope
+//   O^T [512 x NR]        += C^T W'^T + C^T W''^T    four blocks of M = 128 channels, N = NR, K = 128 tokens, twice
+// The tokens lie on the lanes of tensor memory, so a softmax thread has one token of all its rows: 2^{e_j} is one number a
+// thread, weights of consecutive rows pack into words, and the tile's operands keep the full M = 128.  What that layout
+// makes dear, a maximum over tokens, is not needed in every tile: references move only when a vote finds a tile outside
+// the range above; the sums stay in registers, a part a thread, until the piece ends.
+//
+// Work: as in the bf16 decode, one line of tiles in equal runs (kda_latent_line.cuh).  Block: a producer warp (TMA boxes
+// of page rows), an issuing warp, and eight warps that quantise the queries and turn S into W, half of the rows each four.
+#include <atomic>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -12,80 +36,683 @@
 
 #include "kda_internal.h"
 #include "kda_latent_common.cuh"
+#include "kda_latent_line.cuh"
 #include "kda_latent_q8.cuh"
+#include "sm103_primitives.cuh"
 
 namespace kda {
 namespace {
 
 using namespace latent;
+using namespace sm103;
 
-constexpr int kThreads = 128;
+constexpr int kRows = 128;                    // cached rows a tile
+constexpr int kThreads = 384;                 // warps 0-3: producer, issuer, -, (TMEM); warps 4-11: softmax
+constexpr int kSoft = 256;
+constexpr int kBar = 1;                       // named barriers: the softmax warps; each half of them (2, 3)
+constexpr int kShort = 3;                     // sequences of at most so many tiles are not cut (find_run)
+constexpr float kHigh = 8.f, kLow = -2.f, kSet = 4.f;   // log2 of a tile's largest weight: bounds, and where a move puts it
+constexpr float kDeep = 30.f;                 // log2 of how far a reference may lie below the highest before it
 
-__global__ void __launch_bounds__(kThreads) decode_q8_kernel(const LatentDecodeArgs a) {
-    __shared__ float q_s[kLatent + kRope], p_s[kThreads], red_s[kThreads / 32];
-    __shared__ int64_t row_s[kThreads];
-    const int tid = threadIdx.x, width = kLatent + a.c.rope_dim;
-    const int64_t q = blockIdx.x;
-    const int R = a.tokens_per_seq * a.H, n = (int)(q / R), t = (int)(q % R) / a.H;
-    for (int i = tid; i < width; i += kThreads)
-        q_s[i] = __bfloat162float(i < kLatent ? static_cast<const __nv_bfloat16*>(a.q_latent)[q * kLatent + i]
-                                              : static_cast<const __nv_bfloat16*>(a.q_rope)[q * kRope + i - kLatent]);
-    const int seen = clamped_len(a.c, a.seq_lens, n) - a.tokens_per_seq + 1 + t;
-    const uint8_t* cache = static_cast<const uint8_t*>(a.c.cache);
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    auto block_reduce = [&](float x, bool sum) {
-        for (int d = 16; d; d >>= 1) {
-            const float y = __shfl_xor_sync(0xffffffffu, x, d);
-            x = sum ? x + y : fmaxf(x, y);
-        }
-        __syncthreads();
-        if ((tid & 31) == 0) red_s[tid >> 5] = x;
-        __syncthreads();
-        x = red_s[0];
-        for (int w = 1; w < kThreads / 32; ++w) x = sum ? x + red_s[w] : fmaxf(x, red_s[w]);
-        return x;
-    };
-    for (int base = 0; base < seen; base += kThreads) {
-        const int j = base + tid;
-        const int64_t row = j < seen ? cache_row(a.c, n, j) : -1;
-        const float f = row >= 0 ? two_to(power_of(a.c.scales[row])) : 0.f;
-        float s = 0.f;
-        __syncthreads();
-        row_s[tid] = row;
-        if (row >= 0)
-            for (int i = 0; i < width; i += 4) {
-                const uint32_t y = *reinterpret_cast<const uint32_t*>(cache + row * width + i);
-                const float2 u = from_e4m3x2(y), v = from_e4m3x2(y >> 16);
-                s += q_s[i] * u.x + q_s[i + 1] * u.y + q_s[i + 2] * v.x + q_s[i + 3] * v.y;
-            }
-        s = j < seen ? s * f * a.scale : -INFINITY;
-        const float mx = fmaxf(m, block_reduce(s, false));
-        const float p = expf(s - mx), r = expf(m - mx);
-        l = l * r + block_reduce(p, true);
-        p_s[tid] = p * f;
-        m = mx;
-        __syncthreads();
-        for (int k = 0; k < 4; ++k) o[k] *= r;
-        for (int i = 0; i < kThreads; ++i) {
-            if (row_s[i] < 0) continue;
-            const uint32_t y = *reinterpret_cast<const uint32_t*>(cache + row_s[i] * width + 4 * tid);
-            const float2 u = from_e4m3x2(y), v = from_e4m3x2(y >> 16);
-            o[0] += p_s[i] * u.x; o[1] += p_s[i] * u.y; o[2] += p_s[i] * v.x; o[3] += p_s[i] * v.y;
+// Shared memory of a block with NR query rows: queries [slice][2 NR][128 bytes], their rope slice [2 NR][64], weights
+// [2 buffers][2 terms][128 tokens][NR], the rope slices of the tiles in flight, then their latent slices (128 channels).
+template <int NR, bool ROPE>
+struct Cfg {
+    static constexpr uint32_t kQSlice = 2 * NR * 128, kQRope = ROPE ? 2 * NR * 64 : 0;
+    static constexpr uint32_t kPitch = NR == 64 ? 64 : 32, kPTile = kRows * kPitch;
+    static constexpr uint32_t kQ = 0, kQR = 4 * kQSlice, kP = kQR + kQRope;
+    static constexpr uint32_t kRopeSlots = ROPE ? (NR == 64 ? 1 : 2) : 0;
+    static constexpr uint32_t kRopeAt = kP + 4 * kPTile, kSliceAt = kRopeAt + kRopeSlots * 8192;
+    static constexpr uint32_t kSmallBytes = 3072;
+    static constexpr uint32_t kFit = (232448 - kSmallBytes - kSliceAt) / 16384, kSlices = kFit < 12 ? kFit : 12;
+    static constexpr uint32_t kSmall = kSliceAt + kSlices * 16384;
+    static constexpr uint32_t kBytes = kSmall + kSmallBytes;
+    static constexpr uint32_t kCols = NR == 64 ? 512 : (NR == 32 ? 256 : 128);      // TMEM: O^T 4 NR, S 2 x 2 NR
+    static_assert(kBytes <= 232448 && kSlices >= 5, "shared memory");
+    static_assert(kQR % 1024 == 0 && kP % 1024 == 0 && kSliceAt % 1024 == 0, "swizzled tiles");
+};
+
+struct Small : Line {
+    uint64_t full[12], empty[12];             // latent slices
+    uint64_t rope_full[2], rope_empty[2];
+    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t q_full, o_free, drain;
+    uint32_t tmem;
+    int piece[5], more;                       // the softmax warps' piece
+    alignas(16) uint2 vote[2][8];             // a tile's votes, a warp each: rows whose tile is faint; any too large
+    alignas(16) float ref[64], top[64];       // m_r, and the highest it has been
+    alignas(16) float move[64];               // by how much m_r moves; at a piece's end O's factor
+    alignas(16) float unit[64];               // scale log2(e) 2^k of the query row
+    alignas(16) int seen[64];                 // tokens that the row sees
+    alignas(16) float red[2][4][32];          // a half's, a warp's: maxima, sums
+};
+static_assert(sizeof(Small) <= 3072, "small area");
+
+using Walk = WalkOf<kRows>;
+
+// OR and AND of a predicate over the softmax warps; also a barrier between them.
+__device__ __forceinline__ bool soft_or(bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, %2, %3, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)pred), "n"(kBar), "n"(kSoft)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ bool soft_and(bool pred) { return !soft_or(!pred); }
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kSoft) : "memory"); }
+__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, %1;" ::"r"(kBar + 1 + half), "n"(kSoft / 2) : "memory"); }
+
+// N consecutive 32-bit columns of the warp's lanes.
+template <int N>
+__device__ __forceinline__ void load_cols(uint32_t at, uint32_t (&r)[N]) {
+    if constexpr (N == 8) tmem_ld8(at, r);
+    if constexpr (N == 16) tmem_ld16(at, r);
+    if constexpr (N == 32) tmem_ld32(at, r);
+}
+
+// Reduces v[h] over the warp's lanes, for N values at once: each step halves the values a lane still holds, so N - 1 (and
+// a few) exchanges and not 5 N.  The lane h * 32 / N is left with value h.
+template <int N, typename Op>
+__device__ __forceinline__ float reduce_rows(float (&v)[N], const Op& op) {
+    const int lane = threadIdx.x & 31;
+    int d = 16;
+#pragma unroll
+    for (int n = N / 2; n >= 1; n /= 2, d /= 2) {
+        const bool upper = lane & d;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float mine = upper ? v[i + n] : v[i], other = upper ? v[i] : v[i + n];
+            v[i] = op(mine, __shfl_xor_sync(0xffffffffu, other, d));
         }
     }
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    for (int k = 0; k < 4; ++k)
-        static_cast<__nv_bfloat16*>(a.out)[q * kLatent + 4 * tid + k] = __float2bfloat16_rn(o[k] * f);
-    if (a.lse && tid == 0) a.lse[q] = l == 0.f ? -INFINITY : m + logf(l);
+    for (; d >= 1; d /= 2) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], d));
+    return v[0];
+}
+
+struct Maps {
+    CUtensorMap c, r;                         // latent slices, rope slices
+};
+
+template <int NR, bool ROPE>
+__global__ void __launch_bounds__(kThreads, 1)
+latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a, const int groups, const int map_rows) {
+    using G = Cfg<NR, ROPE>;
+    constexpr int NH = NR / 2;                // rows of a half of the softmax warps
+    extern __shared__ __align__(1024) uint8_t sm[];   // swizzled tiles start at multiples of 1024 bytes
+    if (smem_u32(sm) & 1023u) {               // the declaration's alignment
+        if (threadIdx.x == 0) atomicOr(a.status, kStatusTimeout);
+        return;
+    }
+    Small* sw = reinterpret_cast<Small*>(sm + G::kSmall);
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int runs = gridDim.x / groups, run = blockIdx.x / groups, group = blockIdx.x % groups;
+    const int R = a.tokens_per_seq * a.H;
+    const int rows = R - group * NR < NR ? R - group * NR : NR;      // live query rows
+    const int shift = 31 - __clz(a.c.page_size);
+
+    // as in the bf16 decode: this kernel sets itself up while the one before it ends, and the join while this one does
+    allow_next();
+    if (tid == 0) {
+        for (uint32_t i = 0; i < G::kSlices; ++i) { mbar_init(&sw->full[i], 1); mbar_init(&sw->empty[i], 1); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sw->rope_full[i], 1);
+            mbar_init(&sw->rope_empty[i], 1);
+            mbar_init(&sw->s_full[i], 1);
+            mbar_init(&sw->p_full[i], 8);
+            mbar_init(&sw->pv_done[i], 1);
+        }
+        mbar_init(&sw->q_full, 8);
+        mbar_init(&sw->o_free, 8);
+        mbar_init(&sw->drain, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&maps.c);
+        if (ROPE) tma_prefetch_desc(&maps.r);
+    }
+    if (warp == 3) {
+        tmem_alloc(&sw->tmem, G::kCols);
+        tmem_relinquish();
+    }
+    wait_before();
+    find_run<kRows, kShort, kThreads>(a, runs, run, sw, reinterpret_cast<int64_t*>(sw->ref));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = sw->tmem;
+    const uint32_t ts = tb + 4 * NR;          // S buffers
+    bool ok = true;
+    uint32_t loads = 0, rope_loads = 0;       // producer: slices issued
+
+    if (warp == 0) {                          // ------------------------------------------------ producer
+        const int box = a.c.page_size < kRows ? a.c.page_size : kRows;
+        Walk walk(sw);
+        Piece p;
+        Ring<G::kSlices> ring;
+        Ring<ROPE ? G::kRopeSlots : 1> rope;
+        bool used = false, rope_used = false; // the ring has gone round once
+        while (ok && walk.next(a, p)) {
+            const int64_t table = (int64_t)p.n * a.c.max_pages;
+            // the first cache row of this lane's box in tile x; -1: none, map_rows: outside the cache, read as zeros
+            auto row_of = [&](int x) -> int {
+                if (lane * box >= kRows || lane * box >= p.len - x * kRows) return -1;
+                const int pos = x * kRows + lane * box;
+                if (!KDA_INDEX_OK(table + (pos >> shift), (int64_t)a.num_seqs * a.c.max_pages, a.status)) return map_rows;
+                const int page = a.c.block_table[table + (pos >> shift)];
+                return page < 0 || page >= a.c.num_pages ? map_rows : (page << shift) + (pos & (a.c.page_size - 1));
+            };
+            int row = row_of(p.off);
+            for (int j = 0; ok && j < p.tiles; ++j) {
+                const int next_row = j + 1 < p.tiles ? row_of(p.off + j + 1) : -1;
+                const int live = p.len - (p.off + j) * kRows;
+                const int valid = live < 0 ? 0 : (live < kRows ? live : kRows);
+                const uint32_t boxes = (valid + box - 1) / box;
+                for (int k = 0; k < 4; ++k) {
+                    if (used && !(ok = wait_warp(&sw->empty[ring.slot], ring.phase ^ 1u))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&sw->full[ring.slot], boxes * box * 128);
+                    __syncwarp();
+                    if (row >= 0)
+                        tma_load_2d(sm + G::kSliceAt + ring.slot * 16384 + lane * box * 128, &maps.c, k * 128, row,
+                                    &sw->full[ring.slot]);
+                    ring.next();
+                    ++loads;
+                    if (ring.slot == 0) used = true;
+                }
+                if (!ok) break;
+                if constexpr (ROPE) {
+                    if (rope_used && !(ok = wait_warp(&sw->rope_empty[rope.slot], rope.phase ^ 1u))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&sw->rope_full[rope.slot], boxes * box * 64);
+                    __syncwarp();
+                    if (row >= 0)
+                        tma_load_2d(sm + G::kRopeAt + rope.slot * 8192 + lane * box * 64, &maps.r, kLatent, row,
+                                    &sw->rope_full[rope.slot]);
+                    rope.next();
+                    ++rope_loads;
+                    if (rope.slot == 0) rope_used = true;
+                }
+                row = next_row;
+            }
+        }
+        if (!ok && lane == 0) {               // copies in flight land before the block ends
+            for (uint32_t i = 0; i < G::kSlices; ++i)
+                if (loads > i) mbar_wait_bounded(&sw->full[i], ((loads - 1 - i) / G::kSlices) & 1, kWaitNs);
+            if constexpr (ROPE)
+                for (uint32_t i = 0; i < G::kRopeSlots; ++i)
+                    if (rope_loads > i)
+                        mbar_wait_bounded(&sw->rope_full[i], ((rope_loads - 1 - i) / G::kRopeSlots) & 1, kWaitNs);
+        }
+    } else if (warp == 1) {                   // ------------------------------------------------ issuer
+        constexpr uint32_t id_s = idesc_f8_f32(128, 2 * NR, false, false, false);
+        constexpr uint32_t id_o[2] = {idesc_f8_f32(128, NR, false, true, true), idesc_f8_f32(128, NR, true, true, true)};
+        constexpr uint32_t p_swizzle = G::kPitch == 64 ? kSwizzle64B : kSwizzle32B;
+        // base descriptors: queries and cached rows as keys, the rope slices of both, weights, cached rows as values
+        const uint64_t dq = smem_desc(smem_u32(sm + G::kQ), 16, 1024, kSwizzle128B);
+        const uint64_t dqr = smem_desc(smem_u32(sm + G::kQR), 16, 512, kSwizzle64B);
+        const uint64_t dk = smem_desc(smem_u32(sm + G::kSliceAt), 16, 1024, kSwizzle128B);
+        const uint64_t dr = smem_desc(smem_u32(sm + G::kRopeAt), 16, 512, kSwizzle64B);
+        const uint64_t dp = smem_desc(smem_u32(sm + G::kP), 16, 8 * G::kPitch, p_swizzle);
+        const uint64_t dv = smem_desc(smem_u32(sm + G::kSliceAt), 16384, 1024, kSwizzle128B);
+        const uint32_t el = elect_one();
+        Walk walk(sw);
+        Piece p;
+        Ring<G::kSlices> in, out;             // next slice for S, next slice for O
+        Ring<ROPE ? G::kRopeSlots : 1> rope;
+        Ring<2> sb, pb;                       // S / weight buffers
+        uint32_t seg = 0;
+        while (ok && walk.next(a, p)) {
+            if (!(ok = wait_warp(&sw->q_full, seg & 1))) break;
+            tc_fence_after();
+            int qk = 0, pv = 0;
+            while (pv < p.tiles) {
+                bool go = qk == pv;
+                if (!go && qk < p.tiles && qk == pv + 1) {           // ahead only when the tile has landed
+                    Ring<G::kSlices> last = in;
+                    last.next(); last.next(); last.next();
+                    bool landed = mbar_test(&sw->full[last.slot], last.phase);
+                    if (ROPE) landed = landed && mbar_test(&sw->rope_full[rope.slot], rope.phase);
+                    go = __all_sync(0xffffffffu, landed);
+                }
+                if (go) {
+                    const uint32_t d = ts + sb.slot * 2 * NR;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (!(ok = wait_warp(&sw->full[in.slot], in.phase))) break;
+                        tc_fence_after();
+                        const uint64_t y = desc_at(dk, in.slot * 16384);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_f8_ss_elected(d, desc_at(y, i * 32), desc_at(dq, k * G::kQSlice + i * 32), id_s, k > 0 || i > 0, el);
+                        in.next();
+                    }
+                    if (!ok) break;
+                    if constexpr (ROPE) {
+                        if (!(ok = wait_warp(&sw->rope_full[rope.slot], rope.phase))) break;
+                        tc_fence_after();
+                        const uint64_t y = desc_at(dr, rope.slot * 8192);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            mma_f8_ss_elected(d, desc_at(y, i * 32), desc_at(dqr, i * 32), id_s, 1, el);
+                        mma_commit_elected(&sw->rope_empty[rope.slot], el);
+                        rope.next();
+                    }
+                    mma_commit_elected(&sw->s_full[sb.slot], el);
+                    sb.next();
+                    ++qk;
+                } else {
+                    if (!(ok = wait_warp(&sw->p_full[pb.slot], pb.phase))) break;
+                    if (pv == 0 && seg > 0 && !(ok = wait_warp(&sw->o_free, (seg - 1) & 1))) break;
+                    tc_fence_after();
+                    const uint64_t x = desc_at(dp, pb.slot * 2 * G::kPTile);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const uint64_t y = desc_at(dv, out.slot * 16384);
+#pragma unroll
+                        for (int term = 0; term < 2; ++term)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mma_f8_ss_elected(tb + b * NR, desc_at(y, i * 4096),
+                                                  desc_at(x, term * G::kPTile + i * 32 * G::kPitch), id_o[term],
+                                                  pv > 0 || term > 0 || i > 0, el);
+                        mma_commit_elected(&sw->empty[out.slot], el);
+                        out.next();
+                    }
+                    mma_commit_elected(&sw->pv_done[pb.slot], el);
+                    pb.next();
+                    ++pv;
+                }
+            }
+            ++seg;
+        }
+        if (!ok) {                            // products in flight land before TMEM is freed
+            mma_commit_elected(&sw->drain, el);
+            wait_warp(&sw->drain, 0);
+        }
+    } else if (warp >= 4) {                   // ------------------------------------------------ softmax
+        const int w = (warp - 4) & 3, half = (warp - 4) >> 2, t = tid - (kThreads - kSoft);
+        const int tok = 32 * w + lane;        // this thread's token of a tile; its rows are h0 .. h0 + NH - 1
+        const int h0 = half * NH;
+        const uint32_t lanes = tmem_addr(tb, 32 * w, h0);            // O^T: columns of this half
+        const uint32_t s_lanes = tmem_addr(ts, 32 * w, h0);
+        Walk walk(sw);
+        Piece p{};
+        Ring<G::kSlices> in;                  // the tile's first latent slice
+        Ring<2> sb, prev;                     // this tile's buffers; the previous tile's
+        bool first_piece = true, used0 = false, used1 = false;
+        Head head{-1, 0, 0, 0};
+        int64_t at = sw->begin + sw->lead0;   // the piece's first tile in the line
+        while (ok) {
+            // one thread reads the next sequence's length for all: these warps meet at barriers and must agree on the
+            // number of tiles, whatever a caller does to the lengths meanwhile
+            if (t == 0) {
+                sw->more = walk.next(a, p);
+                settle(p, runs);
+                sw->piece[0] = p.n; sw->piece[1] = p.len; sw->piece[2] = p.off; sw->piece[3] = p.tiles; sw->piece[4] = p.all;
+            }
+            soft_sync();
+            if (!sw->more) break;
+            p = Piece{sw->piece[0], sw->piece[1], sw->piece[2], sw->piece[3], sw->piece[4]};
+            // this thread's cached row in tile x: its page, and its scale byte (0, the lowest, where there is none: such a
+            // row reads as zeros and sets no reference)
+            auto page_of = [&](int x) -> int {
+                const int64_t pos = (int64_t)x * kRows + tok;
+                if (x >= p.off + p.tiles || pos >= p.len) return -1;
+                const int64_t i = (int64_t)p.n * a.c.max_pages + (pos >> shift);
+                return KDA_INDEX_OK(i, (int64_t)a.num_seqs * a.c.max_pages, a.status) ? a.c.block_table[i] : -1;
+            };
+            auto byte_of = [&](int x, int page) -> uint8_t {
+                if (page < 0 || page >= a.c.num_pages) return 0;
+                const int64_t i = ((int64_t)page << shift) + ((x * kRows + tok) & (a.c.page_size - 1));
+                return KDA_INDEX_OK(i, (int64_t)a.c.num_pages * a.c.page_size, a.status) ? __ldcg(a.c.scales + i) : 0;
+            };
+            int page = page_of(p.off);
+            int next_page = page_of(p.off + 1);
+
+            // ---- the queries: a warp a row, the previous piece's products with them are done (their S has been read)
+#pragma unroll 1
+            for (int r = warp - 4; r < NR; r += 8) {
+                uint4 x[3];
+                x[0] = x[1] = x[2] = make_uint4(0, 0, 0, 0);
+                const int64_t q = (int64_t)p.n * R + group * NR + r;
+                if (r < rows && KDA_INDEX_OK(q, (int64_t)a.num_seqs * R, a.status)) {
+                    const uint4* src = static_cast<const uint4*>(a.q_latent) + q * (kLatent / 8);
+                    x[0] = __ldcg(src + lane);
+                    x[1] = __ldcg(src + lane + 32);
+                    if (ROPE && lane < 8) x[2] = __ldcg(static_cast<const uint4*>(a.q_rope) + q * (kRope / 8) + lane);
+                }
+                uint32_t most = 0;
+                const uint32_t* xi = reinterpret_cast<const uint32_t*>(x);
+#pragma unroll
+                for (int i = 0; i < 12; ++i) most = max(most, max(xi[i] << 16 & 0x7fff0000u, xi[i] & 0x7fff0000u));
+                const int k = power_for(__reduce_max_sync(0xffffffffu, most));
+                const float f = two_to(-k);
+#pragma unroll
+                for (int c = 0; c < 3; ++c) {
+                    uint32_t y[2][2];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t v = xi[4 * c + i];
+                        const float lo = __uint_as_float(v << 16) * f, hi = __uint_as_float(v & 0xffff0000u) * f;
+                        const uint32_t y1 = to_e4m3x2(lo, hi);
+                        const float2 b = from_e4m3x2(y1);
+                        const uint32_t y2 = to_e4m3x2(lo - b.x, hi - b.y);
+                        if (i & 1) {
+                            y[0][i >> 1] |= y1 << 16;
+                            y[1][i >> 1] |= y2 << 16;
+                        } else {
+                            y[0][i >> 1] = y1;
+                            y[1][i >> 1] = y2;
+                        }
+                    }
+#pragma unroll
+                    for (int term = 0; term < 2; ++term) {
+                        const uint2 v = make_uint2(y[term][0], y[term][1]);
+                        const int row = term * NR + r, chunk = lane + 32 * c;       // eight channels
+                        if (c < 2)
+                            *reinterpret_cast<uint2*>(sm + G::kQ + (chunk >> 4) * G::kQSlice + sw128_offset(row, (chunk & 15) * 8)) = v;
+                        else if (ROPE && lane < 8)
+                            *reinterpret_cast<uint2*>(sm + G::kQR + sw64_offset(row, lane * 8)) = v;
+                    }
+                }
+                if (lane == 0) {
+                    sw->unit[r] = a.scale * 1.44269504088896340736f * two_to(k);
+                    sw->seen[r] = r < rows ? p.len - a.tokens_per_seq + 1 + (group * NR + r) / a.H : 0;
+                    sw->ref[r] = 0.f;
+                    sw->top[r] = -INFINITY;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sw->q_full);
+            soft_sync();
+            const int least = p.len - a.tokens_per_seq + 1 + group * NR / a.H;      // tokens that the first row sees
+
+            uint8_t byte = byte_of(p.off, page);
+            float l[NH];
+#pragma unroll
+            for (int i = 0; i < NH; ++i) l[i] = 0.f;
+            for (int j = 0; j < p.tiles; ++j) {
+                const int base = (p.off + j) * kRows;
+                const int e = power_of(byte);
+                byte = byte_of(p.off + j + 1, next_page);            // a tile ahead, and its page two
+                next_page = page_of(p.off + j + 2);
+                // a wait that runs out is not left alone: the warps meet at barriers, and stop together
+                ok = ok && wait_warp(&sw->s_full[sb.slot], sb.phase);
+                tc_fence_after();
+                float x[NH];                  // log2 of the weights
+                {
+                    constexpr int N = NH < 16 ? NH : 16;
+                    const float two_e = two_to(e), fe = (float)e;
+#pragma unroll
+                    for (int c = 0; c < NH; c += N) {
+                        uint32_t s1[N], s2[N];
+                        load_cols<N>(s_lanes + sb.slot * 2 * NR + c, s1);
+                        load_cols<N>(s_lanes + sb.slot * 2 * NR + NR + c, s2);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < N; i += 4) {
+                            const float4 u = *reinterpret_cast<const float4*>(sw->unit + h0 + c + i);
+                            const float4 m = *reinterpret_cast<const float4*>(sw->ref + h0 + c + i);
+                            const float uu[4] = {u.x, u.y, u.z, u.w}, mm[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+                            for (int n = 0; n < 4; ++n)
+                                x[c + i + n] = fmaf((__uint_as_float(s1[i + n]) + __uint_as_float(s2[i + n])) * two_e, uu[n], fe - mm[n]);
+                        }
+                    }
+                }
+                if (base + kRows > least) {   // tokens that some rows do not see
+#pragma unroll
+                    for (int i = 0; i < NH; ++i)
+                        if (base + tok >= sw->seen[h0 + i]) x[i] = -INFINITY;
+                }
+                uint32_t faint = 0;           // bit i: row NH - 1 - i lies below the range
+                float most = x[0];
+#pragma unroll
+                for (int i = 0; i < NH; ++i) {
+                    faint = __funnelshift_l(__float_as_uint(x[i] - kLow), faint, 1);
+                    most = fmaxf(most, x[i]);
+                }
+                faint = __reduce_and_sync(0xffffffffu, faint);
+                const bool high = __any_sync(0xffffffffu, most > kHigh);
+                if (lane == 0) sw->vote[j & 1][warp - 4] = make_uint2(faint, high);
+                if (p.len - base < kRows) {   // the tile's rows behind the sequence's end become zeros
+                    const int valid = p.len - base < 0 ? 0 : p.len - base;
+                    Ring<G::kSlices> slice = in;
+                    for (int k = 0; k < 4; ++k, slice.next())
+                        for (int i = t; i < (kRows - valid) * 8; i += kSoft)
+                            *reinterpret_cast<uint4*>(sm + G::kSliceAt + slice.slot * 16384 + (valid + (i >> 3)) * 128 + (i & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                }
+                if (soft_or(!ok)) { ok = false; break; }
+                uint32_t all_faint = 0xffffffffu, any_high = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint2 v = sw->vote[j & 1][half * 4 + k];
+                    all_faint &= v.x;
+                    any_high |= v.y;
+                }
+                if (j == 0 || any_high || all_faint) {               // move references (this half of the warps agrees)
+                    float v[NH];
+#pragma unroll
+                    for (int i = 0; i < NH; ++i) v[i] = x[i];
+                    const float mx = reduce_rows<NH>(v, [](float p, float q) { return fmaxf(p, q); });
+                    if (lane % (32 / NH) == 0) sw->red[half][w][lane / (32 / NH)] = mx;
+                    half_sync(half);
+                    const int i = t & 127;
+                    if (i < NH) {
+                        float z = sw->red[half][0][i];
+                        for (int k = 1; k < 4; ++k) z = fmaxf(z, sw->red[half][k][i]);
+                        const float m = sw->ref[h0 + i], top = sw->top[h0 + i];
+                        float n = m;
+                        if (z > -INFINITY && (j == 0 || z > kHigh || z < kLow)) {
+                            n = fmaxf(m + rintf(z - kSet), top - kDeep);
+                            sw->ref[h0 + i] = n;
+                            sw->top[h0 + i] = fmaxf(top, n);
+                        }
+                        sw->move[h0 + i] = n - m;
+                    }
+                    half_sync(half);
+                    if (j > 0) ok = ok && wait_warp(&sw->pv_done[prev.slot], prev.phase);
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < NH; c += 8) {
+                        float f[8];
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) {
+                            const float d = sw->move[h0 + c + n];
+                            x[c + n] -= d;
+                            f[n] = exp2_fast(fminf(fmaxf(-d, -126.f), 100.f));
+                            l[c + n] *= f[n];
+                        }
+                        if (j > 0 && ok) {    // O^T, column r by f_r
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) {
+                                uint32_t o[8];
+                                tmem_ld8(lanes + b * NR + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int n = 0; n < 8; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f[n]);
+                                tmem_st8(lanes + b * NR + c, o);
+                            }
+                        }
+                    }
+                    tmem_wait_st();
+                }
+                // this weight buffer was read by the products of two tiles ago
+                if (sb.slot ? used1 : used0) ok = ok && wait_warp(&sw->pv_done[sb.slot], sb.phase ^ 1u);
+                if (ok) {
+                    uint8_t* pt = sm + G::kP + sb.slot * 2 * G::kPTile;
+                    const float back = two_to(-e);
+                    constexpr int N = NH < 16 ? NH : 16;             // rows a store
+#pragma unroll
+                    for (int c = 0; c < NH; c += N) {
+                        uint32_t y[2][N / 4];
+#pragma unroll
+                        for (int i = 0; i < N; i += 2) {
+                            const float p0 = exp2_fast(x[c + i]), p1 = exp2_fast(x[c + i + 1]);
+                            l[c + i] = fmaf(p0, back, l[c + i]);
+                            l[c + i + 1] = fmaf(p1, back, l[c + i + 1]);
+                            const uint32_t y1 = to_e4m3x2(p0, p1);
+                            const float2 b = from_e4m3x2(y1);
+                            const uint32_t y2 = to_e5m2x2(p0 - b.x, p1 - b.y);
+                            if (i & 2) {
+                                y[0][i / 4] |= y1 << 16;
+                                y[1][i / 4] |= y2 << 16;
+                            } else {
+                                y[0][i / 4] = y1;
+                                y[1][i / 4] = y2;
+                            }
+                        }
+#pragma unroll
+                        for (int term = 0; term < 2; ++term) {
+                            const uint32_t off = NR == 64 ? sw64_offset(tok, h0 + c) : sw32_offset(tok, h0 + c);
+                            if constexpr (N == 16)
+                                *reinterpret_cast<uint4*>(pt + term * G::kPTile + off) = make_uint4(y[term][0], y[term][1], y[term][2], y[term][3]);
+                            else
+                                *reinterpret_cast<uint2*>(pt + term * G::kPTile + off) = make_uint2(y[term][0], y[term][1]);
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(&sw->p_full[sb.slot]);
+                if (sb.slot) used1 = true; else used0 = true;
+                prev = sb;
+                sb.next();
+                in.next(); in.next(); in.next(); in.next();
+            }
+            if (!soft_and(ok)) { ok = false; break; }
+            // ---- the piece is done: its rows' sums, then O^T out of tensor memory
+            const bool whole = is_whole(p);
+            const int slot = blockIdx.x * 2 + (first_piece ? 0 : 1);
+            if (p.off == 0 && !whole) {
+                head.n = p.n;
+                head.first_slot = first_piece ? 0 : 1;
+                // never past the last run, whatever happens to the lengths while the call runs: the join reads by it
+                const int last = run_of(sw->total, sw->runs, at + p.all - 1);
+                head.parts = (last >= run && last < runs ? last : runs - 1) - run + 1;
+            }
+            uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+            float2* ml = reinterpret_cast<float2*>(ws + Work<NR>::ml_at(gridDim.x));
+            float* po = reinterpret_cast<float*>(ws + Work<NR>::o_at(gridDim.x));
+            const float sum = reduce_rows<NH>(l, [](float p, float q) { return p + q; });
+            if (lane % (32 / NH) == 0) sw->red[half][w][lane / (32 / NH)] = sum;
+            ok = soft_and(wait_warp(&sw->pv_done[prev.slot], prev.phase));   // also: the parts of the sums are written
+            if (!ok) break;
+            if (t < NR) {
+                const float* part = &sw->red[t / NH][0][t % NH];
+                const float total = (part[0] + part[32]) + (part[64] + part[96]);
+                // total 2^m = f 2^k, f in [1, 2): no large m against a large logarithm, here and in the join
+                const int power = (int)(__float_as_uint(total) >> 23) - 127;
+                const float f = total == 0.f ? 0.f : total * two_to(-power), k = total == 0.f ? -INFINITY : sw->ref[t] + (float)power;
+                if (whole) {
+                    const int64_t row = (int64_t)p.n * R + group * NR + t;
+                    if (a.lse && t < rows && KDA_INDEX_OK(row, (int64_t)a.num_seqs * R, a.status))
+                        a.lse[row] = total == 0.f ? -INFINITY : k * 0.69314718055994530942f + logf(f);
+                } else if (KDA_INDEX_OK((int64_t)slot * NR + t, (int64_t)gridDim.x * 2 * NR, a.status)) {
+                    ml[(int64_t)slot * NR + t] = make_float2(k, f);
+                }
+                sw->move[t] = total == 0.f ? 0.f : (whole ? 1.f / total : two_to(-power));
+            }
+            soft_sync();
+            tc_fence_after();
+            // column r of block b: row r, channels 128 b ..; a lane stores its channel of 8 rows at a time, so a
+            // warp's store is 64 bytes of a row in bf16, 128 in fp32
+            const int64_t row = whole ? (int64_t)p.n * R + group * NR : (int64_t)slot * NR;
+            const bool inside = whole ? KDA_INDEX_OK(row + rows - 1, (int64_t)a.num_seqs * R, a.status)
+                                      : KDA_INDEX_OK(row + NR - 1, (int64_t)gridDim.x * 2 * NR, a.status);
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (row + h0) * kLatent + tok;
+            float* part = po + (row + h0) * kLatent + tok;
+#pragma unroll
+            for (int c = 0; c < NH; c += 8) {
+                uint32_t o[4][8];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) tmem_ld8(lanes + b * NR + c, o[b]);
+                tmem_wait_ld();
+                const int live = inside ? rows - h0 - c : 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < live) {
+                        const float f = sw->move[h0 + c + i];
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            if (whole)
+                                out[(c + i) * kLatent + b * 128] = __float2bfloat16_rn(__uint_as_float(o[b][i]) * f);
+                            else
+                                part[(c + i) * kLatent + b * 128] = __uint_as_float(o[b][i]) * f;
+                        }
+                    }
+            }
+            tc_fence_before();
+            // everyone has read the sums before the next piece writes them
+            soft_sync();
+            if (lane == 0) mbar_arrive(&sw->o_free);
+            at += p.tiles + kStart;
+            first_piece = false;
+        }
+        if (t == 0) reinterpret_cast<Head*>(a.workspace)[blockIdx.x] = head;
+    }
+    if (!ok && lane == 0) atomicOr(a.status, kStatusTimeout);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 3) tmem_dealloc(tb, G::kCols);
+}
+
+// [rows, width] bytes, boxes of `channels` x box_rows, swizzled over the box's row.
+bool map_rows_2d(CUtensorMap* m, const void* base, int64_t rows, int width, int channels, int box_rows) {
+    const auto fn = encode();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width};
+    cuuint32_t box[2] = {(cuuint32_t)channels, (cuuint32_t)box_rows}, es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              channels == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NR, bool ROPE>
+cudaError_t launch(const LatentDecodeArgs& a, cudaStream_t s) {
+    using G = Cfg<NR, ROPE>;
+    const int R = a.tokens_per_seq * a.H, groups = groups_of(R), grid = runs_of(groups) * groups;
+    const int box = a.c.page_size < kRows ? a.c.page_size : kRows, width = kLatent + (ROPE ? kRope : 0);
+    // a cache without pages: any readable row; every box then starts behind the map's last row
+    const int64_t c_rows = a.c.num_pages > 0 ? (int64_t)a.c.num_pages * a.c.page_size : 1;
+    const void* c_base = a.c.num_pages > 0 ? a.c.cache : a.workspace;
+    Maps maps;
+    if (!map_rows_2d(&maps.c, c_base, c_rows, width, 128, box) || !map_rows_2d(&maps.r, c_base, c_rows, width, kRope, box))
+        return cudaErrorInvalidValue;
+    static std::atomic<bool> ready[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(latent_decode_q8_kernel<NR, ROPE>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kBytes);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true, std::memory_order_release);
+    }
+    const cudaError_t e = launch_overlapped(latent_decode_q8_kernel<NR, ROPE>, grid, kThreads, G::kBytes, s, maps, a, groups,
+                                            (int)c_rows);
+    return e != cudaSuccess ? e : launch_overlapped(latent_join_kernel<NR>, kJoinBlocks, kJoinThreads, 0, s, a, grid, groups);
+}
+
+template <int NR>
+cudaError_t launch_rope(const LatentDecodeArgs& a, cudaStream_t s) {
+    return a.c.rope_dim ? launch<NR, true>(a, s) : launch<NR, false>(a, s);
 }
 
 }  // namespace
 
-size_t latent_decode_q8_workspace_bytes(int, int) { return 256; }
+size_t latent_decode_q8_workspace_bytes(int tokens_per_seq, int H) { return line_workspace_bytes(tokens_per_seq, H); }
 
 cudaError_t launch_latent_decode_q8(const LatentDecodeArgs& a, cudaStream_t s) {
-    decode_q8_kernel<<<(unsigned)(a.num_seqs * a.tokens_per_seq * a.H), kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    switch (rows_a_block(a.tokens_per_seq * a.H)) {
+        case 16: return launch_rope<16>(a, s);
+        case 32: return launch_rope<32>(a, s);
+        default: return launch_rope<64>(a, s);
+    }
 }
 
 }  // namespace kda

@@ -42,6 +42,11 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
     return to_e4m3x2(a, b) | (to_e4m3x2(c, d) << 16);
 }
+__device__ __forceinline__ uint32_t to_e5m2x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 // Two e4m3 numbers (the low 16 bits), exactly.
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t x) {
     uint32_t h;

@@ -13,7 +13,7 @@
 namespace kda {
 namespace latent {
 
-constexpr int kTile = 64;                     // cached rows a tile
+constexpr int kTile = 64;                     // cached rows a tile of the bf16 decode
 // A sequence's places in the line: its tiles, behind kStart places that stand for what starting a piece costs a
 // block (queries in, O out), so that runs with many pieces get fewer tiles.
 constexpr int kStart = 1;
@@ -22,7 +22,8 @@ struct Piece {                                // a run's share of one sequence
     int n, len, off, tiles, all;              // sequence, its length, first tile, tiles here, tiles in all
 };
 
-KDA_RUNS_FN int tiles_of(int len) { return len > kTile ? (len - 1) / kTile + 1 : 1; }
+template <int TILE = kTile>
+KDA_RUNS_FN int tiles_of(int len) { return len > TILE ? (len - 1) / TILE + 1 : 1; }
 
 // The first tile of run p of `runs` over `total` tiles (a 32-bit division where it fits, a fifth of the time), and
 // the run that holds tile x.
@@ -31,8 +32,9 @@ KDA_RUNS_FN int64_t run_begin(int64_t total, int runs, int p) {
 }
 KDA_RUNS_FN int run_of(int64_t total, int runs, int64_t x) { return (int)(((x + 1) * runs - 1) / total); }
 
-// Walks the sequences of a run; length(n) is sequence n's length.
-struct RunWalk {
+// Walks the sequences of a run of tiles of TILE rows; length(n) is sequence n's length.
+template <int TILE>
+struct RunWalkOf {
     int n, off, lead, len;                    // next sequence, its first tile here, start places before it, its length or -1
     int64_t left;                             // places of the run that are left
     template <typename Length>
@@ -41,7 +43,7 @@ struct RunWalk {
         p.n = n;
         p.len = len >= 0 ? len : length(n);
         len = -1;
-        p.all = tiles_of(p.len);
+        p.all = tiles_of<TILE>(p.len);
         p.off = off;
         const int64_t behind = left - lead;   // places of the run behind the sequence's start places
         p.tiles = behind < p.all - off ? (behind > 0 ? (int)behind : 0) : p.all - off;
@@ -52,6 +54,7 @@ struct RunWalk {
         return p.tiles > 0;                   // a run may end inside the start places
     }
 };
+using RunWalk = RunWalkOf<kTile>;
 
 // Whether a piece's result is its sequence's, and goes to the output.  Other pieces go to the workspace, which a line in
 // one run does not have: there every piece is the only one of its sequence (settle), also where a length that grew since
