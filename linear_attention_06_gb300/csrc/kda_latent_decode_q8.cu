@@ -51,7 +51,7 @@ constexpr int kThreads = 384;                 // warps 0-3: producer, issuer, -,
 constexpr int kSoft = 256;
 constexpr int kBar = 1;                       // named barriers: the softmax warps; each half of them (2, 3)
 constexpr int kShort = 3;                     // sequences of at most so many tiles are not cut (find_run)
-constexpr float kHigh = 8.f, kLow = -2.f, kSet = 4.f;   // log2 of a tile's largest weight: bounds, and where a move puts it
+constexpr float kHigh = 8.75f, kLow = -4.f, kSet = 2.f;   // log2 of a tile's largest weight: bounds, and where a move puts it
 constexpr float kDeep = 30.f;                 // log2 of how far a reference may lie below the highest before it
 
 // Shared memory of a block with NR query rows: queries [slice][2 NR][128 bytes], their rope slice [2 NR][64], weights
@@ -343,17 +343,86 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
         bool first_piece = true, used0 = false, used1 = false;
         Head head{-1, 0, 0, 0};
         int64_t at = sw->begin + sw->lead0;   // the piece's first tile in the line
-        while (ok) {
-            // one thread reads the next sequence's length for all: these warps meet at barriers and must agree on the
-            // number of tiles, whatever a caller does to the lengths meanwhile
-            if (t == 0) {
-                sw->more = walk.next(a, p);
-                settle(p, runs);
-                sw->piece[0] = p.n; sw->piece[1] = p.len; sw->piece[2] = p.off; sw->piece[3] = p.tiles; sw->piece[4] = p.all;
+        // the next piece, agreed on: one thread reads its sequence's length for all, since these warps meet at barriers and
+        // must agree on the number of tiles, whatever a caller does to the lengths meanwhile
+        auto announce = [&]() {
+            if (t != 0) return;
+            Piece x{};
+            sw->more = walk.next(a, x);
+            settle(x, runs);
+            sw->piece[0] = x.n; sw->piece[1] = x.len; sw->piece[2] = x.off; sw->piece[3] = x.tiles; sw->piece[4] = x.all;
+        };
+        // a piece's queries into shared memory, a warp a row, the loads of a batch of rows before their use
+        auto take_queries = [&](const Piece& p) {
+            constexpr int kBatchRows = NR / 8 < 4 ? NR / 8 : 4;
+#pragma unroll 1
+            for (int r0 = warp - 4; r0 < NR; r0 += 8 * kBatchRows) {
+                uint4 in[kBatchRows][3];
+#pragma unroll
+                for (int i = 0; i < kBatchRows; ++i) {
+                    in[i][0] = in[i][1] = in[i][2] = make_uint4(0, 0, 0, 0);
+                    const int r = r0 + 8 * i;
+                    const int64_t q = (int64_t)p.n * R + group * NR + r;
+                    if (r < rows && KDA_INDEX_OK(q, (int64_t)a.num_seqs * R, a.status)) {
+                        const uint4* src = static_cast<const uint4*>(a.q_latent) + q * (kLatent / 8);
+                        in[i][0] = __ldcg(src + lane);
+                        in[i][1] = __ldcg(src + lane + 32);
+                        if (ROPE && lane < 8) in[i][2] = __ldcg(static_cast<const uint4*>(a.q_rope) + q * (kRope / 8) + lane);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kBatchRows; ++i) {
+                    const int r = r0 + 8 * i;
+                    const uint32_t* xi = reinterpret_cast<const uint32_t*>(in[i]);
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int n = 0; n < 12; ++n) most = max(most, max(xi[n] << 16 & 0x7fff0000u, xi[n] & 0x7fff0000u));
+                    const int k = power_for(__reduce_max_sync(0xffffffffu, most));
+                    const float f = two_to(-k);
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) {
+                        uint32_t y[2][2];
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            const uint32_t v = xi[4 * c + n];
+                            const float lo = __uint_as_float(v << 16) * f, hi = __uint_as_float(v & 0xffff0000u) * f;
+                            const uint32_t y1 = to_e4m3x2(lo, hi);
+                            const float2 b = from_e4m3x2(y1);
+                            const uint32_t y2 = to_e4m3x2(lo - b.x, hi - b.y);
+                            y[0][n >> 1] = n & 1 ? y[0][n >> 1] | y1 << 16 : y1;
+                            y[1][n >> 1] = n & 1 ? y[1][n >> 1] | y2 << 16 : y2;
+                        }
+#pragma unroll
+                        for (int term = 0; term < 2; ++term) {
+                            const uint2 v = make_uint2(y[term][0], y[term][1]);
+                            const int row = term * NR + r, chunk = lane + 32 * c;       // eight channels
+                            if (c < 2)
+                                *reinterpret_cast<uint2*>(sm + G::kQ + (chunk >> 4) * G::kQSlice + sw128_offset(row, (chunk & 15) * 8)) = v;
+                            else if (ROPE && lane < 8)
+                                *reinterpret_cast<uint2*>(sm + G::kQR + sw64_offset(row, lane * 8)) = v;
+                        }
+                    }
+                    if (lane == 0) {
+                        sw->unit[r] = a.scale * 1.44269504088896340736f * two_to(k);
+                        sw->seen[r] = r < rows ? p.len - a.tokens_per_seq + 1 + (group * NR + r) / a.H : 0;
+                        sw->ref[r] = 0.f;
+                        sw->top[r] = -INFINITY;
+                    }
+                }
             }
-            soft_sync();
-            if (!sw->more) break;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sw->q_full);
+        };
+        announce();
+        soft_sync();
+        bool more = sw->more;
+        if (more) {
             p = Piece{sw->piece[0], sw->piece[1], sw->piece[2], sw->piece[3], sw->piece[4]};
+            take_queries(p);
+            soft_sync();
+        }
+        while (ok && more) {
             // this thread's cached row in tile x: its page, and its scale byte (0, the lowest, where there is none: such a
             // row reads as zeros and sets no reference)
             auto page_of = [&](int x) -> int {
@@ -367,66 +436,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 const int64_t i = ((int64_t)page << shift) + ((x * kRows + tok) & (a.c.page_size - 1));
                 return KDA_INDEX_OK(i, (int64_t)a.c.num_pages * a.c.page_size, a.status) ? __ldcg(a.c.scales + i) : 0;
             };
-            int page = page_of(p.off);
+            const int page = page_of(p.off);
             int next_page = page_of(p.off + 1);
-
-            // ---- the queries: a warp a row, the previous piece's products with them are done (their S has been read)
-#pragma unroll 1
-            for (int r = warp - 4; r < NR; r += 8) {
-                uint4 x[3];
-                x[0] = x[1] = x[2] = make_uint4(0, 0, 0, 0);
-                const int64_t q = (int64_t)p.n * R + group * NR + r;
-                if (r < rows && KDA_INDEX_OK(q, (int64_t)a.num_seqs * R, a.status)) {
-                    const uint4* src = static_cast<const uint4*>(a.q_latent) + q * (kLatent / 8);
-                    x[0] = __ldcg(src + lane);
-                    x[1] = __ldcg(src + lane + 32);
-                    if (ROPE && lane < 8) x[2] = __ldcg(static_cast<const uint4*>(a.q_rope) + q * (kRope / 8) + lane);
-                }
-                uint32_t most = 0;
-                const uint32_t* xi = reinterpret_cast<const uint32_t*>(x);
-#pragma unroll
-                for (int i = 0; i < 12; ++i) most = max(most, max(xi[i] << 16 & 0x7fff0000u, xi[i] & 0x7fff0000u));
-                const int k = power_for(__reduce_max_sync(0xffffffffu, most));
-                const float f = two_to(-k);
-#pragma unroll
-                for (int c = 0; c < 3; ++c) {
-                    uint32_t y[2][2];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t v = xi[4 * c + i];
-                        const float lo = __uint_as_float(v << 16) * f, hi = __uint_as_float(v & 0xffff0000u) * f;
-                        const uint32_t y1 = to_e4m3x2(lo, hi);
-                        const float2 b = from_e4m3x2(y1);
-                        const uint32_t y2 = to_e4m3x2(lo - b.x, hi - b.y);
-                        if (i & 1) {
-                            y[0][i >> 1] |= y1 << 16;
-                            y[1][i >> 1] |= y2 << 16;
-                        } else {
-                            y[0][i >> 1] = y1;
-                            y[1][i >> 1] = y2;
-                        }
-                    }
-#pragma unroll
-                    for (int term = 0; term < 2; ++term) {
-                        const uint2 v = make_uint2(y[term][0], y[term][1]);
-                        const int row = term * NR + r, chunk = lane + 32 * c;       // eight channels
-                        if (c < 2)
-                            *reinterpret_cast<uint2*>(sm + G::kQ + (chunk >> 4) * G::kQSlice + sw128_offset(row, (chunk & 15) * 8)) = v;
-                        else if (ROPE && lane < 8)
-                            *reinterpret_cast<uint2*>(sm + G::kQR + sw64_offset(row, lane * 8)) = v;
-                    }
-                }
-                if (lane == 0) {
-                    sw->unit[r] = a.scale * 1.44269504088896340736f * two_to(k);
-                    sw->seen[r] = r < rows ? p.len - a.tokens_per_seq + 1 + (group * NR + r) / a.H : 0;
-                    sw->ref[r] = 0.f;
-                    sw->top[r] = -INFINITY;
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sw->q_full);
-            soft_sync();
             const int least = p.len - a.tokens_per_seq + 1 + group * NR / a.H;      // tokens that the first row sees
 
             uint8_t byte = byte_of(p.off, page);
@@ -519,22 +530,25 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
 #pragma unroll
                     for (int c = 0; c < NH; c += 8) {
                         float f[8];
+                        bool still = true;    // none of these rows moves
 #pragma unroll
                         for (int n = 0; n < 8; ++n) {
                             const float d = sw->move[h0 + c + n];
+                            still = still && d == 0.f;
                             x[c + n] -= d;
                             f[n] = exp2_fast(fminf(fmaxf(-d, -126.f), 100.f));
                             l[c + n] *= f[n];
                         }
-                        if (j > 0 && ok) {    // O^T, column r by f_r
+                        if (j > 0 && ok && !still) {                 // O^T, column r by f_r
+                            uint32_t o[4][8];
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) tmem_ld8(lanes + b * NR + c, o[b]);
+                            tmem_wait_ld();
 #pragma unroll
                             for (int b = 0; b < 4; ++b) {
-                                uint32_t o[8];
-                                tmem_ld8(lanes + b * NR + c, o);
-                                tmem_wait_ld();
 #pragma unroll
-                                for (int n = 0; n < 8; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f[n]);
-                                tmem_st8(lanes + b * NR + c, o);
+                                for (int n = 0; n < 8; ++n) o[b][n] = __float_as_uint(__uint_as_float(o[b][n]) * f[n]);
+                                tmem_st8(lanes + b * NR + c, o[b]);
                             }
                         }
                     }
@@ -600,8 +614,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             float* po = reinterpret_cast<float*>(ws + Work<NR>::o_at(gridDim.x));
             const float sum = reduce_rows<NH>(l, [](float p, float q) { return p + q; });
             if (lane % (32 / NH) == 0) sw->red[half][w][lane / (32 / NH)] = sum;
-            ok = soft_and(wait_warp(&sw->pv_done[prev.slot], prev.phase));   // also: the parts of the sums are written
-            if (!ok) break;
+            announce();
+            soft_sync();
             if (t < NR) {
                 const float* part = &sw->red[t / NH][0][t % NH];
                 const float total = (part[0] + part[32]) + (part[64] + part[96]);
@@ -618,6 +632,13 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 sw->move[t] = total == 0.f ? 0.f : (whole ? 1.f / total : two_to(-power));
             }
             soft_sync();
+            // the next piece's queries while this one's last products run (those with the queries are done: their S has
+            // been read); its first scores are then computed while this piece's result is written
+            more = sw->more;
+            const Piece next{sw->piece[0], sw->piece[1], sw->piece[2], sw->piece[3], sw->piece[4]};
+            if (more) take_queries(next);
+            ok = soft_and(wait_warp(&sw->pv_done[prev.slot], prev.phase));
+            if (!ok) break;
             tc_fence_after();
             // column r of block b: row r, channels 128 b ..; a lane stores its channel of 8 rows at a time, so a
             // warp's store is 64 bytes of a row in bf16, 128 in fp32
@@ -651,6 +672,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             soft_sync();
             if (lane == 0) mbar_arrive(&sw->o_free);
             at += p.tiles + kStart;
+            p = next;
             first_piece = false;
         }
         if (t == 0) reinterpret_cast<Head*>(a.workspace)[blockIdx.x] = head;
