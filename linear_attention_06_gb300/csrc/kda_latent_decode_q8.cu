@@ -51,7 +51,9 @@ constexpr int kThreads = 384;                 // warps 0-3: producer, issuer, -,
 constexpr int kSoft = 256;
 constexpr int kBar = 1;                       // named barriers: the softmax warps; each half of them (2, 3)
 constexpr int kShort = 3;                     // sequences of at most so many tiles are not cut (find_run)
-constexpr float kHigh = 8.75f, kLow = -4.f, kSet = 2.f;   // log2 of a tile's largest weight: bounds, and where a move puts it
+// log2 of a tile's largest weight: where a piece's first tile is put, the bounds, and where a tile beyond one of them is
+// put: near that bound, so that tiles as they were before stay inside the range.
+constexpr float kSet = 2.f, kHigh = 8.75f, kHighSet = 7.f, kLow = -5.f, kLowSet = -3.f;
 constexpr float kDeep = 30.f;                 // log2 of how far a reference may lie below the highest before it
 
 // Shared memory of a block with NR query rows: queries [slice][2 NR][128 bytes], their rope slice [2 NR][64], weights
@@ -79,8 +81,8 @@ struct Small : Line {
     uint64_t q_full, o_free, drain;
     uint32_t tmem;
     int piece[5], more;                       // the softmax warps' piece
-    alignas(16) uint2 vote[2][8];             // a tile's votes, a warp each: rows whose tile is faint; any too large
-    alignas(16) float ref[64], top[64];       // m_r, and the highest it has been
+    alignas(16) uint2 vote[2][8];             // a tile's votes, a warp each: rows that are bright enough; any too large
+    alignas(16) float ref[64], top[64];       // -m_r, and the highest m_r has been
     alignas(16) float move[64];               // by how much m_r moves; at a piece's end O's factor
     alignas(16) float unit[64];               // scale log2(e) 2^k of the query row
     alignas(16) int seen[64];                 // tokens that the row sees
@@ -132,6 +134,18 @@ __device__ __forceinline__ float reduce_rows(float (&v)[N], const Op& op) {
     }
     for (; d >= 1; d /= 2) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], d));
     return v[0];
+}
+
+__device__ __forceinline__ float2 pair(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
+// What e4m3 leaves of two weights, as e5m2 (exact differences in fp16, whose 11 bits hold the first 8 of the rest).
+__device__ __forceinline__ uint32_t rest_e5m2x2(float lo, float hi, uint32_t e4m3) {
+    uint32_t h, b, r;
+    uint16_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)e4m3));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(b));
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(y) : "r"(r));
+    return y;
 }
 
 struct Maps {
@@ -189,6 +203,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
 
     if (warp == 0) {                          // ------------------------------------------------ producer
         const int box = a.c.page_size < kRows ? a.c.page_size : kRows;
+        constexpr int kWidth = kLatent + (ROPE ? kRope : 0);
         Walk walk(sw);
         Piece p;
         Ring<G::kSlices> ring;
@@ -233,6 +248,13 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                     ++rope_loads;
                     if (rope.slot == 0) rope_used = true;
                 }
+                // The next tile into L2 behind this one's loads, where a request fetches 64 rows or more: its own loads
+                // wait for ring slots and then find it near (64 x 8192 cached tokens, 32 heads: 55.4 us, 58.2 without; two
+                // tiles ahead 57.0, three 58.2; pages of 16 gain nothing).
+                const int next_live = live - kRows - lane * box;
+                if (box >= 64 && next_row >= 0 && next_row < map_rows && next_live > 0)
+                    bulk_prefetch_l2(static_cast<const uint8_t*>(a.c.cache) + (int64_t)next_row * kWidth,
+                                     (uint32_t)(next_live < box ? next_live : box) * kWidth);
                 row = next_row;
             }
         }
@@ -265,32 +287,27 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
         while (ok && walk.next(a, p)) {
             if (!(ok = wait_warp(&sw->q_full, seg & 1))) break;
             tc_fence_after();
-            int qk = 0, pv = 0;
+            // Slices of the next tile are multiplied as they land, between the value products of the tile before it: its
+            // scores are ready soon after its last slice.
+            int qk = 0, part = 0, pv = 0;     // tile and slice that S is at, tile that O is at
+            bool freed = seg == 0;            // O of the piece before has been read
+            uint64_t idle = 0;                // since when nothing could be issued
+            constexpr int kParts = ROPE ? 5 : 4;
             while (pv < p.tiles) {
-                bool go = qk == pv;
-                if (!go && qk < p.tiles && qk == pv + 1) {           // ahead only when the tile has landed
-                    Ring<G::kSlices> last = in;
-                    last.next(); last.next(); last.next();
-                    bool landed = mbar_test(&sw->full[last.slot], last.phase);
-                    if (ROPE) landed = landed && mbar_test(&sw->rope_full[rope.slot], rope.phase);
-                    go = __all_sync(0xffffffffu, landed);
-                }
-                if (go) {
+                bool landed = false, ready = false;
+                if (qk < p.tiles && qk <= pv + 1)
+                    landed = __all_sync(0xffffffffu, part < 4 ? mbar_test(&sw->full[in.slot], in.phase)
+                                                              : mbar_test(&sw->rope_full[rope.slot], rope.phase));
+                if (landed) {
+                    tc_fence_after();
                     const uint32_t d = ts + sb.slot * 2 * NR;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (!(ok = wait_warp(&sw->full[in.slot], in.phase))) break;
-                        tc_fence_after();
-                        const uint64_t y = desc_at(dk, in.slot * 16384);
+                    if (part < 4) {
+                        const uint64_t y = desc_at(dk, in.slot * 16384), x = desc_at(dq, part * G::kQSlice);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            mma_f8_ss_elected(d, desc_at(y, i * 32), desc_at(dq, k * G::kQSlice + i * 32), id_s, k > 0 || i > 0, el);
+                            mma_f8_ss_elected(d, desc_at(y, i * 32), desc_at(x, i * 32), id_s, part > 0 || i > 0, el);
                         in.next();
-                    }
-                    if (!ok) break;
-                    if constexpr (ROPE) {
-                        if (!(ok = wait_warp(&sw->rope_full[rope.slot], rope.phase))) break;
-                        tc_fence_after();
+                    } else {
                         const uint64_t y = desc_at(dr, rope.slot * 8192);
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
@@ -298,30 +315,43 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                         mma_commit_elected(&sw->rope_empty[rope.slot], el);
                         rope.next();
                     }
-                    mma_commit_elected(&sw->s_full[sb.slot], el);
-                    sb.next();
-                    ++qk;
-                } else {
-                    if (!(ok = wait_warp(&sw->p_full[pb.slot], pb.phase))) break;
-                    if (pv == 0 && seg > 0 && !(ok = wait_warp(&sw->o_free, (seg - 1) & 1))) break;
-                    tc_fence_after();
-                    const uint64_t x = desc_at(dp, pb.slot * 2 * G::kPTile);
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const uint64_t y = desc_at(dv, out.slot * 16384);
-#pragma unroll
-                        for (int term = 0; term < 2; ++term)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                mma_f8_ss_elected(tb + b * NR, desc_at(y, i * 4096),
-                                                  desc_at(x, term * G::kPTile + i * 32 * G::kPitch), id_o[term],
-                                                  pv > 0 || term > 0 || i > 0, el);
-                        mma_commit_elected(&sw->empty[out.slot], el);
-                        out.next();
+                    if (++part == kParts) {
+                        mma_commit_elected(&sw->s_full[sb.slot], el);
+                        sb.next();
+                        ++qk;
+                        part = 0;
                     }
-                    mma_commit_elected(&sw->pv_done[pb.slot], el);
-                    pb.next();
-                    ++pv;
+                } else if (pv < qk && !freed) {
+                    ready = freed = __all_sync(0xffffffffu, mbar_test(&sw->o_free, (seg - 1) & 1));
+                } else if (pv < qk) {
+                    ready = __all_sync(0xffffffffu, mbar_test(&sw->p_full[pb.slot], pb.phase));
+                    if (ready) {
+                        tc_fence_after();
+                        const uint64_t x = desc_at(dp, pb.slot * 2 * G::kPTile);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const uint64_t y = desc_at(dv, out.slot * 16384);
+#pragma unroll
+                            for (int term = 0; term < 2; ++term)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    mma_f8_ss_elected(tb + b * NR, desc_at(y, i * 4096),
+                                                      desc_at(x, term * G::kPTile + i * 32 * G::kPitch), id_o[term],
+                                                      pv > 0 || term > 0 || i > 0, el);
+                            mma_commit_elected(&sw->empty[out.slot], el);
+                            out.next();
+                        }
+                        mma_commit_elected(&sw->pv_done[pb.slot], el);
+                        pb.next();
+                        ++pv;
+                    }
+                }
+                if (landed || ready) {
+                    idle = 0;
+                } else {
+                    const uint64_t now = globaltimer_ns();
+                    if (idle == 0) idle = now;
+                    if (!(ok = __all_sync(0xffffffffu, now - idle < kWaitNs))) break;
                 }
             }
             ++seg;
@@ -444,20 +474,23 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             float l[NH];
 #pragma unroll
             for (int i = 0; i < NH; ++i) l[i] = 0.f;
-            for (int j = 0; j < p.tiles; ++j) {
-                const int base = (p.off + j) * kRows;
+            const int len = p.len, off = p.off, tiles = p.tiles;
+            for (int j = 0; j < tiles; ++j) {
+                const int base = (off + j) * kRows;
                 const int e = power_of(byte);
-                byte = byte_of(p.off + j + 1, next_page);            // a tile ahead, and its page two
-                next_page = page_of(p.off + j + 2);
+                byte = byte_of(off + j + 1, next_page);              // a tile ahead, and its page two
+                next_page = page_of(off + j + 2);
                 // a wait that runs out is not left alone: the warps meet at barriers, and stop together
                 ok = ok && wait_warp(&sw->s_full[sb.slot], sb.phase);
                 tc_fence_after();
-                float x[NH];                  // log2 of the weights
-                {
-                    constexpr int N = NH < 16 ? NH : 16;
-                    const float two_e = two_to(e), fe = (float)e;
+                const float2 two_e = make_float2(two_to(e), two_to(e)), fe = make_float2((float)e, (float)e);
+                constexpr int N = NH < 16 ? NH : 16;                 // rows a step
+                float x[NH];                  // the weights
+                uint32_t y[2][NH / 4];        // in 8 bits, both terms
+                bool move = j == 0;           // references have to move: a piece's first tile sets them
+                for (;;) {
 #pragma unroll
-                    for (int c = 0; c < NH; c += N) {
+                    for (int c = 0; c < NH; c += N) {                // log2 of the weights
                         uint32_t s1[N], s2[N];
                         load_cols<N>(s_lanes + sb.slot * 2 * NR + c, s1);
                         load_cols<N>(s_lanes + sb.slot * 2 * NR + NR + c, s2);
@@ -466,133 +499,136 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                         for (int i = 0; i < N; i += 4) {
                             const float4 u = *reinterpret_cast<const float4*>(sw->unit + h0 + c + i);
                             const float4 m = *reinterpret_cast<const float4*>(sw->ref + h0 + c + i);
-                            const float uu[4] = {u.x, u.y, u.z, u.w}, mm[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-                            for (int n = 0; n < 4; ++n)
-                                x[c + i + n] = fmaf((__uint_as_float(s1[i + n]) + __uint_as_float(s2[i + n])) * two_e, uu[n], fe - mm[n]);
+                            const float2 v = fma2(mul2(add2(pair(s1[i], s1[i + 1]), pair(s2[i], s2[i + 1])), two_e),
+                                                  make_float2(u.x, u.y), add2(fe, make_float2(m.x, m.y)));
+                            const float2 w = fma2(mul2(add2(pair(s1[i + 2], s1[i + 3]), pair(s2[i + 2], s2[i + 3])), two_e),
+                                                  make_float2(u.z, u.w), add2(fe, make_float2(m.z, m.w)));
+                            x[c + i] = v.x; x[c + i + 1] = v.y; x[c + i + 2] = w.x; x[c + i + 3] = w.y;
                         }
                     }
-                }
-                if (base + kRows > least) {   // tokens that some rows do not see
+                    if (base + kRows > least) {                      // tokens that some rows do not see
 #pragma unroll
-                    for (int i = 0; i < NH; ++i)
-                        if (base + tok >= sw->seen[h0 + i]) x[i] = -INFINITY;
-                }
-                uint32_t faint = 0;           // bit i: row NH - 1 - i lies below the range
-                float most = x[0];
+                        for (int i = 0; i < NH; ++i)
+                            if (base + tok >= sw->seen[h0 + i]) x[i] = -INFINITY;
+                    }
+                    if (move) {               // this half of the warps agrees
+                        float v[NH];
 #pragma unroll
-                for (int i = 0; i < NH; ++i) {
-                    faint = __funnelshift_l(__float_as_uint(x[i] - kLow), faint, 1);
-                    most = fmaxf(most, x[i]);
+                        for (int i = 0; i < NH; ++i) v[i] = x[i];
+                        const float mx = reduce_rows<NH>(v, [](float p, float q) { return fmaxf(p, q); });
+                        if (lane % (32 / NH) == 0) sw->red[half][w][lane / (32 / NH)] = mx;
+                        half_sync(half);
+                        const int i = t & 127;
+                        if (i < NH) {
+                            const float z = fmaxf(fmaxf(sw->red[half][0][i], sw->red[half][1][i]),
+                                                  fmaxf(sw->red[half][2][i], sw->red[half][3][i]));
+                            const float m = -sw->ref[h0 + i], top = sw->top[h0 + i];
+                            float n = m;
+                            if (z > -INFINITY && (j == 0 || z > kHigh || z < kLow)) {
+                                n = fmaxf(m + rintf(z - (j == 0 ? kSet : z > kHigh ? kHighSet : kLowSet)), top - kDeep);
+                                sw->ref[h0 + i] = -n;
+                                sw->top[h0 + i] = fmaxf(top, n);
+                            }
+                            sw->move[h0 + i] = n - m;
+                        }
+                        half_sync(half);
+                        if (j > 0) ok = ok && wait_warp(&sw->pv_done[prev.slot], prev.phase);
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < NH; c += 8) {
+                            float f[8];
+                            bool still = true;                       // none of these rows moves
+#pragma unroll
+                            for (int n = 0; n < 8; ++n) {
+                                const float d = sw->move[h0 + c + n];
+                                still = still && d == 0.f;
+                                x[c + n] -= d;
+                                f[n] = exp2_fast(fminf(fmaxf(-d, -126.f), 100.f));
+                                l[c + n] *= f[n];
+                            }
+                            if (j > 0 && ok && !still) {             // O^T, column r by f_r
+                                uint32_t o[4][8];
+#pragma unroll
+                                for (int b = 0; b < 4; ++b) tmem_ld8(lanes + b * NR + c, o[b]);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int b = 0; b < 4; ++b) {
+#pragma unroll
+                                    for (int n = 0; n < 8; ++n) o[b][n] = __float_as_uint(__uint_as_float(o[b][n]) * f[n]);
+                                    tmem_st8(lanes + b * NR + c, o[b]);
+                                }
+                            }
+                        }
+                        tmem_wait_st();
+                    }
+                    float most = x[0];
+                    uint32_t bright = 0;      // a bit a row: this token's weight is 2^kLow or more
+#pragma unroll
+                    for (int i = 1; i < NH; ++i) most = fmaxf(most, x[i]);
+#pragma unroll
+                    for (int i = 0; i < NH; i += 2) {
+                        x[i] = exp2_fast(x[i]);
+                        x[i + 1] = exp2_fast(x[i + 1]);
+                        const uint32_t y1 = to_e4m3x2(x[i], x[i + 1]);
+                        const uint32_t y2 = rest_e5m2x2(x[i], x[i + 1], y1);
+                        y[0][i / 4] = i & 2 ? y[0][i / 4] | y1 << 16 : y1;
+                        y[1][i / 4] = i & 2 ? y[1][i / 4] | y2 << 16 : y2;
+                    }
+                    if (move) break;
+                    // e4m3 numbers of 2^-5 or more have one of the bits 0x70
+#pragma unroll
+                    for (int i = 0; i < NH / 4; ++i) bright |= (((y[0][i] & 0x70707070u) + 0x70707070u) & 0x80808080u) >> i;
+                    bright = __reduce_or_sync(0xffffffffu, bright);
+                    const bool high = __any_sync(0xffffffffu, most > kHigh);
+                    if (lane == 0) sw->vote[j & 1][warp - 4] = make_uint2(bright, high);
+                    if (soft_or(!ok)) { ok = false; break; }
+                    uint32_t all_bright = 0, any_high = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint2 v = sw->vote[j & 1][half * 4 + k];
+                        all_bright |= v.x;
+                        any_high |= v.y;
+                    }
+                    constexpr uint32_t kAll = NH == 32 ? 0xffffffffu : NH == 16 ? 0xf0f0f0f0u : 0xc0c0c0c0u;
+                    if (!any_high && all_bright == kAll) break;
+                    move = true;              // once more from the scores
                 }
-                faint = __reduce_and_sync(0xffffffffu, faint);
-                const bool high = __any_sync(0xffffffffu, most > kHigh);
-                if (lane == 0) sw->vote[j & 1][warp - 4] = make_uint2(faint, high);
-                if (p.len - base < kRows) {   // the tile's rows behind the sequence's end become zeros
-                    const int valid = p.len - base < 0 ? 0 : p.len - base;
+                if (!ok && !move) break;
+                if (len - base < kRows) {                  // the tile's rows behind the sequence's end become zeros
+                    const int valid = len - base < 0 ? 0 : len - base;
                     Ring<G::kSlices> slice = in;
                     for (int k = 0; k < 4; ++k, slice.next())
                         for (int i = t; i < (kRows - valid) * 8; i += kSoft)
                             *reinterpret_cast<uint4*>(sm + G::kSliceAt + slice.slot * 16384 + (valid + (i >> 3)) * 128 + (i & 7) * 16) =
                                 make_uint4(0, 0, 0, 0);
                 }
-                if (soft_or(!ok)) { ok = false; break; }
-                uint32_t all_faint = 0xffffffffu, any_high = 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint2 v = sw->vote[j & 1][half * 4 + k];
-                    all_faint &= v.x;
-                    any_high |= v.y;
-                }
-                if (j == 0 || any_high || all_faint) {               // move references (this half of the warps agrees)
-                    float v[NH];
-#pragma unroll
-                    for (int i = 0; i < NH; ++i) v[i] = x[i];
-                    const float mx = reduce_rows<NH>(v, [](float p, float q) { return fmaxf(p, q); });
-                    if (lane % (32 / NH) == 0) sw->red[half][w][lane / (32 / NH)] = mx;
-                    half_sync(half);
-                    const int i = t & 127;
-                    if (i < NH) {
-                        float z = sw->red[half][0][i];
-                        for (int k = 1; k < 4; ++k) z = fmaxf(z, sw->red[half][k][i]);
-                        const float m = sw->ref[h0 + i], top = sw->top[h0 + i];
-                        float n = m;
-                        if (z > -INFINITY && (j == 0 || z > kHigh || z < kLow)) {
-                            n = fmaxf(m + rintf(z - kSet), top - kDeep);
-                            sw->ref[h0 + i] = n;
-                            sw->top[h0 + i] = fmaxf(top, n);
-                        }
-                        sw->move[h0 + i] = n - m;
-                    }
-                    half_sync(half);
-                    if (j > 0) ok = ok && wait_warp(&sw->pv_done[prev.slot], prev.phase);
-                    tc_fence_after();
-#pragma unroll
-                    for (int c = 0; c < NH; c += 8) {
-                        float f[8];
-                        bool still = true;    // none of these rows moves
-#pragma unroll
-                        for (int n = 0; n < 8; ++n) {
-                            const float d = sw->move[h0 + c + n];
-                            still = still && d == 0.f;
-                            x[c + n] -= d;
-                            f[n] = exp2_fast(fminf(fmaxf(-d, -126.f), 100.f));
-                            l[c + n] *= f[n];
-                        }
-                        if (j > 0 && ok && !still) {                 // O^T, column r by f_r
-                            uint32_t o[4][8];
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) tmem_ld8(lanes + b * NR + c, o[b]);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) {
-#pragma unroll
-                                for (int n = 0; n < 8; ++n) o[b][n] = __float_as_uint(__uint_as_float(o[b][n]) * f[n]);
-                                tmem_st8(lanes + b * NR + c, o[b]);
-                            }
-                        }
-                    }
-                    tmem_wait_st();
-                }
                 // this weight buffer was read by the products of two tiles ago
                 if (sb.slot ? used1 : used0) ok = ok && wait_warp(&sw->pv_done[sb.slot], sb.phase ^ 1u);
                 if (ok) {
                     uint8_t* pt = sm + G::kP + sb.slot * 2 * G::kPTile;
-                    const float back = two_to(-e);
-                    constexpr int N = NH < 16 ? NH : 16;             // rows a store
 #pragma unroll
-                    for (int c = 0; c < NH; c += N) {
-                        uint32_t y[2][N / 4];
+                    for (int term = 0; term < 2; ++term)
 #pragma unroll
-                        for (int i = 0; i < N; i += 2) {
-                            const float p0 = exp2_fast(x[c + i]), p1 = exp2_fast(x[c + i + 1]);
-                            l[c + i] = fmaf(p0, back, l[c + i]);
-                            l[c + i + 1] = fmaf(p1, back, l[c + i + 1]);
-                            const uint32_t y1 = to_e4m3x2(p0, p1);
-                            const float2 b = from_e4m3x2(y1);
-                            const uint32_t y2 = to_e5m2x2(p0 - b.x, p1 - b.y);
-                            if (i & 2) {
-                                y[0][i / 4] |= y1 << 16;
-                                y[1][i / 4] |= y2 << 16;
-                            } else {
-                                y[0][i / 4] = y1;
-                                y[1][i / 4] = y2;
-                            }
-                        }
-#pragma unroll
-                        for (int term = 0; term < 2; ++term) {
+                        for (int c = 0; c < NH; c += N) {
+                            const uint32_t* v = &y[term][c / 4];
                             const uint32_t off = NR == 64 ? sw64_offset(tok, h0 + c) : sw32_offset(tok, h0 + c);
                             if constexpr (N == 16)
-                                *reinterpret_cast<uint4*>(pt + term * G::kPTile + off) = make_uint4(y[term][0], y[term][1], y[term][2], y[term][3]);
+                                *reinterpret_cast<uint4*>(pt + term * G::kPTile + off) = make_uint4(v[0], v[1], v[2], v[3]);
                             else
-                                *reinterpret_cast<uint2*>(pt + term * G::kPTile + off) = make_uint2(y[term][0], y[term][1]);
+                                *reinterpret_cast<uint2*>(pt + term * G::kPTile + off) = make_uint2(v[0], v[1]);
                         }
-                    }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0 && ok) mbar_arrive(&sw->p_full[sb.slot]);
+                const float2 back = make_float2(two_to(-e), two_to(-e));
+#pragma unroll
+                for (int i = 0; i < NH; i += 2) {
+                    const float2 v = fma2(make_float2(x[i], x[i + 1]), back, make_float2(l[i], l[i + 1]));
+                    l[i] = v.x;
+                    l[i + 1] = v.y;
+                }
                 if (sb.slot) used1 = true; else used0 = true;
                 prev = sb;
                 sb.next();
@@ -621,7 +657,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 const float total = (part[0] + part[32]) + (part[64] + part[96]);
                 // total 2^m = f 2^k, f in [1, 2): no large m against a large logarithm, here and in the join
                 const int power = (int)(__float_as_uint(total) >> 23) - 127;
-                const float f = total == 0.f ? 0.f : total * two_to(-power), k = total == 0.f ? -INFINITY : sw->ref[t] + (float)power;
+                const float f = total == 0.f ? 0.f : total * two_to(-power), k = total == 0.f ? -INFINITY : (float)power - sw->ref[t];
                 if (whole) {
                     const int64_t row = (int64_t)p.n * R + group * NR + t;
                     if (a.lse && t < rows && KDA_INDEX_OK(row, (int64_t)a.num_seqs * R, a.status))
