@@ -53,18 +53,18 @@ constexpr int kBar = 1;                       // named barriers: the softmax war
 constexpr int kShort = 3;                     // sequences of at most so many tiles are not cut (find_run)
 // log2 of a tile's largest weight: where a piece's first tile is put, the bounds, and where a tile beyond one of them is
 // put: near that bound, so that tiles as they were before stay inside the range.
-constexpr float kSet = 2.f, kHigh = 8.75f, kHighSet = 7.f, kLow = -5.f, kLowSet = -3.f;
+constexpr float kSet = 1.f, kHigh = 8.75f, kHighSet = 8.f, kLow = -5.f, kLowSet = -2.f;
 constexpr float kDeep = 30.f;                 // log2 of how far a reference may lie below the highest before it
 
 // Shared memory of a block with NR query rows: queries [slice][2 NR][128 bytes], their rope slice [2 NR][64], weights
-// [2 buffers][2 terms][128 tokens][NR], the rope slices of the tiles in flight, then their latent slices (128 channels).
+// [2 terms][128 tokens][NR], the rope slices of the tiles in flight, then their latent slices (128 channels).
 template <int NR, bool ROPE>
 struct Cfg {
     static constexpr uint32_t kQSlice = 2 * NR * 128, kQRope = ROPE ? 2 * NR * 64 : 0;
     static constexpr uint32_t kPitch = NR == 64 ? 64 : 32, kPTile = kRows * kPitch;
     static constexpr uint32_t kQ = 0, kQR = 4 * kQSlice, kP = kQR + kQRope;
     static constexpr uint32_t kRopeSlots = ROPE ? (NR == 64 ? 1 : 2) : 0;
-    static constexpr uint32_t kRopeAt = kP + 4 * kPTile, kSliceAt = kRopeAt + kRopeSlots * 8192;
+    static constexpr uint32_t kRopeAt = kP + 2 * kPTile, kSliceAt = kRopeAt + kRopeSlots * 8192;
     static constexpr uint32_t kSmallBytes = 3072;
     static constexpr uint32_t kFit = (232448 - kSmallBytes - kSliceAt) / 16384, kSlices = kFit < 12 ? kFit : 12;
     static constexpr uint32_t kSmall = kSliceAt + kSlices * 16384;
@@ -77,8 +77,9 @@ struct Cfg {
 struct Small : Line {
     uint64_t full[12], empty[12];             // latent slices
     uint64_t rope_full[2], rope_empty[2];
-    uint64_t s_full[2], p_full[2], pv_done[2];
-    uint64_t q_full, o_free, drain;
+    uint64_t s_full[2], p_full, pv_done;
+    uint64_t raw_full, q_full, q_empty;       // queries: bf16 landed, quantised, no longer needed
+    uint64_t o_free, drain;
     uint32_t tmem;
     int piece[5], more;                       // the softmax warps' piece
     alignas(16) uint2 vote[2][8];             // a tile's votes, a warp each: rows that are bright enough; any too large
@@ -137,19 +138,34 @@ __device__ __forceinline__ float reduce_rows(float (&v)[N], const Op& op) {
 }
 
 __device__ __forceinline__ float2 pair(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
-// What e4m3 leaves of two weights, as e5m2 (exact differences in fp16, whose 11 bits hold the first 8 of the rest).
+// The largest magnitude's bits among eight bf16 numbers, as fp32.
+__device__ __forceinline__ uint32_t largest(const uint4& v) {
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max(x[i] << 16 & 0x7fff0000u, x[i] & 0x7fff0000u));
+    return m;
+}
+// Eight bf16 numbers times f as the sum of two e4m3 numbers each.
+__device__ __forceinline__ void two_terms(const uint4& v, float f, uint2 (&y)[2]) {
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t h = to_f16x2(__uint_as_float(x[i] << 16) * f, __uint_as_float(x[i] & 0xffff0000u) * f);
+        a[i] = f16_to_e4m3x2(h);
+        b[i] = f16_to_e4m3x2(sub_f16x2(h, e4m3_to_f16x2(a[i])));
+    }
+    y[0] = make_uint2(a[0] | a[1] << 16, a[2] | a[3] << 16);
+    y[1] = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+}
+// What e4m3 leaves of two weights, as e5m2 (fp16 holds 11 bits of a weight, the difference is exact).
 __device__ __forceinline__ uint32_t rest_e5m2x2(float lo, float hi, uint32_t e4m3) {
-    uint32_t h, b, r;
-    uint16_t y;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)e4m3));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(b));
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(y) : "r"(r));
-    return y;
+    return f16_to_e5m2x2(sub_f16x2(to_f16x2(lo, hi), e4m3_to_f16x2(e4m3)));
 }
 
 struct Maps {
-    CUtensorMap c, r;                         // latent slices, rope slices
+    CUtensorMap q, c, r;                      // queries' latent slices, cached latent slices, cached rope slices
 };
 
 template <int NR, bool ROPE>
@@ -177,13 +193,16 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             mbar_init(&sw->rope_full[i], 1);
             mbar_init(&sw->rope_empty[i], 1);
             mbar_init(&sw->s_full[i], 1);
-            mbar_init(&sw->p_full[i], 8);
-            mbar_init(&sw->pv_done[i], 1);
         }
+        mbar_init(&sw->p_full, 8);
+        mbar_init(&sw->pv_done, 1);
+        mbar_init(&sw->raw_full, 1);
         mbar_init(&sw->q_full, 8);
+        mbar_init(&sw->q_empty, 1);
         mbar_init(&sw->o_free, 8);
         mbar_init(&sw->drain, 1);
         fence_mbar_init();
+        tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.c);
         if (ROPE) tma_prefetch_desc(&maps.r);
     }
@@ -282,7 +301,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
         Piece p;
         Ring<G::kSlices> in, out;             // next slice for S, next slice for O
         Ring<ROPE ? G::kRopeSlots : 1> rope;
-        Ring<2> sb, pb;                       // S / weight buffers
+        Ring<2> sb;                           // S buffers
+        uint32_t products = 0;                // tiles that O has
         uint32_t seg = 0;
         while (ok && walk.next(a, p)) {
             if (!(ok = wait_warp(&sw->q_full, seg & 1))) break;
@@ -317,6 +337,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                     }
                     if (++part == kParts) {
                         mma_commit_elected(&sw->s_full[sb.slot], el);
+                        if (qk + 1 == p.tiles) mma_commit_elected(&sw->q_empty, el);
                         sb.next();
                         ++qk;
                         part = 0;
@@ -324,10 +345,9 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 } else if (pv < qk && !freed) {
                     ready = freed = __all_sync(0xffffffffu, mbar_test(&sw->o_free, (seg - 1) & 1));
                 } else if (pv < qk) {
-                    ready = __all_sync(0xffffffffu, mbar_test(&sw->p_full[pb.slot], pb.phase));
+                    ready = __all_sync(0xffffffffu, mbar_test(&sw->p_full, products & 1));
                     if (ready) {
                         tc_fence_after();
-                        const uint64_t x = desc_at(dp, pb.slot * 2 * G::kPTile);
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
                             const uint64_t y = desc_at(dv, out.slot * 16384);
@@ -336,13 +356,13 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
                                     mma_f8_ss_elected(tb + b * NR, desc_at(y, i * 4096),
-                                                      desc_at(x, term * G::kPTile + i * 32 * G::kPitch), id_o[term],
+                                                      desc_at(dp, term * G::kPTile + i * 32 * G::kPitch), id_o[term],
                                                       pv > 0 || term > 0 || i > 0, el);
                             mma_commit_elected(&sw->empty[out.slot], el);
                             out.next();
                         }
-                        mma_commit_elected(&sw->pv_done[pb.slot], el);
-                        pb.next();
+                        mma_commit_elected(&sw->pv_done, el);
+                        ++products;
                         ++pv;
                     }
                 }
@@ -360,6 +380,26 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             mma_commit_elected(&sw->drain, el);
             wait_warp(&sw->drain, 0);
         }
+    } else if (warp == 2) {                   // ------------------------------------------------ queries
+        // A piece's queries, in bf16, to where they are quantised in place.  Behind the tiles that all blocks have asked
+        // for they would come 3 to 5 us after their request: the next piece's are in L2 by then.
+        Walk walk(sw);
+        Piece p, next;
+        uint32_t seg = 0;
+        for (bool more = walk.next(a, p); more; p = next) {
+            if (seg > 0 && !(ok = wait_warp(&sw->q_empty, (seg - 1) & 1))) break;
+            if (lane == 0) mbar_arrive_expect_tx(&sw->raw_full, 8 * NR * 128);
+            __syncwarp();
+            if (lane < 8) tma_load_2d(sm + G::kQ + lane * NR * 128, &maps.q, lane * 64, p.n * R + group * NR, &sw->raw_full);
+            ++seg;
+            more = walk.next(a, next);
+            const int64_t q = (int64_t)next.n * R + group * NR;
+            if (more && lane == 0 && KDA_INDEX_OK(q + rows - 1, (int64_t)a.num_seqs * R, a.status)) {
+                bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(a.q_latent) + q * kLatent, rows * kLatent * 2);
+                if (ROPE) bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(a.q_rope) + q * kRope, rows * kRope * 2);
+            }
+        }
+        if (seg > 0 && lane == 0) mbar_wait_bounded(&sw->raw_full, (seg - 1) & 1, kWaitNs);   // landed, whatever the others do
     } else if (warp >= 4) {                   // ------------------------------------------------ softmax
         const int w = (warp - 4) & 3, half = (warp - 4) >> 2, t = tid - (kThreads - kSoft);
         const int tok = 32 * w + lane;        // this thread's token of a tile; its rows are h0 .. h0 + NH - 1
@@ -369,8 +409,9 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
         Walk walk(sw);
         Piece p{};
         Ring<G::kSlices> in;                  // the tile's first latent slice
-        Ring<2> sb, prev;                     // this tile's buffers; the previous tile's
-        bool first_piece = true, used0 = false, used1 = false;
+        Ring<2> sb;                           // this tile's S buffer
+        uint32_t tile = 0, pieces = 0;        // tiles before this one, of all pieces; pieces whose queries were taken
+        bool first_piece = true;
         Head head{-1, 0, 0, 0};
         int64_t at = sw->begin + sw->lead0;   // the piece's first tile in the line
         // the next piece, agreed on: one thread reads its sequence's length for all, since these warps meet at barriers and
@@ -382,67 +423,89 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             settle(x, runs);
             sw->piece[0] = x.n; sw->piece[1] = x.len; sw->piece[2] = x.off; sw->piece[3] = x.tiles; sw->piece[4] = x.all;
         };
-        // a piece's queries into shared memory, a warp a row, the loads of a batch of rows before their use
+        // A piece's queries in 8 bits, a warp a row.  The 128 bytes of channels 128 k .. 128 k + 63 of a row in bf16 lie
+        // where the row's first terms of slice k go, those of the next 64 where its second terms go: in place.  The rope
+        // part (four rows a word of a warp) goes through registers.  The loop is not unrolled: it runs once a piece, and
+        // its instructions have to be fetched (unrolled, 3400 cycles of a block's start).
         auto take_queries = [&](const Piece& p) {
-            constexpr int kBatchRows = NR / 8 < 4 ? NR / 8 : 4;
-#pragma unroll 1
-            for (int r0 = warp - 4; r0 < NR; r0 += 8 * kBatchRows) {
-                uint4 in[kBatchRows][3];
+            constexpr int kSets = NR == 64 ? 2 : 1;                  // of four rows
+            uint4 rope[kSets];
+            uint32_t rope_most[kSets];
+            int rope_power[kSets];
+            if constexpr (ROPE) {
 #pragma unroll
-                for (int i = 0; i < kBatchRows; ++i) {
-                    in[i][0] = in[i][1] = in[i][2] = make_uint4(0, 0, 0, 0);
-                    const int r = r0 + 8 * i;
+                for (int k = 0; k < kSets; ++k) {
+                    const int r = warp - 4 + 8 * (4 * k + (lane >> 3));
                     const int64_t q = (int64_t)p.n * R + group * NR + r;
-                    if (r < rows && KDA_INDEX_OK(q, (int64_t)a.num_seqs * R, a.status)) {
-                        const uint4* src = static_cast<const uint4*>(a.q_latent) + q * (kLatent / 8);
-                        in[i][0] = __ldcg(src + lane);
-                        in[i][1] = __ldcg(src + lane + 32);
-                        if (ROPE && lane < 8) in[i][2] = __ldcg(static_cast<const uint4*>(a.q_rope) + q * (kRope / 8) + lane);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kBatchRows; ++i) {
-                    const int r = r0 + 8 * i;
-                    const uint32_t* xi = reinterpret_cast<const uint32_t*>(in[i]);
-                    uint32_t most = 0;
-#pragma unroll
-                    for (int n = 0; n < 12; ++n) most = max(most, max(xi[n] << 16 & 0x7fff0000u, xi[n] & 0x7fff0000u));
-                    const int k = power_for(__reduce_max_sync(0xffffffffu, most));
-                    const float f = two_to(-k);
-#pragma unroll
-                    for (int c = 0; c < 3; ++c) {
-                        uint32_t y[2][2];
-#pragma unroll
-                        for (int n = 0; n < 4; ++n) {
-                            const uint32_t v = xi[4 * c + n];
-                            const float lo = __uint_as_float(v << 16) * f, hi = __uint_as_float(v & 0xffff0000u) * f;
-                            const uint32_t y1 = to_e4m3x2(lo, hi);
-                            const float2 b = from_e4m3x2(y1);
-                            const uint32_t y2 = to_e4m3x2(lo - b.x, hi - b.y);
-                            y[0][n >> 1] = n & 1 ? y[0][n >> 1] | y1 << 16 : y1;
-                            y[1][n >> 1] = n & 1 ? y[1][n >> 1] | y2 << 16 : y2;
-                        }
-#pragma unroll
-                        for (int term = 0; term < 2; ++term) {
-                            const uint2 v = make_uint2(y[term][0], y[term][1]);
-                            const int row = term * NR + r, chunk = lane + 32 * c;       // eight channels
-                            if (c < 2)
-                                *reinterpret_cast<uint2*>(sm + G::kQ + (chunk >> 4) * G::kQSlice + sw128_offset(row, (chunk & 15) * 8)) = v;
-                            else if (ROPE && lane < 8)
-                                *reinterpret_cast<uint2*>(sm + G::kQR + sw64_offset(row, lane * 8)) = v;
-                        }
-                    }
-                    if (lane == 0) {
-                        sw->unit[r] = a.scale * 1.44269504088896340736f * two_to(k);
-                        sw->seen[r] = r < rows ? p.len - a.tokens_per_seq + 1 + (group * NR + r) / a.H : 0;
-                        sw->ref[r] = 0.f;
-                        sw->top[r] = -INFINITY;
-                    }
+                    rope[k] = make_uint4(0, 0, 0, 0);
+                    if (r < rows && KDA_INDEX_OK(q, (int64_t)a.num_seqs * R, a.status))
+                        rope[k] = __ldcg(static_cast<const uint4*>(a.q_rope) + q * (kRope / 8) + (lane & 7));
                 }
             }
+            ok = ok && wait_warp(&sw->raw_full, pieces & 1);
+            if constexpr (ROPE) {
+#pragma unroll
+                for (int k = 0; k < kSets; ++k) {
+                    rope_most[k] = largest(rope[k]);
+                    for (int d = 1; d < 8; d *= 2) rope_most[k] = max(rope_most[k], __shfl_xor_sync(0xffffffffu, rope_most[k], d));
+                }
+            }
+#pragma unroll 1
+            for (int i = 0; i < NR / 8; ++i) {
+                const int r = warp - 4 + 8 * i;
+                uint4 x[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    x[c] = *reinterpret_cast<const uint4*>(sm + G::kQ + (4 * c + (lane >> 3)) * NR * 128 + sw128_offset(r, (lane & 7) * 16));
+                    if (r >= rows) x[c] = make_uint4(0, 0, 0, 0);
+                }
+                uint32_t most = max(largest(x[0]), largest(x[1]));
+                if constexpr (ROPE) {
+                    uint32_t other = __shfl_sync(0xffffffffu, rope_most[0], (i & 3) * 8);
+                    if (kSets > 1 && i >= 4) other = __shfl_sync(0xffffffffu, rope_most[kSets - 1], (i & 3) * 8);
+                    most = max(most, other);
+                }
+                const int k = power_for(__reduce_max_sync(0xffffffffu, most));           // also: all lanes have read the row
+                if constexpr (ROPE) {
+                    if ((lane >> 3) == (i & 3)) {
+                        if (i < 4) rope_power[0] = k;
+                        else rope_power[kSets - 1] = k;
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int slice = 4 * c + (lane >> 3);           // of 64 channels
+                    uint2 y[2];
+                    two_terms(x[c], two_to(-k), y);
+#pragma unroll
+                    for (int term = 0; term < 2; ++term)
+                        *reinterpret_cast<uint2*>(sm + G::kQ + (slice >> 1) * G::kQSlice +
+                                                  sw128_offset(term * NR + r, (slice & 1) * 64 + (lane & 7) * 8)) = y[term];
+                }
+                if (lane == 0) {
+                    sw->unit[r] = a.scale * 1.44269504088896340736f * two_to(k);
+                    sw->seen[r] = r < rows ? p.len - a.tokens_per_seq + 1 + (group * NR + r) / a.H : 0;
+                    sw->ref[r] = 0.f;
+                    sw->top[r] = -INFINITY;
+                }
+            }
+            if constexpr (ROPE) {
+#pragma unroll
+                for (int k = 0; k < kSets; ++k) {
+                    const int r = warp - 4 + 8 * (4 * k + (lane >> 3));
+                    if (r >= NR) continue;
+                    uint2 y[2];
+                    two_terms(rope[k], two_to(-rope_power[k]), y);
+#pragma unroll
+                    for (int term = 0; term < 2; ++term)
+                        *reinterpret_cast<uint2*>(sm + G::kQR + sw64_offset(term * NR + r, (lane & 7) * 8)) = y[term];
+                }
+            }
+            ++pieces;
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sw->q_full);
+            if (lane == 0 && ok) mbar_arrive(&sw->q_full);
         };
         announce();
         soft_sync();
@@ -453,6 +516,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             soft_sync();
         }
         while (ok && more) {
+            announce();                       // all have read this piece's
             // this thread's cached row in tile x: its page, and its scale byte (0, the lowest, where there is none: such a
             // row reads as zeros and sets no reference)
             auto page_of = [&](int x) -> int {
@@ -532,7 +596,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                             sw->move[h0 + i] = n - m;
                         }
                         half_sync(half);
-                        if (j > 0) ok = ok && wait_warp(&sw->pv_done[prev.slot], prev.phase);
+                        if (j > 0) ok = ok && wait_warp(&sw->pv_done, (tile - 1) & 1);
                         tc_fence_after();
 #pragma unroll
                         for (int c = 0; c < NH; c += 8) {
@@ -602,10 +666,10 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                             *reinterpret_cast<uint4*>(sm + G::kSliceAt + slice.slot * 16384 + (valid + (i >> 3)) * 128 + (i & 7) * 16) =
                                 make_uint4(0, 0, 0, 0);
                 }
-                // this weight buffer was read by the products of two tiles ago
-                if (sb.slot ? used1 : used0) ok = ok && wait_warp(&sw->pv_done[sb.slot], sb.phase ^ 1u);
+                // the weights before these have been read
+                if (tile > 0) ok = ok && wait_warp(&sw->pv_done, (tile - 1) & 1);
                 if (ok) {
-                    uint8_t* pt = sm + G::kP + sb.slot * 2 * G::kPTile;
+                    uint8_t* pt = sm + G::kP;
 #pragma unroll
                     for (int term = 0; term < 2; ++term)
 #pragma unroll
@@ -621,7 +685,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(&sw->p_full[sb.slot]);
+                if (lane == 0 && ok) mbar_arrive(&sw->p_full);
                 const float2 back = make_float2(two_to(-e), two_to(-e));
 #pragma unroll
                 for (int i = 0; i < NH; i += 2) {
@@ -629,8 +693,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                     l[i] = v.x;
                     l[i + 1] = v.y;
                 }
-                if (sb.slot) used1 = true; else used0 = true;
-                prev = sb;
+                ++tile;
                 sb.next();
                 in.next(); in.next(); in.next(); in.next();
             }
@@ -650,7 +713,6 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             float* po = reinterpret_cast<float*>(ws + Work<NR>::o_at(gridDim.x));
             const float sum = reduce_rows<NH>(l, [](float p, float q) { return p + q; });
             if (lane % (32 / NH) == 0) sw->red[half][w][lane / (32 / NH)] = sum;
-            announce();
             soft_sync();
             if (t < NR) {
                 const float* part = &sw->red[t / NH][0][t % NH];
@@ -673,7 +735,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             more = sw->more;
             const Piece next{sw->piece[0], sw->piece[1], sw->piece[2], sw->piece[3], sw->piece[4]};
             if (more) take_queries(next);
-            ok = soft_and(wait_warp(&sw->pv_done[prev.slot], prev.phase));
+            ok = soft_and(wait_warp(&sw->pv_done, (tile - 1) & 1));
             if (!ok) break;
             tc_fence_after();
             // column r of block b: row r, channels 128 b ..; a lane stores its channel of 8 rows at a time, so a
@@ -720,15 +782,16 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
     if (warp == 3) tmem_dealloc(tb, G::kCols);
 }
 
-// [rows, width] bytes, boxes of `channels` x box_rows, swizzled over the box's row.
-bool map_rows_2d(CUtensorMap* m, const void* base, int64_t rows, int width, int channels, int box_rows) {
+// [rows, width] elements of 2 or 1 bytes, boxes of `channels` x box_rows, swizzled over the box's row.
+bool map_rows_2d(CUtensorMap* m, const void* base, int bytes, int64_t rows, int width, int channels, int box_rows) {
     const auto fn = encode();
     if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width};
+    cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width * bytes};
     cuuint32_t box[2] = {(cuuint32_t)channels, (cuuint32_t)box_rows}, es[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              channels == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(m, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
+              strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              channels * bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int NR, bool ROPE>
@@ -740,7 +803,8 @@ cudaError_t launch(const LatentDecodeArgs& a, cudaStream_t s) {
     const int64_t c_rows = a.c.num_pages > 0 ? (int64_t)a.c.num_pages * a.c.page_size : 1;
     const void* c_base = a.c.num_pages > 0 ? a.c.cache : a.workspace;
     Maps maps;
-    if (!map_rows_2d(&maps.c, c_base, c_rows, width, 128, box) || !map_rows_2d(&maps.r, c_base, c_rows, width, kRope, box))
+    if (!map_rows_2d(&maps.q, a.q_latent, 2, (int64_t)a.num_seqs * R, kLatent, 64, NR) ||
+        !map_rows_2d(&maps.c, c_base, 1, c_rows, width, 128, box) || !map_rows_2d(&maps.r, c_base, 1, c_rows, width, kRope, box))
         return cudaErrorInvalidValue;
     static std::atomic<bool> ready[64];
     int dev = 0;

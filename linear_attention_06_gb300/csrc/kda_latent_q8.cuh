@@ -42,19 +42,38 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
     return to_e4m3x2(a, b) | (to_e4m3x2(c, d) << 16);
 }
-__device__ __forceinline__ uint32_t to_e5m2x2(float lo, float hi) {
+// The same steps through fp16, two numbers a word.
+__device__ __forceinline__ uint32_t to_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16_to_e4m3x2(uint32_t x) {
     uint16_t r;
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16_to_e5m2x2(uint32_t x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
     return r;
 }
 // Two e4m3 numbers (the low 16 bits), exactly.
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t x) {
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t x) {
     uint32_t h;
-    float2 f;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)x));
+    return h;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t x) {
+    float2 f;
     asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
         : "=f"(f.x), "=f"(f.y)
-        : "r"(h));
+        : "r"(e4m3_to_f16x2(x)));
     return f;
 }
 
