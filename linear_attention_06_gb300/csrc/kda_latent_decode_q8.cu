@@ -53,7 +53,7 @@ constexpr int kBar = 1;                       // named barriers: the softmax war
 constexpr int kShort = 3;                     // sequences of at most so many tiles are not cut (find_run)
 // log2 of a tile's largest weight: where a piece's first tile is put, the bounds, and where a tile beyond one of them is
 // put: near that bound, so that tiles as they were before stay inside the range.
-constexpr float kSet = 1.f, kHigh = 8.75f, kHighSet = 8.f, kLow = -5.f, kLowSet = -2.f;
+constexpr float kSet = -1.f, kHigh = 8.75f, kHighSet = 8.f, kLow = -5.f, kLowSet = -2.f;
 constexpr float kDeep = 30.f;                 // log2 of how far a reference may lie below the highest before it
 
 // Shared memory of a block with NR query rows: queries [slice][2 NR][128 bytes], their rope slice [2 NR][64], weights
@@ -450,7 +450,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                     for (int d = 1; d < 8; d *= 2) rope_most[k] = max(rope_most[k], __shfl_xor_sync(0xffffffffu, rope_most[k], d));
                 }
             }
-#pragma unroll 1
+#pragma unroll 2
             for (int i = 0; i < NR / 8; ++i) {
                 const int r = warp - 4 + 8 * i;
                 uint4 x[2];
@@ -535,6 +535,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             const int least = p.len - a.tokens_per_seq + 1 + group * NR / a.H;      // tokens that the first row sees
 
             uint8_t byte = byte_of(p.off, page);
+            uint32_t faint = 0;               // rows whose tile before was below the range
+            bool lower = false;               // some row's two tiles before were
             float l[NH];
 #pragma unroll
             for (int i = 0; i < NH; ++i) l[i] = 0.f;
@@ -551,7 +553,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 constexpr int N = NH < 16 ? NH : 16;                 // rows a step
                 float x[NH];                  // the weights
                 uint32_t y[2][NH / 4];        // in 8 bits, both terms
-                bool move = j == 0;           // references have to move: a piece's first tile sets them
+                bool move = j == 0 || lower;  // references have to move: a piece's first tile sets them
+                bool voted = false, stop = false;
                 for (;;) {
 #pragma unroll
                     for (int c = 0; c < NH; c += N) {                // log2 of the weights
@@ -624,6 +627,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                             }
                         }
                         tmem_wait_st();
+                        faint = 0;
+                        lower = false;
                     }
                     float most = x[0];
                     uint32_t bright = 0;      // a bit a row: this token's weight is 2^kLow or more
@@ -638,14 +643,16 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                         y[0][i / 4] = i & 2 ? y[0][i / 4] | y1 << 16 : y1;
                         y[1][i / 4] = i & 2 ? y[1][i / 4] | y2 << 16 : y2;
                     }
-                    if (move) break;
+                    if (j == 0 || voted) break;
                     // e4m3 numbers of 2^-5 or more have one of the bits 0x70
 #pragma unroll
                     for (int i = 0; i < NH / 4; ++i) bright |= (((y[0][i] & 0x70707070u) + 0x70707070u) & 0x80808080u) >> i;
                     bright = __reduce_or_sync(0xffffffffu, bright);
                     const bool high = __any_sync(0xffffffffu, most > kHigh);
                     if (lane == 0) sw->vote[j & 1][warp - 4] = make_uint2(bright, high);
-                    if (soft_or(!ok)) { ok = false; break; }
+                    // once a tile, by both halves, whatever their references do: the barrier is all softmax warps'
+                    if (soft_or(!ok)) { stop = true; break; }
+                    voted = true;
                     uint32_t all_bright = 0, any_high = 0;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -654,10 +661,14 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                         any_high |= v.y;
                     }
                     constexpr uint32_t kAll = NH == 32 ? 0xffffffffu : NH == 16 ? 0xf0f0f0f0u : 0xc0c0c0c0u;
-                    if (!any_high && all_bright == kAll) break;
+                    if (!any_high) {
+                        lower = faint & ~all_bright & kAll;
+                        faint = ~all_bright;
+                        break;
+                    }
                     move = true;              // once more from the scores
                 }
-                if (!ok && !move) break;
+                if (stop) { ok = false; break; }
                 if (len - base < kRows) {                  // the tile's rows behind the sequence's end become zeros
                     const int valid = len - base < 0 ? 0 : len - base;
                     Ring<G::kSlices> slice = in;
