@@ -47,9 +47,11 @@ using namespace latent;
 using namespace sm103;
 
 constexpr int kRows = 128;                    // cached rows a tile
-constexpr int kThreads = 384;                 // warps 0-3: producer, issuer, -, (TMEM); warps 4-11: softmax
-constexpr int kSoft = 256;
-constexpr int kBar = 1;                       // named barriers: the softmax warps; each half of them (2, 3)
+// Softmax warps work in teams of four (a warp for each quarter of a tile's tokens), the rows shared by the teams.
+constexpr int teams_of(int nr) { return nr >= 64 ? 4 : 2; }
+constexpr int soft_of(int nr) { return 128 * teams_of(nr); }
+constexpr int threads_of(int nr) { return 128 + soft_of(nr); }       // before them: producer, issuer, queries, (TMEM)
+constexpr int kBar = 1;                       // named barriers: all softmax warps; behind it one for each team
 constexpr int kShort = 3;                     // sequences of at most so many tiles are not cut (find_run)
 // log2 of a tile's largest weight: where a piece's first tile is put, the bounds, and where a tile beyond one of them is
 // put: near that bound, so that tiles as they were before stay inside the range.
@@ -82,18 +84,19 @@ struct Small : Line {
     uint64_t o_free, drain;
     uint32_t tmem;
     int piece[5], more;                       // the softmax warps' piece
-    alignas(16) uint2 vote[2][8];             // a tile's votes, a warp each: rows that are bright enough; any too large
+    alignas(16) uint2 vote[2][16];            // a tile's votes, a warp each: rows that are bright enough; any too large
     alignas(16) float ref[64], top[64];       // -m_r, and the highest m_r has been
     alignas(16) float move[64];               // by how much m_r moves; at a piece's end O's factor
     alignas(16) float unit[64];               // scale log2(e) 2^k of the query row
     alignas(16) int seen[64];                 // tokens that the row sees
-    alignas(16) float red[2][4][32];          // a half's, a warp's: maxima, sums
+    alignas(16) float red[4][4][16];          // a team's, a warp's: maxima, sums
 };
 static_assert(sizeof(Small) <= 3072, "small area");
 
 using Walk = WalkOf<kRows>;
 
 // OR and AND of a predicate over the softmax warps; also a barrier between them.
+template <int SOFT>
 __device__ __forceinline__ bool soft_or(bool pred) {
     uint32_t r;
     asm volatile(
@@ -102,13 +105,15 @@ __device__ __forceinline__ bool soft_or(bool pred) {
         "bar.red.or.pred p, %2, %3, q;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)pred), "n"(kBar), "n"(kSoft)
+        : "r"((uint32_t)pred), "n"(kBar), "n"(SOFT)
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ bool soft_and(bool pred) { return !soft_or(!pred); }
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kSoft) : "memory"); }
-__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, %1;" ::"r"(kBar + 1 + half), "n"(kSoft / 2) : "memory"); }
+template <int SOFT>
+__device__ __forceinline__ bool soft_and(bool pred) { return !soft_or<SOFT>(!pred); }
+template <int SOFT>
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(SOFT) : "memory"); }
+__device__ __forceinline__ void team_sync(int team) { asm volatile("bar.sync %0, 128;" ::"r"(kBar + 1 + team) : "memory"); }
 
 // N consecutive 32-bit columns of the warp's lanes.
 template <int N>
@@ -169,10 +174,11 @@ struct Maps {
 };
 
 template <int NR, bool ROPE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(NR), 1)
 latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a, const int groups, const int map_rows) {
     using G = Cfg<NR, ROPE>;
-    constexpr int NH = NR / 2;                // rows of a half of the softmax warps
+    constexpr int kTeams = teams_of(NR), kSoft = soft_of(NR), kThreads = threads_of(NR), kWarps = kSoft / 32;
+    constexpr int NH = NR / kTeams;           // rows of a team
     extern __shared__ __align__(1024) uint8_t sm[];   // swizzled tiles start at multiples of 1024 bytes
     if (smem_u32(sm) & 1023u) {               // the declaration's alignment
         if (threadIdx.x == 0) atomicOr(a.status, kStatusTimeout);
@@ -194,12 +200,12 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             mbar_init(&sw->rope_empty[i], 1);
             mbar_init(&sw->s_full[i], 1);
         }
-        mbar_init(&sw->p_full, 8);
+        mbar_init(&sw->p_full, kWarps);
         mbar_init(&sw->pv_done, 1);
         mbar_init(&sw->raw_full, 1);
-        mbar_init(&sw->q_full, 8);
+        mbar_init(&sw->q_full, kWarps);
         mbar_init(&sw->q_empty, 1);
-        mbar_init(&sw->o_free, 8);
+        mbar_init(&sw->o_free, kWarps);
         mbar_init(&sw->drain, 1);
         fence_mbar_init();
         tma_prefetch_desc(&maps.q);
@@ -401,10 +407,10 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
         }
         if (seg > 0 && lane == 0) mbar_wait_bounded(&sw->raw_full, (seg - 1) & 1, kWaitNs);   // landed, whatever the others do
     } else if (warp >= 4) {                   // ------------------------------------------------ softmax
-        const int w = (warp - 4) & 3, half = (warp - 4) >> 2, t = tid - (kThreads - kSoft);
+        const int w = (warp - 4) & 3, team = (warp - 4) >> 2, t = tid - (kThreads - kSoft);
         const int tok = 32 * w + lane;        // this thread's token of a tile; its rows are h0 .. h0 + NH - 1
-        const int h0 = half * NH;
-        const uint32_t lanes = tmem_addr(tb, 32 * w, h0);            // O^T: columns of this half
+        const int h0 = team * NH;
+        const uint32_t lanes = tmem_addr(tb, 32 * w, h0);            // O^T: columns of this team
         const uint32_t s_lanes = tmem_addr(ts, 32 * w, h0);
         Walk walk(sw);
         Piece p{};
@@ -425,34 +431,28 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
         };
         // A piece's queries in 8 bits, a warp a row.  The 128 bytes of channels 128 k .. 128 k + 63 of a row in bf16 lie
         // where the row's first terms of slice k go, those of the next 64 where its second terms go: in place.  The rope
-        // part (four rows a word of a warp) goes through registers.  The loop is not unrolled: it runs once a piece, and
+        // part (a lane has a part of one of its warp's rows) goes through registers.  The loop is not unrolled: it runs once a piece, and
         // its instructions have to be fetched (unrolled, 3400 cycles of a block's start).
         auto take_queries = [&](const Piece& p) {
-            constexpr int kSets = NR == 64 ? 2 : 1;                  // of four rows
-            uint4 rope[kSets];
-            uint32_t rope_most[kSets];
-            int rope_power[kSets];
+            constexpr int kMine = NR / kWarps;                       // rows of a warp
+            static_assert(kMine <= 4, "a lane has one part of a row");
+            const int rope_row = warp - 4 + kWarps * (lane >> 3);
+            uint4 rope = make_uint4(0, 0, 0, 0);
+            uint32_t rope_most = 0;
+            int rope_power = 0;
             if constexpr (ROPE) {
-#pragma unroll
-                for (int k = 0; k < kSets; ++k) {
-                    const int r = warp - 4 + 8 * (4 * k + (lane >> 3));
-                    const int64_t q = (int64_t)p.n * R + group * NR + r;
-                    rope[k] = make_uint4(0, 0, 0, 0);
-                    if (r < rows && KDA_INDEX_OK(q, (int64_t)a.num_seqs * R, a.status))
-                        rope[k] = __ldcg(static_cast<const uint4*>(a.q_rope) + q * (kRope / 8) + (lane & 7));
-                }
+                const int64_t q = (int64_t)p.n * R + group * NR + rope_row;
+                if (rope_row < rows && KDA_INDEX_OK(q, (int64_t)a.num_seqs * R, a.status))
+                    rope = __ldcg(static_cast<const uint4*>(a.q_rope) + q * (kRope / 8) + (lane & 7));
             }
             ok = ok && wait_warp(&sw->raw_full, pieces & 1);
             if constexpr (ROPE) {
-#pragma unroll
-                for (int k = 0; k < kSets; ++k) {
-                    rope_most[k] = largest(rope[k]);
-                    for (int d = 1; d < 8; d *= 2) rope_most[k] = max(rope_most[k], __shfl_xor_sync(0xffffffffu, rope_most[k], d));
-                }
+                rope_most = largest(rope);
+                for (int d = 1; d < 8; d *= 2) rope_most = max(rope_most, __shfl_xor_sync(0xffffffffu, rope_most, d));
             }
-#pragma unroll 2
-            for (int i = 0; i < NR / 8; ++i) {
-                const int r = warp - 4 + 8 * i;
+#pragma unroll 1
+            for (int i = 0; i < kMine; ++i) {
+                const int r = warp - 4 + kWarps * i;
                 uint4 x[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -460,18 +460,9 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                     if (r >= rows) x[c] = make_uint4(0, 0, 0, 0);
                 }
                 uint32_t most = max(largest(x[0]), largest(x[1]));
-                if constexpr (ROPE) {
-                    uint32_t other = __shfl_sync(0xffffffffu, rope_most[0], (i & 3) * 8);
-                    if (kSets > 1 && i >= 4) other = __shfl_sync(0xffffffffu, rope_most[kSets - 1], (i & 3) * 8);
-                    most = max(most, other);
-                }
+                if constexpr (ROPE) most = max(most, __shfl_sync(0xffffffffu, rope_most, i * 8));
                 const int k = power_for(__reduce_max_sync(0xffffffffu, most));           // also: all lanes have read the row
-                if constexpr (ROPE) {
-                    if ((lane >> 3) == (i & 3)) {
-                        if (i < 4) rope_power[0] = k;
-                        else rope_power[kSets - 1] = k;
-                    }
-                }
+                if ((lane >> 3) == i) rope_power = k;
                 __syncwarp();
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -490,17 +481,12 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                     sw->top[r] = -INFINITY;
                 }
             }
-            if constexpr (ROPE) {
+            if (ROPE && rope_row < NR) {
+                uint2 y[2];
+                two_terms(rope, two_to(-rope_power), y);
 #pragma unroll
-                for (int k = 0; k < kSets; ++k) {
-                    const int r = warp - 4 + 8 * (4 * k + (lane >> 3));
-                    if (r >= NR) continue;
-                    uint2 y[2];
-                    two_terms(rope[k], two_to(-rope_power[k]), y);
-#pragma unroll
-                    for (int term = 0; term < 2; ++term)
-                        *reinterpret_cast<uint2*>(sm + G::kQR + sw64_offset(term * NR + r, (lane & 7) * 8)) = y[term];
-                }
+                for (int term = 0; term < 2; ++term)
+                    *reinterpret_cast<uint2*>(sm + G::kQR + sw64_offset(term * NR + rope_row, (lane & 7) * 8)) = y[term];
             }
             ++pieces;
             fence_proxy_async_smem();
@@ -508,12 +494,12 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             if (lane == 0 && ok) mbar_arrive(&sw->q_full);
         };
         announce();
-        soft_sync();
+        soft_sync<kSoft>();
         bool more = sw->more;
         if (more) {
             p = Piece{sw->piece[0], sw->piece[1], sw->piece[2], sw->piece[3], sw->piece[4]};
             take_queries(p);
-            soft_sync();
+            soft_sync<kSoft>();
         }
         while (ok && more) {
             announce();                       // all have read this piece's
@@ -550,7 +536,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 ok = ok && wait_warp(&sw->s_full[sb.slot], sb.phase);
                 tc_fence_after();
                 const float2 two_e = make_float2(two_to(e), two_to(e)), fe = make_float2((float)e, (float)e);
-                constexpr int N = NH < 16 ? NH : 16;                 // rows a step
+                constexpr int N = NH;                                // rows a step
                 float x[NH];                  // the weights
                 uint32_t y[2][NH / 4];        // in 8 bits, both terms
                 bool move = j == 0 || lower;  // references have to move: a piece's first tile sets them
@@ -578,17 +564,17 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                         for (int i = 0; i < NH; ++i)
                             if (base + tok >= sw->seen[h0 + i]) x[i] = -INFINITY;
                     }
-                    if (move) {               // this half of the warps agrees
+                    if (move) {               // the team agrees
                         float v[NH];
 #pragma unroll
                         for (int i = 0; i < NH; ++i) v[i] = x[i];
                         const float mx = reduce_rows<NH>(v, [](float p, float q) { return fmaxf(p, q); });
-                        if (lane % (32 / NH) == 0) sw->red[half][w][lane / (32 / NH)] = mx;
-                        half_sync(half);
+                        if (lane % (32 / NH) == 0) sw->red[team][w][lane / (32 / NH)] = mx;
+                        team_sync(team);
                         const int i = t & 127;
                         if (i < NH) {
-                            const float z = fmaxf(fmaxf(sw->red[half][0][i], sw->red[half][1][i]),
-                                                  fmaxf(sw->red[half][2][i], sw->red[half][3][i]));
+                            const float z = fmaxf(fmaxf(sw->red[team][0][i], sw->red[team][1][i]),
+                                                  fmaxf(sw->red[team][2][i], sw->red[team][3][i]));
                             const float m = -sw->ref[h0 + i], top = sw->top[h0 + i];
                             float n = m;
                             if (z > -INFINITY && (j == 0 || z > kHigh || z < kLow)) {
@@ -598,7 +584,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                             }
                             sw->move[h0 + i] = n - m;
                         }
-                        half_sync(half);
+                        team_sync(team);
                         if (j > 0) ok = ok && wait_warp(&sw->pv_done, (tile - 1) & 1);
                         tc_fence_after();
 #pragma unroll
@@ -650,17 +636,17 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                     bright = __reduce_or_sync(0xffffffffu, bright);
                     const bool high = __any_sync(0xffffffffu, most > kHigh);
                     if (lane == 0) sw->vote[j & 1][warp - 4] = make_uint2(bright, high);
-                    // once a tile, by both halves, whatever their references do: the barrier is all softmax warps'
-                    if (soft_or(!ok)) { stop = true; break; }
+                    // once a tile, by all teams, whatever their references do: the barrier is all softmax warps'
+                    if (soft_or<kSoft>(!ok)) { stop = true; break; }
                     voted = true;
                     uint32_t all_bright = 0, any_high = 0;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint2 v = sw->vote[j & 1][half * 4 + k];
+                        const uint2 v = sw->vote[j & 1][team * 4 + k];
                         all_bright |= v.x;
                         any_high |= v.y;
                     }
-                    constexpr uint32_t kAll = NH == 32 ? 0xffffffffu : NH == 16 ? 0xf0f0f0f0u : 0xc0c0c0c0u;
+                    constexpr uint32_t kAll = NH == 16 ? 0xf0f0f0f0u : 0xc0c0c0c0u;
                     if (!any_high) {
                         lower = faint & ~all_bright & kAll;
                         faint = ~all_bright;
@@ -708,7 +694,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 sb.next();
                 in.next(); in.next(); in.next(); in.next();
             }
-            if (!soft_and(ok)) { ok = false; break; }
+            if (!soft_and<kSoft>(ok)) { ok = false; break; }
             // ---- the piece is done: its rows' sums, then O^T out of tensor memory
             const bool whole = is_whole(p);
             const int slot = blockIdx.x * 2 + (first_piece ? 0 : 1);
@@ -723,11 +709,11 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             float2* ml = reinterpret_cast<float2*>(ws + Work<NR>::ml_at(gridDim.x));
             float* po = reinterpret_cast<float*>(ws + Work<NR>::o_at(gridDim.x));
             const float sum = reduce_rows<NH>(l, [](float p, float q) { return p + q; });
-            if (lane % (32 / NH) == 0) sw->red[half][w][lane / (32 / NH)] = sum;
-            soft_sync();
+            if (lane % (32 / NH) == 0) sw->red[team][w][lane / (32 / NH)] = sum;
+            soft_sync<kSoft>();
             if (t < NR) {
                 const float* part = &sw->red[t / NH][0][t % NH];
-                const float total = (part[0] + part[32]) + (part[64] + part[96]);
+                const float total = (part[0] + part[16]) + (part[32] + part[48]);
                 // total 2^m = f 2^k, f in [1, 2): no large m against a large logarithm, here and in the join
                 const int power = (int)(__float_as_uint(total) >> 23) - 127;
                 const float f = total == 0.f ? 0.f : total * two_to(-power), k = total == 0.f ? -INFINITY : (float)power - sw->ref[t];
@@ -740,13 +726,13 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 }
                 sw->move[t] = total == 0.f ? 0.f : (whole ? 1.f / total : two_to(-power));
             }
-            soft_sync();
+            soft_sync<kSoft>();
             // the next piece's queries while this one's last products run (those with the queries are done: their S has
             // been read); its first scores are then computed while this piece's result is written
             more = sw->more;
             const Piece next{sw->piece[0], sw->piece[1], sw->piece[2], sw->piece[3], sw->piece[4]};
             if (more) take_queries(next);
-            ok = soft_and(wait_warp(&sw->pv_done, (tile - 1) & 1));
+            ok = soft_and<kSoft>(wait_warp(&sw->pv_done, (tile - 1) & 1));
             if (!ok) break;
             tc_fence_after();
             // column r of block b: row r, channels 128 b ..; a lane stores its channel of 8 rows at a time, so a
@@ -778,7 +764,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             }
             tc_fence_before();
             // everyone has read the sums before the next piece writes them
-            soft_sync();
+            soft_sync<kSoft>();
             if (lane == 0) mbar_arrive(&sw->o_free);
             at += p.tiles + kStart;
             p = next;
@@ -826,7 +812,7 @@ cudaError_t launch(const LatentDecodeArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
-    const cudaError_t e = launch_overlapped(latent_decode_q8_kernel<NR, ROPE>, grid, kThreads, G::kBytes, s, maps, a, groups,
+    const cudaError_t e = launch_overlapped(latent_decode_q8_kernel<NR, ROPE>, grid, threads_of(NR), G::kBytes, s, maps, a, groups,
                                             (int)c_rows);
     return e != cudaSuccess ? e : launch_overlapped(latent_join_kernel<NR>, kJoinBlocks, kJoinThreads, 0, s, a, grid, groups);
 }

@@ -10,6 +10,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kda_internal.h"
 #include "kda_latent_common.cuh"
 #include "kda_latent_runs.h"
@@ -148,7 +150,7 @@ __device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Line* sw, i
 // warps every eighth piece, in one round of loads for a sequence over the whole card: the rounds' latency is all that
 // such a join takes (9000 cycles in three rounds, 41.5 us of a call; 6400 in one).
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kFewParts = 32, kMostParts = 256, kMostGrid = kJoinThreads,
-              kJoinBlocks = 5 * kSMs, kBatch = 20;
+              kJoinBlocks = 2 * kSMs, kBatch = 20;
 template <int NR>
 __global__ void __launch_bounds__(kJoinThreads, 2) latent_join_kernel(const LatentDecodeArgs a, const int grid, const int groups) {
     __shared__ Head heads_s[kMostGrid];
@@ -200,7 +202,6 @@ __global__ void __launch_bounds__(kJoinThreads, 2) latent_join_kernel(const Late
         return x;
     };
     auto slot = [&](const Task& x, int i) { return ((int64_t)(x.block + i * groups) * 2 + (i == 0 ? x.h.first_slot : 0)) * NR + x.r; };
-    auto part = [&](const Task& x, int i) { return po[slot(x, i) * (kLatent / 4) + x.side * 32 + lane]; };
     auto part2 = [&](const Task& x, int i) {
         return reinterpret_cast<const float2*>(po)[slot(x, i) * (kLatent / 2) + x.side * 32 + lane];
     };
@@ -211,41 +212,58 @@ __global__ void __launch_bounds__(kJoinThreads, 2) latent_join_kernel(const Late
     auto add = [](float4& acc, float w, float4 x) {
         acc.x += w * x.x; acc.y += w * x.y; acc.z += w * x.z; acc.w += w * x.w;
     };
-    for (int t = blockIdx.x * kJoinWarps + warp; t < count[0] * NR * 4; t += gridDim.x * kJoinWarps) {
-        const Task x = task(0, t);
-        if (!x.live) continue;
-        const float2 y = lane < x.h.parts ? ml[slot(x, lane)] : make_float2(-INFINITY, 0.f);
-        float4 o[8];                          // the first loads go out before the weights are known
+    // The few pieces of a sequence's row: QUARTERS quarters of it, BATCH pieces' loads in flight; the same sums in the same
+    // order for every split.
+    auto join_few = [&](auto quarters_c, auto batch_c) {
+        constexpr int QUARTERS = decltype(quarters_c)::value, BATCH = decltype(batch_c)::value;
+        for (int t = blockIdx.x * kJoinWarps + warp; t < count[0] * NR * 4 / QUARTERS; t += gridDim.x * kJoinWarps) {
+            const Task x = task(0, t * QUARTERS);
+            if (!x.live) continue;
+            const float2 y = lane < x.h.parts ? ml[slot(x, lane)] : make_float2(-INFINITY, 0.f);
+            float4 o[BATCH][QUARTERS], acc[QUARTERS];
+            auto load = [&](int i) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < x.h.parts) o[k] = part(x, k);
-        float mx = y.x;
-        for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        const float w = y.x == -INFINITY ? 0.f : exp2_fast(y.x - mx);
-        float total = w * y.y;
-        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < x.h.parts; i += 8) {
-            if (i > 0) {
+                for (int k = 0; k < BATCH; ++k)
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (i + k < x.h.parts) o[k] = part(x, i + k);
+                    for (int q = 0; q < QUARTERS; ++q)
+                        if (i + k < x.h.parts) o[k][q] = po[slot(x, i + k) * (kLatent / 4) + (x.side + q) * 32 + lane];
+            };
+            load(0);                          // the first loads go out before the weights are known
+            float mx = y.x;
+            for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float w = y.x == -INFINITY ? 0.f : exp2_fast(y.x - mx);
+            float total = w * y.y;
+            for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+#pragma unroll
+            for (int q = 0; q < QUARTERS; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < x.h.parts; i += BATCH) {
+                if (i > 0) load(i);
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const float wk = __shfl_sync(0xffffffffu, w, (i + k) & 31);
+#pragma unroll
+                    for (int q = 0; q < QUARTERS; ++q)
+                        if (i + k < x.h.parts) add(acc[q], wk, o[k][q]);
+                }
             }
+            if (KDA_INDEX_OK(x.row, (int64_t)a.num_seqs * R, a.status)) {
+                const float f = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, w, (i + k) & 31);
-                if (i + k < x.h.parts) add(acc, wk, o[k]);
+                for (int q = 0; q < QUARTERS; ++q) {
+                    uint2 v;
+                    v.x = pack_bf16x2(acc[q].x * f, acc[q].y * f);
+                    v.y = pack_bf16x2(acc[q].z * f, acc[q].w * f);
+                    reinterpret_cast<uint2*>(a.out)[x.row * (kLatent / 4) + (x.side + q) * 32 + lane] = v;
+                }
+                store_lse(x, mx, total);
             }
         }
-        if (KDA_INDEX_OK(x.row, (int64_t)a.num_seqs * R, a.status)) {
-            const float f = total == 0.f ? 0.f : 1.f / total;
-            uint2 v;
-            v.x = pack_bf16x2(acc.x * f, acc.y * f);
-            v.y = pack_bf16x2(acc.z * f, acc.w * f);
-            reinterpret_cast<uint2*>(a.out)[x.row * (kLatent / 4) + x.side * 32 + lane] = v;
-            store_lse(x, mx, total);
-        }
-    }
+    };
+    using std::integral_constant;
+    if (count[0] * NR * 4 <= (int)gridDim.x * kJoinWarps)
+        join_few(integral_constant<int, 1>(), integral_constant<int, 8>());
+    else                                      // more quarter rows than warps: whole rows, in one round of loads for four pieces
+        join_few(integral_constant<int, 4>(), integral_constant<int, 4>());
     for (int t = blockIdx.x; t < count[1] * NR * 8; t += gridDim.x) {
         const Task x = task(1, t);
         if (!x.live) continue;                // uniform
