@@ -176,18 +176,20 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const LatentGatherArgs
         const int i = tid + k * kThreads, j = i / CHUNKS, c = i % CHUNKS;
         if (i >= ROWS * CHUNKS || row_s[j] < -1) continue;
         const float f = scale_s[j];
-        uint4 y;
-        uint32_t* yi = reinterpret_cast<uint32_t*>(&y);
+        uint32_t y[4];
+        e4m3x4_to_f16(x[k].x, y[0], y[1]);
+        e4m3x4_to_f16(x[k].y, y[2], y[3]);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            const float2 v = from_e4m3x2((h & 2 ? x[k].y : x[k].x) >> (16 * (h & 1)));
+            const float2 v = f16x2_to_floats(y[h]);
             const __nv_bfloat162 b = __floats2bfloat162_rn(v.x * f, v.y * f);                 // exact
-            yi[h] = *reinterpret_cast<const uint32_t*>(&b);
+            y[h] = *reinterpret_cast<const uint32_t*>(&b);
         }
+        const uint4 row = make_uint4(y[0], y[1], y[2], y[3]);
         if (c < kLat)
-            static_cast<uint4*>(a.latent)[(t0 + j) * kLat + c] = y;
+            static_cast<uint4*>(a.latent)[(t0 + j) * kLat + c] = row;
         else
-            static_cast<uint4*>(a.k_rope)[(t0 + j) * (CHUNKS - kLat) + c - kLat] = y;
+            static_cast<uint4*>(a.k_rope)[(t0 + j) * (CHUNKS - kLat) + c - kLat] = row;
     }
 }
 

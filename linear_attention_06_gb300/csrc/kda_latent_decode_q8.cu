@@ -145,28 +145,22 @@ __device__ __forceinline__ float reduce_rows(float (&v)[N], const Op& op) {
 __device__ __forceinline__ float2 pair(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
 // The largest magnitude's bits among eight bf16 numbers, as fp32.
 __device__ __forceinline__ uint32_t largest(const uint4& v) {
-    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max(x[i] << 16 & 0x7fff0000u, x[i] & 0x7fff0000u));
-    return m;
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs), __vmaxu2(v.z & kAbs, v.w & kAbs));
+    return max(m << 16, m & 0xffff0000u);
 }
 // Eight bf16 numbers times f as the sum of two e4m3 numbers each.
 __device__ __forceinline__ void two_terms(const uint4& v, float f, uint2 (&y)[2]) {
     const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-    uint32_t a[4], b[4];
+    uint32_t h[4], b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t h = to_f16x2(__uint_as_float(x[i] << 16) * f, __uint_as_float(x[i] & 0xffff0000u) * f);
-        a[i] = f16_to_e4m3x2(h);
-        b[i] = f16_to_e4m3x2(sub_f16x2(h, e4m3_to_f16x2(a[i])));
-    }
-    y[0] = make_uint2(a[0] | a[1] << 16, a[2] | a[3] << 16);
-    y[1] = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
-}
-// What e4m3 leaves of two weights, as e5m2 (fp16 holds 11 bits of a weight, the difference is exact).
-__device__ __forceinline__ uint32_t rest_e5m2x2(float lo, float hi, uint32_t e4m3) {
-    return f16_to_e5m2x2(sub_f16x2(to_f16x2(lo, hi), e4m3_to_f16x2(e4m3)));
+    for (int i = 0; i < 4; ++i) h[i] = to_f16x2(__uint_as_float(x[i] << 16) * f, __uint_as_float(x[i] & 0xffff0000u) * f);
+    y[0] = make_uint2(f16_to_e4m3x4(h[0], h[1]), f16_to_e4m3x4(h[2], h[3]));
+    e4m3x4_to_f16(y[0].x, b[0], b[1]);
+    e4m3x4_to_f16(y[0].y, b[2], b[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = sub_f16x2(h[i], b[i]);
+    y[1] = make_uint2(f16_to_e4m3x4(b[0], b[1]), f16_to_e4m3x4(b[2], b[3]));
 }
 
 struct Maps {
@@ -445,6 +439,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 if (rope_row < rows && KDA_INDEX_OK(q, (int64_t)a.num_seqs * R, a.status))
                     rope = __ldcg(static_cast<const uint4*>(a.q_rope) + q * (kRope / 8) + (lane & 7));
             }
+            if (t < NR) sw->seen[t] = t < rows ? p.len - a.tokens_per_seq + 1 + (group * NR + t) / a.H : 0;
             ok = ok && wait_warp(&sw->raw_full, pieces & 1);
             if constexpr (ROPE) {
                 rope_most = largest(rope);
@@ -476,7 +471,6 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 }
                 if (lane == 0) {
                     sw->unit[r] = a.scale * 1.44269504088896340736f * two_to(k);
-                    sw->seen[r] = r < rows ? p.len - a.tokens_per_seq + 1 + (group * NR + r) / a.H : 0;
                     sw->ref[r] = 0.f;
                     sw->top[r] = -INFINITY;
                 }
@@ -505,28 +499,29 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             announce();                       // all have read this piece's
             // this thread's cached row in tile x: its page, and its scale byte (0, the lowest, where there is none: such a
             // row reads as zeros and sets no reference)
+            const int64_t entry = (int64_t)p.n * a.c.max_pages;
+            const int len = p.len, off = p.off, tiles = p.tiles;
             auto page_of = [&](int x) -> int {
-                const int64_t pos = (int64_t)x * kRows + tok;
-                if (x >= p.off + p.tiles || pos >= p.len) return -1;
-                const int64_t i = (int64_t)p.n * a.c.max_pages + (pos >> shift);
-                return KDA_INDEX_OK(i, (int64_t)a.num_seqs * a.c.max_pages, a.status) ? a.c.block_table[i] : -1;
+                const uint32_t pos = (uint32_t)x * kRows + tok;      // below 2^31 + 2^9
+                if (pos >= (uint32_t)len) return -1;
+                return KDA_INDEX_OK(entry + (pos >> shift), (int64_t)a.num_seqs * a.c.max_pages, a.status)
+                           ? a.c.block_table[entry + (pos >> shift)] : -1;
             };
             auto byte_of = [&](int x, int page) -> uint8_t {
-                if (page < 0 || page >= a.c.num_pages) return 0;
-                const int64_t i = ((int64_t)page << shift) + ((x * kRows + tok) & (a.c.page_size - 1));
+                if ((uint32_t)page >= (uint32_t)a.c.num_pages) return 0;
+                const int64_t i = (uint32_t)(page << shift) + (((uint32_t)x * kRows + tok) & (uint32_t)(a.c.page_size - 1));
                 return KDA_INDEX_OK(i, (int64_t)a.c.num_pages * a.c.page_size, a.status) ? __ldcg(a.c.scales + i) : 0;
             };
-            const int page = page_of(p.off);
-            int next_page = page_of(p.off + 1);
+            const int page = page_of(off);
+            int next_page = page_of(off + 1);
             const int least = p.len - a.tokens_per_seq + 1 + group * NR / a.H;      // tokens that the first row sees
 
-            uint8_t byte = byte_of(p.off, page);
+            uint8_t byte = byte_of(off, page);
             uint32_t faint = 0;               // rows whose tile before was below the range
             bool lower = false;               // some row's two tiles before were
             float l[NH];
 #pragma unroll
             for (int i = 0; i < NH; ++i) l[i] = 0.f;
-            const int len = p.len, off = p.off, tiles = p.tiles;
             for (int j = 0; j < tiles; ++j) {
                 const int base = (off + j) * kRows;
                 const int e = power_of(byte);
@@ -621,13 +616,13 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
 #pragma unroll
                     for (int i = 1; i < NH; ++i) most = fmaxf(most, x[i]);
 #pragma unroll
-                    for (int i = 0; i < NH; i += 2) {
-                        x[i] = exp2_fast(x[i]);
-                        x[i + 1] = exp2_fast(x[i + 1]);
-                        const uint32_t y1 = to_e4m3x2(x[i], x[i + 1]);
-                        const uint32_t y2 = rest_e5m2x2(x[i], x[i + 1], y1);
-                        y[0][i / 4] = i & 2 ? y[0][i / 4] | y1 << 16 : y1;
-                        y[1][i / 4] = i & 2 ? y[1][i / 4] | y2 << 16 : y2;
+                    for (int i = 0; i < NH; i += 4) {                // (fp16 holds 11 bits of a weight, differences are exact)
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) x[i + n] = exp2_fast(x[i + n]);
+                        uint32_t lo, hi;
+                        y[0][i / 4] = to_e4m3x4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        e4m3x4_to_f16(y[0][i / 4], lo, hi);
+                        y[1][i / 4] = f16_to_e5m2x4(sub_f16x2(to_f16x2(x[i], x[i + 1]), lo), sub_f16x2(to_f16x2(x[i + 2], x[i + 3]), hi));
                     }
                     if (j == 0 || voted) break;
                     // e4m3 numbers of 2^-5 or more have one of the bits 0x70

@@ -33,16 +33,23 @@ __device__ __forceinline__ int power_of(uint8_t byte) {
     return e < kLeastPower ? kLeastPower : (e > kMostPower ? kMostPower : e);
 }
 
-// Two numbers to e4m3, lo in the low byte: to nearest even, beyond 448 to 448.
+// Four numbers to e4m3, a in the low byte: to nearest even, beyond 448 to 448.
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, u;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 u, %4, %3;\n\t"
+        "mov.b32 %0, {l, u};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
-    return to_e4m3x2(a, b) | (to_e4m3x2(c, d) << 16);
-}
-// The same steps through fp16, two numbers a word.
+// The same from and to fp16, two numbers a word.
 __device__ __forceinline__ uint32_t to_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -53,27 +60,40 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t f16_to_e4m3x2(uint32_t x) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+__device__ __forceinline__ uint32_t f16_to_e4m3x4(uint32_t lo, uint32_t hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, u;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 l, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 u, %2;\n\t"
+        "mov.b32 %0, {l, u};\n\t}"
+        : "=r"(r)
+        : "r"(lo), "r"(hi));
     return r;
 }
-__device__ __forceinline__ uint32_t f16_to_e5m2x2(uint32_t x) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+__device__ __forceinline__ uint32_t f16_to_e5m2x4(uint32_t lo, uint32_t hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, u;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 l, %1;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 u, %2;\n\t"
+        "mov.b32 %0, {l, u};\n\t}"
+        : "=r"(r)
+        : "r"(lo), "r"(hi));
     return r;
 }
-// Two e4m3 numbers (the low 16 bits), exactly.
-__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t x) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)x));
-    return h;
+// Four e4m3 numbers, exactly.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, u;\n\t"
+        "mov.b32 {l, u}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
 }
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t x) {
+__device__ __forceinline__ float2 f16x2_to_floats(uint32_t x) {
     float2 f;
     asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
         : "=f"(f.x), "=f"(f.y)
-        : "r"(e4m3_to_f16x2(x)));
+        : "r"(x));
     return f;
 }
 
