@@ -70,7 +70,7 @@ def _start_binding(force: bool):
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     cmd += [x for i in inc for x in ("-isystem", i)] + [src, "-o", os.path.join(BUILD, "latent_binding.so")]
     cmd += [f"-L{p}" for p in cpp_extension.library_paths()]
-    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
     return src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
 
 

@@ -219,7 +219,7 @@ cudaError_t launch_latent_append_q8(const LatentAppendArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_latent_gather_q8(const LatentGatherArgs& a, cudaStream_t s) {
-    return a.total_tokens < 8192 ? gather<4>(a, false, s) : gather<32>(a, true, s);
+    return a.total_tokens < 4096 ? gather<4>(a, false, s) : gather<16>(a, true, s);
 }
 
 }  // namespace kda

@@ -5,6 +5,7 @@
 // The entry points are called through addresses that the package hands over (bind), so the module works on whichever
 // build of the library the package has loaded.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -99,8 +100,9 @@ kda_stream_t stream_of(c10::DeviceIndex device) {
     return reinterpret_cast<kda_stream_t>(c10::cuda::getCurrentCUDAStream(device).stream());
 }
 
+// Uninitialised memory, without the dispatcher: an output's share of a short call.
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+    return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
 }
 
 // The descriptor of a call on a cache (8-bit where it has scales) and its table, checked.
