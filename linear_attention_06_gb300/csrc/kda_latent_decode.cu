@@ -85,7 +85,7 @@ struct Small : Line {
 };
 static_assert(sizeof(Small) <= 1024, "small area");
 
-using Walk = WalkOf<kTile>;
+using Walk = WalkOf<kTile, kStart>;
 
 // Sequences of at most so many tiles are not cut (find_run).  The
 // partial results of two pieces cost more than the unevenness: 182 sequences of up to 285 tokens, 64 heads, 26.4 us
@@ -154,7 +154,7 @@ latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a
         tmem_relinquish();
     }
     wait_before();
-    find_run<kTile, kShort, kThreads>(a, runs, run, sw, reinterpret_cast<int64_t*>(sw->fac));
+    find_run<kTile, kStart, kShort, kThreads>(a, runs, run, sw, reinterpret_cast<int64_t*>(sw->fac));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -52,7 +52,11 @@ constexpr int teams_of(int nr) { return nr >= 64 ? 4 : 2; }
 constexpr int soft_of(int nr) { return 128 * teams_of(nr); }
 constexpr int threads_of(int nr) { return 128 + soft_of(nr); }       // before them: producer, issuer, queries, (TMEM)
 constexpr int kBar = 1;                       // named barriers: all softmax warps; behind it one for each team
-constexpr int kShort = 3;                     // sequences of at most so many tiles are not cut (find_run)
+// The line (kda_latent_line.cuh): a piece's start and end take a block as long as three tiles (64 x 8192 cached tokens, 32
+// heads: 47.2 us, 48.8 with one place; 32 x 4096, 4 tokens x 16 heads: 30.4, 32.8; with four places 48.0 and 30.5), and
+// sequences of at most three tiles are not cut (57 of up to 1084, 8 tokens x 12 heads: 35.5 us, 38.4 with four; 182 of up to
+// 285, 64 heads: 28.9, 30.3 with one).
+constexpr int kPlaces = 3, kShort = 3;
 // log2 of a tile's largest weight: where a piece's first tile is put, the bounds, and where a tile beyond one of them is
 // put: near that bound, so that tiles as they were before stay inside the range.
 constexpr float kSet = -1.f, kHigh = 8.75f, kHighSet = 8.f, kLow = -5.f, kLowSet = -2.f;
@@ -93,7 +97,7 @@ struct Small : Line {
 };
 static_assert(sizeof(Small) <= 3072, "small area");
 
-using Walk = WalkOf<kRows>;
+using Walk = WalkOf<kRows, kPlaces>;
 
 // OR and AND of a predicate over the softmax warps; also a barrier between them.
 template <int SOFT>
@@ -211,7 +215,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
         tmem_relinquish();
     }
     wait_before();
-    find_run<kRows, kShort, kThreads>(a, runs, run, sw, reinterpret_cast<int64_t*>(sw->ref));
+    find_run<kRows, kPlaces, kShort, kThreads>(a, runs, run, sw, reinterpret_cast<int64_t*>(sw->ref));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -761,7 +765,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             // everyone has read the sums before the next piece writes them
             soft_sync<kSoft>();
             if (lane == 0) mbar_arrive(&sw->o_free);
-            at += p.tiles + kStart;
+            at += p.tiles + kPlaces;
             p = next;
             first_piece = false;
         }

@@ -42,11 +42,11 @@ struct Line {
 };
 
 // Walks the sequences of this block's run; every role walks by itself.
-template <int TILE>
-struct WalkOf : RunWalkOf<TILE> {
-    __device__ WalkOf(const Line* sw) : RunWalkOf<TILE>{sw->seq0, sw->off0, sw->lead0, sw->len0, sw->end - sw->begin} {}
+template <int TILE, int START>
+struct WalkOf : RunWalkOf<TILE, START> {
+    __device__ WalkOf(const Line* sw) : RunWalkOf<TILE, START>{sw->seq0, sw->off0, sw->lead0, sw->len0, sw->end - sw->begin} {}
     __device__ __forceinline__ bool next(const LatentDecodeArgs& a, Piece& p) {
-        return RunWalkOf<TILE>::next(a.num_seqs, [&](int seq) { return clamped_len(a.c, a.seq_lens, seq); }, p);
+        return RunWalkOf<TILE, START>::next(a.num_seqs, [&](int seq) { return clamped_len(a.c, a.seq_lens, seq); }, p);
     }
 };
 
@@ -71,14 +71,14 @@ struct Work {
 // All threads: the run of this block and the sequence it starts in.  Rounds of a sequence a thread; with up to
 // THREADS sequences the lengths are read once.  Sequences of at most SHORT tiles are not cut, if runs have two places or
 // more: the cut goes to the nearer end.
-template <int TILE, int SHORT, int THREADS>
+template <int TILE, int START, int SHORT, int THREADS>
 __device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Line* sw, int64_t* scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int len = 0;
     auto tiles_at = [&](int n) {
         if (n >= a.num_seqs) return 0;
         len = clamped_len(a.c, a.seq_lens, n);
-        return kStart + tiles_of<TILE>(len);
+        return START + tiles_of<TILE>(len);
     };
     // the round's places before this thread's sequence, and in all
     auto scan = [&](int mine, int64_t& round) {
@@ -121,7 +121,7 @@ __device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Line* sw, i
         const int64_t first = before + at;
         // where a cut at place x of this thread's sequence goes
         auto cut = [&](int64_t x) {
-            if (spare || mine > kStart + SHORT) return x;
+            if (spare || mine > START + SHORT) return x;
             return x - first <= first + mine - x ? first : first + mine;
         };
         if (mine > 0 && first <= begin && begin < first + mine) {
@@ -130,8 +130,8 @@ __device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Line* sw, i
             const bool next = into == mine;   // the run starts with the next sequence
             sw->begin = x;
             sw->seq0 = n0 + tid + (next ? 1 : 0);
-            sw->off0 = next || into < kStart ? 0 : into - kStart;
-            sw->lead0 = next ? kStart : (into < kStart ? kStart - into : 0);
+            sw->off0 = next || into < START ? 0 : into - START;
+            sw->lead0 = next ? START : (into < START ? START - into : 0);
             sw->len0 = next ? -1 : mine_len;
         }
         if (mine > 0 && end < total && first <= end && end < first + mine) sw->end = cut(end);

@@ -14,9 +14,9 @@ namespace kda {
 namespace latent {
 
 constexpr int kTile = 64;                     // cached rows a tile of the bf16 decode
-// A sequence's places in the line: its tiles, behind kStart places that stand for what starting a piece costs a
+// A sequence's places in the line: its tiles, behind START places that stand for what starting a piece costs a
 // block (queries in, O out), so that runs with many pieces get fewer tiles.
-constexpr int kStart = 1;
+constexpr int kStart = 1;                     // of the bf16 decode
 
 struct Piece {                                // a run's share of one sequence
     int n, len, off, tiles, all;              // sequence, its length, first tile, tiles here, tiles in all
@@ -33,7 +33,7 @@ KDA_RUNS_FN int64_t run_begin(int64_t total, int runs, int p) {
 KDA_RUNS_FN int run_of(int64_t total, int runs, int64_t x) { return (int)(((x + 1) * runs - 1) / total); }
 
 // Walks the sequences of a run of tiles of TILE rows; length(n) is sequence n's length.
-template <int TILE>
+template <int TILE, int START>
 struct RunWalkOf {
     int n, off, lead, len;                    // next sequence, its first tile here, start places before it, its length or -1
     int64_t left;                             // places of the run that are left
@@ -48,13 +48,13 @@ struct RunWalkOf {
         const int64_t behind = left - lead;   // places of the run behind the sequence's start places
         p.tiles = behind < p.all - off ? (behind > 0 ? (int)behind : 0) : p.all - off;
         left = behind - p.tiles;
-        lead = kStart;
+        lead = START;
         off = 0;
         ++n;
         return p.tiles > 0;                   // a run may end inside the start places
     }
 };
-using RunWalk = RunWalkOf<kTile>;
+using RunWalk = RunWalkOf<kTile, kStart>;
 
 // Whether a piece's result is its sequence's, and goes to the output.  Other pieces go to the workspace, which a line in
 // one run does not have: there every piece is the only one of its sequence (settle), also where a length that grew since
