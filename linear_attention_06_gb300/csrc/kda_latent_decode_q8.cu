@@ -63,14 +63,15 @@ constexpr float kSet = -1.f, kHigh = 8.75f, kHighSet = 8.f, kLow = -5.f, kLowSet
 constexpr float kDeep = 30.f;                 // log2 of how far a reference may lie below the highest before it
 
 // Shared memory of a block with NR query rows: queries [slice][2 NR][128 bytes], their rope slice [2 NR][64], weights
-// [2 terms][128 tokens][NR], the rope slices of the tiles in flight, then their latent slices (128 channels).
+// [buffers][2 terms][128 tokens][NR], a tile's rope slice, then the latent slices (128 channels) of the tiles in flight.
+// With 64 rows there is room for two whole tiles beside one weight buffer.
 template <int NR, bool ROPE>
 struct Cfg {
     static constexpr uint32_t kQSlice = 2 * NR * 128, kQRope = ROPE ? 2 * NR * 64 : 0;
     static constexpr uint32_t kPitch = NR == 64 ? 64 : 32, kPTile = kRows * kPitch;
     static constexpr uint32_t kQ = 0, kQR = 4 * kQSlice, kP = kQR + kQRope;
-    static constexpr uint32_t kRopeSlots = ROPE ? (NR == 64 ? 1 : 2) : 0;
-    static constexpr uint32_t kRopeAt = kP + 2 * kPTile, kSliceAt = kRopeAt + kRopeSlots * 8192;
+    static constexpr uint32_t kBuffers = NR == 64 ? 1 : 2;
+    static constexpr uint32_t kRopeAt = kP + kBuffers * 2 * kPTile, kSliceAt = kRopeAt + (ROPE ? 8192 : 0);
     static constexpr uint32_t kSmallBytes = 3072;
     static constexpr uint32_t kFit = (232448 - kSmallBytes - kSliceAt) / 16384, kSlices = kFit < 12 ? kFit : 12;
     static constexpr uint32_t kSmall = kSliceAt + kSlices * 16384;
@@ -82,8 +83,8 @@ struct Cfg {
 
 struct Small : Line {
     uint64_t full[12], empty[12];             // latent slices
-    uint64_t rope_full[2], rope_empty[2];
-    uint64_t s_full[2], p_full, pv_done;
+    uint64_t rope_full, rope_empty;
+    uint64_t s_full[2], p_full[2], pv_done[2];
     uint64_t raw_full, q_full, q_empty;       // queries: bf16 landed, quantised, no longer needed
     uint64_t o_free, drain;
     uint32_t tmem;
@@ -194,12 +195,12 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
     if (tid == 0) {
         for (uint32_t i = 0; i < G::kSlices; ++i) { mbar_init(&sw->full[i], 1); mbar_init(&sw->empty[i], 1); }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sw->rope_full[i], 1);
-            mbar_init(&sw->rope_empty[i], 1);
             mbar_init(&sw->s_full[i], 1);
+            mbar_init(&sw->p_full[i], kWarps);
+            mbar_init(&sw->pv_done[i], 1);
         }
-        mbar_init(&sw->p_full, kWarps);
-        mbar_init(&sw->pv_done, 1);
+        mbar_init(&sw->rope_full, 1);
+        mbar_init(&sw->rope_empty, 1);
         mbar_init(&sw->raw_full, 1);
         mbar_init(&sw->q_full, kWarps);
         mbar_init(&sw->q_empty, 1);
@@ -222,7 +223,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
     const uint32_t tb = sw->tmem;
     const uint32_t ts = tb + 4 * NR;          // S buffers
     bool ok = true;
-    uint32_t loads = 0, rope_loads = 0;       // producer: slices issued
+    uint32_t loads = 0, rope_loads = 0;       // producer: latent and rope slices issued
 
     if (warp == 0) {                          // ------------------------------------------------ producer
         const int box = a.c.page_size < kRows ? a.c.page_size : kRows;
@@ -230,8 +231,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
         Walk walk(sw);
         Piece p;
         Ring<G::kSlices> ring;
-        Ring<ROPE ? G::kRopeSlots : 1> rope;
-        bool used = false, rope_used = false; // the ring has gone round once
+        bool used = false;                    // the ring has gone round once
         while (ok && walk.next(a, p)) {
             const int64_t table = (int64_t)p.n * a.c.max_pages;
             // the first cache row of this lane's box in tile x; -1: none, map_rows: outside the cache, read as zeros
@@ -261,15 +261,11 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 }
                 if (!ok) break;
                 if constexpr (ROPE) {
-                    if (rope_used && !(ok = wait_warp(&sw->rope_empty[rope.slot], rope.phase ^ 1u))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&sw->rope_full[rope.slot], boxes * box * 64);
+                    if (rope_loads > 0 && !(ok = wait_warp(&sw->rope_empty, (rope_loads - 1) & 1))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&sw->rope_full, boxes * box * 64);
                     __syncwarp();
-                    if (row >= 0)
-                        tma_load_2d(sm + G::kRopeAt + rope.slot * 8192 + lane * box * 64, &maps.r, kLatent, row,
-                                    &sw->rope_full[rope.slot]);
-                    rope.next();
+                    if (row >= 0) tma_load_2d(sm + G::kRopeAt + lane * box * 64, &maps.r, kLatent, row, &sw->rope_full);
                     ++rope_loads;
-                    if (rope.slot == 0) rope_used = true;
                 }
                 // The next tile into L2 behind this one's loads, where a request fetches 64 rows or more: its own loads
                 // wait for ring slots and then find it near (64 x 8192 cached tokens, 32 heads: 55.4 us, 58.2 without; two
@@ -284,10 +280,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
         if (!ok && lane == 0) {               // copies in flight land before the block ends
             for (uint32_t i = 0; i < G::kSlices; ++i)
                 if (loads > i) mbar_wait_bounded(&sw->full[i], ((loads - 1 - i) / G::kSlices) & 1, kWaitNs);
-            if constexpr (ROPE)
-                for (uint32_t i = 0; i < G::kRopeSlots; ++i)
-                    if (rope_loads > i)
-                        mbar_wait_bounded(&sw->rope_full[i], ((rope_loads - 1 - i) / G::kRopeSlots) & 1, kWaitNs);
+            if (ROPE && rope_loads > 0) mbar_wait_bounded(&sw->rope_full, (rope_loads - 1) & 1, kWaitNs);
         }
     } else if (warp == 1) {                   // ------------------------------------------------ issuer
         constexpr uint32_t id_s = idesc_f8_f32(128, 2 * NR, false, false, false);
@@ -304,9 +297,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
         Walk walk(sw);
         Piece p;
         Ring<G::kSlices> in, out;             // next slice for S, next slice for O
-        Ring<ROPE ? G::kRopeSlots : 1> rope;
         Ring<2> sb;                           // S buffers
-        uint32_t products = 0;                // tiles that O has
+        uint32_t scores = 0, products = 0;    // tiles that S, O have
         uint32_t seg = 0;
         while (ok && walk.next(a, p)) {
             if (!(ok = wait_warp(&sw->q_full, seg & 1))) break;
@@ -321,7 +313,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 bool landed = false, ready = false;
                 if (qk < p.tiles && qk <= pv + 1)
                     landed = __all_sync(0xffffffffu, part < 4 ? mbar_test(&sw->full[in.slot], in.phase)
-                                                              : mbar_test(&sw->rope_full[rope.slot], rope.phase));
+                                                              : mbar_test(&sw->rope_full, scores & 1));
                 if (landed) {
                     tc_fence_after();
                     const uint32_t d = ts + sb.slot * 2 * NR;
@@ -332,26 +324,26 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                             mma_f8_ss_elected(d, desc_at(y, i * 32), desc_at(x, i * 32), id_s, part > 0 || i > 0, el);
                         in.next();
                     } else {
-                        const uint64_t y = desc_at(dr, rope.slot * 8192);
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            mma_f8_ss_elected(d, desc_at(y, i * 32), desc_at(dqr, i * 32), id_s, 1, el);
-                        mma_commit_elected(&sw->rope_empty[rope.slot], el);
-                        rope.next();
+                            mma_f8_ss_elected(d, desc_at(dr, i * 32), desc_at(dqr, i * 32), id_s, 1, el);
+                        mma_commit_elected(&sw->rope_empty, el);
                     }
                     if (++part == kParts) {
                         mma_commit_elected(&sw->s_full[sb.slot], el);
                         if (qk + 1 == p.tiles) mma_commit_elected(&sw->q_empty, el);
                         sb.next();
+                        ++scores;
                         ++qk;
                         part = 0;
                     }
                 } else if (pv < qk && !freed) {
                     ready = freed = __all_sync(0xffffffffu, mbar_test(&sw->o_free, (seg - 1) & 1));
                 } else if (pv < qk) {
-                    ready = __all_sync(0xffffffffu, mbar_test(&sw->p_full, products & 1));
+                    ready = __all_sync(0xffffffffu, mbar_test(&sw->p_full[products % G::kBuffers], products / G::kBuffers & 1));
                     if (ready) {
                         tc_fence_after();
+                        const uint64_t x = desc_at(dp, products % G::kBuffers * 2 * G::kPTile);
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
                             const uint64_t y = desc_at(dv, out.slot * 16384);
@@ -360,12 +352,12 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
                                     mma_f8_ss_elected(tb + b * NR, desc_at(y, i * 4096),
-                                                      desc_at(dp, term * G::kPTile + i * 32 * G::kPitch), id_o[term],
+                                                      desc_at(x, term * G::kPTile + i * 32 * G::kPitch), id_o[term],
                                                       pv > 0 || term > 0 || i > 0, el);
                             mma_commit_elected(&sw->empty[out.slot], el);
                             out.next();
                         }
-                        mma_commit_elected(&sw->pv_done, el);
+                        mma_commit_elected(&sw->pv_done[products % G::kBuffers], el);
                         ++products;
                         ++pv;
                     }
@@ -415,6 +407,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
         Ring<G::kSlices> in;                  // the tile's first latent slice
         Ring<2> sb;                           // this tile's S buffer
         uint32_t tile = 0, pieces = 0;        // tiles before this one, of all pieces; pieces whose queries were taken
+        // the value products of tile n are done
+        auto have_products = [&](uint32_t n) { return wait_warp(&sw->pv_done[n % G::kBuffers], n / G::kBuffers & 1); };
         bool first_piece = true;
         Head head{-1, 0, 0, 0};
         int64_t at = sw->begin + sw->lead0;   // the piece's first tile in the line
@@ -584,7 +578,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                             sw->move[h0 + i] = n - m;
                         }
                         team_sync(team);
-                        if (j > 0) ok = ok && wait_warp(&sw->pv_done, (tile - 1) & 1);
+                        if (j > 0) ok = ok && have_products(tile - 1);
                         tc_fence_after();
 #pragma unroll
                         for (int c = 0; c < NH; c += 8) {
@@ -662,10 +656,10 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                             *reinterpret_cast<uint4*>(sm + G::kSliceAt + slice.slot * 16384 + (valid + (i >> 3)) * 128 + (i & 7) * 16) =
                                 make_uint4(0, 0, 0, 0);
                 }
-                // the weights before these have been read
-                if (tile > 0) ok = ok && wait_warp(&sw->pv_done, (tile - 1) & 1);
+                // the weights that were here have been read
+                if (tile >= G::kBuffers) ok = ok && have_products(tile - G::kBuffers);
                 if (ok) {
-                    uint8_t* pt = sm + G::kP;
+                    uint8_t* pt = sm + G::kP + tile % G::kBuffers * 2 * G::kPTile;
 #pragma unroll
                     for (int term = 0; term < 2; ++term)
 #pragma unroll
@@ -681,7 +675,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(&sw->p_full);
+                if (lane == 0 && ok) mbar_arrive(&sw->p_full[tile % G::kBuffers]);
                 const float2 back = make_float2(two_to(-e), two_to(-e));
 #pragma unroll
                 for (int i = 0; i < NH; i += 2) {
@@ -731,7 +725,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             more = sw->more;
             const Piece next{sw->piece[0], sw->piece[1], sw->piece[2], sw->piece[3], sw->piece[4]};
             if (more) take_queries(next);
-            ok = soft_and<kSoft>(wait_warp(&sw->pv_done, (tile - 1) & 1));
+            ok = soft_and<kSoft>(have_products(tile - 1));
             if (!ok) break;
             tc_fence_after();
             // column r of block b: row r, channels 128 b ..; a lane stores its channel of 8 rows at a time, so a
