@@ -498,10 +498,14 @@ kda_status kda_latent_gather_q8(const kda_latent_shape* shape, const void* cache
 
 /*
  * kda_latent_decode_q8 -- kda_latent_decode over an 8-bit cache: the same formulas, on the rows' values.  Scores,
- * maxima, sums and partial results are fp32.  The tensor cores multiply e4m3 numbers: a query row and a row of softmax
- * weights go in as the sum of two e4m3 numbers under one power of two, which holds 8 significant bits (those of bf16)
- * down to 2^-10 of a query row's largest channel and to 2^-13 of a row's largest weight, and absolute steps
- * of 2^-18 and 2^-21 of these below.
+ * maxima, sums and partial results are fp32.  The tensor cores multiply 8-bit numbers, so queries and softmax weights go
+ * in as sums of two:
+ * - a query row as two e4m3 numbers a channel under one power of two: all eight bits of a bf16 channel down to about
+ *   2^-10 of the row's largest, absolute steps of 2^-18 of that below;
+ * - a weight, times its row's 2^e, as e4m3 + e5m2: off by at most 2^-8 of itself (bf16's half step), or, where it is
+ *   less than 2^-1 of it, of the largest weight in its and the two preceding tiles of 128 rows.  What lies 2^25 below the
+ *   largest weight of the rows before counts for nothing.
+ * A row of the cache that holds NaN reaches its sequence's results.
  * Errors: kda_latent_decode's, with kda_latent_decode_q8_workspace_size; KDA_ERR_INVALID_ARG also for scales NULL with
  * num_pages > 0.
  */

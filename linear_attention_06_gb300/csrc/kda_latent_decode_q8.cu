@@ -6,27 +6,38 @@
 //     s_rj = scale 2^{e_j} x_r . y_j,   o_r = sum_j p_rj 2^{e_j} c_j / sum_j p_rj,   p_rj = e^{s_rj}.
 //
 // The cache's bytes bound the call, half as many as in bf16, so the tile has to be multiplied as it lies in memory:
-// widening it to 16 bits in shared memory would move four times its bytes there.  tcgen05 multiplies 8-bit operands; the
-// other operand, where it is not 8-bit by nature, goes in as the sum of two 8-bit numbers:
+// widened to 16 bits it would move through shared memory three times more.  tcgen05 multiplies 8-bit operands; the other
+// operand, where it is not 8-bit by nature, goes in as the sum of two 8-bit numbers:
 //
 // - A query row under a power of two, x = 2^k (x' + x''), both e4m3: eight significant bits, all of a bf16 channel, down
 //   to 2^-10 of the row's largest.  x' and x'' are two rows of one operand, so that the tile is read once for both.
 // - A weight w_rj = 2^{log2 p_rj + e_j - m_r} as e4m3 + e5m2: 2^-8 of it, as in bf16.  The e5m2 part, whose smallest number
-//   is 2^-16, keeps faint weights from being lost: m_r, the row's reference, is held where the largest weight of every
-//   tile lies in 2^-2 .. 2^8, and is lowered as well as raised (a first token that takes nearly all weight and a long
-//   faint tail behind it is what models really do), but never to more than 2^30 above the faintest reference that counts:
-//   O and the sums then stay far inside fp32.
+//   is 2^-16, keeps faint weights from being lost.  The row's reference m_r is a whole number (scores near 0 keep their
+//   bits beside e_j, and moves are exact) and is held where the tiles' largest weights lie in 2^-5 .. 2^8.75: raised at
+//   once, lowered where two tiles in turn were below (a first token that takes nearly all weight and a long faint tail
+//   behind it is what models really do), but never to more than 2^30 under the highest before it: O and the sums then
+//   stay far inside fp32.
 //
 // Products, per tile of 128 cached rows (NR = query rows of a block, 16, 32 or 64):
 //   S [128 tokens x 2 NR]  = Y X^T            M = 128, N = 2 NR (x' and x'' of each row), K = 512 + rope
 //   O^T [512 x NR]        += C^T W'^T + C^T W''^T    four blocks of M = 128 channels, N = NR, K = 128 tokens, twice
-// The tokens lie on the lanes of tensor memory, so a softmax thread has one token of all its rows: 2^{e_j} is one number a
-// thread, weights of consecutive rows pack into words, and the tile's operands keep the full M = 128.  What that layout
-// makes dear, a maximum over tokens, is not needed in every tile: references move only when a vote finds a tile outside
-// the range above; the sums stay in registers, a part a thread, until the piece ends.
+// The tokens lie on the lanes of tensor memory, so a softmax thread has one token of its rows: 2^{e_j} is one number a
+// thread, weights of consecutive rows pack into words, and the tile's operands keep the full M = 128 (with the rows on the
+// lanes a product of 64 rows takes as long, and the sum of the two terms crosses warps).  What that layout makes dear, a
+// maximum over tokens, is not needed in every tile: references move only when a vote finds a tile outside the range
+// above; the sums stay in registers, a part a thread, until the piece ends.
 //
 // Work: as in the bf16 decode, one line of tiles in equal runs (kda_latent_line.cuh).  Block: a producer warp (TMA boxes
-// of page rows), an issuing warp, and eight warps that quantise the queries and turn S into W, half of the rows each four.
+// of page rows), an issuing warp, a query loader, and two or four teams of four warps that quantise the queries and turn S
+// into W.
+//
+// Measured (GB300, 6761 GB/s measured copy rate; ragged lengths of 1/4 to all of the stated context), one token: 64
+// sequences of up to 8192, 32 heads, 46.5 us (0.59 of that rate; bf16 cache 70 us); 64 heads 59.0 us, 744 TFLOP/s; 256 of up
+// to 8192, no rope, 128.6 us (0.78; bf16 210 us); one of 131072 26.3 us (0.43; bf16 36.8 us).  What is missing, at 32 heads:
+// 17% in the tiles (a tile's 3400 cycles are a chain: its load behind freed slots, 900 cycles of products for S, 1700 from S
+// to W, 1300 of products for O; the slots hold two tiles and a half), and what is fixed: 1.6 us until a block knows its run,
+// 3 us until its queries are quantised, 2 us from its last row to its stored result, 4 us of join.  At 64 heads the slots
+// hold two tiles and the chain takes 4100 cycles.
 #include <atomic>
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -5,11 +5,12 @@ Bounds, beside those of tests/latent_reference.py.
 - The tensor cores take a query as the sum of two e4m3 numbers under one power of two.  Two e4m3 numbers hold eight
   significant bits; the last step is 2^-9 of the power, so a channel is off by at most 2^-10 * 2^e_q, with
   2^e_q <= max |q| / 224: a score is off by that times sum_i |k_i|, on top of its products' rounding.
-- A softmax weight, times the row's 2^e_j, goes in as an e4m3 and an e5m2 number.  e4m3 leaves at most 2^-4 of it, of
-  which e5m2 (three significant bits) leaves 2^-3 / 2: 2^-8 in all (U).  Where the weight lies below 2^-6, e4m3 leaves up
-  to 2^-10 and e5m2 up to 2^-13 of that scale, which is chosen so that the largest weight of each tile of 128 rows lies
-  above 2^-2 (but where it is 2^-28 of the largest of the rows before, or less, and counts for nothing): at most
-  2^-11 of the tile's largest weight.
+- A softmax weight, times the row's 2^e_j, goes in as an e4m3 and an e5m2 number, under a reference that is the row's and
+  changes from tile to tile (128 cached rows).  e4m3 leaves at most 2^-4 of a weight of 2^-6 or more (in units of the
+  reference), of which e5m2 (three significant bits) leaves 2^-3 / 2: 2^-8 in all (U).  Of a smaller weight e4m3 leaves at
+  most 2^-10, of which e5m2 leaves 2^-13; e5m2 itself ends at steps of 2^-16.  A tile's largest weight may lie below 2^-5
+  at most twice in turn (the third such tile lowers the reference), so that the largest among a tile and the two before it
+  is 2^-5 or more, and a weight is off by at most 2^-13 = 2^-8 * 2^-5: 2^-8 of that largest one.
 """
 import math
 
@@ -95,8 +96,10 @@ def decode(q_latent, q_rope, cache, scales, table, lens, scale):
             z = torch.where(seen <= 0, torch.zeros_like(lse), lse)
             p = torch.exp(s - z[:, None]).masked_fill(hidden, 0.0)
             w = torch.nn.functional.pad(p * two(e), (0, -length % TILE)).view(p.shape[0], -1, TILE)
-            top = w.amax(-1, keepdim=True).expand_as(w).reshape(p.shape[0], -1)[:, :length]
-            low = torch.where(hidden, torch.zeros_like(top), 2.0 ** -11 * top) @ y[:, :512].abs()
+            top = torch.nn.functional.pad(w.amax(-1), (2, 0))
+            top = torch.maximum(torch.maximum(top[:, 2:], top[:, 1:-1]), top[:, :-2])        # of a tile and the two before it
+            top = top[:, :, None].expand_as(w).reshape(p.shape[0], -1)[:, :length]
+            low = torch.where(hidden, torch.zeros_like(top), U * top) @ y[:, :512].abs()
             bo = bo + 2 * off[:, None] * (p @ c[:, :512].abs()) + low
             bs = bs + off
         parts.append((o, lse, bo, bs))

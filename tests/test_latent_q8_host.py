@@ -1,5 +1,7 @@
 """The 8-bit latent cache on the host: what the C ABI and the binding refuse, before any CUDA call."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
@@ -123,3 +125,67 @@ def test_the_reference_rounds_as_the_format_does():
     e = q8.power_of_rows(most[:, None])
     assert e.tolist() == [0, 1, 0, -1, 0, -8, -7, -64, -64, -64]
     assert torch.equal(q8.two(torch.tensor([-64, 0, 120])), torch.tensor([2.0 ** -64, 1.0, 2.0 ** 120], dtype=torch.float64))
+
+
+def test_runs_of_the_line_take_every_tile_once(tmp_path):
+    """The walk of kda_latent_runs.h with the 8-bit decode's tiles and start places: every tile of every sequence in
+    exactly one run, whatever the lengths, and no part for the workspace where one run is all there is."""
+    src, exe = tmp_path / "runs.cpp", tmp_path / "runs"
+    src.write_text(RUNS)
+    subprocess.run([os.environ.get("CXX", "g++"), "-std=c++17", "-O1", "-I", kbuild.CSRC, str(src), "-o", str(exe)], check=True)
+    done = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert done.returncode == 0 and done.stdout == "ok\n", done.stdout
+
+
+RUNS = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+#include "kda_latent_runs.h"
+using namespace kda::latent;
+constexpr int TILE = 128, START = 3;
+
+static int walk(const std::vector<int>& lens, int runs, std::vector<int>& tiles) {
+    const int count = (int)lens.size();
+    int64_t total = 0;
+    std::vector<int64_t> first;
+    for (int x : lens) { first.push_back(total); total += START + tiles_of<TILE>(x); }
+    if (total < runs) runs = (int)total;
+    int partial = 0;
+    for (int r = 0; r < runs; ++r) {
+        const int64_t begin = run_begin(total, runs, r), end = run_begin(total, runs, r + 1);
+        int n = count - 1;
+        while (first[n] > begin) --n;
+        const int into = (int)(begin - first[n]);
+        RunWalkOf<TILE, START> w{n, into < START ? 0 : into - START, into < START ? START - into : 0, lens[n], end - begin};
+        Piece p;
+        int64_t at = begin + w.lead;          // the piece's first tile in the line, as the kernel follows it
+        while (w.next(count, [&](int n) { return lens[n]; }, p)) {
+            if (p.off < 0 || p.tiles <= 0 || p.off + p.tiles > p.all) return -1;
+            if (at != first[p.n] + START + p.off || run_of(total, runs, at) != r) return -2;
+            tiles[p.n] += p.tiles;
+            settle(p, runs);
+            partial += !is_whole(p);
+            at += p.tiles + START;
+        }
+    }
+    return partial;
+}
+
+int main() {
+    srand(2);
+    for (int round = 0; round < 4000; ++round) {
+        std::vector<int> lens(1 + rand() % 12);
+        for (int& x : lens) x = rand() % 4 ? rand() % 700 : rand() % 20000;
+        for (int runs : {1, 2 + rand() % 150, 152}) {
+            std::vector<int> tiles(lens.size());
+            const int partial = walk(lens, runs, tiles);
+            if (partial < 0 || (runs == 1 && partial)) return printf("runs %d: %d\n", runs, partial), 1;
+            for (size_t n = 0; n < lens.size(); ++n)
+                if (tiles[n] != tiles_of<TILE>(lens[n])) return printf("tiles missed or taken twice\n"), 1;
+        }
+    }
+    printf("ok\n");
+    return 0;
+}
+"""
