@@ -504,7 +504,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             take_queries(p);
             soft_sync<kSoft>();
         }
-        while (ok && more) {
+        while (more) {                        // (a warp whose wait ran out leaves at a barrier, with the others)
             announce();                       // all have read this piece's
             // this thread's cached row in tile x: its page, and its scale byte (0, the lowest, where there is none: such a
             // row reads as zeros and sets no reference)
@@ -563,7 +563,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                             x[c + i] = v.x; x[c + i + 1] = v.y; x[c + i + 2] = w.x; x[c + i + 3] = w.y;
                         }
                     }
-                    if (base + kRows > least) {                      // tokens that some rows do not see
+                    if (least - base < kRows) {                      // tokens that some rows do not see
 #pragma unroll
                         for (int i = 0; i < NH; ++i)
                             if (base + tok >= sw->seen[h0 + i]) x[i] = -INFINITY;
@@ -736,7 +736,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             more = sw->more;
             const Piece next{sw->piece[0], sw->piece[1], sw->piece[2], sw->piece[3], sw->piece[4]};
             if (more) take_queries(next);
-            ok = soft_and<kSoft>(have_products(tile - 1));
+            ok = soft_and<kSoft>(ok && have_products(tile - 1));
             if (!ok) break;
             tc_fence_after();
             // column r of block b: row r, channels 128 b ..; a lane stores its channel of 8 rows at a time, so a

@@ -5,7 +5,7 @@
 // The entry points are called through addresses that the package hands over (bind), so the module works on whichever
 // build of the library the package has loaded.
 #include <ATen/ATen.h>
-#include <ATen/cuda/EmptyTensor.h>
+#include <ATen/ops/empty_native.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -102,7 +102,7 @@ kda_stream_t stream_of(c10::DeviceIndex device) {
 
 // Uninitialised memory, without the dispatcher: an output's share of a short call.
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
-    return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+    return at::native::empty_cuda(shape, type, std::nullopt, like.device(), std::nullopt, std::nullopt);
 }
 
 // The descriptor of a call on a cache (8-bit where it has scales) and its table, checked.

@@ -177,3 +177,20 @@ def test_captured_calls_behind_two_branches():
                                  torch.arange(n, dtype=torch.int32, device=DEV)[:, None], lens, 0.07)
         ref.assert_within(out[1], o, bo, "out")
         ref.assert_within(lse[1], s, bs, "lse")
+
+
+def test_the_longest_context():
+    """A table row of nearly 2^31 rows, whose last tile ends at 2^31 - 16: what lies behind the end is not seen."""
+    page, per = 16, 2 ** 27 - 1
+    table = torch.zeros((1, per), dtype=torch.int32, device=DEV)
+    table[0, -1] = 1
+    length = per * page - 5
+    cache = torch.zeros(2, page, 512, dtype=U8, device=DEV)
+    scales = torch.full((2, page), 127, dtype=U8, device=DEV)
+    cache[1, page - 5:] = 0x78                                 # 256 in every channel, behind the end
+    out, lse = kda.kda_latent_decode_q8(torch.ones(1, 1, 512, dtype=BF, device=DEV), None, cache.view(q8.E4M3), scales.view(q8.E8M0),
+                                        table, i32([length]), 0.01, lse=True)
+    clean()
+    # every thread adds 2^31 / 128 / 152 equal terms in fp32, each sum off by at most 2^-24 of itself
+    steps = 2 ** 31 / 128 / 152
+    assert bool((out == 0).all()) and abs(float(lse) - torch.tensor(float(length), dtype=torch.float64).log()) < 1.1 * steps * 2.0 ** -24
