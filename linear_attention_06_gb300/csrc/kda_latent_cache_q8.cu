@@ -28,9 +28,10 @@ __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(
 
 // TOK tokens a block, a warp a row: a lane has two chunks of eight latent channels and one pair of rotated ones, so that
 // a row's largest magnitude is one reduction of the warp.  As in the bf16 append, rows and queries are requested before
-// anything else and arrive while the block finds its tokens' sequences, pages and angles.
+// anything else and arrive while the block finds its tokens' sequences, pages and angles.  Four blocks an SM (8 prompts
+// of up to 2048 tokens, 32 heads, written and read back: 21.7 us; 22.9 with three, 25.3 with five).
 template <int TOK, Turning TURN>
-__global__ void __launch_bounds__(kThreads, 3) append_kernel(const LatentAppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const LatentAppendArgs a) {
     static_assert(TOK <= kWarps, "a warp a token");
     constexpr int kQ = 4;
     __shared__ Turn turn_s[TOK][kRope / 2];
@@ -214,6 +215,9 @@ cudaError_t gather(const LatentGatherArgs& a, bool overlapped, cudaStream_t s) {
 
 }  // namespace
 
+// As in bf16: calls of few tokens take few rows a block, so that every SM has some, and are launched plainly; they end
+// sooner than the host makes the next call.  Rows a block for many: a gather of 16 x 16384 rows takes 47.8 us with 16, 57.0
+// with 8, 49.8 with 32, 55.7 with 64; prompts of 8 x 2048 tokens are appended in 25 us with 8 tokens a block, 56 with one.
 cudaError_t launch_latent_append_q8(const LatentAppendArgs& a, cudaStream_t s) {
     return a.total_tokens < 2048 ? append<1>(a, false, s) : append<8>(a, true, s);
 }

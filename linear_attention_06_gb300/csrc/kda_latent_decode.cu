@@ -87,10 +87,10 @@ static_assert(sizeof(Small) <= 1024, "small area");
 
 using Walk = WalkOf<kTile, kStart>;
 
-// Sequences of at most so many tiles are not cut (find_run).  The
-// partial results of two pieces cost more than the unevenness: 182 sequences of up to 285 tokens, 64 heads, 26.4 us
-// against 34.7 when cut (28.9 with a limit of 4 tiles); 100 of up to 400, 32 heads, 16.8 against 19.7; with a limit of
-// 8 tiles unevenness wins (57 of up to 1084, 8 tokens x 12 heads: 45 us, 39 with 6, 37 when cut).
+// Sequences of at most so many tiles are not cut (find_run).  The partial results of two pieces cost more than the
+// unevenness: 182 sequences of up to 285 tokens, 64 heads, 26.4 us against 34.7 when cut (28.9 with a limit of 4 tiles);
+// 100 of up to 400, 32 heads, 16.8 against 19.7; with a limit of 8 tiles unevenness wins (57 of up to 1084, 8 tokens x
+// 12 heads: 45 us, 39 with 6, 37 when cut).
 constexpr int kShort = 6;
 
 // OR and AND of a predicate over the softmax warps; also a barrier between them.

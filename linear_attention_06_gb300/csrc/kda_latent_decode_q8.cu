@@ -83,7 +83,7 @@ struct Cfg {
     static constexpr uint32_t kQ = 0, kQR = 4 * kQSlice, kP = kQR + kQRope;
     static constexpr uint32_t kBuffers = NR == 64 ? 1 : 2;
     static constexpr uint32_t kRopeAt = kP + kBuffers * 2 * kPTile, kSliceAt = kRopeAt + (ROPE ? 8192 : 0);
-    static constexpr uint32_t kSmallBytes = 3072;
+    static constexpr uint32_t kSmallBytes = 3 * 1024;
     static constexpr uint32_t kFit = (232448 - kSmallBytes - kSliceAt) / 16384, kSlices = kFit < 12 ? kFit : 12;
     static constexpr uint32_t kSmall = kSliceAt + kSlices * 16384;
     static constexpr uint32_t kBytes = kSmall + kSmallBytes;
@@ -107,7 +107,7 @@ struct Small : Line {
     alignas(16) int seen[64];                 // tokens that the row sees
     alignas(16) float red[4][4][16];          // a team's, a warp's: maxima, sums
 };
-static_assert(sizeof(Small) <= 3072, "small area");
+static_assert(sizeof(Small) <= 3 * 1024, "small area");
 
 using Walk = WalkOf<kRows, kPlaces>;
 
