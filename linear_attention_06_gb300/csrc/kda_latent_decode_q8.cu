@@ -58,7 +58,8 @@ using namespace latent;
 using namespace sm103;
 
 constexpr int kRows = 128;                    // cached rows a tile
-// Softmax warps work in teams of four (a warp for each quarter of a tile's tokens), the rows shared by the teams.
+// Softmax warps work in teams of four (a warp for each quarter of a tile's tokens), the rows shared by the teams: sixteen a
+// team (64 x 8192 cached tokens, 64 heads: 63.7 us with four teams, 69.6 with two; 32 heads: 51.8 with four, 50.4 with two).
 constexpr int teams_of(int nr) { return nr >= 64 ? 4 : 2; }
 constexpr int soft_of(int nr) { return 128 * teams_of(nr); }
 constexpr int threads_of(int nr) { return 128 + soft_of(nr); }       // before them: producer, issuer, queries, (TMEM)

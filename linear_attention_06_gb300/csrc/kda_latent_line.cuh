@@ -82,19 +82,22 @@ __device__ void find_run(const LatentDecodeArgs& a, int runs, int p, Line* sw, i
     };
     // the round's places before this thread's sequence, and in all
     auto scan = [&](int mine, int64_t& round) {
-        int64_t x = mine;
+        int part = mine;                      // a warp's sum stays below 2^31: 32 sequences of at most 2^25 + START places
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
+            const int y = __shfl_up_sync(0xffffffffu, part, o);
+            if (lane >= o) part += y;
         }
-        if (lane == 31) scratch[warp] = x;
+        if (lane == 31) scratch[warp] = part;
         __syncthreads();
+        int64_t x = part;
         round = 0;
+#pragma unroll
         for (int w = 0; w < THREADS / 32; ++w) {
-            if (w < warp) x += scratch[w];
-            round += scratch[w];
+            const int64_t other = scratch[w];
+            if (w < warp) x += other;
+            round += other;
         }
-        __syncthreads();
+        if (a.num_seqs > THREADS) __syncthreads();                   // scratch is written again
         return x - mine;
     };
     int mine = tiles_at(tid);
