@@ -502,7 +502,7 @@ kda_status kda_latent_gather_q8(const kda_latent_shape* shape, const void* cache
  * in as sums of two:
  * - a query row as two e4m3 numbers a channel under one power of two: all eight bits of a bf16 channel down to about
  *   2^-10 of the row's largest, absolute steps of 2^-18 of that below;
- * - a weight, times its row's 2^e, as e4m3 + e5m2: off by at most 2^-8 of itself, which is bf16's half step, or by 2^-8
+ * - a weight, times its row's 2^e, as e4m3 and e4m3 or e5m2: off by at most 2^-8 of itself, which is bf16's half step, or by 2^-8
  *   of the largest weight in its and the two preceding tiles of 128 rows, whichever is more.  Weights of 2^-30 of the
  *   largest before them, or less, may be lost.
  * A row of the cache that holds NaN reaches its sequence's results.

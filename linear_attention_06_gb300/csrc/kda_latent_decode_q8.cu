@@ -11,16 +11,18 @@
 //
 // - A query row under a power of two, x = 2^k (x' + x''), both e4m3: eight significant bits, all of a bf16 channel, down
 //   to 2^-10 of the row's largest.  x' and x'' are two rows of one operand, so that the tile is read once for both.
-// - A weight w_rj = 2^{log2 p_rj + e_j - m_r} as e4m3 + e5m2: 2^-8 of it, as in bf16.  The e5m2 part, whose smallest number
-//   is 2^-16, keeps faint weights from being lost.  The row's reference m_r is a whole number (scores near 0 keep their
-//   bits beside e_j, and moves are exact) and is held where the tiles' largest weights lie in 2^-5 .. 2^8.75: raised at
-//   once, lowered where two tiles in turn were below (a first token that takes nearly all weight and a long faint tail
-//   behind it is what models really do), but never to more than 2^30 under the highest before it: O and the sums then
-//   stay far inside fp32.
+// - A weight w_rj = 2^{log2 p_rj + e_j - m_r} as e4m3 and, of what that leaves, 2^7 times in e4m3 with accumulators of its
+//   own (up to 32 rows) or e5m2 in the same ones (64 rows, whose accumulators take all there is): 2^-9 or 2^-8 of the
+//   weight (bf16: 2^-8), and steps of 2^-16 where it is faint.  The row's reference m_r is a whole number (scores near 0
+//   keep their bits beside e_j, and moves are exact) and is held where the tiles' largest weights lie in 2^-5 .. 2^6 or
+//   2^8.75: raised at once, lowered where two tiles in turn were below (a first token that takes nearly all weight and a
+//   long faint tail behind it is what models really do), but never to more than 2^30 under the highest before it: O and the
+//   sums then stay far inside fp32.
 //
 // Products, per tile of 128 cached rows (NR = query rows of a block, 16, 32 or 64):
 //   S [128 tokens x 2 NR]  = Y X^T            M = 128, N = 2 NR (x' and x'' of each row), K = 512 + rope
-//   O^T [512 x NR]        += C^T W'^T + C^T W''^T    four blocks of M = 128 channels, N = NR, K = 128 tokens, twice
+//   O^T [512 x 2 NR]      += C^T [W' W'']^T          four blocks of M = 128 channels, N = 2 NR, K = 128 tokens (64 rows:
+//                                                     [512 x NR], N = NR, twice, each time reading the tile)
 // The tokens lie on the lanes of tensor memory, so a softmax thread has one token of its rows: 2^{e_j} is one number a
 // thread, weights of consecutive rows pack into words, and the tile's operands keep the full M = 128 (with the rows on the
 // lanes a product of 64 rows takes as long, and the sum of the two terms crosses warps).  What that layout makes dear, a
@@ -35,7 +37,7 @@
 // sequences of up to 8192, 32 heads, 46.5 us (0.59 of that rate; bf16 cache 70 us); 64 heads 59.0 us, 744 TFLOP/s; 256 of up
 // to 8192, no rope, 128.6 us (0.78; bf16 210 us); one of 131072 26.3 us (0.43; bf16 36.8 us).  What is missing, at 32 heads:
 // 17% in the tiles (a tile's 3400 cycles are a chain: its load behind freed slots, 900 cycles of products for S, 1700 from S
-// to W, 1300 of products for O; the slots hold two tiles and a half), and what is fixed: 1.6 us until a block knows its run,
+// to W, 1000 of products for O; the slots hold two tiles and a half), and what is fixed: 1.6 us until a block knows its run,
 // 3 us until its queries are quantised, 2 us from its last row to its stored result, 4 us of join.  At 64 heads the slots
 // hold two tiles and the chain takes 4100 cycles.
 #include <atomic>
@@ -71,24 +73,30 @@ constexpr int kBar = 1;                       // named barriers: all softmax war
 constexpr int kPlaces = 3, kShort = 3;
 // log2 of a tile's largest weight: where a piece's first tile is put, the bounds, and where a tile beyond one of them is
 // put: near that bound, so that tiles as they were before stay inside the range.
-constexpr float kSet = -1.f, kHigh = 8.75f, kHighSet = 8.f, kLow = -5.f, kLowSet = -2.f;
+constexpr float kSet = -1.f, kLow = -5.f, kLowSet = -2.f;
 constexpr float kDeep = 30.f;                 // log2 of how far a reference may lie below the highest before it
 
 // Shared memory of a block with NR query rows: queries [slice][2 NR][128 bytes], their rope slice [2 NR][64], weights
-// [buffers][2 terms][128 tokens][NR], a tile's rope slice, then the latent slices (128 channels) of the tiles in flight.
-// With 64 rows there is room for two whole tiles beside one weight buffer.
+// [buffers][128 tokens][2 NR] or, with 64 rows, [2 terms][128 tokens][NR], a tile's rope slice, then the latent slices (128 channels) of the tiles in flight.
+// With 64 rows there is room for two whole tiles beside one buffer of weights.
 template <int NR, bool ROPE>
 struct Cfg {
     static constexpr uint32_t kQSlice = 2 * NR * 128, kQRope = ROPE ? 2 * NR * 64 : 0;
-    static constexpr uint32_t kPitch = NR == 64 ? 64 : 32, kPTile = kRows * kPitch;
+    // both terms of the weights side by side, with accumulators of their own (kO columns a block of channels): tensor
+    // memory has room for that up to 32 rows
+    static constexpr bool kWide = NR <= 32;
+    static constexpr uint32_t kO = kWide ? 2 * NR : NR, kTiles = kWide ? 1 : 2;
+    static constexpr uint32_t kPitch = NR == 16 ? 32 : 64, kPTile = kRows * kPitch;
+    // log2 of the largest weight that fits, and where a larger one is put: 64, whose rest times 2^7 is at most 256, and 448
+    static constexpr float kHigh = kWide ? 6.f : 8.75f, kHighSet = kWide ? 5.f : 8.f;
     static constexpr uint32_t kQ = 0, kQR = 4 * kQSlice, kP = kQR + kQRope;
     static constexpr uint32_t kBuffers = NR == 64 ? 1 : 2;
-    static constexpr uint32_t kRopeAt = kP + kBuffers * 2 * kPTile, kSliceAt = kRopeAt + (ROPE ? 8192 : 0);
+    static constexpr uint32_t kRopeAt = kP + kBuffers * kTiles * kPTile, kSliceAt = kRopeAt + (ROPE ? 8192 : 0);
     static constexpr uint32_t kSmallBytes = 3 * 1024;
     static constexpr uint32_t kFit = (232448 - kSmallBytes - kSliceAt) / 16384, kSlices = kFit < 12 ? kFit : 12;
     static constexpr uint32_t kSmall = kSliceAt + kSlices * 16384;
     static constexpr uint32_t kBytes = kSmall + kSmallBytes;
-    static constexpr uint32_t kCols = NR == 64 ? 512 : (NR == 32 ? 256 : 128);      // TMEM: O^T 4 NR, S 2 x 2 NR
+    static constexpr uint32_t kCols = NR == 16 ? 256 : 512;   // TMEM: O^T 4 kO, S 2 x 2 NR
     static_assert(kBytes <= 232448 && kSlices >= 5, "shared memory");
     static_assert(kQR % 1024 == 0 && kP % 1024 == 0 && kSliceAt % 1024 == 0, "swizzled tiles");
 };
@@ -233,7 +241,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = sw->tmem;
-    const uint32_t ts = tb + 4 * NR;          // S buffers
+    const uint32_t ts = tb + 4 * G::kO;       // S buffers
     bool ok = true;
     uint32_t loads = 0, rope_loads = 0;       // producer: latent and rope slices issued
 
@@ -296,7 +304,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
         }
     } else if (warp == 1) {                   // ------------------------------------------------ issuer
         constexpr uint32_t id_s = idesc_f8_f32(128, 2 * NR, false, false, false);
-        constexpr uint32_t id_o[2] = {idesc_f8_f32(128, NR, false, true, true), idesc_f8_f32(128, NR, true, true, true)};
+        constexpr uint32_t id_o[2] = {idesc_f8_f32(128, G::kO, false, true, true), idesc_f8_f32(128, NR, true, true, true)};
         constexpr uint32_t p_swizzle = G::kPitch == 64 ? kSwizzle64B : kSwizzle32B;
         // base descriptors: queries and cached rows as keys, the rope slices of both, weights, cached rows as values
         const uint64_t dq = smem_desc(smem_u32(sm + G::kQ), 16, 1024, kSwizzle128B);
@@ -355,15 +363,15 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                     ready = __all_sync(0xffffffffu, mbar_test(&sw->p_full[products % G::kBuffers], products / G::kBuffers & 1));
                     if (ready) {
                         tc_fence_after();
-                        const uint64_t x = desc_at(dp, products % G::kBuffers * 2 * G::kPTile);
+                        const uint64_t x = desc_at(dp, products % G::kBuffers * G::kTiles * G::kPTile);
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
                             const uint64_t y = desc_at(dv, out.slot * 16384);
 #pragma unroll
-                            for (int term = 0; term < 2; ++term)
+                            for (int term = 0; term < (int)G::kTiles; ++term)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
-                                    mma_f8_ss_elected(tb + b * NR, desc_at(y, i * 4096),
+                                    mma_f8_ss_elected(tb + b * G::kO, desc_at(y, i * 4096),
                                                       desc_at(x, term * G::kPTile + i * 32 * G::kPitch), id_o[term],
                                                       pv > 0 || term > 0 || i > 0, el);
                             mma_commit_elected(&sw->empty[out.slot], el);
@@ -582,8 +590,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                                                   fmaxf(sw->red[team][2][i], sw->red[team][3][i]));
                             const float m = -sw->ref[h0 + i], top = sw->top[h0 + i];
                             float n = m;
-                            if (z > -INFINITY && (j == 0 || z > kHigh || z < kLow)) {
-                                n = fmaxf(m + rintf(z - (j == 0 ? kSet : z > kHigh ? kHighSet : kLowSet)), top - kDeep);
+                            if (z > -INFINITY && (j == 0 || z > G::kHigh || z < kLow)) {
+                                n = fmaxf(m + rintf(z - (j == 0 ? kSet : z > G::kHigh ? G::kHighSet : kLowSet)), top - kDeep);
                                 sw->ref[h0 + i] = -n;
                                 sw->top[h0 + i] = fmaxf(top, n);
                             }
@@ -605,15 +613,18 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                                 l[c + n] *= f[n];
                             }
                             if (j > 0 && ok && !still) {             // O^T, column r by f_r
-                                uint32_t o[4][8];
+#pragma unroll 1
+                                for (uint32_t at = 0; at < G::kO; at += NR) {
+                                    uint32_t o[4][8];
 #pragma unroll
-                                for (int b = 0; b < 4; ++b) tmem_ld8(lanes + b * NR + c, o[b]);
-                                tmem_wait_ld();
+                                    for (int b = 0; b < 4; ++b) tmem_ld8(lanes + b * G::kO + at + c, o[b]);
+                                    tmem_wait_ld();
 #pragma unroll
-                                for (int b = 0; b < 4; ++b) {
+                                    for (int b = 0; b < 4; ++b) {
 #pragma unroll
-                                    for (int n = 0; n < 8; ++n) o[b][n] = __float_as_uint(__uint_as_float(o[b][n]) * f[n]);
-                                    tmem_st8(lanes + b * NR + c, o[b]);
+                                        for (int n = 0; n < 8; ++n) o[b][n] = __float_as_uint(__uint_as_float(o[b][n]) * f[n]);
+                                        tmem_st8(lanes + b * G::kO + at + c, o[b]);
+                                    }
                                 }
                             }
                         }
@@ -629,17 +640,19 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                     for (int i = 0; i < NH; i += 4) {                // (fp16 holds 11 bits of a weight, differences are exact)
 #pragma unroll
                         for (int n = 0; n < 4; ++n) x[i + n] = exp2_fast(x[i + n]);
-                        uint32_t lo, hi;
                         y[0][i / 4] = to_e4m3x4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        uint32_t lo, hi;
                         e4m3x4_to_f16(y[0][i / 4], lo, hi);
-                        y[1][i / 4] = f16_to_e5m2x4(sub_f16x2(to_f16x2(x[i], x[i + 1]), lo), sub_f16x2(to_f16x2(x[i + 2], x[i + 3]), hi));
+                        lo = sub_f16x2(to_f16x2(x[i], x[i + 1]), lo);
+                        hi = sub_f16x2(to_f16x2(x[i + 2], x[i + 3]), hi);
+                        y[1][i / 4] = G::kWide ? f16_to_e4m3x4(mul_f16x2(lo, k128), mul_f16x2(hi, k128)) : f16_to_e5m2x4(lo, hi);
                     }
                     if (j == 0 || voted) break;
                     // e4m3 numbers of 2^-5 or more have one of the bits 0x70
 #pragma unroll
                     for (int i = 0; i < NH / 4; ++i) bright |= (((y[0][i] & 0x70707070u) + 0x70707070u) & 0x80808080u) >> i;
                     bright = __reduce_or_sync(0xffffffffu, bright);
-                    const bool high = __any_sync(0xffffffffu, most > kHigh);
+                    const bool high = __any_sync(0xffffffffu, most > G::kHigh);
                     if (lane == 0) sw->vote[j & 1][warp - 4] = make_uint2(bright, high);
                     // once a tile, by all teams, whatever their references do: the barrier is all softmax warps'
                     if (soft_or<kSoft>(!ok)) { stop = true; break; }
@@ -671,17 +684,19 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 // the weights that were here have been read
                 if (tile >= G::kBuffers) ok = ok && have_products(tile - G::kBuffers);
                 if (ok) {
-                    uint8_t* pt = sm + G::kP + tile % G::kBuffers * 2 * G::kPTile;
+                    uint8_t* pt = sm + G::kP + tile % G::kBuffers * G::kTiles * G::kPTile;
 #pragma unroll
                     for (int term = 0; term < 2; ++term)
 #pragma unroll
                         for (int c = 0; c < NH; c += N) {
                             const uint32_t* v = &y[term][c / 4];
-                            const uint32_t off = NR == 64 ? sw64_offset(tok, h0 + c) : sw32_offset(tok, h0 + c);
+                            const int col = h0 + c + (G::kWide ? term * NR : 0);
+                            const uint32_t off = (G::kWide ? 0 : term * G::kPTile) +
+                                                 (G::kPitch == 64 ? sw64_offset(tok, col) : sw32_offset(tok, col));
                             if constexpr (N == 16)
-                                *reinterpret_cast<uint4*>(pt + term * G::kPTile + off) = make_uint4(v[0], v[1], v[2], v[3]);
+                                *reinterpret_cast<uint4*>(pt + off) = make_uint4(v[0], v[1], v[2], v[3]);
                             else
-                                *reinterpret_cast<uint2*>(pt + term * G::kPTile + off) = make_uint2(v[0], v[1]);
+                                *reinterpret_cast<uint2*>(pt + off) = make_uint2(v[0], v[1]);
                         }
                 }
                 fence_proxy_async_smem();
@@ -749,10 +764,20 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             float* part = po + (row + h0) * kLatent + tok;
 #pragma unroll
             for (int c = 0; c < NH; c += 8) {
-                uint32_t o[4][8];
+                uint32_t o[4][8], rest[4][8];
 #pragma unroll
-                for (int b = 0; b < 4; ++b) tmem_ld8(lanes + b * NR + c, o[b]);
+                for (int b = 0; b < 4; ++b) {
+                    tmem_ld8(lanes + b * G::kO + c, o[b]);
+                    if (G::kWide) tmem_ld8(lanes + b * G::kO + NR + c, rest[b]);
+                }
                 tmem_wait_ld();
+                if constexpr (G::kWide) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            o[b][i] = __float_as_uint(fmaf(__uint_as_float(rest[b][i]), 0x1p-7f, __uint_as_float(o[b][i])));
+                }
                 const int live = inside ? rows - h0 - c : 0;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)

@@ -60,6 +60,12 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+constexpr uint32_t k128 = 0x58005800u;        // (2^7, 2^7)
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t f16_to_e4m3x4(uint32_t lo, uint32_t hi) {
     uint32_t r;
     asm("{\n\t.reg .b16 l, u;\n\t"

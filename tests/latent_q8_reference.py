@@ -5,12 +5,13 @@ Bounds, beside those of tests/latent_reference.py.
 - The tensor cores take a query as the sum of two e4m3 numbers under one power of two.  Two e4m3 numbers hold eight
   significant bits; the last step is 2^-9 of the power, so a channel is off by at most 2^-10 * 2^e_q, with
   2^e_q <= max |q| / 224: a score is off by that times sum_i |k_i|, on top of its products' rounding.
-- A softmax weight, times the row's 2^e_j, goes in as an e4m3 and an e5m2 number, under a reference that is the row's and
-  changes from tile to tile (128 cached rows).  e4m3 leaves at most 2^-4 of a weight of 2^-6 or more (in units of the
-  reference), of which e5m2 (three significant bits) leaves 2^-3 / 2: 2^-8 in all (U).  Of a smaller weight e4m3 leaves at
-  most 2^-10, of which e5m2 leaves 2^-13; e5m2 itself ends at steps of 2^-16.  A tile's largest weight may lie below 2^-5
-  at most twice in turn (the third such tile lowers the reference), so that the largest among a tile and the two before it
-  is 2^-5 or more, and a weight is off by at most 2^-13 = 2^-8 * 2^-5: 2^-8 of that largest one.
+- A softmax weight, times the row's 2^e_j, goes in as an e4m3 and a second 8-bit number, under a reference that is the
+  row's and changes from tile to tile (128 cached rows).  e4m3 leaves at most 2^-4 of a weight of 2^-6 or more (in units of
+  the reference).  Of that the second number, e5m2 with three significant bits, leaves 2^-3 / 2 and so 2^-8 in all (U);
+  e4m3 of 2^7 times the rest, with four bits, leaves half as much.  Of a smaller weight e4m3 leaves at most 2^-10, of which
+  e5m2 leaves 2^-13 (e4m3 of 2^7 times it: 2^-14); both end at 2^-17.  A tile's largest weight may lie below 2^-5 at most
+  twice in turn (the third such tile lowers the reference), so that the largest among a tile and the two before it is 2^-5
+  or more, and a weight is off by at most 2^-13 = 2^-8 * 2^-5: 2^-8 of that largest one.
 """
 import math
 
