@@ -34,8 +34,8 @@
 // into W.
 //
 // Measured (GB300, 6761 GB/s measured copy rate; ragged lengths of 1/4 to all of the stated context), one token: 64
-// sequences of up to 8192, 32 heads, 46.5 us (0.59 of that rate; bf16 cache 70 us); 64 heads 59.0 us, 744 TFLOP/s; 256 of up
-// to 8192, no rope, 128.6 us (0.78; bf16 210 us); one of 131072 26.3 us (0.43; bf16 36.8 us).  What is missing, at 32 heads:
+// sequences of up to 8192, 32 heads, 45.7 us (0.60 of that rate; bf16 cache 70 us); 64 heads 58.6 us, 749 TFLOP/s; 256 of up
+// to 8192, no rope, 128.4 us (0.78; bf16 209 us); one of 131072 25.9 us (0.43; bf16 36.6 us).  What is missing, at 32 heads:
 // 17% in the tiles (a tile's 3400 cycles are a chain: its load behind freed slots, 900 cycles of products for S, 1700 from S
 // to W, 1000 of products for O; the slots hold two tiles and a half), and what is fixed: 1.6 us until a block knows its run,
 // 3 us until its queries are quantised, 2 us from its last row to its stored result, 4 us of join.  At 64 heads the slots
