@@ -12,6 +12,9 @@ Bounds, beside those of tests/latent_reference.py.
   e5m2 leaves 2^-13 (e4m3 of 2^7 times it: 2^-14); both end at 2^-17.  A tile's largest weight may lie below 2^-5 at most
   twice in turn (the third such tile lowers the reference), so that the largest among a tile and the two before it is 2^-5
   or more, and a weight is off by at most 2^-13 = 2^-8 * 2^-5: 2^-8 of that largest one.
+- The reference is not the maximum: the exponent of the largest weight lies in -5 .. 9 and not at 0, is rounded to 2^-21 at
+  most, and the exponential of it is good to 2^-22.  A weight moves by a share of 2^-21 ln 2 + 2^-22, and so does the sum:
+  2^-20 bounds the two logarithms' roundings with it (lse near 0 would otherwise have no room for them).
 """
 import math
 
@@ -101,6 +104,7 @@ def decode(q_latent, q_rope, cache, scales, table, lens, scale):
             top = torch.maximum(torch.maximum(top[:, 2:], top[:, 1:-1]), top[:, :-2])        # of a tile and the two before it
             top = top[:, :, None].expand_as(w).reshape(p.shape[0], -1)[:, :length]
             low = torch.where(hidden, torch.zeros_like(top), U * top) @ y[:, :512].abs()
+            off = off + 2.0 ** -20
             bo = bo + 2 * off[:, None] * (p @ c[:, :512].abs()) + low
             bs = bs + off
         parts.append((o, lse, bo, bs))
