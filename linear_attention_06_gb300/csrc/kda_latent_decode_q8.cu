@@ -145,7 +145,6 @@ template <int N>
 __device__ __forceinline__ void load_cols(uint32_t at, uint32_t (&r)[N]) {
     if constexpr (N == 8) tmem_ld8(at, r);
     if constexpr (N == 16) tmem_ld16(at, r);
-    if constexpr (N == 32) tmem_ld32(at, r);
 }
 
 // Reduces v[h] over the warp's lanes, for N values at once: each step halves the values a lane still holds, so N - 1 (and
