@@ -473,7 +473,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 }
                 uint32_t most = max(largest(x[0]), largest(x[1]));
                 if constexpr (ROPE) most = max(most, __shfl_sync(0xffffffffu, rope_most, i * 8));
-                const int k = power_for(__reduce_max_sync(0xffffffffu, most));           // also: all lanes have read the row
+                most = __reduce_max_sync(0xffffffffu, most);         // also: all lanes have read the row
+                const int k = power_for(most);
                 if ((lane >> 3) == i) rope_power = k;
                 __syncwarp();
 #pragma unroll
@@ -487,7 +488,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                                                   sw128_offset(term * NR + r, (slice & 1) * 64 + (lane & 7) * 8)) = y[term];
                 }
                 if (lane == 0) {
-                    sw->unit[r] = a.scale * 1.44269504088896340736f * two_to(k);
+                    // (8-bit numbers end at 448: an infinite channel makes its row's scores NaN here)
+                    sw->unit[r] = most < 0x7f800000u ? a.scale * 1.44269504088896340736f * two_to(k) : NAN;
                     sw->ref[r] = 0.f;
                     sw->top[r] = -INFINITY;
                 }

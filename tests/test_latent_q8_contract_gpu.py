@@ -125,6 +125,28 @@ def test_nan_reaches_no_neighbour():
     assert torch.equal(out[0], want[0]) and torch.equal(out[2], want[2]) and bool(out[1].isnan().any())
 
 
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("H", [16, 32, 64])
+def test_an_infinite_query_is_not_answered(H, value):
+    """An infinite channel has no 8-bit number: its row of the results is NaN, as a NaN channel's is, the others as before; a
+    row that sees nothing stays empty."""
+    g = gen(52)
+    cache, scales = full_cache(g, 60, 64, 64)
+    table = torch.arange(60, dtype=torch.int32, device=DEV).view(3, 20)
+    q, qr = randn(g, 3, H, 512), randn(g, 3, H, 64)
+    args = (q, qr, cache, scales, table, i32([1200, 100, 0]), 0.07)
+    want, wl = kda.kda_latent_decode_q8(*args, lse=True)
+    keep = torch.ones(3, H, dtype=torch.bool, device=DEV)
+    for x, n, h, i in ((q, 0, 5, 300), (qr, 0, H - 1, 63), (q, 1, 0, 0), (q, 2, 3, 9)):
+        x[n, h, i] = value
+        keep[n, h] = n == 2
+    out, lse = kda.kda_latent_decode_q8(*args, lse=True)
+    clean()
+    assert bool(out[~keep].isnan().all()) and bool(lse[~keep].isnan().all())
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], wl[keep])
+    assert bool((out[2] == 0).all()) and bool((lse[2] == -float("inf")).all())
+
+
 def test_captured_calls_behind_two_branches():
     """A capture that forks and joins: calls that may start early behind work of two streams, replayed with new rows."""
     g = gen(41)
