@@ -14,10 +14,16 @@
 // - A weight w_rj = 2^{log2 p_rj + e_j - m_r} as e4m3 and, of what that leaves, 2^7 times in e4m3 with accumulators of its
 //   own (up to 32 rows) or e5m2 in the same ones (64 rows, whose accumulators take all there is): 2^-9 or 2^-8 of the
 //   weight (bf16: 2^-8), and steps of 2^-16 where it is faint.  The row's reference m_r is a whole number (scores near 0
-//   keep their bits beside e_j, and moves are exact) and is held where the tiles' largest weights lie in 2^-5 .. 2^6 or
-//   2^8.75: raised at once, lowered where two tiles in turn were below (a first token that takes nearly all weight and a
-//   long faint tail behind it is what models really do), but never to more than 2^30 under the highest before it: O and the
-//   sums then stay far inside fp32.
+//   keep their bits beside e_j, and moves are exact).  It is raised at once where a weight would pass 2^6 or 2^8.75.  It is
+//   lowered where faint weights count: a token of 2^-12 is lost in silence, a thousand of them beside a few bright ones (a
+//   first token that takes nearly all weight and a long flat tail behind it is what models really do) are not.  So each row
+//   keeps an account of what its weights lost, |w - w' - w''|, less 2^-8.5 of the weights, and a row in debt puts the next
+//   tile at kLowSet and starts anew.  A tile's losses are known two tiles later: they are summed behind its products, and
+//   the accounts meet at the next vote.  A tile loses 2^-8 (2^-7 with e5m2) at most, if all 128 weights lie where the steps
+//   are coarsest, beside a first tile of 2^kSet; what is lost in all is below 2^-7 of the sum, and 3.6e-3 of it at most in
+//   8192 tokens with bright ones every 1 to 8 tiles and tails of 2^-8 .. 2^-20.  (With references held by the tiles'
+//   largest weights alone, 2^-5 or more in one tile of three, the same tails lost up to 8%.)  Never lower than 2^-30 of the
+//   highest reference before it: O and the sums then stay far inside fp32.
 //
 // Products, per tile of 128 cached rows (NR = query rows of a block, 16, 32 or 64):
 //   S [128 tokens x 2 NR]  = Y X^T            M = 128, N = 2 NR (x' and x'' of each row), K = 512 + rope
@@ -26,8 +32,8 @@
 // The tokens lie on the lanes of tensor memory, so a softmax thread has one token of its rows: 2^{e_j} is one number a
 // thread, weights of consecutive rows pack into words, and the tile's operands keep the full M = 128 (with the rows on the
 // lanes a product of 64 rows takes as long, and the sum of the two terms crosses warps).  What that layout makes dear, a
-// maximum over tokens, is not needed in every tile: references move only when a vote finds a tile outside the range
-// above; the sums stay in registers, a part a thread, until the piece ends.
+// maximum over tokens, is not needed in every tile: references move only when a vote finds a weight too large or a row in
+// debt; the sums stay in registers, a part a thread, until the piece ends.
 //
 // Work: as in the bf16 decode, one line of tiles in equal runs (kda_latent_line.cuh).  Block: a producer warp (TMA boxes
 // of page rows), an issuing warp, a query loader, and two or four teams of four warps that quantise the queries and turn S
@@ -71,9 +77,6 @@ constexpr int kBar = 1;                       // named barriers: all softmax war
 // sequences of at most three tiles are not cut (57 of up to 1084, 8 tokens x 12 heads: 35.5 us, 38.4 with four; 182 of up to
 // 285, 64 heads: 28.9, 30.3 with one).
 constexpr int kPlaces = 3, kShort = 3;
-// log2 of a tile's largest weight: where a piece's first tile is put, the bounds, and where a tile beyond one of them is
-// put: near that bound, so that tiles as they were before stay inside the range.
-constexpr float kSet = -1.f, kLow = -5.f, kLowSet = -2.f;
 constexpr float kDeep = 30.f;                 // log2 of how far a reference may lie below the highest before it
 
 // Shared memory of a block with NR query rows: queries [slice][2 NR][128 bytes], their rope slice [2 NR][64], weights
@@ -87,8 +90,12 @@ struct Cfg {
     static constexpr bool kWide = NR <= 32;
     static constexpr uint32_t kO = kWide ? 2 * NR : NR, kTiles = kWide ? 1 : 2;
     static constexpr uint32_t kPitch = NR == 16 ? 32 : 64, kPTile = kRows * kPitch;
-    // log2 of the largest weight that fits, and where a larger one is put: 64, whose rest times 2^7 is at most 256, and 448
-    static constexpr float kHigh = kWide ? 6.f : 8.75f, kHighSet = kWide ? 5.f : 8.f;
+    // log2 of a tile's largest weight: the largest that fits (64, whose rest times 2^7 is at most 256, and 448) and where a
+    // larger one is put, where a piece's first tile is put, and where a tile is put whose row has lost too much
+    static constexpr float kHigh = kWide ? 6.f : 8.75f, kHighSet = kWide ? 4.f : 6.f;
+    static constexpr float kSet = kWide ? 1.f : 2.f, kLowSet = kWide ? 2.f : 3.f;
+    // -2^-8.5, the share of its weights that a row may lose, in fp16 pairs; the rest of a wide weight is held times 2^7
+    static constexpr uint32_t kShare = kWide ? 0xb5a8b5a8u : 0x99a899a8u;
     static constexpr uint32_t kQ = 0, kQR = 4 * kQSlice, kP = kQR + kQRope;
     static constexpr uint32_t kBuffers = NR == 64 ? 1 : 2;
     static constexpr uint32_t kRopeAt = kP + kBuffers * kTiles * kPTile, kSliceAt = kRopeAt + (ROPE ? 8192 : 0);
@@ -109,12 +116,15 @@ struct Small : Line {
     uint64_t o_free, drain;
     uint32_t tmem;
     int piece[5], more;                       // the softmax warps' piece
-    alignas(16) uint2 vote[2][16];            // a tile's votes, a warp each: rows that are bright enough; any too large
+    uint32_t vote[2][16];                     // a tile's votes, a warp each: any weight too large
     alignas(16) float ref[64], top[64];       // -m_r, and the highest m_r has been
     alignas(16) float move[64];               // by how much m_r moves; at a piece's end O's factor
     alignas(16) float unit[64];               // scale log2(e) 2^k of the query row
     alignas(16) int seen[64];                 // tokens that the row sees
-    alignas(16) float red[4][4][16];          // a team's, a warp's: maxima, sums
+    union {                                   // each team's part, whichever it is
+        alignas(16) float red[4][4][16];      // a team's, a warp's: maxima, sums
+        uint32_t loss[4][2][4][8];            // a team's, a tile's, a warp's: what its rows lost, in pairs
+    };
 };
 static_assert(sizeof(Small) <= 3 * 1024, "small area");
 
@@ -163,6 +173,23 @@ __device__ __forceinline__ float reduce_rows(float (&v)[N], const Op& op) {
         }
     }
     for (; d >= 1; d /= 2) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], d));
+    return v[0];
+}
+// The same sum of N pairs of fp16 numbers.
+template <int N>
+__device__ __forceinline__ uint32_t sum_pairs(uint32_t (&v)[N]) {
+    const int lane = threadIdx.x & 31;
+    int d = 16;
+#pragma unroll
+    for (int n = N / 2; n >= 1; n /= 2, d /= 2) {
+        const bool upper = lane & d;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const uint32_t mine = upper ? v[i + n] : v[i], other = upper ? v[i] : v[i + n];
+            v[i] = add_f16x2(mine, __shfl_xor_sync(0xffffffffu, other, d));
+        }
+    }
+    for (; d >= 1; d /= 2) v[0] = add_f16x2(v[0], __shfl_xor_sync(0xffffffffu, v[0], d));
     return v[0];
 }
 
@@ -536,8 +563,13 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             const int least = p.len - a.tokens_per_seq + 1 + group * NR / a.H;      // tokens that the first row sees
 
             uint8_t byte = byte_of(off, page);
-            uint32_t faint = 0;               // rows whose tile before was below the range
-            bool lower = false;               // some row's two tiles before were
+            // What a lane knows of two of its team's rows (as every warp of the team does): what they lost so far less their
+            // share, by how much their references moved in this tile; its warp's losses in the tile before; and which rows
+            // lost too much, the even and the odd ones.
+            constexpr int kPairs = NH / 2;
+            const int pair_row = h0 + 2 * (lane % kPairs);
+            float2 lost = make_float2(0.f, 0.f), moved = make_float2(1.f, 1.f);
+            uint32_t lost_here = 0, sick[2] = {0, 0};
             float l[NH];
 #pragma unroll
             for (int i = 0; i < NH; ++i) l[i] = 0.f;
@@ -553,7 +585,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 constexpr int N = NH;                                // rows a step
                 float x[NH];                  // the weights
                 uint32_t y[2][NH / 4];        // in 8 bits, both terms
-                bool move = j == 0 || lower;  // references have to move: a piece's first tile sets them
+                uint32_t held[kPairs], rest[kPairs], theirs = 0;     // the weights in fp16, what the first term left
+                bool move = j == 0 || sick[0] != 0 || sick[1] != 0;  // references have to move: a piece's first tile sets them
                 bool voted = false, stop = false;
                 for (;;) {
 #pragma unroll
@@ -583,6 +616,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
 #pragma unroll
                         for (int i = 0; i < NH; ++i) v[i] = x[i];
                         const float mx = reduce_rows<NH>(v, [](float p, float q) { return fmaxf(p, q); });
+                        team_sync(team);                             // the losses that were here have been read
                         if (lane % (32 / NH) == 0) sw->red[team][w][lane / (32 / NH)] = mx;
                         team_sync(team);
                         const int i = t & 127;
@@ -590,9 +624,10 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                             const float z = fmaxf(fmaxf(sw->red[team][0][i], sw->red[team][1][i]),
                                                   fmaxf(sw->red[team][2][i], sw->red[team][3][i]));
                             const float m = -sw->ref[h0 + i], top = sw->top[h0 + i];
+                            const bool low = (i & 1 ? sick[1] : sick[0]) >> (i >> 1) & 1 && z < G::kLowSet - 0.5f;
                             float n = m;
-                            if (z > -INFINITY && (j == 0 || z > G::kHigh || z < kLow)) {
-                                n = fmaxf(m + rintf(z - (j == 0 ? kSet : z > G::kHigh ? G::kHighSet : kLowSet)), top - kDeep);
+                            if (z > -INFINITY && (j == 0 || z > G::kHigh || low)) {
+                                n = fmaxf(m + rintf(z - (j == 0 ? G::kSet : z > G::kHigh ? G::kHighSet : G::kLowSet)), top - kDeep);
                                 sw->ref[h0 + i] = -n;
                                 sw->top[h0 + i] = fmaxf(top, n);
                             }
@@ -630,11 +665,16 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                             }
                         }
                         tmem_wait_st();
-                        faint = 0;
-                        lower = false;
+                        // a row that was told to move starts a new account
+                        const uint32_t bit = 1u << lane % kPairs;
+                        const float2 f = make_float2(exp2_fast(fminf(fmaxf(-sw->move[pair_row], -126.f), 100.f)),
+                                                     exp2_fast(fminf(fmaxf(-sw->move[pair_row + 1], -126.f), 100.f)));
+                        lost = make_float2((sick[0] & bit ? fminf(lost.x, 0.f) : lost.x) * f.x,
+                                           (sick[1] & bit ? fminf(lost.y, 0.f) : lost.y) * f.y);
+                        moved = make_float2(moved.x * f.x, moved.y * f.y);
+                        sick[0] = sick[1] = 0;
                     }
                     float most = x[0];
-                    uint32_t bright = 0;      // a bit a row: this token's weight is 2^kLow or more
 #pragma unroll
                     for (int i = 1; i < NH; ++i) most = fmaxf(most, x[i]);
 #pragma unroll
@@ -644,33 +684,26 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                         y[0][i / 4] = to_e4m3x4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                         uint32_t lo, hi;
                         e4m3x4_to_f16(y[0][i / 4], lo, hi);
-                        lo = sub_f16x2(to_f16x2(x[i], x[i + 1]), lo);
-                        hi = sub_f16x2(to_f16x2(x[i + 2], x[i + 3]), hi);
-                        y[1][i / 4] = G::kWide ? f16_to_e4m3x4(mul_f16x2(lo, k128), mul_f16x2(hi, k128)) : f16_to_e5m2x4(lo, hi);
+                        held[i / 2] = to_f16x2(x[i], x[i + 1]);
+                        held[i / 2 + 1] = to_f16x2(x[i + 2], x[i + 3]);
+                        lo = sub_f16x2(held[i / 2], lo);
+                        hi = sub_f16x2(held[i / 2 + 1], hi);
+                        rest[i / 2] = G::kWide ? mul_f16x2(lo, k128) : lo;
+                        rest[i / 2 + 1] = G::kWide ? mul_f16x2(hi, k128) : hi;
+                        y[1][i / 4] = G::kWide ? f16_to_e4m3x4(rest[i / 2], rest[i / 2 + 1]) : f16_to_e5m2x4(rest[i / 2], rest[i / 2 + 1]);
                     }
                     if (j == 0 || voted) break;
-                    // e4m3 numbers of 2^-5 or more have one of the bits 0x70
-#pragma unroll
-                    for (int i = 0; i < NH / 4; ++i) bright |= (((y[0][i] & 0x70707070u) + 0x70707070u) & 0x80808080u) >> i;
-                    bright = __reduce_or_sync(0xffffffffu, bright);
                     const bool high = __any_sync(0xffffffffu, most > G::kHigh);
-                    if (lane == 0) sw->vote[j & 1][warp - 4] = make_uint2(bright, high);
+                    if (lane == 0) sw->vote[j & 1][warp - 4] = high;
+                    if (lane % (32 / kPairs) == 0) sw->loss[team][j & 1][w][lane / (32 / kPairs)] = lost_here;
                     // once a tile, by all teams, whatever their references do: the barrier is all softmax warps'
                     if (soft_or<kSoft>(!ok)) { stop = true; break; }
                     voted = true;
-                    uint32_t all_bright = 0, any_high = 0;
+                    uint32_t any_high = 0;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint2 v = sw->vote[j & 1][team * 4 + k];
-                        all_bright |= v.x;
-                        any_high |= v.y;
-                    }
-                    constexpr uint32_t kAll = NH == 16 ? 0xf0f0f0f0u : 0xc0c0c0c0u;
-                    if (!any_high) {
-                        lower = faint & ~all_bright & kAll;
-                        faint = ~all_bright;
-                        break;
-                    }
+                    for (int k = 0; k < 4; ++k) any_high |= sw->vote[j & 1][team * 4 + k];
+                    theirs = sw->loss[team][j & 1][lane / kPairs & 3][lane % kPairs];
+                    if (!any_high) break;
                     move = true;              // once more from the scores
                 }
                 if (stop) { ok = false; break; }
@@ -711,6 +744,29 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                     l[i] = v.x;
                     l[i + 1] = v.y;
                 }
+                // what the tile before lost joins the accounts; this one's loss is summed over the warp for the next vote
+                float2 loss = f16x2_to_floats(theirs);
+#pragma unroll
+                for (int d = kPairs; d <= 2 * kPairs; d *= 2) {
+                    loss.x += __shfl_xor_sync(0xffffffffu, loss.x, d);
+                    loss.y += __shfl_xor_sync(0xffffffffu, loss.y, d);
+                }
+                lost = make_float2(fmaf(loss.x, moved.x, lost.x), fmaf(loss.y, moved.y, lost.y));
+                moved = make_float2(1.f, 1.f);
+                constexpr uint32_t kRowPairs = (1u << kPairs) - 1;
+                sick[0] = __ballot_sync(0xffffffffu, lost.x > 0.f) & kRowPairs;
+                sick[1] = __ballot_sync(0xffffffffu, lost.y > 0.f) & kRowPairs;
+#pragma unroll
+                for (int i = 0; i < NH; i += 4) {
+                    uint32_t lo, hi;
+                    if constexpr (G::kWide)
+                        e4m3x4_to_f16(y[1][i / 4], lo, hi);
+                    else
+                        e5m2x4_to_f16(y[1][i / 4], lo, hi);
+                    rest[i / 2] = fma_f16x2(held[i / 2], G::kShare, sub_f16x2(rest[i / 2], lo) & 0x7fff7fffu);
+                    rest[i / 2 + 1] = fma_f16x2(held[i / 2 + 1], G::kShare, sub_f16x2(rest[i / 2 + 1], hi) & 0x7fff7fffu);
+                }
+                lost_here = sum_pairs<kPairs>(rest);
                 ++tile;
                 sb.next();
                 in.next(); in.next(); in.next(); in.next();

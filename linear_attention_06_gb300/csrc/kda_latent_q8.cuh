@@ -60,6 +60,16 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
 constexpr uint32_t k128 = 0x58005800u;        // (2^7, 2^7)
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -92,6 +102,14 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t
         "mov.b32 {l, u}, %2;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
         "cvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+}
+__device__ __forceinline__ void e5m2x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, u;\n\t"
+        "mov.b32 {l, u}, %2;\n\t"
+        "cvt.rn.f16x2.e5m2x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e5m2x2 %1, u;\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(x));
 }
