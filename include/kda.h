@@ -497,14 +497,14 @@ kda_status kda_latent_gather_q8(const kda_latent_shape* shape, const void* cache
                                 void* latent, void* k_rope, kda_stream_t stream);
 
 /*
- * kda_latent_decode_q8 -- kda_latent_decode over an 8-bit cache: the same formulas, on the rows' values.  Scores,
- * maxima, sums and partial results are fp32.  The tensor cores multiply 8-bit numbers, so queries and softmax weights go
+ * kda_latent_decode_q8 -- kda_latent_decode over an 8-bit cache: the same formulas, on the rows' values.  Scores and the
+ * products behind them, maxima, sums and partial results are fp32.  The tensor cores multiply 8-bit numbers, so queries and softmax weights go
  * in as sums of two:
  * - a query row as two e4m3 numbers a channel under one power of two: all eight bits of a bf16 channel down to about
  *   2^-10 of the row's largest, absolute steps of 2^-18 of that below;
  * - a weight, times its row's 2^e, as e4m3 and e4m3 or e5m2: off by at most 2^-8 of itself, which is bf16's half step, or,
  *   where it is faint beside others, by more; the weights of a query row, each times its 2^e, are together off by at most
- *   2^-7 of their sum (of two or three tenths of that in common use).
+ *   2^-7 of their sum, and in common use by about 2^-9.
  * A row of the cache that holds NaN reaches its sequence's results; an infinite or NaN channel of a query makes that
  * query's own row of out and lse NaN (where it sees any token).
  * Errors: kda_latent_decode's, with kda_latent_decode_q8_workspace_size; KDA_ERR_INVALID_ARG also for scales NULL with

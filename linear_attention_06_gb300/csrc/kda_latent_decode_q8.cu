@@ -25,6 +25,9 @@
 //   largest weights alone, 2^-5 or more in one tile of three, the same tails lost up to 8%.)  Never lower than 2^-30 of the
 //   highest reference before it: O and the sums then stay far inside fp32.
 //
+// The sums are those of w 2^-e, exact powers, while e is at most kPlainPower; rows of larger e beside rows of zeros would
+// spread them over more than fp32 has, and then they are taken of p itself, under references of their own (`apart`).
+//
 // Products, per tile of 128 cached rows (NR = query rows of a block, 16, 32 or 64):
 //   S [128 tokens x 2 NR]  = Y X^T            M = 128, N = 2 NR (x' and x'' of each row), K = 512 + rope
 //   O^T [512 x 2 NR]      += C^T [W' W'']^T          four blocks of M = 128 channels, N = 2 NR, K = 128 tokens (64 rows:
@@ -50,6 +53,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -78,6 +82,9 @@ constexpr int kBar = 1;                       // named barriers: all softmax war
 // 285, 64 heads: 28.9, 30.3 with one).
 constexpr int kPlaces = 3, kShort = 3;
 constexpr float kDeep = 30.f;                 // log2 of how far a reference may lie below the highest before it
+// The sums of p are those of the weights times 2^-e, in units of 2^m too, while all rows' e are at most this: a row's sum is
+// then 2^-15 or more, and what a weight below 2^-126 would have added to it, 2^-62 at most, is nothing.
+constexpr int kPlainPower = 15;
 
 // Shared memory of a block with NR query rows: queries [slice][2 NR][128 bytes], their rope slice [2 NR][64], weights
 // [buffers][128 tokens][2 NR] or, with 64 rows, [2 terms][128 tokens][NR], a tile's rope slice, then the latent slices (128 channels) of the tiles in flight.
@@ -116,9 +123,10 @@ struct Small : Line {
     uint64_t o_free, drain;
     uint32_t tmem;
     int piece[5], more;                       // the softmax warps' piece
-    uint32_t vote[2][16];                     // a tile's votes, a warp each: any weight too large
+    uint32_t vote[2][16];                     // a tile's votes, a warp each: any weight too large, any e above kPlainPower
     alignas(16) float ref[64], top[64];       // -m_r, and the highest m_r has been
-    alignas(16) float move[64];               // by how much m_r moves; at a piece's end O's factor
+    alignas(16) float move[64];               // by how much m_r moves; at a piece's end O's (second) factor
+    alignas(16) float off[64];                // the sums' reference less m_r; at a piece's end O's first factor
     alignas(16) float unit[64];               // scale log2(e) 2^k of the query row
     alignas(16) int seen[64];                 // tokens that the row sees
     union {                                   // each team's part, whichever it is
@@ -570,6 +578,44 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             const int pair_row = h0 + 2 * (lane % kPairs);
             float2 lost = make_float2(0.f, 0.f), moved = make_float2(1.f, 1.f);
             uint32_t lost_here = 0, sick[2] = {0, 0};
+            // The sums under references of their own, in the smallest code rather than the fastest (unrolled, it cost ordinary
+            // calls 3%: 256 x 8192 cached tokens, no rope, 143 us and not 138): from then on l stands still.  The team's
+            // thread of a row's number has the sum of the tiles since, and by how much the reference has risen since.
+            bool apart = false;
+            float sum_apart = 0.f, risen = 0.f;
+            auto add_apart = [&](uint32_t s_at, float two_e, int unseen) {
+#pragma unroll 1
+                for (int round = 0; round < 2; ++round) {            // maxima, sums
+                    team_sync(team);                                 // what was here has been read
+#pragma unroll 1
+                    for (int i = 0; i < NH; ++i) {
+                        const float s = __uint_as_float(tmem_ld1(s_at + i)) + __uint_as_float(tmem_ld1(s_at + NR + i));
+                        float u = fmaf(s * two_e, sw->unit[h0 + i], sw->ref[h0 + i] - sw->off[h0 + i]);
+                        if (unseen >= sw->seen[h0 + i]) u = -INFINITY;
+                        if (round) u = exp2_fast(u);
+#pragma unroll 1
+                        for (int d = 16; d; d >>= 1) {
+                            const float other = __shfl_xor_sync(0xffffffffu, u, d);
+                            u = round ? u + other : fmaxf(u, other);
+                        }
+                        if (lane == 0) sw->red[team][w][i] = u;
+                    }
+                    team_sync(team);
+                    const int i = t & 127;
+                    if (i < NH) {
+                        const float* r = &sw->red[team][0][i];
+                        if (round) {
+                            sum_apart += (r[0] + r[16]) + (r[32] + r[48]);
+                        } else {
+                            const float up = fmaxf(rintf(fmaxf(fmaxf(r[0], r[16]), fmaxf(r[32], r[48]))), 0.f);
+                            sw->off[h0 + i] += up;
+                            sum_apart *= exp2_fast(-up);
+                            risen += up;
+                        }
+                    }
+                }
+                team_sync(team);
+            };
             float l[NH];
 #pragma unroll
             for (int i = 0; i < NH; ++i) l[i] = 0.f;
@@ -583,6 +629,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 tc_fence_after();
                 const float2 two_e = make_float2(two_to(e), two_to(e)), fe = make_float2((float)e, (float)e);
                 constexpr int N = NH;                                // rows a step
+                const int unseen = least - base < kRows ? base + tok : INT_MIN;      // where some rows do not see some tokens
+                const uint32_t s_at = s_lanes + sb.slot * 2 * NR;
                 float x[NH];                  // the weights
                 uint32_t y[2][NH / 4];        // in 8 bits, both terms
                 uint32_t held[kPairs], rest[kPairs], theirs = 0;     // the weights in fp16, what the first term left
@@ -592,8 +640,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
 #pragma unroll
                     for (int c = 0; c < NH; c += N) {                // log2 of the weights
                         uint32_t s1[N], s2[N];
-                        load_cols<N>(s_lanes + sb.slot * 2 * NR + c, s1);
-                        load_cols<N>(s_lanes + sb.slot * 2 * NR + NR + c, s2);
+                        load_cols<N>(s_at + c, s1);
+                        load_cols<N>(s_at + NR + c, s2);
                         tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < N; i += 4) {
@@ -606,10 +654,10 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                             x[c + i] = v.x; x[c + i + 1] = v.y; x[c + i + 2] = w.x; x[c + i + 3] = w.y;
                         }
                     }
-                    if (least - base < kRows) {                      // tokens that some rows do not see
+                    if (unseen >= 0) {
 #pragma unroll
                         for (int i = 0; i < NH; ++i)
-                            if (base + tok >= sw->seen[h0 + i]) x[i] = -INFINITY;
+                            if (unseen >= sw->seen[h0 + i]) x[i] = -INFINITY;
                     }
                     if (move) {               // the team agrees
                         float v[NH];
@@ -619,8 +667,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                         team_sync(team);                             // the losses that were here have been read
                         if (lane % (32 / NH) == 0) sw->red[team][w][lane / (32 / NH)] = mx;
                         team_sync(team);
-                        const int i = t & 127;
-                        if (i < NH) {
+                        if (const int i = t & 127; i < NH) {
                             const float z = fmaxf(fmaxf(sw->red[team][0][i], sw->red[team][1][i]),
                                                   fmaxf(sw->red[team][2][i], sw->red[team][3][i]));
                             const float m = -sw->ref[h0 + i], top = sw->top[h0 + i];
@@ -632,6 +679,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                                 sw->top[h0 + i] = fmaxf(top, n);
                             }
                             sw->move[h0 + i] = n - m;
+                            if (j == 0 || apart) sw->off[h0 + i] = j == 0 ? 0.f : sw->off[h0 + i] - (n - m);
                         }
                         team_sync(team);
                         if (j > 0) ok = ok && have_products(tile - 1);
@@ -645,8 +693,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                                 const float d = sw->move[h0 + c + n];
                                 still = still && d == 0.f;
                                 x[c + n] -= d;
-                                f[n] = exp2_fast(fminf(fmaxf(-d, -126.f), 100.f));
-                                l[c + n] *= f[n];
+                                f[n] = exp2_fast(fminf(-d, 100.f));  // 0 where it is below 2^-126
+                                if (!apart) l[c + n] *= f[n];
                             }
                             if (j > 0 && ok && !still) {             // O^T, column r by f_r
 #pragma unroll 1
@@ -667,8 +715,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                         tmem_wait_st();
                         // a row that was told to move starts a new account
                         const uint32_t bit = 1u << lane % kPairs;
-                        const float2 f = make_float2(exp2_fast(fminf(fmaxf(-sw->move[pair_row], -126.f), 100.f)),
-                                                     exp2_fast(fminf(fmaxf(-sw->move[pair_row + 1], -126.f), 100.f)));
+                        const float2 f = make_float2(exp2_fast(fminf(-sw->move[pair_row], 100.f)),
+                                                     exp2_fast(fminf(-sw->move[pair_row + 1], 100.f)));
                         lost = make_float2((sick[0] & bit ? fminf(lost.x, 0.f) : lost.x) * f.x,
                                            (sick[1] & bit ? fminf(lost.y, 0.f) : lost.y) * f.y);
                         moved = make_float2(moved.x * f.x, moved.y * f.y);
@@ -692,21 +740,25 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                         rest[i / 2 + 1] = G::kWide ? mul_f16x2(hi, k128) : hi;
                         y[1][i / 4] = G::kWide ? f16_to_e4m3x4(rest[i / 2], rest[i / 2 + 1]) : f16_to_e5m2x4(rest[i / 2], rest[i / 2 + 1]);
                     }
-                    if (j == 0 || voted) break;
-                    const bool high = __any_sync(0xffffffffu, most > G::kHigh);
-                    if (lane == 0) sw->vote[j & 1][warp - 4] = high;
+                    if (voted) break;
+                    // (a large e in a later tile: once more too, without a move)
+                    uint32_t vote = __any_sync(0xffffffffu, most > G::kHigh || e > kPlainPower);
+                    if (vote) vote |= __any_sync(0xffffffffu, e > kPlainPower) ? 2 : 0;
+                    if (lane == 0) sw->vote[j & 1][warp - 4] = vote;
                     if (lane % (32 / kPairs) == 0) sw->loss[team][j & 1][w][lane / (32 / kPairs)] = lost_here;
                     // once a tile, by all teams, whatever their references do: the barrier is all softmax warps'
                     if (soft_or<kSoft>(!ok)) { stop = true; break; }
                     voted = true;
-                    uint32_t any_high = 0;
+                    uint32_t votes = 0;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) any_high |= sw->vote[j & 1][team * 4 + k];
+                    for (int k = 0; k < 4; ++k) votes |= sw->vote[j & 1][team * 4 + k];
+                    apart = apart || (votes & 2) != 0;
                     theirs = sw->loss[team][j & 1][lane / kPairs & 3][lane % kPairs];
-                    if (!any_high) break;
+                    if ((votes & 1) == 0) break;
                     move = true;              // once more from the scores
                 }
                 if (stop) { ok = false; break; }
+                if (__builtin_expect(apart, 0)) add_apart(s_at, two_to(e), unseen);
                 if (len - base < kRows) {                  // the tile's rows behind the sequence's end become zeros
                     const int valid = len - base < 0 ? 0 : len - base;
                     Ring<G::kSlices> slice = in;
@@ -720,24 +772,22 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 if (ok) {
                     uint8_t* pt = sm + G::kP + tile % G::kBuffers * G::kTiles * G::kPTile;
 #pragma unroll
-                    for (int term = 0; term < 2; ++term)
-#pragma unroll
-                        for (int c = 0; c < NH; c += N) {
-                            const uint32_t* v = &y[term][c / 4];
-                            const int col = h0 + c + (G::kWide ? term * NR : 0);
-                            const uint32_t off = (G::kWide ? 0 : term * G::kPTile) +
-                                                 (G::kPitch == 64 ? sw64_offset(tok, col) : sw32_offset(tok, col));
-                            if constexpr (N == 16)
-                                *reinterpret_cast<uint4*>(pt + off) = make_uint4(v[0], v[1], v[2], v[3]);
-                            else
-                                *reinterpret_cast<uint2*>(pt + off) = make_uint2(v[0], v[1]);
-                        }
+                    for (int term = 0; term < 2; ++term) {
+                        const uint32_t* v = y[term];
+                        const int col = h0 + (G::kWide ? term * NR : 0);
+                        const uint32_t off = (G::kWide ? 0 : term * G::kPTile) +
+                                             (G::kPitch == 64 ? sw64_offset(tok, col) : sw32_offset(tok, col));
+                        if constexpr (NH == 16)
+                            *reinterpret_cast<uint4*>(pt + off) = make_uint4(v[0], v[1], v[2], v[3]);
+                        else
+                            *reinterpret_cast<uint2*>(pt + off) = make_uint2(v[0], v[1]);
+                    }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0 && ok) mbar_arrive(&sw->p_full[tile % G::kBuffers]);
-                const float2 back = make_float2(two_to(-e), two_to(-e));
+                const float2 back = apart ? make_float2(0.f, 0.f) : make_float2(two_to(-e), two_to(-e));
 #pragma unroll
                 for (int i = 0; i < NH; i += 2) {
                     const float2 v = fma2(make_float2(x[i], x[i + 1]), back, make_float2(l[i], l[i + 1]));
@@ -787,13 +837,18 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             float* po = reinterpret_cast<float*>(ws + Work<NR>::o_at(gridDim.x));
             const float sum = reduce_rows<NH>(l, [](float p, float q) { return p + q; });
             if (lane % (32 / NH) == 0) sw->red[team][w][lane / (32 / NH)] = sum;
+            if (const int i = t & 127; i < NH) {                     // (a row's unit is not needed any more)
+                sw->move[h0 + i] = sum_apart;
+                sw->unit[h0 + i] = exp2_fast(-risen);
+            }
             soft_sync<kSoft>();
             if (t < NR) {
                 const float* part = &sw->red[t / NH][0][t % NH];
-                const float total = (part[0] + part[16]) + (part[32] + part[48]);
-                // total 2^m = f 2^k, f in [1, 2): no large m against a large logarithm, here and in the join
+                const float total = fmaf((part[0] + part[16]) + (part[32] + part[48]), sw->unit[t], sw->move[t]);
+                // total 2^(m + off) = f 2^k, f in [1, 2): no large m against a large logarithm, here and in the join
+                const float off = sw->off[t];
                 const int power = (int)(__float_as_uint(total) >> 23) - 127;
-                const float f = total == 0.f ? 0.f : total * two_to(-power), k = total == 0.f ? -INFINITY : (float)power - sw->ref[t];
+                const float f = total == 0.f ? 0.f : total * two_to(-power), k = total == 0.f ? -INFINITY : (float)power + (off - sw->ref[t]);
                 if (whole) {
                     const int64_t row = (int64_t)p.n * R + group * NR + t;
                     if (a.lse && t < rows && KDA_INDEX_OK(row, (int64_t)a.num_seqs * R, a.status))
@@ -801,7 +856,10 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                 } else if (KDA_INDEX_OK((int64_t)slot * NR + t, (int64_t)gridDim.x * 2 * NR, a.status)) {
                     ml[(int64_t)slot * NR + t] = make_float2(k, f);
                 }
-                sw->move[t] = total == 0.f ? 0.f : (whole ? 1.f / total : two_to(-power));
+                // O is in units of 2^m: times 2^-off in two steps, since O / total may be far from O 2^-off / total
+                const int half = -(int)off >> 1;
+                sw->move[t] = total == 0.f ? 0.f : (whole ? 1.f / total : two_to(-power)) * two_to(-(int)off - half);
+                sw->off[t] = two_to(half);
             }
             soft_sync<kSoft>();
             // the next piece's queries while this one's last products run (those with the queries are done: their S has
@@ -834,6 +892,14 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             o[b][i] = __float_as_uint(fmaf(__uint_as_float(rest[b][i]), 0x1p-7f, __uint_as_float(o[b][i])));
+                }
+                if (__builtin_expect(apart, 0)) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float g = sw->off[h0 + c + i];
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) o[b][i] = __float_as_uint(__uint_as_float(o[b][i]) * g);
+                    }
                 }
                 const int live = inside ? rows - h0 - c : 0;
 #pragma unroll

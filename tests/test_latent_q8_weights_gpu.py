@@ -27,6 +27,16 @@ def clean():
     assert kda.kda_device_status() == 0
 
 
+def paged(y, e, page):
+    """Numbers and powers of one sequence's rows on consecutive pages, NaN bytes behind its end."""
+    pages = -(-y.shape[0] // page)
+    cache = torch.full((pages * page, 512), 0x7F, dtype=torch.uint8, device=DEV)
+    scales = torch.zeros(pages * page, dtype=torch.uint8, device=DEV)
+    cache[:y.shape[0]] = q8.bytes_of(y).view(torch.uint8)
+    scales[:y.shape[0]] = (e + 127).to(torch.uint8)
+    return cache.view(q8.E4M3).view(pages, page, 512), scales.view(q8.E8M0).view(pages, page)
+
+
 def exact(q, y, e, scale):
     """Outputs, lse and bounds of rows q [R, 512] over cached rows (numbers y, powers e), all in 64 bits."""
     c = y * q8.two(e)[:, None]
@@ -102,10 +112,7 @@ def test_weights_that_fall_and_rise(H, T, rate, rising):
     x[:, 0] = -rate * math.log(2) * ((length - 1 - at if rising else at) // 128)
     x[::700, 0] += 6 * math.log(2)
     y, e = q8.quantise(x)
-    pad = -length % page
-    cache = torch.cat([q8.bytes_of(y).view(torch.uint8), torch.full((pad, 512), 0x7F, dtype=torch.uint8, device=DEV)])
-    cache = cache.view(q8.E4M3).view(-1, page, 512)
-    scales = torch.cat([q8.powers_of(e).view(torch.uint8), torch.zeros(pad, dtype=torch.uint8, device=DEV)]).view(q8.E8M0).view(-1, page)
+    cache, scales = paged(y, e, page)
     table = torch.arange(cache.shape[0], dtype=torch.int32, device=DEV).expand(n, -1).contiguous()
     q = torch.zeros(n * T, H, 512, device=DEV)
     q[..., 0] = torch.linspace(0.5, 1.0, H, device=DEV)
@@ -119,3 +126,101 @@ def test_weights_that_fall_and_rise(H, T, rate, rising):
             o, s, bo, bs = exact(q[i * T + t].double(), y[:seen], e[:seen], 1.0)
             ref.assert_within(lse[i * T + t], s, bs, "lse")
             ref.assert_within(out[i * T + t], o, bo, "out")
+
+
+# ---------------------------------------------------------------- rows of very different powers
+
+def numbers(g, count):
+    """e4m3 numbers of 64 .. 200, no channel that a query sees."""
+    y = q8.to_e4m3((64 + 136 * torch.rand(count, 512, generator=g, device=DEV, dtype=torch.float64)))
+    y[:, :2] = 0
+    return y
+
+
+def check_powers(y, e, score, H, sequences, page=64, T=1):
+    """Decodes rows of numbers y and powers e under scores `score` (natural logarithms; only rows of e <= 0 may have one),
+    seen by queries that weigh them by 1/2 to 1.  Zero channels of a query and of a row multiply to exact zeros, so the
+    scores are good to a few 2^-24 of themselves whatever the other channels are."""
+    y = y.clone()
+    y[:, 0] = q8.to_e4m3(score * q8.two(-e))
+    score = y[:, 0] * q8.two(e)
+    n = y.shape[0]
+    cache, scales = paged(y, e, page)
+    table = torch.arange(cache.shape[0], dtype=torch.int32, device=DEV).expand(sequences, -1).contiguous()
+    q = torch.zeros(sequences * T, H, 512, device=DEV)
+    q[..., 0] = torch.linspace(0.5, 1.0, H, device=DEV)
+    q[:, -1] = 0                                               # and one that weighs all alike
+    q = q.to(BF)
+    out, lse = kda.kda_latent_decode_q8(q, None, cache, scales, table,
+                                        torch.full((sequences,), n, dtype=torch.int32, device=DEV), 1.0, lse=True)
+    clean()
+    for i in (0, sequences - 1):
+        for t in range(T):
+            seen = n - T + 1 + t
+            row = i * T + t
+            c = y[:seen] * q8.two(e[:seen])[:, None]
+            s = q[row, :, 0].double()[:, None] * score[None, :seen]
+            z = torch.logsumexp(s, -1)
+            p = torch.exp(s - z[:, None])
+            size = s.abs().amax(-1)
+            # the sum: 2^-20 holds its 2^4 roundings a thread, the exponential's and the logarithms'
+            delta = 2.0 ** -22 * size + 2.0 ** -20 * (1 + size + z.abs())
+            ref.assert_within(lse[row], z, delta, "lse")
+            o = p @ c
+            held = (p * q8.two(e[:seen])).sum(-1, keepdim=True)
+            bound = q8.U * o.abs() + 2.0 ** -7 * held * y[:seen].abs().amax(0) + 4 * delta[:, None] * (p @ c.abs())
+            ref.assert_within(out[row], o, bound, "out")
+
+
+@pytest.mark.parametrize("H", [16, 32, 64])
+@pytest.mark.parametrize("top", [6, 16, 60, 70, 100, 119])
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed", "late"])
+def test_rows_of_powers_far_apart(H, top, order):
+    """Rows of zeros and rows of the largest powers beside each other, in one tile and tiles apart."""
+    g = gen(top + H)
+    count = 700
+    y = numbers(g, count)
+    if order == "mixed":
+        e = torch.randint(-64, top + 1, (count,), generator=g, device=DEV).double()
+    else:
+        e = torch.full((count,), float(top), dtype=torch.float64, device=DEV)
+        zeros = {"rising": slice(0, 256), "falling": slice(444, count), "late": slice(0, 650)}[order]
+        e[zeros] = -64
+        y[zeros] = 0
+    score = torch.zeros(count, dtype=torch.float64, device=DEV)
+    for sequences in (1, 152):
+        check_powers(y, e, score, H, sequences)
+
+
+@pytest.mark.parametrize("H,T", [(16, 1), (8, 4), (32, 2), (64, 1)])
+@pytest.mark.parametrize("seed", range(6))
+def test_rows_of_any_power_under_scores(H, T, seed):
+    """Powers of the whole format in random order, the small rows under scores that move the sums' reference."""
+    g = gen(100 + seed)
+    count = [300, 1000, 2500][seed % 3]
+    y = numbers(g, count)
+    e = torch.randint(-64, 120, (count,), generator=g, device=DEV).double()
+    steady = torch.arange(count, device=DEV) % 400 < [150, 390, 250][seed // 2]        # stretches of ordinary rows
+    e = torch.where(steady, torch.randint(-9, -4, (count,), generator=g, device=DEV).double(), e)
+    score = torch.where(steady, 3 * torch.randn(count, generator=g, device=DEV, dtype=torch.float64), 0.0)
+    score = score + torch.where(steady, 2.0 * (torch.arange(count, device=DEV) // 400), 0.0)
+    score = score.clamp(-448 * 2.0 ** -9, 448 * 2.0 ** -9) * (8 if seed % 2 else 1)
+    e = torch.where(steady & (score.abs() > 0), torch.maximum(e, torch.full_like(e, -6 if seed % 2 else -9)), e)
+    check_powers(y, e, score, H, 2, T=T)
+
+
+def test_missing_pages_before_large_rows():
+    """Pages outside the cache count as rows of zeros: 2 x 128 of them, then rows of the largest power."""
+    for top, H, N in ((70, 4, 152), (119, 32, 1), (119, 32, 152), (119, 64, 152)):
+        g = gen(top)
+        y, e = numbers(g, 256), torch.full((256,), float(top), dtype=torch.float64, device=DEV)
+        cache, scales = paged(y, e, 64)
+        table = torch.tensor([[-1, -1, 9, 9, 0, 1, 2, 3]] * N, dtype=torch.int32, device=DEV)
+        q = torch.zeros(N, H, 512, dtype=BF, device=DEV)
+        out, lse = kda.kda_latent_decode_q8(q, None, cache, scales, table, torch.tensor([512] * N, dtype=torch.int32, device=DEV),
+                                            1.0, lse=True)
+        clean()
+        o = (y * q8.two(e)[:, None]).sum(0) / 512
+        assert float((lse.double() - math.log(512)).abs().max()) <= 2.0 ** -20 * 8
+        for n in (0, N - 1):
+            ref.assert_within(out[n], o.expand(H, -1), (2 * q8.U + 2.0 ** -7) * o.abs().expand(H, -1), "out")
