@@ -118,10 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 latent_decode_kernel(const __grid_constant__ Maps maps, const LatentDecodeArgs a, const int groups, const int map_rows) {
     using G = Cfg<NR, ROPE>;
     extern __shared__ __align__(1024) uint8_t sm[];   // swizzled tiles start at multiples of 1024 bytes
-    if (smem_u32(sm) & 1023u) {               // the declaration's alignment
-        if (threadIdx.x == 0) atomicOr(a.status, kStatusTimeout);
-        return;
-    }
+    if (misaligned(sm, a)) return;
     Small* sw = reinterpret_cast<Small*>(sm + G::kSmall);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int runs = gridDim.x / groups, run = blockIdx.x / groups, group = blockIdx.x % groups;

@@ -233,10 +233,7 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
     constexpr int kTeams = teams_of(NR), kSoft = soft_of(NR), kThreads = threads_of(NR), kWarps = kSoft / 32;
     constexpr int NH = NR / kTeams;           // rows of a team
     extern __shared__ __align__(1024) uint8_t sm[];   // swizzled tiles start at multiples of 1024 bytes
-    if (smem_u32(sm) & 1023u) {               // the declaration's alignment
-        if (threadIdx.x == 0) atomicOr(a.status, kStatusTimeout);
-        return;
-    }
+    if (misaligned(sm, a)) return;
     Small* sw = reinterpret_cast<Small*>(sm + G::kSmall);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int runs = gridDim.x / groups, run = blockIdx.x / groups, group = blockIdx.x % groups;

@@ -59,6 +59,20 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
 struct Head {
     int n, parts, first_slot, pad;            // n = -1: none
 };
+// Whether a block's shared memory does not start at a multiple of 1024 bytes, as its declaration says and swizzled tiles
+// need.  Such a block computes nothing: it reports itself, and leaves the join, which reads every block's header, one that
+// names no sequence.  (With -DKDA_TEST_MISALIGNED every block is taken for one, to test just that.)
+__device__ __forceinline__ bool misaligned(const void* sm, const LatentDecodeArgs& a) {
+#ifndef KDA_TEST_MISALIGNED
+    if ((smem_u32(sm) & 1023u) == 0) return false;
+#endif
+    wait_before();                            // the call before may still read its headers there
+    if (threadIdx.x == 0) {
+        reinterpret_cast<Head*>(a.workspace)[blockIdx.x] = Head{-1, 0, 0, 0};
+        atomicOr(a.status, kStatusTimeout);
+    }
+    return true;
+}
 template <int NR>
 struct Work {
     static __host__ __device__ size_t ml_at(int grid) { return ((size_t)grid * sizeof(Head) + 255) / 256 * 256; }
