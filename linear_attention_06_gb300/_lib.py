@@ -420,15 +420,15 @@ def _on(stream, t):
     return torch.cuda.stream(stream)
 
 
-def _table(table, rows, t):
-    """A cu_seqlens argument: a CUDA tensor as it is, a host table validated (for ``rows``: a tensor of them, or their
-    number) and copied to t's device."""
+def _table(table, t, rows=None, tokens=None):
+    """A cu_seqlens argument: a CUDA tensor as it is, a host table validated (for the tensor ``rows``, or for a number of
+    tokens) and copied to t's device."""
     if table is None or (isinstance(table, torch.Tensor) and table.is_cuda):
         return table
     if not t.is_cuda:
         raise ValueError("tensor arguments must be CUDA tensors")
     host = torch.as_tensor(table, dtype=torch.int32).cpu()
-    kda_check_cu_seqlens(host, rows.shape[0] if isinstance(rows, torch.Tensor) else rows)
+    kda_check_cu_seqlens(host, tokens if rows is None else rows.shape[0])
     return host.to(t.device)
 
 
@@ -448,7 +448,7 @@ def kda_latent_append(latent, k_rope, cache, block_table, seq_lens, inv_freq=Non
             return kda_latent_append(latent, k_rope, cache, block_table, seq_lens, inv_freq, interleaved, q_rope,
                                      q_rope_out, cu_seqlens)
     return (_native or _latent()).append(latent, k_rope, cache, block_table, seq_lens, inv_freq, interleaved, q_rope,
-                                         q_rope_out, _table(cu_seqlens, latent, cache))
+                                         q_rope_out, _table(cu_seqlens, cache, rows=latent))
 
 
 def kda_latent_gather(cache, block_table, cu_seqlens, total_tokens, starts=None, out=None, stream=None):
@@ -458,7 +458,7 @@ def kda_latent_gather(cache, block_table, cu_seqlens, total_tokens, starts=None,
         with _on(stream, cache):
             return kda_latent_gather(cache, block_table, cu_seqlens, total_tokens, starts, out)
     latent, k_rope = (None, None) if out is None else out
-    return (_native or _latent()).gather(cache, block_table, _table(cu_seqlens, total_tokens, cache), total_tokens, starts,
+    return (_native or _latent()).gather(cache, block_table, _table(cu_seqlens, cache, tokens=total_tokens), total_tokens, starts,
                                          latent, k_rope)
 
 
@@ -501,7 +501,7 @@ def kda_latent_append_q8(latent, k_rope, cache, scales, block_table, seq_lens, i
             return kda_latent_append_q8(latent, k_rope, cache, scales, block_table, seq_lens, inv_freq, interleaved,
                                         q_rope, q_rope_out, cu_seqlens)
     return (_native or _latent()).append_q8(latent, k_rope, cache, scales, block_table, seq_lens, inv_freq, interleaved,
-                                            q_rope, q_rope_out, _table(cu_seqlens, latent, cache))
+                                            q_rope, q_rope_out, _table(cu_seqlens, cache, rows=latent))
 
 
 def kda_latent_gather_q8(cache, scales, block_table, cu_seqlens, total_tokens, starts=None, out=None, stream=None):
@@ -511,7 +511,7 @@ def kda_latent_gather_q8(cache, scales, block_table, cu_seqlens, total_tokens, s
         with _on(stream, cache):
             return kda_latent_gather_q8(cache, scales, block_table, cu_seqlens, total_tokens, starts, out)
     latent, k_rope = (None, None) if out is None else out
-    return (_native or _latent()).gather_q8(cache, scales, block_table, _table(cu_seqlens, total_tokens, cache),
+    return (_native or _latent()).gather_q8(cache, scales, block_table, _table(cu_seqlens, cache, tokens=total_tokens),
                                             total_tokens, starts, latent, k_rope)
 
 
@@ -546,8 +546,8 @@ def kda_latent_prefill(q, k, v, k_rope, scale, cu_seqlens=None, cu_seqlens_k=Non
         with _on(stream, q):
             return kda_latent_prefill(q, k, v, k_rope, scale, cu_seqlens, cu_seqlens_k, num_seqs, out, lse)
     new = lse is True
-    return (_native or _latent()).prefill(q, k, v, k_rope, scale, _table(cu_seqlens, q, q),
-                                          _table(cu_seqlens_k, k, q), num_seqs, out,
+    return (_native or _latent()).prefill(q, k, v, k_rope, scale, _table(cu_seqlens, q, rows=q),
+                                          _table(cu_seqlens_k, q, rows=k), num_seqs, out,
                                           None if new else lse, new)
 
 

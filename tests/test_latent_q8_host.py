@@ -189,3 +189,27 @@ int main() {
     return 0;
 }
 """
+
+
+@pytest.mark.parametrize("total", [2, torch.tensor(2), torch.tensor([2])])
+@pytest.mark.parametrize("gather", [kda.kda_latent_gather, kda.kda_latent_gather_q8])
+def test_a_host_table_takes_its_total_from_a_tensor_too(gather, total, monkeypatch):
+    """total_tokens as the table's own last entry, a number or a tensor of one: validated and handed on as it is."""
+    class Cuda:                                                # a cache that says it is on a device
+        is_cuda, device = True, torch.device("cpu")
+
+    class Native:
+        @staticmethod
+        def gather(cache, table, cu, tokens, *rest):
+            return cu, tokens
+
+        @staticmethod
+        def gather_q8(cache, scales, table, cu, tokens, *rest):
+            return cu, tokens
+
+    monkeypatch.setattr(_lib, "_native", Native)
+    cache = (Cuda(),) if gather is kda.kda_latent_gather else (Cuda(), None)
+    cu, tokens = gather(*cache, None, [0, 1, 2], total)
+    assert cu.tolist() == [0, 1, 2] and tokens is total
+    with pytest.raises(kda.KdaError):
+        gather(*cache, None, [0, 1, 3], total)
