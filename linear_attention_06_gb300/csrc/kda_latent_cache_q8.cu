@@ -28,8 +28,8 @@ __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(
 
 // TOK tokens a block, a warp a row: a lane has two chunks of eight latent channels and one pair of rotated ones, so that
 // a row's largest magnitude is one reduction of the warp.  As in the bf16 append, rows and queries are requested before
-// anything else and arrive while the block finds its tokens' sequences, pages and angles.  Four blocks an SM (8 prompts
-// of up to 2048 tokens, 32 heads, written and read back: 21.7 us; 22.9 with three, 25.3 with five).
+// anything else and arrive while the block finds its tokens' sequences, pages and angles.  Four blocks an SM (8 x
+// 1000 tokens, 32 heads: 12.8 us; 13.9 with three, 15.9 with five).
 template <int TOK, Turning TURN>
 __global__ void __launch_bounds__(kThreads, 4) append_kernel(const LatentAppendArgs a) {
     static_assert(TOK <= kWarps, "a warp a token");
@@ -216,10 +216,11 @@ cudaError_t gather(const LatentGatherArgs& a, bool overlapped, cudaStream_t s) {
 }  // namespace
 
 // As in bf16: calls of few tokens take few rows a block, so that every SM has some, and are launched plainly; they end
-// sooner than the host makes the next call.  Rows a block for many: a gather of 16 x 16384 rows takes 47.8 us with 16, 57.0
-// with 8, 49.8 with 32, 55.7 with 64; prompts of 8 x 2048 tokens are appended in 25 us with 8 tokens a block, 56 with one.
+// sooner than the host makes the next call.  Tokens a block of an append, 32 heads: 1024 tokens take 6.3 us with 8, 9.8 with
+// one, 1536 8.3 and 12.4, 8000 13.1 and 39.8; up to 512 the host's 6.3 us bound both.  Rows a block of a gather: 140000 take
+// 38.4 us with 16, 45.1 with 8, 39.8 with 32, 63.6 with 4; 16000 5.8 with 16, 7.7 with 4; 4096 3.5 with either.
 cudaError_t launch_latent_append_q8(const LatentAppendArgs& a, cudaStream_t s) {
-    return a.total_tokens < 2048 ? append<1>(a, false, s) : append<8>(a, true, s);
+    return a.total_tokens < 1024 ? append<1>(a, false, s) : append<8>(a, true, s);
 }
 
 cudaError_t launch_latent_gather_q8(const LatentGatherArgs& a, cudaStream_t s) {
