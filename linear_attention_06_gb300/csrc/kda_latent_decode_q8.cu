@@ -43,12 +43,13 @@
 // into W.
 //
 // Measured (GB300, 6761 GB/s measured copy rate; ragged lengths of 1/4 to all of the stated context), one token: 64
-// sequences of up to 8192, 32 heads, 45.7 us (0.60 of that rate; bf16 cache 70 us); 64 heads 58.6 us, 749 TFLOP/s; 256 of up
-// to 8192, no rope, 128.4 us (0.78; bf16 209 us); one of 131072 25.9 us (0.43; bf16 36.6 us).  What is missing, at 32 heads:
-// 17% in the tiles (a tile's 3400 cycles are a chain: its load behind freed slots, 900 cycles of products for S, 1700 from S
-// to W, 1000 of products for O; the slots hold two tiles and a half), and what is fixed: 1.6 us until a block knows its run,
-// 3 us until its queries are quantised, 2 us from its last row to its stored result, 4 us of join.  At 64 heads the slots
-// hold two tiles and the chain takes 4100 cycles.
+// sequences of up to 8192, 32 heads, 47.2 us (0.58 of that rate; bf16 cache 69.9 us); 64 heads 64.0 us, 686 TFLOP/s (bf16
+// 77.2 us); 256 of up to 8192, no rope, 135 us (0.74; bf16 210 us); one of 131072 26.8 us (0.42; bf16 36.7 us).  What is
+// missing, at 32 heads: a fifth in the tiles (a tile's 3500 cycles are a chain: its load behind freed slots, 900 cycles of
+// products for S, 1700 from S to W, 1000 of products for O; the slots hold two tiles and a half), and what is fixed: 1.6 us
+// until a block knows its run, 3 us until its queries are quantised, 2 us from its last row to its stored result, 4 us of
+// join.  At 64 heads the slots hold two tiles, the chain takes 4500 cycles, and the accounts are part of it (without them 58.6
+// us).
 #include <atomic>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -71,15 +72,15 @@ using namespace sm103;
 
 constexpr int kRows = 128;                    // cached rows a tile
 // Softmax warps work in teams of four (a warp for each quarter of a tile's tokens), the rows shared by the teams: sixteen a
-// team (64 x 8192 cached tokens, 64 heads: 63.7 us with four teams, 69.6 with two; 32 heads: 51.8 with four, 50.4 with two).
+// team (64 x 8192 cached tokens, 32 heads: 47.9 us, with four teams of eight 50.3; 256 x 8192, no rope, 138 and 147).
 constexpr int teams_of(int nr) { return nr >= 64 ? 4 : 2; }
 constexpr int soft_of(int nr) { return 128 * teams_of(nr); }
 constexpr int threads_of(int nr) { return 128 + soft_of(nr); }       // before them: producer, issuer, queries, (TMEM)
 constexpr int kBar = 1;                       // named barriers: all softmax warps; behind it one for each team
 // The line (kda_latent_line.cuh): a piece's start and end take a block as long as three tiles (64 x 8192 cached tokens, 32
-// heads: 47.2 us, 48.8 with one place; 32 x 4096, 4 tokens x 16 heads: 30.4, 32.8; with four places 48.0 and 30.5), and
-// sequences of at most three tiles are not cut (57 of up to 1084, 8 tokens x 12 heads: 35.5 us, 38.4 with four; 182 of up to
-// 285, 64 heads: 28.9, 30.3 with one).
+// heads: 47.8 us, 49.4 with one place; 32 x 4096, 4 tokens x 16 heads: 31.0, 32.9; with four places 47.8 and 30.9), and
+// sequences of at most three tiles are not cut (before the accounts, 57 of up to 1084, 8 tokens x 12 heads: 35.5 us, 38.4
+// with four; 182 of up to 285, 64 heads: 28.9, 30.3 with one).
 constexpr int kPlaces = 3, kShort = 3;
 constexpr float kDeep = 30.f;                 // log2 of how far a reference may lie below the highest before it
 // The sums of p are those of the weights times 2^-e, in units of 2^m too, while all rows' e are at most this: a row's sum is
@@ -319,8 +320,8 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
                     ++rope_loads;
                 }
                 // The next tile into L2 behind this one's loads, where a request fetches 64 rows or more: its own loads
-                // wait for ring slots and then find it near (64 x 8192 cached tokens, 32 heads: 55.4 us, 58.2 without; two
-                // tiles ahead 57.0, three 58.2; pages of 16 gain nothing).
+                // wait for ring slots and then find it near (64 x 8192 cached tokens, 32 heads: 47.8 us, 49.8 without;
+                // pages of 16 gain nothing).
                 const int next_live = live - kRows - lane * box;
                 if (box >= 64 && next_row >= 0 && next_row < map_rows && next_live > 0)
                     bulk_prefetch_l2(static_cast<const uint8_t*>(a.c.cache) + (int64_t)next_row * kWidth,

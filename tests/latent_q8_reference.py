@@ -9,9 +9,10 @@ Bounds, beside those of tests/latent_reference.py.
   row's and changes from tile to tile (128 cached rows).  e4m3 leaves at most 2^-4 of a weight of 2^-6 or more (in units of
   the reference).  Of that the second number, e5m2 with three significant bits, leaves 2^-3 / 2 and so 2^-8 in all (U);
   e4m3 of 2^7 times the rest, with four bits, leaves half as much.  Of a smaller weight e4m3 leaves at most 2^-10, of which
-  e5m2 leaves 2^-13 (e4m3 of 2^7 times it: 2^-14); both end at 2^-17.  A tile's largest weight may lie below 2^-5 at most
-  twice in turn (the third such tile lowers the reference), so that the largest among a tile and the two before it is 2^-5
-  or more, and a weight is off by at most 2^-13 = 2^-8 * 2^-5: 2^-8 of that largest one.
+  e5m2 leaves 2^-13 (e4m3 of 2^7 times it: 2^-14); both end at 2^-17.  A row's weights together are off by at most 2^-7 of
+  their sum.  The bound here is looser: 2^-8 of the largest weight among a tile and the two before it for every weight,
+  which is 2^-8 of the sum where all weights are alike and more where a few are bright.  What faint weights beside bright
+  ones may lose is tested in tests/test_latent_q8_weights_gpu.py, with 2^-7 of the sum.
 - The reference is not the maximum: the exponent of the largest weight lies in -5 .. 9 and not at 0, is rounded to 2^-21 at
   most, and the exponential of it is good to 2^-22.  A weight moves by a share of 2^-21 ln 2 + 2^-22, and so does the sum:
   2^-20 bounds the two logarithms' roundings with it (lse near 0 would otherwise have no room for them).
