@@ -843,9 +843,10 @@ latent_decode_q8_kernel(const __grid_constant__ Maps maps, const LatentDecodeArg
             if (t < NR) {
                 const float* part = &sw->red[t / NH][0][t % NH];
                 const float total = fmaf((part[0] + part[16]) + (part[32] + part[48]), sw->unit[t], sw->move[t]);
-                // total 2^(m + off) = f 2^k, f in [1, 2): no large m against a large logarithm, here and in the join
+                // total 2^(m + off) = f 2^k: no large m against a large logarithm, here and in the join.  f is in [1, 2), and
+                // in [2^-10, 2^-9) where the join adds up to 152 pieces' f times their mean: values end above 2^127
                 const float off = sw->off[t];
-                const int power = (int)(__float_as_uint(total) >> 23) - 127;
+                const int power = (int)(__float_as_uint(total) >> 23) - 127 + (whole ? 0 : 10);
                 const float f = total == 0.f ? 0.f : total * two_to(-power), k = total == 0.f ? -INFINITY : (float)power + (off - sw->ref[t]);
                 if (whole) {
                     const int64_t row = (int64_t)p.n * R + group * NR + t;
